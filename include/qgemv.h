@@ -313,7 +313,8 @@ QGEMV_API int qgemv_last_cuda_error(void);
  * 44..51 per-channel INT8 W8A16 (one count per GEMV launch at m <= 8); 53 launches of the 16-row build
  * (m = 9..16, any format); 52 launches with the fused argmax; 33 launches that quantized fp32
  * activations in-kernel, 34 launches over >= 2 matrices, 35 launches with programmatic dependent launch
- * (quantizer included), 54 launches that covered one K-chunk of long rows.
+ * (quantizer included), 54 launches that covered one K-chunk of long rows; 55 rotary positions, 56 and 57
+ * attention (which kernel ran), 58 sampling.
  */
 #define QGEMV_ROUTE_FUSED 33
 #define QGEMV_ROUTE_GROUPED 34
@@ -323,7 +324,11 @@ QGEMV_API int qgemv_last_cuda_error(void);
 #define QGEMV_ROUTE_ARGMAX 52
 #define QGEMV_ROUTE_M16 53 /* a launch of the 16-row build (m = 9..16), any format */
 #define QGEMV_ROUTE_CHUNKED 54 /* a launch that covered one K-chunk of the rows (also counted by format) */
-#define QGEMV_NUM_ROUTES 55
+#define QGEMV_ROUTE_ROPE 55        /* qgemv_rope launches */
+#define QGEMV_ROUTE_ATTN_ROWS 56   /* qgemv_attn launches of the 16-row kernel (decode, drafts) */
+#define QGEMV_ROUTE_ATTN_TILES 57  /* qgemv_attn launches of the 128-row tensor-memory kernel (chunks, prompts) */
+#define QGEMV_ROUTE_SAMPLE 58      /* qgemv_sample launches */
+#define QGEMV_NUM_ROUTES 59
 QGEMV_API int qgemv_route_counts(unsigned long long* out, int n);
 QGEMV_API void qgemv_route_reset(void);
 
@@ -393,6 +398,173 @@ QGEMV_API int qgemv_device_error(unsigned int* out, int reset);
 QGEMV_API int qgemv_trace_info(int* launches, int* ctas, int* fields);
 QGEMV_API int qgemv_trace_begin(void);
 QGEMV_API int qgemv_trace_read(unsigned long long* host, size_t bytes, int* launches);
+
+/*
+ * ---------------------------------------------------------------------------------------------------
+ * The operators between the GEMVs of a serving step: rotary positions with the write into a paged cache,
+ * attention of new tokens over that cache, and sampling from the lm_head's logits.  They follow the common
+ * rules above (caller-owned device memory, host-side checks before anything is enqueued, results in stream
+ * order, QGEMV_FLAG_PDL) and serve any number of tokens, not only 1..16.  They serve inference: no gradients.
+ */
+
+/*
+ * A paged key/value cache.  Token `o` of page `p`, key/value head `h`, is the `dim` consecutive 16-bit values at
+ * element offset p * k_page + o * k_token + h * k_head of `k` (and likewise of `v`), so both [page, token, head,
+ * dim] and [page, head, token, dim] orders, and caches inside a larger allocation, are described by strides.
+ * kind: QGEMV_ACT_BF16 or QGEMV_ACT_F16.  k, v: 16-byte aligned; strides non-negative multiples of 8 elements.
+ * num_pages, page_size, heads >= 1; dim a multiple of 8, 8..256.  Slot s of the cache is token s % page_size of page
+ * s / page_size.
+ */
+typedef struct {
+    void* k;
+    void* v;
+    long long k_page, k_token, k_head; /* strides, elements */
+    long long v_page, v_token, v_head;
+    int kind;
+    int num_pages, page_size, heads, dim;
+} qgemv_cache;
+
+/* Pairing of the rotated elements of a head. */
+typedef enum {
+    QGEMV_ROPE_HALF = 0,       /* element i with element i + rot_dim/2 */
+    QGEMV_ROPE_INTERLEAVED = 1 /* element 2i with element 2i + 1       */
+} qgemv_rope_layout;
+
+/* Scaling of the rotary frequencies for contexts longer than the trained one (qgemv_rope_freqs). */
+typedef enum {
+    QGEMV_ROPE_SCALE_NONE = 0,
+    QGEMV_ROPE_SCALE_LINEAR = 1, /* every frequency divided by `factor` */
+    QGEMV_ROPE_SCALE_BASE = 2,   /* theta multiplied by factor^(rot_dim / (rot_dim - 2)): the slowest pair is slowed by
+                                    `factor`, the fastest keeps its frequency                                           */
+    QGEMV_ROPE_SCALE_PARTS = 3,  /* pairs that turn fewer than `low` times over `trained` positions are divided by
+                                    `factor`, those that turn more than `high` times are kept, a ramp linear in the pair
+                                    index lies between; *mscale = 0.1 ln(factor) + 1                                     */
+    QGEMV_ROPE_SCALE_BANDS = 4   /* wavelengths above trained/low divided by `factor`, below trained/high kept, between
+                                    them a ramp linear in trained/wavelength                                             */
+} qgemv_rope_scaling;
+
+/*
+ * Rotary frequencies, host arithmetic in 64 bits: out[i], i < rot_dim/2, is the turn of pair i per position in units of
+ * 2^-64 of a turn, round(f_i / (2 pi) * 2^64) with f_i = theta^(-2i/rot_dim), scaled as asked.  The caller copies the
+ * rot_dim/2 values to the device once.  The angle of position p is then 2 pi * frac(p * out[i] / 2^64): the product
+ * wraps in 64-bit integer arithmetic, so whole turns fall away exactly and a position of a million is as exact as
+ * position 1.  *mscale (may be NULL) receives the factor of the rotated values that the scaling asks for (1 unless
+ * QGEMV_ROPE_SCALE_PARTS).  out is HOST memory.
+ * rot_dim even, 2..256; theta > 1; factor >= 1 except for NONE; trained >= 1 and 0 < low < high for PARTS and BANDS.
+ */
+QGEMV_API int qgemv_rope_freqs(int rot_dim, double theta, int scaling, double factor, double trained, double low,
+                               double high, unsigned long long* out, float* mscale);
+
+/*
+ * Rotary positions of new tokens' queries and keys, with the write of keys and values into a paged cache:
+ *     (a, b) -> (mscale (a cos t - b sin t), mscale (b cos t + a sin t)),  t = angle of the token's position and the pair
+ * for the first rot_dim elements of every query and key head; the other elements, and the values, are copied.  The
+ * arithmetic is fp32 and each result is rounded once to the type it is stored in.
+ *
+ * q [tokens, heads, dim], k and v [tokens, kv_heads, dim], of kind x_kind (QGEMV_ACT_F32: a GEMV's output, e.g. three
+ * slices of one qkv row; QGEMV_ACT_BF16; QGEMV_ACT_F16), the last dimension contiguous, token and head strides in elements.
+ * q_out [tokens, heads, dim] and k_out [tokens, kv_heads, dim]: QGEMV_ACT_BF16 / QGEMV_ACT_F16 / QGEMV_ACT_F32 by
+ * out_kind.  cache (may be NULL): rotated keys and the values go to slot slots[t] of it (of the cache's kind); a
+ * negative slot writes nothing (a padding token).  A slot beyond the cache writes nothing and sets
+ * QGEMV_DEVERR_BAD_INDEX in the device error word.  Slots that are >= 0 must differ: two tokens with one slot leave
+ * unspecified values there.
+ * q with q_out, or k with k_out and / or a cache, may be left out (NULL, and heads or kv_heads 0); v goes with the cache.
+ * q_out may be q itself and k_out k itself (same kind and strides); other overlaps of an output with an input, or of
+ * outputs, are refused.  positions: int[tokens] (any 32-bit value; negative positions turn backwards).
+ * freqs: device copy of qgemv_rope_freqs' output, 8-byte aligned.  rot_dim even, 2..dim; dim a multiple of 8, 8..256.
+ * Pointers 16-byte aligned; strides multiples of 16 bytes (of 8 elements for fp32).  tokens = 0 is valid and does nothing.
+ */
+typedef struct {
+    const void* q;
+    const void* k;
+    const void* v;
+    void* q_out;
+    void* k_out;
+    long long q_token, q_head, k_token, k_head, v_token, v_head; /* strides, elements */
+    long long q_out_token, q_out_head, k_out_token, k_out_head;
+    const int* positions;
+    const unsigned long long* freqs;
+    const qgemv_cache* cache;
+    const long long* slots;
+    int x_kind, out_kind;
+    int tokens, heads, kv_heads, dim, rot_dim;
+    int layout; /* qgemv_rope_layout */
+    float mscale;
+} qgemv_rope_args;
+
+QGEMV_API int qgemv_rope(const qgemv_rope_args* args, unsigned flags, void* stream);
+
+/*
+ * Attention of new tokens over a paged cache.  Sequence b (b < seqs) has the new tokens q_start[b] .. q_start[b+1] - 1 of
+ * q (n_b of them, 0 allowed) and a context of kv_len[b] tokens in the cache, the new ones included: context token t is
+ * token t % page_size of page pages[b * pages_stride + t / page_size].  New token j sits at position
+ * kv_len[b] - n_b + j.  With query head h reading key/value head h / (heads / cache->heads):
+ *     s_t = scale * <q, k_t>,  out = sum_t softmax(s)_t v_t,  lse = ln sum_t exp(s_t)
+ * over the context tokens t that the new token sees: all of them, or with causal != 0 those up to its own position, and
+ * with window > 0 only the `window` tokens that end at its position.  A token that sees nothing (a context of length 0, or
+ * a position below 0) gets out = 0 and lse = -inf.
+ * Scores, softmax statistics and sums are fp32; the probabilities meet the values in the 16-bit type of q (each rounded
+ * once, unnormalised, their sum taken before the rounding); out is rounded once.
+ *
+ * kind (QGEMV_ACT_BF16 / QGEMV_ACT_F16): type of q and out, and the cache's.  q, out [tokens, heads, cache->dim], last
+ * dimension contiguous, 16-byte aligned, strides multiples of 8 elements.  lse: fp32 [tokens, heads] or NULL.
+ * max_q, max_kv: bounds of n_b and kv_len[b] over the batch, for the launch's shape (a loose bound costs idle blocks);
+ * the values on the device must keep to them: tokens beyond max_q are left unwritten, context beyond max_kv or beyond the
+ * row of the page table (pages_stride * page_size) is not read.  A page number outside the cache reads as if its tokens
+ * were masked and sets QGEMV_DEVERR_BAD_INDEX in the device error word.
+ * What lies in the cache beyond kv_len is never used, whatever its bits.  Keys and values inside the context must be finite.
+ * scratch: at least qgemv_attn_scratch_bytes(...) bytes, 16-byte aligned, whose first QGEMV_ATTN_SCRATCH_HEAD bytes must be
+ * zero before the first call (e.g. cudaMemset once); each call leaves them zero again, so calls of any sizes may share one
+ * scratch that is large enough for each.  Calls that share a scratch must be ordered.
+ * The result does not depend on timing: parts of a long context are joined in a fixed order.
+ * heads a multiple of cache->heads.  tokens = 0 or seqs = 0 does nothing.
+ */
+typedef struct {
+    const void* q;
+    void* out;
+    float* lse;
+    long long q_token, q_head, out_token, out_head; /* strides, elements */
+    const qgemv_cache* cache;
+    const int* pages;
+    long long pages_stride;
+    const int* q_start; /* [seqs + 1] */
+    const int* kv_len;  /* [seqs] */
+    void* scratch;
+    size_t scratch_bytes;
+    int kind;
+    int tokens, heads, seqs;
+    int max_q, max_kv;
+    float scale;
+    int causal, window;
+} qgemv_attn_args;
+
+QGEMV_API int qgemv_attn(const qgemv_attn_args* args, unsigned flags, void* stream);
+/* Scratch of a call with these sizes (0 for invalid sizes).  No device needed. */
+#define QGEMV_ATTN_SCRATCH_HEAD 65536
+QGEMV_API size_t qgemv_attn_scratch_bytes(int seqs, int tokens, int heads, int kv_heads, int dim, int max_q, int max_kv);
+
+/*
+ * Sampling: one token per row of logits [m, N] (kind QGEMV_ACT_F32 / BF16 / F16, rows `row_stride` elements apart), from
+ * one given uniform number u[i] in [0, 1) per row.  With top = max_n x_n and T = temperature[i]:
+ *     e_n = exp((x_n - top) * (1 / T)),  w_n = floor(2^42 e_n)
+ * (fp32 up to e_n; the w_n are whole numbers, so their sums are exact and do not depend on any order).  Tokens are ranked by
+ * x_n, ties by the lower index.  A token is kept if its rank is below top_k[i], the w before it in that order sum to less
+ * than top_p[i] times the sum of those that top_k keeps (the products in fp64), and e_n >= min_p[i]; rank 0 is always kept.  With W the sum
+ * of the kept w, the token is the first n, in index order, whose running sum of kept w exceeds floor(u[i] * W).
+ * token_out[i]: that n; prob_out[i] (may be NULL): e_n * 2^42 / W.
+ * temperature <= 0 is greedy (rank 0, prob 1).  top_k <= 0, top_p >= 1 and min_p <= 0 filter nothing; NULL for any of the
+ * four means: temperature 1, no filter.
+ * -inf logits are never taken; a row of nothing but -inf gives token -1 and prob 0.  A row with a NaN gives the first NaN's
+ * index, else a row with +inf the first +inf's, with prob NaN: the caller's model has failed there.
+ * logits: 16-byte aligned; row_stride >= N (any, but rows that all start 16-byte aligned are read faster).
+ * 1 <= N <= 2^20; m >= 0 (0 does nothing).  token_out, prob_out must not overlap the inputs or each other.
+ */
+QGEMV_API int qgemv_sample(int kind, const void* logits, long long row_stride, int m, int N, const float* temperature,
+                           const int* top_k, const float* top_p, const float* min_p, const float* u, int* token_out,
+                           float* prob_out, unsigned flags, void* stream);
+
+/* Bit of the device error word: an index in device memory (cache slot, page number) was outside its range and skipped. */
+#define QGEMV_DEVERR_BAD_INDEX 4u
 
 #ifdef __cplusplus
 }

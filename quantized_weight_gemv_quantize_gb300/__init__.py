@@ -21,18 +21,50 @@ QGEMV_FLAG_PDL = 1
 QGEMV_FLAG_PDL_LATE_TRIGGER = 2
 QGEMV_MAX_GROUP = 8
 QGEMV_ARGMAX_STATIC_SCRATCH_BYTES = 16384
+QGEMV_ROPE_HALF, QGEMV_ROPE_INTERLEAVED = 0, 1
+ROPE_LAYOUT = {"half": QGEMV_ROPE_HALF, "interleaved": QGEMV_ROPE_INTERLEAVED}
+ROPE_SCALING = {"none": 0, "linear": 1, "base": 2, "parts": 3, "bands": 4}
+QGEMV_ATTN_SCRATCH_HEAD = 65536
+QGEMV_DEVERR_BAD_INDEX = 4
 ROUTE_FUSED, ROUTE_GROUPED, ROUTE_PDL, ROUTE_Q5_K_M1, ROUTE_W8A16_CHANNEL_M1, ROUTE_ARGMAX, ROUTE_M16 = (
     33, 34, 35, 36, 44, 52, 53)
 ROUTE_CHUNKED = 54
+ROUTE_ROPE, ROUTE_ATTN_ROWS, ROUTE_ATTN_TILES, ROUTE_SAMPLE = 55, 56, 57, 58
 STATUS = {0: "QGEMV_OK", 1: "QGEMV_ERR_INVALID_ARG", 2: "QGEMV_ERR_UNSUPPORTED", 3: "QGEMV_ERR_MISALIGNED",
           4: "QGEMV_ERR_CUDA", 5: "QGEMV_ERR_DEVICE", 6: "QGEMV_ERR_OVERLAP"}
-NUM_ROUTES = 55
+NUM_ROUTES = 59
 
 _lib = None
 
 
 class QgemvMat(ctypes.Structure):
     _fields_ = [("W", ctypes.c_void_p), ("y", ctypes.c_void_p), ("N", ctypes.c_int)]
+
+
+_i32, _i64, _vp, _f32 = ctypes.c_int, ctypes.c_longlong, ctypes.c_void_p, ctypes.c_float
+
+
+class QgemvCache(ctypes.Structure):
+    _fields_ = [("k", _vp), ("v", _vp), ("k_page", _i64), ("k_token", _i64), ("k_head", _i64), ("v_page", _i64),
+                ("v_token", _i64), ("v_head", _i64), ("kind", _i32), ("num_pages", _i32), ("page_size", _i32),
+                ("heads", _i32), ("dim", _i32)]
+
+
+class QgemvRopeArgs(ctypes.Structure):
+    _fields_ = [("q", _vp), ("k", _vp), ("v", _vp), ("q_out", _vp), ("k_out", _vp), ("q_token", _i64),
+                ("q_head", _i64), ("k_token", _i64), ("k_head", _i64), ("v_token", _i64), ("v_head", _i64),
+                ("q_out_token", _i64), ("q_out_head", _i64), ("k_out_token", _i64), ("k_out_head", _i64),
+                ("positions", _vp), ("freqs", _vp), ("cache", ctypes.POINTER(QgemvCache)), ("slots", _vp),
+                ("x_kind", _i32), ("out_kind", _i32), ("tokens", _i32), ("heads", _i32), ("kv_heads", _i32),
+                ("dim", _i32), ("rot_dim", _i32), ("layout", _i32), ("mscale", _f32)]
+
+
+class QgemvAttnArgs(ctypes.Structure):
+    _fields_ = [("q", _vp), ("out", _vp), ("lse", _vp), ("q_token", _i64), ("q_head", _i64), ("out_token", _i64),
+                ("out_head", _i64), ("cache", ctypes.POINTER(QgemvCache)), ("pages", _vp), ("pages_stride", _i64),
+                ("q_start", _vp), ("kv_len", _vp), ("scratch", _vp), ("scratch_bytes", ctypes.c_size_t),
+                ("kind", _i32), ("tokens", _i32), ("heads", _i32), ("seqs", _i32), ("max_q", _i32), ("max_kv", _i32),
+                ("scale", _f32), ("causal", _i32), ("window", _i32)]
 
 
 class QgemvError(RuntimeError):
@@ -105,6 +137,17 @@ def lib():
         L.qgemv_plan_info_chunk.restype = i32
         L.qgemv_tune_override.argtypes = [i32, i32, i32, i32, i32]
         L.qgemv_tune_override.restype = None
+        dbl, u64p = ctypes.c_double, ctypes.POINTER(ctypes.c_ulonglong)
+        L.qgemv_rope_freqs.argtypes = [i32, dbl, i32, dbl, dbl, dbl, dbl, u64p, ctypes.POINTER(ctypes.c_float)]
+        L.qgemv_rope_freqs.restype = i32
+        L.qgemv_rope.argtypes = [ctypes.POINTER(QgemvRopeArgs), ctypes.c_uint, vp]
+        L.qgemv_rope.restype = i32
+        L.qgemv_attn.argtypes = [ctypes.POINTER(QgemvAttnArgs), ctypes.c_uint, vp]
+        L.qgemv_attn.restype = i32
+        L.qgemv_attn_scratch_bytes.argtypes = [i32] * 7
+        L.qgemv_attn_scratch_bytes.restype = sz
+        L.qgemv_sample.argtypes = [i32, vp, ctypes.c_longlong, i32, i32, vp, vp, vp, vp, vp, vp, vp, ctypes.c_uint, vp]
+        L.qgemv_sample.restype = i32
         ip = ctypes.POINTER(ctypes.c_int)
         L.qgemv_trace_info.argtypes = [ip, ip, ip]
         L.qgemv_trace_info.restype = i32
@@ -248,6 +291,150 @@ def qgemv_multi(fmt, mats, act_kind, act, m: int, K: int, xq_out=None, flags: in
     kind = ACT[act_kind] if isinstance(act_kind, str) else int(act_kind)
     _check(lib().qgemv_multi(_fmt(fmt), len(arr), arr, kind, _ptr(act), _ptr(xq_out), m, K, flags,
                              _stream(stream)), "qgemv_multi")
+
+
+_TORCH_ACT = {"torch.float32": QGEMV_ACT_F32, "torch.bfloat16": QGEMV_ACT_BF16, "torch.float16": QGEMV_ACT_F16}
+
+
+def _kind(t):
+    """QGEMV_ACT_* of a tensor's type; types outside the library's are refused."""
+    if str(t.dtype) not in _TORCH_ACT:
+        raise QgemvError(1, f"tensor of {t.dtype}")
+    return _TORCH_ACT[str(t.dtype)]
+
+
+def _need(ok, what):
+    if not ok:
+        raise QgemvError(1, what)
+
+
+def _typed(t, dtype, what):
+    """A contiguous tensor of the given type (or a raw address, which is passed on as it is)."""
+    if t is None or isinstance(t, int):
+        return t
+    _need(str(t.dtype) == "torch." + dtype and t.is_contiguous(), f"{what}: a contiguous {dtype} tensor")
+    return t
+
+
+def kv_cache(k, v) -> QgemvCache:
+    """The paged cache of two tensors [pages, page_size, heads, dim] (views with any strides; a [pages, heads, page_size,
+    dim] allocation is passed as ``t.transpose(1, 2)``).  Keep the tensors alive as long as the result."""
+    _need(k.dim() == 4 and k.shape == v.shape and k.dtype == v.dtype, "kv_cache: k and v alike, of four dimensions")
+    _need(k.stride(3) == 1 and v.stride(3) == 1, "kv_cache: the last dimension contiguous")
+    c = QgemvCache(_ptr(k), _ptr(v), *k.stride()[:3], *v.stride()[:3], _kind(k), *k.shape)
+    c.tensors = (k, v)
+    return c
+
+
+def _heads_first(t, what):
+    _need(t.dim() == 3 and t.stride(2) == 1, f"{what}: [tokens, heads, dim], the last dimension contiguous")
+    return t.stride(0), t.stride(1)
+
+
+def qgemv_rope_freqs(rot_dim: int, theta: float = 10000.0, scaling="none", factor: float = 1.0, trained: float = 0.0,
+                     low: float = 1.0, high: float = 32.0):
+    """(frequencies, mscale): a CPU int64 tensor of rot_dim/2 turns per position in units of 2^-64, to be copied to the
+    device once, and the factor of the rotated values.  scaling: "none", "linear", "base", "parts" or "bands"."""
+    import torch
+    out = (ctypes.c_ulonglong * max(1, rot_dim // 2))()
+    ms = ctypes.c_float()
+    code = ROPE_SCALING[scaling] if isinstance(scaling, str) else int(scaling)
+    _check(lib().qgemv_rope_freqs(rot_dim, theta, code, factor, trained, low, high, out, ctypes.byref(ms)),
+           "qgemv_rope_freqs")
+    return torch.tensor([ctypes.c_longlong(v).value for v in out], dtype=torch.int64), float(ms.value)
+
+
+def rope_args(q, k, v, positions, freqs, q_out=None, k_out=None, cache=None, slots=None, rot_dim=None, layout="half",
+              mscale: float = 1.0) -> QgemvRopeArgs:
+    """Arguments of qgemv_rope from tensors: q [tokens, heads, dim], k and v [tokens, kv_heads, dim] (q, or k with v, may
+    be None).  The result holds the tensors' addresses and keeps the tensors alive; it may be used for many calls."""
+    a = QgemvRopeArgs()
+    x = q if q is not None else k
+    _need(x is not None, "rope_args: q or k")
+    for t, name in ((q, "q"), (k, "k"), (v, "v")):
+        if t is not None:
+            token, head = _heads_first(t, f"rope_args: {name}")
+            _need(t.dtype == x.dtype and t.shape[0] == x.shape[0] and t.shape[2] == x.shape[2], f"rope_args: {name} unlike the others")
+            setattr(a, name, _ptr(t)), setattr(a, name + "_token", token), setattr(a, name + "_head", head)
+    out = q_out if q_out is not None else k_out
+    for t, src, name in ((q_out, q, "q_out"), (k_out, k, "k_out")):
+        if t is not None:
+            token, head = _heads_first(t, f"rope_args: {name}")
+            _need(src is not None and t.shape == src.shape and t.dtype == out.dtype, f"rope_args: {name} unlike its input")
+            setattr(a, name, _ptr(t)), setattr(a, name + "_token", token), setattr(a, name + "_head", head)
+    _need(v is None or (k is not None and v.shape == k.shape), "rope_args: v unlike k")
+    a.positions, a.freqs = _ptr(_typed(positions, "int32", "positions")), _ptr(_typed(freqs, "int64", "freqs"))
+    a.slots = _ptr(_typed(slots, "int64", "slots"))
+    a.tokens, a.dim = x.shape[0], x.shape[2]
+    a.heads, a.kv_heads = (0 if q is None else q.shape[1]), (0 if k is None else k.shape[1])
+    a.rot_dim = a.dim if rot_dim is None else rot_dim
+    for t, name, n in ((positions, "positions", a.tokens), (slots, "slots", a.tokens), (freqs, "freqs", a.rot_dim // 2)):
+        _need(t is None or isinstance(t, int) or t.numel() >= n, f"rope_args: {name} too short")
+    a.x_kind, a.out_kind = _kind(x), (_kind(out) if out is not None else _kind(x))
+    a.layout = ROPE_LAYOUT[layout] if isinstance(layout, str) else int(layout)
+    a.mscale = mscale
+    if cache is not None:
+        a.cache = ctypes.pointer(cache)
+    a.tensors = (q, k, v, q_out, k_out, positions, freqs, slots, cache)
+    return a
+
+
+def qgemv_rope(args: QgemvRopeArgs, flags: int = 0, stream=None) -> None:
+    """Rotary positions of q and k, with the write of k and v into the cache; args from rope_args()."""
+    _check(lib().qgemv_rope(args, flags, _stream(stream)), "qgemv_rope")
+
+
+def qgemv_attn_scratch_bytes(seqs: int, tokens: int, heads: int, kv_heads: int, dim: int, max_q: int, max_kv: int) -> int:
+    """Scratch of a qgemv_attn call with these sizes; its first QGEMV_ATTN_SCRATCH_HEAD bytes must start as zeros."""
+    return int(lib().qgemv_attn_scratch_bytes(seqs, tokens, heads, kv_heads, dim, max_q, max_kv))
+
+
+def attn_args(q, cache: QgemvCache, pages, q_start, kv_len, out, scratch, max_q: int, max_kv: int, scale: float,
+              causal: bool = True, window: int = 0, lse=None) -> QgemvAttnArgs:
+    """Arguments of qgemv_attn from tensors: q and out [tokens, heads, dim], pages int32 [seqs, pages of a row],
+    q_start int32 [seqs + 1], kv_len int32 [seqs], scratch uint8, lse fp32 [tokens, heads] or None.  The result holds the
+    tensors' addresses and keeps the tensors alive; it may be used for many calls."""
+    a = QgemvAttnArgs()
+    a.q_token, a.q_head = _heads_first(q, "attn_args: q")
+    a.out_token, a.out_head = _heads_first(out, "attn_args: out")
+    _need(q.shape == out.shape and q.dtype == out.dtype and q.shape[2] == cache.dim, "attn_args: q, out and the cache unlike")
+    _need(pages.dim() == 2 and str(pages.dtype) == "torch.int32" and (pages.shape[1] == 0 or pages.stride(1) == 1),
+          "attn_args: pages int32 [seqs, pages]")
+    a.q, a.out, a.lse = _ptr(q), _ptr(out), _ptr(_typed(lse, "float32", "lse"))
+    a.cache = ctypes.pointer(cache)
+    a.seqs = pages.shape[0]
+    # the table's row: its stride when rows are apart, and no more of it than there is
+    _need(a.seqs <= 1 or pages.stride(0) == pages.shape[1], "attn_args: pages contiguous")
+    a.pages, a.pages_stride = _ptr(pages), pages.shape[1]
+    a.q_start, a.kv_len = _ptr(_typed(q_start, "int32", "q_start")), _ptr(_typed(kv_len, "int32", "kv_len"))
+    _need(isinstance(q_start, int) or q_start.numel() == a.seqs + 1, "attn_args: q_start has seqs + 1 values")
+    _need(isinstance(kv_len, int) or kv_len.numel() == a.seqs, "attn_args: kv_len has seqs values")
+    _need(lse is None or isinstance(lse, int) or lse.shape == q.shape[:2], "attn_args: lse [tokens, heads]")
+    a.scratch, a.scratch_bytes = _ptr(scratch), scratch.numel() * scratch.element_size()
+    a.kind, a.tokens, a.heads = _kind(q), q.shape[0], q.shape[1]
+    a.max_q, a.max_kv, a.scale, a.causal, a.window = max_q, max_kv, scale, 1 if causal else 0, window
+    a.tensors = (q, cache, pages, q_start, kv_len, out, scratch, lse)
+    return a
+
+
+def qgemv_attn(args: QgemvAttnArgs, flags: int = 0, stream=None) -> None:
+    """Attention of new tokens over a paged cache; args from attn_args()."""
+    _check(lib().qgemv_attn(args, flags, _stream(stream)), "qgemv_attn")
+
+
+def qgemv_sample(logits, temperature, top_k, top_p, min_p, u, token_out, prob_out=None, flags: int = 0,
+                 stream=None) -> None:
+    """One token per row of logits [m, N] from the uniform numbers u [m]; temperature, top_p, min_p fp32 [m] and top_k
+    int32 [m], each or None."""
+    _need(logits.dim() == 2 and (logits.shape[1] <= 1 or logits.stride(1) == 1), "qgemv_sample: logits [m, N], rows contiguous")
+    m, n = logits.shape
+    for t, dtype, name in ((temperature, "float32", "temperature"), (top_k, "int32", "top_k"), (top_p, "float32", "top_p"),
+                           (min_p, "float32", "min_p"), (u, "float32", "u"), (token_out, "int32", "token_out"),
+                           (prob_out, "float32", "prob_out")):
+        _need(t is None or isinstance(t, int) or _typed(t, dtype, name).numel() == m, f"qgemv_sample: {name} has m values")
+    _check(lib().qgemv_sample(_kind(logits), _ptr(logits), logits.stride(0) if m > 1 else n, m, n, _ptr(temperature),
+                              _ptr(top_k), _ptr(top_p), _ptr(min_p), _ptr(u), _ptr(token_out), _ptr(prob_out), flags,
+                              _stream(stream)), "qgemv_sample")
 
 
 def qgemv_weight_bytes(fmt, N: int, K: int) -> int:

@@ -255,6 +255,23 @@ static bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
 
 static bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
+int api_device(int* sms, unsigned** err) {
+    DeviceInfo* dev = nullptr;
+    const int st = device_info(&dev);
+    if (st) return st;
+    *sms = dev->sms;
+    *err = dev->err;
+    return QGEMV_OK;
+}
+bool api_injected(int* status) { return take_injected_failure(status); }
+int api_cuda_fail(cudaError_t e) { return cuda_fail(e); }
+void api_route(int route, bool pdl) {
+    g_routes[route].fetch_add(1, std::memory_order_relaxed);
+    if (pdl) g_routes[QGEMV_ROUTE_PDL].fetch_add(1, std::memory_order_relaxed);
+}
+bool api_overlaps(const void* a, size_t na, const void* b, size_t nb) { return overlaps(a, na, b, nb); }
+bool api_aligned(const void* p, uintptr_t a) { return aligned(p, a); }
+
 // ---------------------------------------------------------------------------------------------------
 // Planner: lanes per row, rows per tile, ring depth, grid.  A deterministic function of
 // (variant, m, N, K, SM count).

@@ -128,4 +128,42 @@ cudaError_t launch_gemv(int variant, int kind, const GemvArgs& a, int grid, int 
 // late: the next kernel may start only after this one's own dependency wait (QGEMV_FLAG_PDL_LATE_TRIGGER).
 cudaError_t launch_quantize(int x_kind, const void* x, int m, int K, uint8_t* xq, bool pdl, bool late, cudaStream_t s);
 
+// Host services of api.cu for the other entry points: the current device (QGEMV_OK, or the status to return), the
+// failure-injection hook, the record of a CUDA error, the route counters and the pointer checks.
+int api_device(int* sms, unsigned** err);
+bool api_injected(int* status);
+int api_cuda_fail(cudaError_t e);
+void api_route(int route, bool pdl);
+bool api_overlaps(const void* a, size_t na, const void* b, size_t nb);
+bool api_aligned(const void* p, uintptr_t a);
+
+// A launch with optional programmatic dependent launch and cluster attributes.
+template <class Args>
+cudaError_t launch_step(const void* fn, dim3 grid, unsigned threads, unsigned smem, unsigned cluster, bool pdl,
+                        cudaStream_t s, const Args& a) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    unsigned n = 0;
+    if (pdl) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    if (cluster > 1) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = cluster;
+        attr[n].val.clusterDim.y = 1;
+        attr[n++].val.clusterDim.z = 1;
+    }
+    cfg.attrs = attr;
+    cfg.numAttrs = n;
+    Args copy = a;
+    void* args[] = {&copy};
+    cudaError_t e = cudaLaunchKernelExC(&cfg, fn, args);
+    return e != cudaSuccess ? e : cudaPeekAtLastError();
+}
+
 }  // namespace qg

@@ -1,0 +1,80 @@
+// Arguments of the kernels between the GEMVs (rotary positions, attention, sampling), shared by step_api.cu and the
+// kernels' translation units.
+#pragma once
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "../../include/qgemv.h"
+
+namespace qg {
+
+struct RopeArgs {
+    const void *q, *k, *v;
+    void *q_out, *k_out;
+    void *k_cache, *v_cache;
+    long long q_token, q_head, k_token, k_head, v_token, v_head;
+    long long q_out_token, q_out_head, k_out_token, k_out_head;
+    long long kc_page, kc_token, kc_head, vc_page, vc_token, vc_head;
+    const int* positions;
+    const unsigned long long* freqs;
+    const long long* slots;
+    unsigned* err;
+    int out_kind, cache_kind;
+    int tokens, heads, kv_heads, dim, rot;
+    int page_size;
+    long long num_slots;
+    float mscale;
+};
+
+// vec: heads are handled in 8-element pieces (the rotated part splits into whole pieces); half: the pairing.
+const void* rope_kernel_ptr(int x_kind, bool half, bool vec);
+
+struct AttnArgs {
+    const void* q;
+    void* out;
+    float* lse;
+    long long q_token, q_head, out_token, out_head;
+    const uint16_t *k, *v;
+    long long k_page, k_token, k_head, v_page, v_token, v_head;
+    const int* pages;
+    long long pages_stride;
+    const int *q_start, *kv_len;
+    unsigned* count;  // arrival counters, one per row tile; zero between calls
+    float* part;      // parts of split row tiles: [tile][part][rows_part][dim + 2] (m, l, then the unnormalised sums)
+    unsigned* err;
+    int num_pages, page_size, kv_heads, dim;
+    int tokens, heads, group, seqs, max_q, max_kv;
+    float scale_log2;   // scale * log2(e): the softmax runs in base 2
+    int causal, window;
+    int chunk;       // context tokens per part
+    int parts;       // parts of a row tile in the grid
+    int row_tiles;   // row tiles of a sequence and key/value head in the grid
+    int rows_part;   // rows of a part's record
+};
+
+struct AttnPlan {
+    bool tiles;  // the 128-row tensor-memory kernel (else the 16-row one)
+    int chunk, parts, row_tiles, rows_part;
+    long long grid;
+    unsigned smem, threads;
+    size_t scratch;
+};
+
+constexpr unsigned ATTN_MAX_COUNTERS = QGEMV_ATTN_SCRATCH_HEAD / 4;
+
+const void* attn_rows_kernel_ptr(bool bf16, int dim, unsigned* smem, unsigned* threads);
+
+struct SampleArgs {
+    const void* x;
+    long long row_stride;
+    int m, N;
+    const float* temperature;
+    const int* top_k;
+    const float *top_p, *min_p, *u;
+    int* token;
+    float* prob;
+};
+
+const void* sample_kernel_ptr(int kind);
+
+}  // namespace qg

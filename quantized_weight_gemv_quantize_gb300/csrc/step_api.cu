@@ -1,0 +1,398 @@
+// C ABI of the operators between the GEMVs: rotary positions, attention over the paged cache, sampling.  Every check
+// runs on the host before anything is enqueued.
+#include <limits.h>
+#include <math.h>
+#include <mutex>
+#include <stddef.h>
+
+#include "../../include/qgemv.h"
+#include "internal.h"
+#include "step.h"
+
+namespace qg {
+
+static int elem_size(int kind) {
+    return kind == QGEMV_ACT_F32 ? 4 : kind == QGEMV_ACT_BF16 || kind == QGEMV_ACT_F16 ? 2 : 0;
+}
+
+// A tensor [n0, n1, dim] with strides s0, s1 (elements of `size` bytes), as the memory it covers.
+struct Region {
+    const void* p;
+    long long n0, s0, n1, s1, dim;
+    int size;
+    size_t bytes() const {
+        if (n0 < 1 || n1 < 1) return 0;
+        return static_cast<size_t>((n0 - 1) * s0 + (n1 - 1) * s1 + dim) * size;
+    }
+    bool ok() const {  // strides in range, and no product below overflows
+        return s0 >= 0 && s1 >= 0 && s0 <= (1ll << 40) && s1 <= (1ll << 40) && (s0 * size) % 16 == 0 && (s1 * size) % 16 == 0;
+    }
+};
+
+// Whether two tensors may share a byte.  Ranges that are apart do not; two that are slices of one buffer with the same
+// outer stride do not when their spans within that stride are apart.  Anything else counts as an overlap.
+static bool meet(const Region& a, const Region& b) {
+    if (!a.p || !b.p || !a.bytes() || !b.bytes()) return false;
+    if (!api_overlaps(a.p, a.bytes(), b.p, b.bytes())) return false;
+    const long long stride = a.s0 * a.size;
+    if (a.n0 > 1 && b.n0 > 1 && stride == b.s0 * b.size) {
+        const long long wa = ((a.n1 - 1) * a.s1 + a.dim) * a.size, wb = ((b.n1 - 1) * b.s1 + b.dim) * b.size;
+        if (wa <= stride && wb <= stride) {
+            const long long d = static_cast<long long>(reinterpret_cast<uintptr_t>(b.p) - reinterpret_cast<uintptr_t>(a.p));
+            const long long at = ((d % stride) + stride) % stride;
+            return !(at >= wa && at + wb <= stride);
+        }
+    }
+    return true;
+}
+
+static bool same(const Region& a, const Region& b) {
+    return a.p == b.p && a.s0 == b.s0 && a.s1 == b.s1 && a.size == b.size && a.n1 == b.n1;
+}
+
+// A cache as two regions of pages: [num_pages, the span of a page].
+static size_t cache_bytes(const qgemv_cache& c, long long page, long long token, long long head) {
+    return static_cast<size_t>((c.num_pages - 1) * page + (c.page_size - 1) * token + (c.heads - 1) * head + c.dim) * 2;
+}
+
+static int check_cache(const qgemv_cache* c) {
+    if (!c->k || !c->v) return QGEMV_ERR_INVALID_ARG;
+    if (c->kind != QGEMV_ACT_BF16 && c->kind != QGEMV_ACT_F16) return QGEMV_ERR_INVALID_ARG;
+    if (c->num_pages < 1 || c->page_size < 1 || c->heads < 1 || c->dim < 8 || c->dim % 8) return QGEMV_ERR_INVALID_ARG;
+    if (c->dim > 256) return QGEMV_ERR_UNSUPPORTED;
+    const long long s[6] = {c->k_page, c->k_token, c->k_head, c->v_page, c->v_token, c->v_head};
+    for (long long v : s) {
+        if (v < 0 || v > (1ll << 40)) return QGEMV_ERR_INVALID_ARG;
+        if (v % 8) return QGEMV_ERR_MISALIGNED;
+    }
+    // no product of the kernels' offset arithmetic leaves 64 bits: 2^31 pages of strides below 2^31 elements or fewer
+    // pages of larger ones
+    const double span = static_cast<double>(c->num_pages) * (c->k_page > c->v_page ? c->k_page : c->v_page);
+    if (span > 9e15) return QGEMV_ERR_UNSUPPORTED;
+    if (!api_aligned(c->k, 16) || !api_aligned(c->v, 16)) return QGEMV_ERR_MISALIGNED;
+    return QGEMV_OK;
+}
+
+// ---------------------------------------------------------------------------------------------- rotary positions
+
+static int run_rope(const qgemv_rope_args* a, unsigned flags, void* stream) {
+    if (!a || (flags & ~QGEMV_FLAG_PDL)) return QGEMV_ERR_INVALID_ARG;
+    const int xs = elem_size(a->x_kind), os = elem_size(a->out_kind);
+    if (!xs || !os) return QGEMV_ERR_INVALID_ARG;
+    if (a->layout != QGEMV_ROPE_HALF && a->layout != QGEMV_ROPE_INTERLEAVED) return QGEMV_ERR_INVALID_ARG;
+    if (a->tokens < 0 || a->heads < 0 || a->kv_heads < 0 || a->heads + static_cast<long long>(a->kv_heads) < 1)
+        return QGEMV_ERR_INVALID_ARG;
+    if (a->dim < 8 || a->dim % 8 || a->rot_dim < 2 || a->rot_dim % 2 || a->rot_dim > a->dim) return QGEMV_ERR_INVALID_ARG;
+    if (a->dim > 256 || a->heads > 65536 || a->kv_heads > 65536) return QGEMV_ERR_UNSUPPORTED;
+    if (!a->positions || !a->freqs) return QGEMV_ERR_INVALID_ARG;
+    const bool has_q = a->heads > 0, has_k = a->kv_heads > 0, has_c = a->cache != nullptr;
+    if (has_q != (a->q != nullptr) || has_q != (a->q_out != nullptr) || has_k != (a->k != nullptr)) return QGEMV_ERR_INVALID_ARG;
+    if (has_c != (a->v != nullptr) || has_c != (a->slots != nullptr)) return QGEMV_ERR_INVALID_ARG;
+    if ((has_k && !a->k_out && !has_c) || (!has_k && (a->k_out || has_c))) return QGEMV_ERR_INVALID_ARG;
+    int st;
+    if (has_c) {
+        if ((st = check_cache(a->cache))) return st;
+        if (a->cache->heads != a->kv_heads || a->cache->dim != a->dim) return QGEMV_ERR_INVALID_ARG;
+    }
+    const long long T = a->tokens;
+    const Region q = {a->q, T, a->q_token, a->heads, a->q_head, a->dim, xs};
+    const Region k = {a->k, T, a->k_token, a->kv_heads, a->k_head, a->dim, xs};
+    const Region v = {a->v, T, a->v_token, a->kv_heads, a->v_head, a->dim, xs};
+    const Region qo = {a->q_out, T, a->q_out_token, a->heads, a->q_out_head, a->dim, os};
+    const Region ko = {a->k_out, T, a->k_out_token, a->kv_heads, a->k_out_head, a->dim, os};
+    const Region* all[5] = {&q, &k, &v, &qo, &ko};
+    for (const Region* r : all) {
+        if (!r->p) continue;
+        if (r->s0 < 0 || r->s1 < 0 || r->s0 > (1ll << 40) || r->s1 > (1ll << 40)) return QGEMV_ERR_INVALID_ARG;
+        if (!r->ok() || r->s0 % 8 || r->s1 % 8 || !api_aligned(r->p, 16)) return QGEMV_ERR_MISALIGNED;
+    }
+    if (!api_aligned(a->positions, 4) || !api_aligned(a->freqs, 8) || (a->slots && !api_aligned(a->slots, 8)))
+        return QGEMV_ERR_MISALIGNED;
+    if (T == 0) return QGEMV_OK;
+    const size_t nf = static_cast<size_t>(a->rot_dim / 2) * 8, np = static_cast<size_t>(T) * 4, ns = static_cast<size_t>(T) * 8;
+    const Region* outs[2] = {&qo, &ko};
+    for (const Region* o : outs) {
+        if (!o->p) continue;
+        const Region* own = o == &qo ? &q : &k;
+        for (const Region* in : {&q, &k, &v})
+            if (meet(*o, *in) && !(in == own && same(*o, *in) && a->x_kind == a->out_kind)) return QGEMV_ERR_OVERLAP;
+        if (api_overlaps(o->p, o->bytes(), a->positions, np) || api_overlaps(o->p, o->bytes(), a->freqs, nf) ||
+            (a->slots && api_overlaps(o->p, o->bytes(), a->slots, ns)))
+            return QGEMV_ERR_OVERLAP;
+    }
+    if (meet(qo, ko)) return QGEMV_ERR_OVERLAP;
+    if (has_c) {
+        const qgemv_cache& c = *a->cache;
+        const size_t kb = cache_bytes(c, c.k_page, c.k_token, c.k_head), vb = cache_bytes(c, c.v_page, c.v_token, c.v_head);
+        for (const Region* r : all)
+            if (r->p && (api_overlaps(c.k, kb, r->p, r->bytes()) || api_overlaps(c.v, vb, r->p, r->bytes())))
+                return QGEMV_ERR_OVERLAP;
+        const void* side[3] = {a->positions, a->freqs, a->slots};
+        const size_t size[3] = {np, nf, ns};
+        for (int i = 0; i < 3; ++i)
+            if (api_overlaps(c.k, kb, side[i], size[i]) || api_overlaps(c.v, vb, side[i], size[i])) return QGEMV_ERR_OVERLAP;
+    }
+    int sms;
+    unsigned* err;
+    if ((st = api_device(&sms, &err))) return st;
+    RopeArgs r = {};
+    r.q = a->q, r.k = a->k, r.v = a->v, r.q_out = a->q_out, r.k_out = a->k_out;
+    r.q_token = a->q_token, r.q_head = a->q_head, r.k_token = a->k_token, r.k_head = a->k_head;
+    r.v_token = a->v_token, r.v_head = a->v_head;
+    r.q_out_token = a->q_out_token, r.q_out_head = a->q_out_head, r.k_out_token = a->k_out_token, r.k_out_head = a->k_out_head;
+    r.positions = a->positions, r.freqs = a->freqs, r.slots = a->slots, r.err = err;
+    r.out_kind = a->out_kind, r.tokens = a->tokens, r.heads = a->heads, r.kv_heads = a->kv_heads;
+    r.dim = a->dim, r.rot = a->rot_dim, r.mscale = a->mscale, r.page_size = 1;
+    if (has_c) {
+        const qgemv_cache& c = *a->cache;
+        r.k_cache = c.k, r.v_cache = c.v, r.cache_kind = c.kind;
+        r.kc_page = c.k_page, r.kc_token = c.k_token, r.kc_head = c.k_head;
+        r.vc_page = c.v_page, r.vc_token = c.v_token, r.vc_head = c.v_head;
+        r.page_size = c.page_size, r.num_slots = static_cast<long long>(c.num_pages) * c.page_size;
+    }
+    const bool half = a->layout == QGEMV_ROPE_HALF, vec = a->rot_dim % (half ? 16 : 8) == 0;
+    // Blocks of a token: as many as its pieces fill once, until the tokens alone fill the GPU.
+    const int w = vec ? 8 : 1;
+    const long long per_token = static_cast<long long>(a->heads + 2 * a->kv_heads) * a->dim / w;
+    long long y = (per_token + 127) / 128;
+    const long long enough = (16ll * sms + T - 1) / T;
+    if (y > enough) y = enough;
+    const bool pdl = (flags & QGEMV_FLAG_PDL) != 0;
+    cudaError_t e = launch_step(rope_kernel_ptr(a->x_kind, half, vec), dim3(static_cast<unsigned>(T), static_cast<unsigned>(y)),
+                                128, 0, 1, pdl, static_cast<cudaStream_t>(stream), r);
+    if (e != cudaSuccess) return api_cuda_fail(e);
+    api_route(QGEMV_ROUTE_ROPE, pdl);
+    return QGEMV_OK;
+}
+
+// ---------------------------------------------------------------------------------------------------- attention
+
+static int attn_plan(int seqs, int tokens, int heads, int kv_heads, int dim, int max_q, int max_kv, AttnPlan* p) {
+    if (seqs < 0 || tokens < 0 || heads < 1 || kv_heads < 1 || heads % kv_heads || dim < 8 || dim % 8 || max_q < 0 ||
+        max_kv < 0)
+        return QGEMV_ERR_INVALID_ARG;
+    if (dim > 256 || heads > 65536) return QGEMV_ERR_UNSUPPORTED;
+    *p = AttnPlan{};
+    p->scratch = QGEMV_ATTN_SCRATCH_HEAD;
+    if (seqs == 0 || tokens == 0 || max_q == 0) return QGEMV_OK;
+    constexpr int SMS = 152;
+    if (max_q > tokens) max_q = tokens;
+    const long long rows = static_cast<long long>(max_q) * (heads / kv_heads);
+    const int tile = 16;
+    const long long row_tiles = (rows + tile - 1) / tile;
+    const long long tiles = row_tiles * kv_heads * seqs;
+    if (row_tiles > INT_MAX || tiles > INT_MAX) return QGEMV_ERR_UNSUPPORTED;
+    p->row_tiles = static_cast<int>(row_tiles);
+    p->rows_part = static_cast<int>(rows < tile ? rows : tile);
+    // Parts: enough to give every SM four blocks, of at least 128 keys.
+    long long parts = (4 * SMS + tiles - 1) / tiles;
+    const long long most = (max_kv + 127) / 128;
+    if (parts > most) parts = most;
+    if (parts < 1 || tiles > ATTN_MAX_COUNTERS) parts = 1;
+    const long long chunk = ((max_kv + parts - 1) / parts + 15) / 16 * 16;
+    p->chunk = static_cast<int>(chunk < 16 ? 16 : chunk > INT_MAX - 15 ? INT_MAX - 15 : chunk);
+    p->parts = max_kv > 0 ? static_cast<int>((static_cast<long long>(max_kv) + p->chunk - 1) / p->chunk) : 1;
+    p->grid = tiles * p->parts;
+    if (p->grid > INT_MAX) return QGEMV_ERR_UNSUPPORTED;
+    if (p->parts > 1) p->scratch += static_cast<size_t>(p->grid) * p->rows_part * (dim + 2) * sizeof(float);
+    return QGEMV_OK;
+}
+
+// Dynamic shared memory of a kernel, set once per device.
+static int allow_smem(const void* fn, unsigned smem) {
+    static std::mutex mu;
+    static const void* done[64][16];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return api_cuda_fail(e);
+    if (dev < 0 || dev >= 64) return QGEMV_ERR_DEVICE;
+    std::lock_guard<std::mutex> lk(mu);
+    for (const void*& f : done[dev]) {
+        if (f == fn) return QGEMV_OK;
+        if (f) continue;
+        if ((e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem))) != cudaSuccess)
+            return api_cuda_fail(e);
+        f = fn;
+        return QGEMV_OK;
+    }
+    return QGEMV_ERR_UNSUPPORTED;
+}
+
+static int run_attn(const qgemv_attn_args* a, unsigned flags, void* stream) {
+    if (!a || (flags & ~QGEMV_FLAG_PDL)) return QGEMV_ERR_INVALID_ARG;
+    if (a->kind != QGEMV_ACT_BF16 && a->kind != QGEMV_ACT_F16) return QGEMV_ERR_INVALID_ARG;
+    if (!a->cache || !a->q || !a->out || !a->pages || !a->q_start || !a->kv_len || !a->scratch) return QGEMV_ERR_INVALID_ARG;
+    int st;
+    if ((st = check_cache(a->cache))) return st;
+    const qgemv_cache& c = *a->cache;
+    if (c.kind != a->kind || a->tokens < 0 || a->seqs < 0 || a->pages_stride < 0 || a->window < 0) return QGEMV_ERR_INVALID_ARG;
+    if (!(fabsf(a->scale) <= 3.0e38f)) return QGEMV_ERR_INVALID_ARG;  // NaN and infinities too
+    AttnPlan p;
+    if ((st = attn_plan(a->seqs, a->tokens, a->heads, c.heads, c.dim, a->max_q, a->max_kv, &p))) return st;
+    if (a->pages_stride > (1ll << 40)) return QGEMV_ERR_UNSUPPORTED;
+    if (a->scratch_bytes < p.scratch) return QGEMV_ERR_INVALID_ARG;
+    const Region q = {a->q, a->tokens, a->q_token, a->heads, a->q_head, c.dim, 2};
+    const Region o = {a->out, a->tokens, a->out_token, a->heads, a->out_head, c.dim, 2};
+    for (const Region* r : {&q, &o}) {
+        if (r->s0 < 0 || r->s1 < 0 || r->s0 > (1ll << 40) || r->s1 > (1ll << 40)) return QGEMV_ERR_INVALID_ARG;
+        if (!r->ok() || !api_aligned(r->p, 16)) return QGEMV_ERR_MISALIGNED;
+    }
+    if (!api_aligned(a->scratch, 16) || !api_aligned(a->pages, 4) || !api_aligned(a->q_start, 4) || !api_aligned(a->kv_len, 4) ||
+        (a->lse && !api_aligned(a->lse, 4)))
+        return QGEMV_ERR_MISALIGNED;
+    if (a->tokens == 0 || a->seqs == 0 || p.grid == 0) return QGEMV_OK;
+    // outputs: out, lse, scratch; inputs: q, the cache, the tables
+    struct Span { const void* p; size_t n; };
+    const Span in[] = {{c.k, cache_bytes(c, c.k_page, c.k_token, c.k_head)},
+                       {c.v, cache_bytes(c, c.v_page, c.v_token, c.v_head)},
+                       {a->pages, (static_cast<size_t>(a->seqs) * a->pages_stride) * 4},
+                       {a->q_start, (static_cast<size_t>(a->seqs) + 1) * 4},
+                       {a->kv_len, static_cast<size_t>(a->seqs) * 4}};
+    const size_t lse_bytes = a->lse ? static_cast<size_t>(a->tokens) * a->heads * 4 : 0;
+    const Span out[] = {{a->out, o.bytes()}, {a->lse, lse_bytes}, {a->scratch, a->scratch_bytes}};
+    for (int i = 0; i < 3; ++i) {
+        if (!out[i].n) continue;
+        for (const Span& s : in)
+            if (s.n && api_overlaps(out[i].p, out[i].n, s.p, s.n)) return QGEMV_ERR_OVERLAP;
+        if (i > 0 && api_overlaps(out[i].p, out[i].n, a->q, q.bytes())) return QGEMV_ERR_OVERLAP;
+        for (int j = 0; j < i; ++j)
+            if (out[j].n && api_overlaps(out[i].p, out[i].n, out[j].p, out[j].n)) return QGEMV_ERR_OVERLAP;
+    }
+    if (meet(o, q)) return QGEMV_ERR_OVERLAP;
+    int sms;
+    unsigned* err;
+    if ((st = api_device(&sms, &err))) return st;
+    AttnArgs k = {};
+    k.q = a->q, k.out = a->out, k.lse = a->lse;
+    k.q_token = a->q_token, k.q_head = a->q_head, k.out_token = a->out_token, k.out_head = a->out_head;
+    k.k = static_cast<const uint16_t*>(c.k), k.v = static_cast<const uint16_t*>(c.v);
+    k.k_page = c.k_page, k.k_token = c.k_token, k.k_head = c.k_head;
+    k.v_page = c.v_page, k.v_token = c.v_token, k.v_head = c.v_head;
+    k.pages = a->pages, k.pages_stride = a->pages_stride, k.q_start = a->q_start, k.kv_len = a->kv_len;
+    k.count = static_cast<unsigned*>(a->scratch);
+    k.part = reinterpret_cast<float*>(static_cast<uint8_t*>(a->scratch) + QGEMV_ATTN_SCRATCH_HEAD);
+    k.err = err, k.num_pages = c.num_pages, k.page_size = c.page_size, k.kv_heads = c.heads, k.dim = c.dim;
+    k.tokens = a->tokens, k.heads = a->heads, k.group = a->heads / c.heads, k.seqs = a->seqs;
+    k.max_q = a->max_q, k.max_kv = a->max_kv;
+    k.scale_log2 = a->scale * 1.44269504088896341f;
+    k.window = a->window, k.causal = a->causal || a->window > 0;
+    k.chunk = p.chunk, k.parts = p.parts, k.row_tiles = p.row_tiles, k.rows_part = p.rows_part;
+    const bool pdl = (flags & QGEMV_FLAG_PDL) != 0;
+    unsigned smem, threads;
+    const void* fn = attn_rows_kernel_ptr(a->kind == QGEMV_ACT_BF16, c.dim, &smem, &threads);
+    if ((st = allow_smem(fn, smem))) return st;
+    cudaError_t e = launch_step(fn, dim3(static_cast<unsigned>(p.grid)), threads, smem, 1, pdl,
+                                static_cast<cudaStream_t>(stream), k);
+    if (e != cudaSuccess) return api_cuda_fail(e);
+    api_route(QGEMV_ROUTE_ATTN_ROWS, pdl);
+    return QGEMV_OK;
+}
+
+// ----------------------------------------------------------------------------------------------------- sampling
+
+static int run_sample(const SampleArgs& s, int kind, unsigned flags, void* stream) {
+    const int size = elem_size(kind);
+    if (!size || (flags & ~QGEMV_FLAG_PDL)) return QGEMV_ERR_INVALID_ARG;
+    if (s.m < 0 || s.N < 1 || s.row_stride < s.N || !s.x || !s.u || !s.token) return QGEMV_ERR_INVALID_ARG;
+    if (s.N > 1 << 20 || s.row_stride > (1ll << 40)) return QGEMV_ERR_UNSUPPORTED;
+    if (!api_aligned(s.x, 16)) return QGEMV_ERR_MISALIGNED;
+    const void* words[] = {s.temperature, s.top_k, s.top_p, s.min_p, s.u, s.token, s.prob};
+    for (const void* w : words)
+        if (w && !api_aligned(w, 4)) return QGEMV_ERR_MISALIGNED;
+    if (s.m == 0) return QGEMV_OK;
+    const size_t n = static_cast<size_t>(s.m) * 4;
+    const size_t xb = (static_cast<size_t>(s.m - 1) * s.row_stride + s.N) * size;
+    const void* outs[] = {s.token, s.prob};
+    for (const void* o : outs) {
+        if (!o) continue;
+        if (api_overlaps(o, n, s.x, xb)) return QGEMV_ERR_OVERLAP;
+        for (int i = 0; i < 5; ++i)
+            if (words[i] && api_overlaps(o, n, words[i], n)) return QGEMV_ERR_OVERLAP;
+    }
+    if (s.prob && api_overlaps(s.token, n, s.prob, n)) return QGEMV_ERR_OVERLAP;
+    int sms, st;
+    unsigned* err;
+    if ((st = api_device(&sms, &err))) return st;
+    const bool pdl = (flags & QGEMV_FLAG_PDL) != 0;
+    cudaError_t e = launch_step(sample_kernel_ptr(kind), dim3(static_cast<unsigned>(s.m)), 1024, 0, 1, pdl,
+                                static_cast<cudaStream_t>(stream), s);
+    if (e != cudaSuccess) return api_cuda_fail(e);
+    api_route(QGEMV_ROUTE_SAMPLE, pdl);
+    return QGEMV_OK;
+}
+
+}  // namespace qg
+
+using namespace qg;
+
+extern "C" {
+
+int qgemv_rope_freqs(int rot_dim, double theta, int scaling, double factor, double trained, double low, double high,
+                     unsigned long long* out, float* mscale) {
+    int st;
+    if (api_injected(&st)) return st;
+    if (!out || rot_dim < 2 || rot_dim % 2 || rot_dim > 256 || !(theta > 1.0) || !(theta < 1e300)) return QGEMV_ERR_INVALID_ARG;
+    if (scaling < QGEMV_ROPE_SCALE_NONE || scaling > QGEMV_ROPE_SCALE_BANDS) return QGEMV_ERR_INVALID_ARG;
+    if (scaling != QGEMV_ROPE_SCALE_NONE && !(factor >= 1.0 && factor < 1e9)) return QGEMV_ERR_INVALID_ARG;
+    const bool windowed = scaling == QGEMV_ROPE_SCALE_PARTS || scaling == QGEMV_ROPE_SCALE_BANDS;
+    if (windowed && !(trained >= 1.0 && trained < 1e18 && low > 0.0 && high > low && high < 1e18)) return QGEMV_ERR_INVALID_ARG;
+    if (scaling == QGEMV_ROPE_SCALE_BASE && rot_dim < 4) return QGEMV_ERR_INVALID_ARG;
+    const double pi = 3.14159265358979323846;
+    const int half = rot_dim / 2;
+    if (scaling == QGEMV_ROPE_SCALE_BASE) theta *= pow(factor, static_cast<double>(rot_dim) / (rot_dim - 2));
+    // PARTS: the (real) pair index that turns `turns` times over the trained positions, and the ramp between two of them
+    auto pair = [&](double turns) { return rot_dim * log(trained / (turns * 2 * pi)) / (2 * log(theta)); };
+    double first = 0, last = 0;
+    if (scaling == QGEMV_ROPE_SCALE_PARTS) {
+        first = floor(pair(high)), last = ceil(pair(low));
+        if (first < 0) first = 0;
+        if (last > rot_dim - 1) last = rot_dim - 1;
+    }
+    for (int i = 0; i < half; ++i) {
+        double f = pow(theta, -2.0 * i / rot_dim);
+        if (scaling == QGEMV_ROPE_SCALE_LINEAR) f /= factor;
+        if (scaling == QGEMV_ROPE_SCALE_PARTS) {
+            const double width = last - first > 1e-3 ? last - first : 1e-3;
+            double g = (i - first) / width;
+            g = g < 0 ? 0 : g > 1 ? 1 : g;
+            f = f / factor * g + f * (1 - g);
+        }
+        if (scaling == QGEMV_ROPE_SCALE_BANDS) {
+            const double turns = trained * f / (2 * pi);  // trained / wavelength
+            double g = (turns - low) / (high - low);
+            g = g < 0 ? 0 : g > 1 ? 1 : g;
+            f = f / factor * (1 - g) + f * g;
+        }
+        out[i] = static_cast<unsigned long long>(f / (2 * pi) * 18446744073709551616.0 + 0.5);
+    }
+    if (mscale) *mscale = scaling == QGEMV_ROPE_SCALE_PARTS ? static_cast<float>(0.1 * log(factor) + 1.0) : 1.f;
+    return QGEMV_OK;
+}
+
+int qgemv_rope(const qgemv_rope_args* args, unsigned flags, void* stream) {
+    int st;
+    if (api_injected(&st)) return st;
+    return run_rope(args, flags, stream);
+}
+
+size_t qgemv_attn_scratch_bytes(int seqs, int tokens, int heads, int kv_heads, int dim, int max_q, int max_kv) {
+    AttnPlan p;
+    return attn_plan(seqs, tokens, heads, kv_heads, dim, max_q, max_kv, &p) ? 0 : (p.scratch + 255) / 256 * 256;
+}
+
+int qgemv_attn(const qgemv_attn_args* args, unsigned flags, void* stream) {
+    int st;
+    if (api_injected(&st)) return st;
+    return run_attn(args, flags, stream);
+}
+
+int qgemv_sample(int kind, const void* logits, long long row_stride, int m, int N, const float* temperature,
+                 const int* top_k, const float* top_p, const float* min_p, const float* u, int* token_out,
+                 float* prob_out, unsigned flags, void* stream) {
+    int st;
+    if (api_injected(&st)) return st;
+    const SampleArgs s = {logits, row_stride, m, N, temperature, top_k, top_p, min_p, u, token_out, prob_out};
+    return run_sample(s, kind, flags, stream);
+}
+
+}  // extern "C"
