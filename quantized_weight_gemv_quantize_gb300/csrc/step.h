@@ -73,8 +73,13 @@ struct SampleArgs {
     const float *top_p, *min_p, *u;
     int* token;
     float* prob;
+    int blocks;  // blocks (one cluster) of a row
+    int slice;   // tokens of a block, a multiple of 8
+    int staged;  // the slice is kept in shared memory
 };
 
+constexpr int SAMPLE_THREADS = 512;
+unsigned sample_smem_base();  // shared memory beside the slice
 const void* sample_kernel_ptr(int kind);
 
 }  // namespace qg

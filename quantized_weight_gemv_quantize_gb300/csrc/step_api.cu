@@ -290,6 +290,8 @@ static int run_attn(const qgemv_attn_args* a, unsigned flags, void* stream) {
 
 // ----------------------------------------------------------------------------------------------------- sampling
 
+constexpr unsigned SAMPLE_SMEM_MAX = 220 * 1024;
+
 static int run_sample(const SampleArgs& s, int kind, unsigned flags, void* stream) {
     const int size = elem_size(kind);
     if (!size || (flags & ~QGEMV_FLAG_PDL)) return QGEMV_ERR_INVALID_ARG;
@@ -313,9 +315,21 @@ static int run_sample(const SampleArgs& s, int kind, unsigned flags, void* strea
     int sms, st;
     unsigned* err;
     if ((st = api_device(&sms, &err))) return st;
+    // Blocks of a row: slices of at most 20480 tokens, up to the 8 blocks of a portable cluster.  A slice stays in shared
+    // memory where it fits (always up to 388,000 fp32 or 777,000 16-bit logits); longer ones are read again from L2.
+    SampleArgs k = s;
+    k.blocks = 1;
+    while (k.blocks < 8 && (s.N + k.blocks - 1) / k.blocks > 20480) k.blocks *= 2;
+    k.slice = ((s.N + k.blocks - 1) / k.blocks + 7) / 8 * 8;
+    const unsigned room = SAMPLE_SMEM_MAX - sample_smem_base();
+    k.staged = static_cast<unsigned>(k.slice) * size <= room;
+    if (static_cast<long long>(s.m) * k.blocks > INT_MAX) return QGEMV_ERR_UNSUPPORTED;
+    const void* fn = sample_kernel_ptr(kind);
+    if ((st = allow_smem(fn, SAMPLE_SMEM_MAX))) return st;
     const bool pdl = (flags & QGEMV_FLAG_PDL) != 0;
-    cudaError_t e = launch_step(sample_kernel_ptr(kind), dim3(static_cast<unsigned>(s.m)), 1024, 0, 1, pdl,
-                                static_cast<cudaStream_t>(stream), s);
+    cudaError_t e = launch_step(fn, dim3(static_cast<unsigned>(s.m * k.blocks)), SAMPLE_THREADS,
+                                sample_smem_base() + (k.staged ? static_cast<unsigned>(k.slice) * size : 0u),
+                                static_cast<unsigned>(k.blocks), pdl, static_cast<cudaStream_t>(stream), k);
     if (e != cudaSuccess) return api_cuda_fail(e);
     api_route(QGEMV_ROUTE_SAMPLE, pdl);
     return QGEMV_OK;
@@ -391,7 +405,7 @@ int qgemv_sample(int kind, const void* logits, long long row_stride, int m, int 
                  float* prob_out, unsigned flags, void* stream) {
     int st;
     if (api_injected(&st)) return st;
-    const SampleArgs s = {logits, row_stride, m, N, temperature, top_k, top_p, min_p, u, token_out, prob_out};
+    const SampleArgs s = {logits, row_stride, m, N, temperature, top_k, top_p, min_p, u, token_out, prob_out, 0, 0, 0};
     return run_sample(s, kind, flags, stream);
 }
 
