@@ -517,7 +517,7 @@ QGEMV_API int qgemv_rope(const qgemv_rope_args* args, unsigned flags, void* stre
  * zero before the first call (e.g. cudaMemset once); each call leaves them zero again, so calls of any sizes may share one
  * scratch that is large enough for each.  Calls that share a scratch must be ordered.
  * The result does not depend on timing: parts of a long context are joined in a fixed order.
- * heads a multiple of cache->heads.  tokens = 0 or seqs = 0 does nothing.
+ * heads a multiple of cache->heads; 0 < scale <= 1e30.  tokens = 0 or seqs = 0 does nothing.
  */
 typedef struct {
     const void* q;

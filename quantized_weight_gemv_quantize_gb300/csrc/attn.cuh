@@ -34,16 +34,18 @@ struct Tile {
     int first_pos;                  // position of the sequence's new token 0
     int k0, k1;                     // keys of this part
     int kv_len;                     // keys that may be read
-    long long index;                // index of (seq, kv_head, row tile)
+    long long index;                // number of (seq, kv_head, row tile) in the grid
 };
 
-// False: nothing to do for this block (past the sequence's rows or the tile's parts).
-template <int ROWS>
+// False: nothing to do for this block (past the sequence's rows or the tile's parts).  LAST_FIRST: the row tiles with the
+// most keys (the last ones, under a causal mask) of all sequences and heads come first, so that the grid ends with short ones.
+template <int ROWS, bool LAST_FIRST>
 __device__ __forceinline__ bool find_tile(const AttnArgs& a, long long block, Tile* t) {
     t->part = static_cast<int>(block % a.parts);
     t->index = block / a.parts;
-    const int rt = static_cast<int>(t->index % a.row_tiles);
-    const long long sh = t->index / a.row_tiles;
+    const int pairs = a.kv_heads * a.seqs;
+    const int rt = static_cast<int>(LAST_FIRST ? a.row_tiles - 1 - t->index / pairs : t->index % a.row_tiles);
+    const int sh = static_cast<int>(LAST_FIRST ? t->index % pairs : t->index / a.row_tiles);
     t->kv_head = static_cast<int>(sh % a.kv_heads);
     t->seq = static_cast<int>(sh / a.kv_heads);
     // the values on the device are held to the bounds that the launch was shaped for

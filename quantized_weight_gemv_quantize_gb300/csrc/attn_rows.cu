@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(RowsShape<DP>::WARPS * 32) attn_rows_kernel(co
     pdl_launch_dependents();
     pdl_wait();
     Tile t;
-    if (!find_tile<16>(a, blockIdx.x, &t)) return;
+    if (!find_tile<16, false>(a, blockIdx.x, &t)) return;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t ring = smem_addr(smem) + warp * S::STAGES * S::STAGE;
 

@@ -63,6 +63,7 @@ struct AttnPlan {
 constexpr unsigned ATTN_MAX_COUNTERS = QGEMV_ATTN_SCRATCH_HEAD / 4;
 
 const void* attn_rows_kernel_ptr(bool bf16, int dim, unsigned* smem, unsigned* threads);
+const void* attn_tiles_kernel_ptr(bool bf16, int dim, unsigned* smem, unsigned* threads);
 
 struct SampleArgs {
     const void* x;

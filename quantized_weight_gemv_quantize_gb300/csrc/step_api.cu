@@ -178,15 +178,17 @@ static int attn_plan(int seqs, int tokens, int heads, int kv_heads, int dim, int
     constexpr int SMS = 152;
     if (max_q > tokens) max_q = tokens;
     const long long rows = static_cast<long long>(max_q) * (heads / kv_heads);
-    const int tile = 16;
+    // More than 32 rows go to the 128-row kernel (heads of up to 128).
+    p->tiles = rows > 32 && dim <= 128;
+    const int tile = p->tiles ? 256 : 16;
     const long long row_tiles = (rows + tile - 1) / tile;
     const long long tiles = row_tiles * kv_heads * seqs;
     if (row_tiles > INT_MAX || tiles > INT_MAX) return QGEMV_ERR_UNSUPPORTED;
     p->row_tiles = static_cast<int>(row_tiles);
     p->rows_part = static_cast<int>(rows < tile ? rows : tile);
-    // Parts: enough to give every SM four blocks, of at least 128 keys.
+    // Parts: enough to give every SM four blocks, of at least 128 keys (16-row kernel; 1024 for the other).
     long long parts = (4 * SMS + tiles - 1) / tiles;
-    const long long most = (max_kv + 127) / 128;
+    const long long most = p->tiles ? (max_kv + 1023) / 1024 : (max_kv + 127) / 128;
     if (parts > most) parts = most;
     if (parts < 1 || tiles > ATTN_MAX_COUNTERS) parts = 1;
     const long long chunk = ((max_kv + parts - 1) / parts + 15) / 16 * 16;
@@ -226,7 +228,7 @@ static int run_attn(const qgemv_attn_args* a, unsigned flags, void* stream) {
     if ((st = check_cache(a->cache))) return st;
     const qgemv_cache& c = *a->cache;
     if (c.kind != a->kind || a->tokens < 0 || a->seqs < 0 || a->pages_stride < 0 || a->window < 0) return QGEMV_ERR_INVALID_ARG;
-    if (!(fabsf(a->scale) <= 3.0e38f)) return QGEMV_ERR_INVALID_ARG;  // NaN and infinities too
+    if (!(a->scale > 0.f && a->scale <= 1e30f)) return QGEMV_ERR_INVALID_ARG;  // NaN too
     AttnPlan p;
     if ((st = attn_plan(a->seqs, a->tokens, a->heads, c.heads, c.dim, a->max_q, a->max_kv, &p))) return st;
     if (a->pages_stride > (1ll << 40)) return QGEMV_ERR_UNSUPPORTED;
@@ -279,12 +281,12 @@ static int run_attn(const qgemv_attn_args* a, unsigned flags, void* stream) {
     k.chunk = p.chunk, k.parts = p.parts, k.row_tiles = p.row_tiles, k.rows_part = p.rows_part;
     const bool pdl = (flags & QGEMV_FLAG_PDL) != 0;
     unsigned smem, threads;
-    const void* fn = attn_rows_kernel_ptr(a->kind == QGEMV_ACT_BF16, c.dim, &smem, &threads);
+    const void* fn = (p.tiles ? attn_tiles_kernel_ptr : attn_rows_kernel_ptr)(a->kind == QGEMV_ACT_BF16, c.dim, &smem, &threads);
     if ((st = allow_smem(fn, smem))) return st;
     cudaError_t e = launch_step(fn, dim3(static_cast<unsigned>(p.grid)), threads, smem, 1, pdl,
                                 static_cast<cudaStream_t>(stream), k);
     if (e != cudaSuccess) return api_cuda_fail(e);
-    api_route(QGEMV_ROUTE_ATTN_ROWS, pdl);
+    api_route(p.tiles ? QGEMV_ROUTE_ATTN_TILES : QGEMV_ROUTE_ATTN_ROWS, pdl);
     return QGEMV_OK;
 }
 

@@ -110,7 +110,8 @@ ATTN_REFUSED = [
     (dict(kind=F32), 1), (dict(kind=F16), 1), (dict(cache=None), 1), (dict(q=None), 1), (dict(out=None), 1),
     (dict(pages=None), 1), (dict(q_start=None), 1), (dict(kv_len=None), 1), (dict(scratch=None), 1), (dict(tokens=-1), 1),
     (dict(seqs=-1), 1), (dict(heads=31), 1), (dict(heads=0), 1), (dict(max_q=-1), 1), (dict(max_kv=-1), 1),
-    (dict(window=-1), 1), (dict(pages_stride=-1), 1), (dict(scale=float("nan")), 1), (dict(scale=float("inf")), 1),
+    (dict(window=-1), 1), (dict(pages_stride=-1), 1), (dict(scale=float("nan")), 1), (dict(scale=float("inf")), 1), (dict(scale=0.0), 1),
+    (dict(scale=-0.1), 1),
     (dict(scratch_bytes=qg.QGEMV_ATTN_SCRATCH_HEAD - 1), 1), (dict(q_head=-128), 1),
     (dict(cache=cache(dim=264)), 2), (dict(heads=8 * 10000), 2),
     (dict(q=Q + 2), 3), (dict(out=QO + 8), 3), (dict(out_head=132), 3), (dict(scratch=SCR + 4), 3), (dict(pages=TAB + 2), 3),
