@@ -163,20 +163,18 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) attn_tiles_kernel(const AttnA
         auto place = [&](uint32_t base, int r) {
             return base + (c / 8) * S::HALF_BYTES + r * 128 + (((c % 8) ^ (r & 7)) << 4);
         };
-        int loads = 0;  // groups committed
         bool ok = true;
-        auto arrive = [&](int x) {  // group x has landed: 0 is Q, then K_0, V_0, K_1, ...
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            const int j = (x - 1) / 2;
-            mbar_arrive(smem_addr(x == 0 ? &sh.q_full : x % 2 ? &sh.k_full[j & 1] : &sh.v_full[j & 1]));
+        // The barrier counts this thread's arrival when its copies so far have landed; the thread itself goes on.
+        auto arrive_when_landed = [&](unsigned long long& bar) {
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(&bar)) : "memory");
         };
-        auto commit = [&] {
-            asm volatile("cp.async.commit_group;" ::: "memory");
-            if (++loads > 2) {  // two groups stay in flight
-                asm volatile("cp.async.wait_group 2;" ::: "memory");
-                arrive(loads - 3);
-            }
+        const int* table = a.pages + t.seq * a.pages_stride;
+        // The page of this thread's key of block j, read one block ahead; -1 past the end.
+        auto page_of = [&](int j) {
+            const int key = t.k0 + j * TK + lt;
+            return key < t.k1 ? table[key / a.page_size] : -1;
         };
+        int page = page_of(0);
         if (blocks > 0) {
             const uint16_t* q = static_cast<const uint16_t*>(a.q);
             for (int r0 = 0; r0 < tiles * TR; r0 += ROWS_PASS) {
@@ -185,28 +183,19 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) attn_tiles_kernel(const AttnA
                 const long long off = in ? out_at(a, t, r, a.q_token, a.q_head) + c * 8 : 0;
                 cp16(place(smem + S::Q_AT + (r / TR) * S::TILE_BYTES, r % TR), q + off, in);
             }
-            commit();
+            arrive_when_landed(sh.q_full);
         }
-        const int* table = a.pages + t.seq * a.pages_stride;
         for (int j = 0; j < blocks && ok; ++j) {
             const int st = j & 1;
             {
-                const int key = t.k0 + j * TK + lt;
-                bool live = key < t.k1;
-                long long ko = -1, vo = -1;
-                if (live) {
-                    const int page = table[key / a.page_size], off = key % a.page_size;
-                    live = page >= 0 && page < a.num_pages;
-                    if (live) {
-                        ko = page * a.k_page + off * a.k_token + t.kv_head * a.k_head;
-                        vo = page * a.v_page + off * a.v_token + t.kv_head * a.v_head;
-                    } else {
-                        atomicOr(a.err, ERR_BAD_INDEX);
-                    }
-                }
-                sh.k_off[st][lt] = ko, sh.v_off[st][lt] = vo;
+                const int key = t.k0 + j * TK + lt, off = key % a.page_size;
+                const bool live = page >= 0 && page < a.num_pages;
+                if (!live && key < t.k1) atomicOr(a.err, ERR_BAD_INDEX);
+                sh.k_off[st][lt] = live ? page * a.k_page + off * a.k_token + t.kv_head * a.k_head : -1;
+                sh.v_off[st][lt] = live ? page * a.v_page + off * a.v_token + t.kv_head * a.v_head : -1;
                 const unsigned mask = __ballot_sync(0xffffffffu, live);
                 if (lane == 0) sh.live[j & 3][lw] = mask;
+                page = page_of(j + 1);
             }
             asm volatile("bar.sync 1, 128;" ::: "memory");
             if (j >= 2) ok = wait(sh.k_empty[st], (j / 2 - 1) & 1);
@@ -217,7 +206,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) attn_tiles_kernel(const AttnA
                 const bool in = off >= 0 && col;
                 cp16(place(smem + S::K_AT + st * S::TILE_BYTES, r), a.k + (in ? off + c * 8 : 0), in);
             }
-            commit();
+            arrive_when_landed(sh.k_full[st]);
             if (j >= 2) ok = wait(sh.v_empty[st], (j / 2 - 1) & 1);
             if (!ok) break;
 #pragma unroll 8
@@ -226,11 +215,9 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) attn_tiles_kernel(const AttnA
                 const bool in = off >= 0 && col;
                 cp16(place(smem + S::V_AT + st * S::TILE_BYTES, r), a.v + (in ? off + c * 8 : 0), in);
             }
-            commit();
+            arrive_when_landed(sh.v_full[st]);
         }
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
-        if (ok)
-            for (int x = loads > 2 ? loads - 2 : 0; x < loads; ++x) arrive(x);
+        asm volatile("cp.async.wait_all;" ::: "memory");
     } else if (warp == MMA_WARP) {
         // ---- one thread issues every product
         if (lane == 0 && blocks > 0) {
@@ -244,7 +231,13 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) attn_tiles_kernel(const AttnA
                 }
                 tc_commit(smem_addr(&sh.s_full[i]));
             };
-            bool ok = wait(sh.q_full, 0) && wait(sh.k_full[0], 0);
+            // the copies were made through the generic proxy, the tensor cores read through the asynchronous one
+            auto landed = [&](unsigned long long& bar, int parity) {
+                const bool ok = wait(bar, parity);
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                return ok;
+            };
+            bool ok = landed(sh.q_full, 0) && landed(sh.k_full[0], 0);
             if (ok) {
                 tc_fence_after();
                 for (int i = 0; i < tiles; ++i) scores(i, 0);
@@ -254,7 +247,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) attn_tiles_kernel(const AttnA
                 const int st = j & 1;
                 for (int i = 0; i < tiles; ++i) {
                     ok = wait(sh.p_full[i], j & 1);
-                    if (ok && i == 0) ok = wait(sh.v_full[st], (j / 2) & 1);
+                    if (ok && i == 0) ok = landed(sh.v_full[st], (j / 2) & 1);
                     if (!ok) break;
                     tc_fence_after();
 #pragma unroll
@@ -264,7 +257,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) attn_tiles_kernel(const AttnA
                     if (i == tiles - 1) tc_commit(smem_addr(&sh.v_empty[st]));
                     if (j + 1 < blocks) {
                         if (i == 0) {
-                            ok = wait(sh.k_full[st ^ 1], ((j + 1) / 2) & 1);
+                            ok = landed(sh.k_full[st ^ 1], ((j + 1) / 2) & 1);
                             if (!ok) break;
                             tc_fence_after();
                         }
@@ -304,7 +297,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) attn_tiles_kernel(const AttnA
             const uint32_t* live = sh.live[j & 3];
             const bool mask = key0 + TK - 1 > all_hi || key0 < all_lo || (live[0] & live[1] & live[2] & live[3]) != 0xffffffffu;
             float s0[32], s1[32];
-            float top = NEG_INF;
+            float tops[4] = {NEG_INF, NEG_INF, NEG_INF, NEG_INF};  // four chains
             auto hide = [&](float (&s)[32], int q) {  // the keys that this row does not see
                 if (!mask) return;
                 const uint32_t lv = live[q];
@@ -315,7 +308,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) attn_tiles_kernel(const AttnA
             };
             auto largest = [&](const float (&s)[32]) {
 #pragma unroll
-                for (int e = 0; e < 32; ++e) top = fmaxf(top, s[e]);
+                for (int e = 0; e < 32; ++e) tops[e & 3] = fmaxf(tops[e & 3], s[e]);
             };
             tc_ld32(s0, s_at), tc_ld32(s1, s_at + 32);
             tc_wait_ld(s0), tc_wait_ld(s1);
@@ -325,7 +318,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) attn_tiles_kernel(const AttnA
             tc_wait_ld(s0), tc_wait_ld(s1);
             hide(s0, 2), hide(s1, 3);
             largest(s0), largest(s1);
-            top *= a.scale_log2;
+            const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * a.scale_log2;
             // move the maximum only when it has to: by more than 2^8
             const bool move = top > m + 8.f;
             if (__any_sync(0xffffffffu, move)) {
@@ -348,12 +341,14 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) attn_tiles_kernel(const AttnA
             const float base = m == NEG_INF ? 0.f : m;
             auto weigh = [&](float (&s)[32], uint32_t to) {
                 uint32_t p[16];
+                float sum[4] = {};
 #pragma unroll
                 for (int e = 0; e < 32; e += 2) {
                     const float x = exp2_approx(fmaf(s[e], a.scale_log2, -base)), y = exp2_approx(fmaf(s[e + 1], a.scale_log2, -base));
-                    l += x + y;
+                    sum[e & 2] += x, sum[(e & 2) + 1] += y;
                     p[e / 2] = pack16<BF>(x, y);
                 }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                 tc_st16(to, p);
             };
             // keys 64..127 first: their scores are in registers, and P goes where those were
