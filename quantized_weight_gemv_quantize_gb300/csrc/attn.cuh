@@ -65,6 +65,7 @@ __device__ __forceinline__ bool find_tile(const AttnArgs& a, long long block, Ti
     int lo = 0, hi = usable;
     if (a.window > 0) lo = max(0, pos_lo - a.window + 1);
     if (a.causal) hi = min(hi, pos_hi + 1);
+    if (LAST_FIRST) lo = lo / 128 * 128;  // the 128-row kernel's key tiles start at multiples of their size
     hi = max(hi, lo);
     t->parts = max(1, (hi - lo + a.chunk - 1) / a.chunk);
     if (t->part >= t->parts) return false;

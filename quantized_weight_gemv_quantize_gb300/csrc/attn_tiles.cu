@@ -1,8 +1,8 @@
 // Attention of many rows (chunks of a prompt, whole prompts) over a paged cache on the fifth-generation tensor cores: two
 // tiles of 128 rows a block against tiles of 128 keys.
 //
-// For each key tile j and row tile i: S_i = Q_i K_j^T into tensor memory (fp32), softmax by one thread a row, P_i (16 bits)
-// back into the upper half of S_i's columns, O_i += P_i V_j with P_i read from tensor memory.  While the tensor cores work
+// For each key tile j and row tile i: S_i = Q_i K_j^T into tensor memory (fp32), softmax by two threads a row, P_i (16 bits)
+// back into S_i's columns, O_i += P_i V_j with P_i read from tensor memory.  While the tensor cores work
 // on one row tile, the other's softmax runs.  The running maximum that the exponent is taken against moves only when the
 // true one has grown by more than 2^8: then O_i and l are rescaled; p stays below 2^8, so nothing is lost by the delay.
 // The keys of a tile lie on pages anywhere: four warps look the rows up and copy them 16 bytes at a time into the
@@ -14,8 +14,10 @@ namespace qg {
 
 constexpr int TR = 128;          // rows of a row tile
 constexpr int TK = 128;          // keys of a key tile
-constexpr int TILE_THREADS = 13 * 32;
-constexpr int LOAD_WARP = 8, MMA_WARP = 12;
+// Warps 0..15: softmax, two groups of four a row tile; 16, 17: copies of keys and of values; 18: products.  With at most five
+// warps a quarter of the SM a thread has 96 registers, enough for its 64 scores (spills would go past the small L1 that is left).
+constexpr int K_WARP = 16, V_WARP = 17, MMA_WARP = 18;
+constexpr int TILE_THREADS = 19 * 32;
 
 template <int DP>
 struct TilesShape {
@@ -36,8 +38,13 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
 }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_commit(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+// The products and commits are issued by the one lane with `one` set, in code that the whole warp runs: control flow,
+// descriptors and addresses then stay uniform over the warp.
+__device__ __forceinline__ void tc_commit(uint32_t bar, uint32_t one) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar), "r"(one)
+        : "memory");
 }
 
 // Shared-memory operand: 128-byte swizzle, 16-byte units; lbo between 64-column groups (MN-major), sbo between groups of
@@ -52,17 +59,32 @@ __device__ __forceinline__ constexpr uint32_t tc_idesc(int n, bool transb) {
     return 1u << 4 | (BF ? 1u : 0u) << 7 | (BF ? 1u : 0u) << 10 | (transb ? 1u : 0u) << 16 |
            static_cast<uint32_t>(n / 8) << 17 | static_cast<uint32_t>(TR / 16) << 24;
 }
-__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate, uint32_t one) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(one)
         : "memory");
 }
-__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate, uint32_t one) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(one)
         : "memory");
+}
+
+// Two fp32 operations in one instruction, and the largest of three.
+__device__ __forceinline__ void fma2(float& x, float& y, float a, float b, float m, float c) {
+    asm("{\n\t.reg .b64 p, q, r;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %4};\n\tmov.b64 r, {%5, %5};\n\t"
+        "fma.rn.f32x2 p, p, q, r;\n\tmov.b64 {%0, %1}, p;\n\t}" : "=f"(x), "=f"(y) : "f"(a), "f"(b), "f"(m), "f"(c));
+}
+__device__ __forceinline__ void add2(float& x, float& y, float a, float b) {
+    asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\tadd.rn.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;\n\t}"
+        : "+f"(x), "+f"(y) : "f"(a), "f"(b));
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
 }
 
 #define QG_R32(X) X(0), X(1), X(2), X(3), X(4), X(5), X(6), X(7), X(8), X(9), X(10), X(11), X(12), X(13), X(14), X(15), X(16), \
@@ -81,17 +103,27 @@ __device__ __forceinline__ void tc_wait_ld(float (&r)[32]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;" : QG_R32(X) : : "memory");
 #undef X
 }
-__device__ __forceinline__ void tc_st32(uint32_t addr, const float (&r)[32]) {
-#define X(i) "f"(r[i])
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], " QG_LIST32 ";" ::QG_R32(X), "r"(addr) : "memory");
+#define QG_R16(X) X(0), X(1), X(2), X(3), X(4), X(5), X(6), X(7), X(8), X(9), X(10), X(11), X(12), X(13), X(14), X(15)
+#define QG_LIST16 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}"
+__device__ __forceinline__ void tc_ld16(float (&r)[16], uint32_t addr) {
+#define X(i) "=f"(r[i])
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 " QG_LIST16 ", [%16];" : QG_R16(X) : "r"(addr) : "memory");
 #undef X
 }
-__device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
-        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
-        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(addr)
-        : "memory");
+__device__ __forceinline__ void tc_wait_ld(float (&r)[16]) {
+#define X(i) "+f"(r[i])
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : QG_R16(X) : : "memory");
+#undef X
+}
+__device__ __forceinline__ void tc_st16(uint32_t addr, const float (&r)[16]) {
+#define X(i) "f"(r[i])
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], " QG_LIST16 ";" ::QG_R16(X), "r"(addr) : "memory");
+#undef X
+}
+__device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t (&r)[32]) {
+#define X(i) "r"(r[i])
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], " QG_LIST32 ";" ::QG_R32(X), "r"(addr) : "memory");
+#undef X
 }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -100,17 +132,32 @@ __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool live) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
 
+// Copies `box` tokens of one page, 64 elements of one head, into swizzled rows; completion is counted on the barrier.
+__device__ __forceinline__ void tma_box(uint32_t dst, const unsigned long long* map, int x, int token, int page, int head,
+                                        uint32_t bar, uint32_t one) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %7, 0;\n\t"
+        "@q cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];\n\t}" ::"r"(dst),
+        "l"(map), "r"(x), "r"(token), "r"(page), "r"(head), "r"(bar), "r"(one)
+        : "memory");
+}
+__device__ __forceinline__ uint32_t elect() {
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one;
+}
+
 struct TilesShared {
     unsigned long long q_full, k_full[2], v_full[2], k_empty[2], v_empty[2], s_full[2], p_full[2], o_full[2], drain;
-    long long k_off[2][TK], v_off[2][TK];
-    uint32_t live[4][TK / 32];
+    uint32_t live[4][TK / 32];  // which keys of a key tile are there, one bit each
+    float row[2][2][TR];  // by row tile and half of the keys: a row's maximum, at the end its sum
     uint32_t tmem;
-    int failed;
 };
 
 template <int DP, bool BF>
-__global__ void __launch_bounds__(TILE_THREADS, 1) attn_tiles_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(TILE_THREADS, 1) attn_tiles_kernel(const __grid_constant__ AttnTileArgs ta) {
     using S = TilesShape<DP>;
+    const AttnArgs& a = ta.a;
     extern __shared__ uint8_t smem_raw[];
     __shared__ TilesShared sh;
     pdl_launch_dependents();
@@ -123,15 +170,14 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) attn_tiles_kernel(const AttnA
     const int tiles = t.rows > TR ? 2 : 1;
 
     if (threadIdx.x == 0) {
-        sh.failed = 0;
-        mbar_init(smem_addr(&sh.q_full), 128);
+        mbar_init(smem_addr(&sh.q_full), static_cast<uint32_t>(256 * tiles));
         for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_addr(&sh.k_full[i]), 128);
-            mbar_init(smem_addr(&sh.v_full[i]), 128);
+            mbar_init(smem_addr(&sh.k_full[i]), 32);
+            mbar_init(smem_addr(&sh.v_full[i]), 32);
             mbar_init(smem_addr(&sh.k_empty[i]), 1);
             mbar_init(smem_addr(&sh.v_empty[i]), 1);
             mbar_init(smem_addr(&sh.s_full[i]), 1);
-            mbar_init(smem_addr(&sh.p_full[i]), 128);
+            mbar_init(smem_addr(&sh.p_full[i]), 8);
             mbar_init(smem_addr(&sh.o_full[i]), 1);
         }
         mbar_init(smem_addr(&sh.drain), 1);
@@ -144,182 +190,220 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) attn_tiles_kernel(const AttnA
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = sh.tmem;
-    volatile int* failed = &sh.failed;
-    // A bounded wait; one that runs out (it cannot in a correct run) ends every role.
+    constexpr uint32_t tmem = 0;  // all 512 columns are this block's, so they start at column 0
+    // A bounded wait; where one runs out (it cannot in a correct run) the role ends, and those that wait for it likewise.
     auto wait = [&](unsigned long long& bar, int parity) {
-        if (mbar_wait_bounded(smem_addr(&bar), static_cast<uint32_t>(parity))) return !*failed;
-        *failed = 1;
+        if (mbar_wait_bounded(smem_addr(&bar), static_cast<uint32_t>(parity))) return true;
         atomicOr(a.err, ERR_WAIT_TIMEOUT);
         return false;
     };
 
-    if (warp >= LOAD_WARP && warp < MMA_WARP) {
-        // ---- four warps copy Q once, then the key tiles
-        const int lt = threadIdx.x - LOAD_WARP * 32, lw = lt / 32;
-        constexpr int PER_ROW = DP / 8, ROWS_PASS = 128 / PER_ROW;  // 16-byte pieces of a row; rows of a pass of 128 threads
-        const int c = lt % PER_ROW, r_in = lt / PER_ROW;
-        const bool col = c * 8 < a.dim;
-        auto place = [&](uint32_t base, int r) {
-            return base + (c / 8) * S::HALF_BYTES + r * 128 + (((c % 8) ^ (r & 7)) << 4);
+    // 16-byte piece c of row r in a tile's swizzled layout
+    auto place = [&](uint32_t base, int r, int c) {
+        return base + (c / 8) * S::HALF_BYTES + r * 128 + (((c % 8) ^ (r & 7)) << 4);
+    };
+    constexpr int PER_ROW = DP / 8;  // 16-byte pieces of a row
+
+    if (warp == K_WARP || warp == V_WARP) {
+        // ---- copies of the key tiles, one warp for each side
+        const bool side = warp == V_WARP;
+        const uint32_t one = elect();
+        unsigned long long* const full = side ? sh.v_full : sh.k_full;
+        unsigned long long* const empty = side ? sh.v_empty : sh.k_empty;
+        const uint16_t* const src = (side ? a.v : a.k) + t.kv_head * (side ? a.v_head : a.k_head);
+        const long long page_stride = side ? a.v_page : a.k_page, token_stride = side ? a.v_token : a.k_token;
+        const unsigned long long* const map = side ? ta.v_map : ta.k_map;
+        const int* const table = a.pages + t.seq * a.pages_stride;
+        // Page and token of this lane's four keys (lane, lane + 32, ..) of block j, read one block ahead; page -1: no such key.
+        int page[4], token[4];
+        auto look_up = [&](int j) {
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                const int key = t.k0 + j * TK + h * 32 + lane, nth = key / a.page_size;
+                token[h] = key - nth * a.page_size;
+                page[h] = key < t.k1 ? table[nth] : -1;
+            }
+        };
+        auto of_row = [&](const int (&v)[4], int row) {
+            return __shfl_sync(0xffffffffu, row < 64 ? (row < 32 ? v[0] : v[1]) : (row < 96 ? v[2] : v[3]), row & 31);
         };
         bool ok = true;
-        // The barrier counts this thread's arrival when its copies so far have landed; the thread itself goes on.
-        auto arrive_when_landed = [&](unsigned long long& bar) {
-            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(&bar)) : "memory");
-        };
-        const int* table = a.pages + t.seq * a.pages_stride;
-        // The page of this thread's key of block j, read one block ahead; -1 past the end.
-        auto page_of = [&](int j) {
-            const int key = t.k0 + j * TK + lt;
-            return key < t.k1 ? table[key / a.page_size] : -1;
-        };
-        int page = page_of(0);
-        if (blocks > 0) {
-            const uint16_t* q = static_cast<const uint16_t*>(a.q);
-            for (int r0 = 0; r0 < tiles * TR; r0 += ROWS_PASS) {
-                const int r = r0 + r_in;
-                const bool in = r < t.rows && col;
-                const long long off = in ? out_at(a, t, r, a.q_token, a.q_head) + c * 8 : 0;
-                cp16(place(smem + S::Q_AT + (r / TR) * S::TILE_BYTES, r % TR), q + off, in);
-            }
-            arrive_when_landed(sh.q_full);
-        }
-        for (int j = 0; j < blocks && ok; ++j) {
+        look_up(0);
+        for (int j = 0; j < blocks; ++j) {
             const int st = j & 1;
-            {
-                const int key = t.k0 + j * TK + lt, off = key % a.page_size;
-                const bool live = page >= 0 && page < a.num_pages;
-                if (!live && key < t.k1) atomicOr(a.err, ERR_BAD_INDEX);
-                sh.k_off[st][lt] = live ? page * a.k_page + off * a.k_token + t.kv_head * a.k_head : -1;
-                sh.v_off[st][lt] = live ? page * a.v_page + off * a.v_token + t.kv_head * a.v_head : -1;
-                const unsigned mask = __ballot_sync(0xffffffffu, live);
-                if (lane == 0) sh.live[j & 3][lw] = mask;
-                page = page_of(j + 1);
+            uint32_t all = 0xffffffffu;
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                const bool live = page[h] >= 0 && page[h] < a.num_pages;
+                if (!live && !side && t.k0 + j * TK + h * 32 + lane < t.k1) atomicOr(a.err, ERR_BAD_INDEX);
+                if (!live) page[h] = -1;
+                const uint32_t mask = __ballot_sync(0xffffffffu, live);
+                if (!side && lane == 0) sh.live[j & 3][h] = mask;
+                all &= mask;
             }
-            asm volatile("bar.sync 1, 128;" ::: "memory");
-            if (j >= 2) ok = wait(sh.k_empty[st], (j / 2 - 1) & 1);
+            if (j >= 2) ok = __all_sync(0xffffffffu, wait(empty[st], (j / 2 - 1) & 1));
             if (!ok) break;
+            const uint32_t to = smem + (side ? S::V_AT : S::K_AT) + st * S::TILE_BYTES, bar = smem_addr(&full[st]);
+            if (a.box && all == 0xffffffffu) {  // every key is there: one tensor-map copy a box of tokens and 64 columns
+                if (lane == 0) mbar_arrive_expect_tx(bar, S::TILE_BYTES);
+                else mbar_arrive(bar);
+                for (int row = 0; row < TK; row += a.box) {
+                    const int tk = of_row(token, row), pg = of_row(page, row);
+#pragma unroll
+                    for (int h = 0; h < S::HALVES; ++h)
+                        tma_box(to + h * S::HALF_BYTES + row * 128, map, h * 64, tk, pg, t.kv_head, bar, one);
+                }
+            } else {  // row by row, the missing ones as zeros
+                const int c = lane % PER_ROW;
 #pragma unroll 8
-            for (int r = r_in; r < TK; r += ROWS_PASS) {
-                const long long off = sh.k_off[st][r];
-                const bool in = off >= 0 && col;
-                cp16(place(smem + S::K_AT + st * S::TILE_BYTES, r), a.k + (in ? off + c * 8 : 0), in);
+                for (int r0 = 0; r0 < TK; r0 += 32 / PER_ROW) {
+                    const int r = r0 + lane / PER_ROW;
+                    int pg = 0, tk = 0;
+#pragma unroll
+                    for (int h = 0; h < 32 / PER_ROW; ++h) {
+                        const int p = of_row(page, r0 + h), k = of_row(token, r0 + h);
+                        if (h == lane / PER_ROW) pg = p, tk = k;
+                    }
+                    const bool in = pg >= 0 && c * 8 < a.dim;
+                    cp16(place(to, r, c), src + (in ? pg * page_stride + tk * token_stride + c * 8 : 0), in);
+                }
+                // the barrier counts this lane's arrival when its copies have landed; the lane itself goes on
+                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
             }
-            arrive_when_landed(sh.k_full[st]);
-            if (j >= 2) ok = wait(sh.v_empty[st], (j / 2 - 1) & 1);
-            if (!ok) break;
-#pragma unroll 8
-            for (int r = r_in; r < TK; r += ROWS_PASS) {
-                const long long off = sh.v_off[st][r];
-                const bool in = off >= 0 && col;
-                cp16(place(smem + S::V_AT + st * S::TILE_BYTES, r), a.v + (in ? off + c * 8 : 0), in);
-            }
-            arrive_when_landed(sh.v_full[st]);
+            look_up(j + 1);
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
     } else if (warp == MMA_WARP) {
         // ---- one thread issues every product
-        if (lane == 0 && blocks > 0) {
+        if (blocks > 0) {
+            const uint32_t one = elect();
             constexpr uint32_t qk = tc_idesc<BF>(TK, false), pv = tc_idesc<BF>(DP, true);
+            const uint64_t q_desc = tc_desc(smem + S::Q_AT, 16, 1024), k_desc = tc_desc(smem + S::K_AT, 16, 1024),
+                           v_desc = tc_desc(smem + S::V_AT, S::HALF_BYTES, 1024);
             auto scores = [&](int i, int st) {
 #pragma unroll
                 for (int kk = 0; kk < DP / 16; ++kk) {
-                    const uint32_t off = (kk / 4) * S::HALF_BYTES + (kk % 4) * 32;
-                    tc_mma_ss(tmem + S::S_COL + i * TK, tc_desc(smem + S::Q_AT + i * S::TILE_BYTES + off, 16, 1024),
-                              tc_desc(smem + S::K_AT + st * S::TILE_BYTES + off, 16, 1024), qk, kk > 0);
+                    const uint32_t off = (kk / 4) * S::HALF_BYTES + (kk % 4) * 32;  // descriptors count 16 bytes
+                    tc_mma_ss(S::S_COL + i * TK, q_desc + ((i * S::TILE_BYTES + off) >> 4),
+                              k_desc + ((st * S::TILE_BYTES + off) >> 4), qk, kk > 0, one);
                 }
-                tc_commit(smem_addr(&sh.s_full[i]));
+                tc_commit(smem_addr(&sh.s_full[i]), one);
             };
-            // the copies were made through the generic proxy, the tensor cores read through the asynchronous one
-            auto landed = [&](unsigned long long& bar, int parity) {
-                const bool ok = wait(bar, parity);
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                return ok;
+            auto await = [&](unsigned long long& bar, int parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
+            // Tiles that were copied row by row came through the generic proxy, and the tensor cores read through the
+            // asynchronous one.
+            auto landed = [&](unsigned long long& bar, int j) {
+                if (!await(bar, (j / 2) & 1)) return false;
+                const uint32_t* lv = sh.live[j & 3];
+                if (!a.box || (lv[0] & lv[1] & lv[2] & lv[3]) != 0xffffffffu) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                return true;
             };
-            bool ok = landed(sh.q_full, 0) && landed(sh.k_full[0], 0);
+            bool ok = await(sh.q_full, 0) && landed(sh.k_full[0], 0);
             if (ok) {
                 tc_fence_after();
                 for (int i = 0; i < tiles; ++i) scores(i, 0);
-                tc_commit(smem_addr(&sh.k_empty[0]));
+                tc_commit(smem_addr(&sh.k_empty[0]), one);
             }
             for (int j = 0; j < blocks && ok; ++j) {
                 const int st = j & 1;
                 for (int i = 0; i < tiles; ++i) {
-                    ok = wait(sh.p_full[i], j & 1);
-                    if (ok && i == 0) ok = landed(sh.v_full[st], (j / 2) & 1);
+                    if (i == 0) {  // waited for while the softmax runs
+                        ok = landed(sh.v_full[st], j);
+                        if (ok && j + 1 < blocks) ok = landed(sh.k_full[st ^ 1], j + 1);
+                    }
+                    if (ok) ok = await(sh.p_full[i], j & 1);
                     if (!ok) break;
                     tc_fence_after();
 #pragma unroll
                     for (int kk = 0; kk < TK / 16; ++kk)
-                        tc_mma_ts(tmem + S::O_COL + i * DP, tmem + S::S_COL + i * TK + TK / 2 + kk * 8,
-                                  tc_desc(smem + S::V_AT + st * S::TILE_BYTES + kk * 2048, S::HALF_BYTES, 1024), pv, j > 0 || kk > 0);
-                    if (i == tiles - 1) tc_commit(smem_addr(&sh.v_empty[st]));
+                        tc_mma_ts(S::O_COL + i * DP, S::S_COL + i * TK + kk / 4 * 64 + kk % 4 * 8,
+                                  v_desc + ((st * S::TILE_BYTES + kk * 2048) >> 4), pv, j > 0 || kk > 0, one);
+                    if (i == tiles - 1) tc_commit(smem_addr(&sh.v_empty[st]), one);
                     if (j + 1 < blocks) {
-                        if (i == 0) {
-                            ok = landed(sh.k_full[st ^ 1], ((j + 1) / 2) & 1);
-                            if (!ok) break;
-                            tc_fence_after();
-                        }
                         scores(i, st ^ 1);
-                        if (i == tiles - 1) tc_commit(smem_addr(&sh.k_empty[st ^ 1]));
+                        if (i == tiles - 1) tc_commit(smem_addr(&sh.k_empty[st ^ 1]), one);
                     } else {
-                        tc_commit(smem_addr(&sh.o_full[i]));
+                        tc_commit(smem_addr(&sh.o_full[i]), one);
                     }
                 }
             }
             // nothing is left in flight when the block ends
-            tc_commit(smem_addr(&sh.drain));
+            tc_commit(smem_addr(&sh.drain), one);
             (void)mbar_wait_bounded(smem_addr(&sh.drain), 0);
         }
         __syncwarp();
-    } else if (warp / 4 < tiles) {
-        // ---- softmax: one thread a row
-        const int i = warp / 4, r = i * TR + threadIdx.x % TR;  // row of the pair of tiles
+    } else if (warp / 8 < tiles) {
+        // ---- softmax: two threads a row, one for each half of the keys
+        const int i = warp / 8, half = warp / 4 % 2, tr = threadIdx.x % TR, r = i * TR + tr;  // r: row of the two tiles
         const uint32_t lanes = static_cast<uint32_t>(warp % 4) << 21;  // 32 lanes a warp, in the upper half of the address
-        const uint32_t s_at = tmem + lanes + S::S_COL + i * TK, o_at = tmem + lanes + S::O_COL + i * DP;
+        const uint32_t s_at = tmem + lanes + S::S_COL + i * TK, o_at = tmem + lanes + S::O_COL + i * DP + half * (DP / 2);
         const int last = min(t.rows, (i + 1) * TR) - 1;  // last row of this tile
         const int pos = row_pos(a, t, r);
         const int hi = a.causal ? min(t.k1 - 1, pos) : t.k1 - 1, lo = a.window > 0 ? pos - a.window + 1 : 0;
         // keys that all rows of the tile see
         const int all_hi = a.causal ? min(t.k1 - 1, row_pos(a, t, i * TR)) : t.k1 - 1;
         const int all_lo = a.window > 0 ? row_pos(a, t, last) - a.window + 1 : 0;
+        // the two warps of the same rows
+        auto pair_sync = [&] { asm volatile("bar.sync %0, 64;" ::"r"(2 + i * 4 + warp % 4) : "memory"); };
+        // this tile's rows of Q
+        if (blocks > 0) {
+            const uint16_t* q = static_cast<const uint16_t*>(a.q);
+            const int lt = threadIdx.x % 256, c = lt % PER_ROW;
+#pragma unroll 4
+            for (int qr = lt / PER_ROW; qr < TR; qr += 256 / PER_ROW) {
+                const bool in = i * TR + qr < t.rows && c * 8 < a.dim;
+                const long long off = in ? out_at(a, t, i * TR + qr, a.q_token, a.q_head) + c * 8 : 0;
+                cp16(place(smem + S::Q_AT + i * S::TILE_BYTES, qr, c), q + off, in);
+            }
+            asm volatile("cp.async.wait_all;\n\tfence.proxy.async.shared::cta;" ::: "memory");
+            mbar_arrive(smem_addr(&sh.q_full));
+        }
         float m = NEG_INF, l = 0.f;  // m: the maximum in use, in units of the scaled scores (base 2)
         bool ok = true;
         for (int j = 0; j < blocks; ++j) {
-            ok = wait(sh.s_full[i], j & 1);
-            if (!__all_sync(0xffffffffu, ok)) {
-                ok = false;
-                break;
-            }
+            ok = __all_sync(0xffffffffu, wait(sh.s_full[i], j & 1));
+            if (!ok) break;
             tc_fence_after();
-            const int key0 = t.k0 + j * TK;
-            const uint32_t* live = sh.live[j & 3];
-            const bool mask = key0 + TK - 1 > all_hi || key0 < all_lo || (live[0] & live[1] & live[2] & live[3]) != 0xffffffffu;
-            float s0[32], s1[32];
-            float tops[4] = {NEG_INF, NEG_INF, NEG_INF, NEG_INF};  // four chains
-            auto hide = [&](float (&s)[32], int q) {  // the keys that this row does not see
-                if (!mask) return;
-                const uint32_t lv = live[q];
-                const int k = key0 + q * 32;
+            const int key0 = t.k0 + j * TK + half * 64;
+            const uint32_t at = s_at + half * 64;  // this half's scores, and then its probabilities
+            const uint32_t* live = sh.live[j & 3] + half * 2;
+            const bool mask = key0 + 63 > all_hi || key0 < all_lo || (live[0] & live[1]) != 0xffffffffu;
+            // 64 scores: p = 2^(s - base) in 16 bits; the sum of p and the maximum of s.
+            uint32_t p[32];
+            float top, sum;
+            auto weigh = [&](float base) {
+                float s[2][32], tops[2] = {NEG_INF, NEG_INF}, sums[4] = {};
+                tc_ld32(s[0], at), tc_ld32(s[1], at + 32);
+                tc_wait_ld(s[0]), tc_wait_ld(s[1]);
 #pragma unroll
-                for (int e = 0; e < 32; ++e)
-                    if (!(lv >> e & 1u) || k + e > hi || k + e < lo) s[e] = NEG_INF;
-            };
-            auto largest = [&](const float (&s)[32]) {
+                for (int q = 0; q < 2; ++q) {
+                    float (&c)[32] = s[q];
+                    if (mask) {  // the keys that this row does not see
+                        const uint32_t lv = live[q];
+                        const int k = key0 + q * 32;
 #pragma unroll
-                for (int e = 0; e < 32; ++e) tops[e & 3] = fmaxf(tops[e & 3], s[e]);
+                        for (int e = 0; e < 32; ++e)
+                            if (!(lv >> e & 1u) || k + e > hi || k + e < lo) c[e] = NEG_INF;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        tops[e / 2 & 1] = max3(tops[e / 2 & 1], c[e], c[e + 1]);
+                        float x, y;
+                        fma2(x, y, c[e], c[e + 1], a.scale_log2, -base);
+                        x = exp2_approx(x), y = exp2_approx(y);
+                        add2(sums[e & 2], sums[(e & 2) + 1], x, y);
+                        p[q * 16 + e / 2] = pack16<BF>(x, y);
+                    }
+                }
+                top = fmaxf(tops[0], tops[1]);
+                sum = (sums[0] + sums[1]) + (sums[2] + sums[3]);
             };
-            tc_ld32(s0, s_at), tc_ld32(s1, s_at + 32);
-            tc_wait_ld(s0), tc_wait_ld(s1);
-            hide(s0, 0), hide(s1, 1);
-            largest(s0), largest(s1);
-            tc_ld32(s0, s_at + 64), tc_ld32(s1, s_at + 96);
-            tc_wait_ld(s0), tc_wait_ld(s1);
-            hide(s0, 2), hide(s1, 3);
-            largest(s0), largest(s1);
-            const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * a.scale_log2;
-            // move the maximum only when it has to: by more than 2^8
+            // The exponentials are taken against the maximum in use while the new one is being found; only where that turns out
+            // to be larger by more than 2^8 (and for the first keys that a row sees) are they taken again.
+            weigh(m == NEG_INF ? 0.f : m);
+            sh.row[i][half][tr] = top;
+            pair_sync();
+            top = fmaxf(top, sh.row[i][half ^ 1][tr]) * a.scale_log2;
             const bool move = top > m + 8.f;
             if (__any_sync(0xffffffffu, move)) {
                 const float f = move ? exp2_approx(m - top) : 1.f;  // 0 for the first keys that the row sees
@@ -327,53 +411,42 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) attn_tiles_kernel(const AttnA
                 l *= f;
                 if (j > 0) {
                     // S_j is there, so the product before it, into O, has ended
-                    float o[32];
+                    float o[16];
 #pragma unroll 1
-                    for (int d = 0; d < DP; d += 32) {
-                        tc_ld32(o, o_at + d);
+                    for (int d = 0; d < DP / 2; d += 16) {
+                        tc_ld16(o, o_at + d);
                         tc_wait_ld(o);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] *= f;
-                        tc_st32(o_at + d, o);
+                        for (int e = 0; e < 16; ++e) o[e] *= f;
+                        tc_st16(o_at + d, o);
                     }
                 }
+                weigh(m == NEG_INF ? 0.f : m);
             }
-            const float base = m == NEG_INF ? 0.f : m;
-            auto weigh = [&](float (&s)[32], uint32_t to) {
-                uint32_t p[16];
-                float sum[4] = {};
-#pragma unroll
-                for (int e = 0; e < 32; e += 2) {
-                    const float x = exp2_approx(fmaf(s[e], a.scale_log2, -base)), y = exp2_approx(fmaf(s[e + 1], a.scale_log2, -base));
-                    sum[e & 2] += x, sum[(e & 2) + 1] += y;
-                    p[e / 2] = pack16<BF>(x, y);
-                }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                tc_st16(to, p);
-            };
-            // keys 64..127 first: their scores are in registers, and P goes where those were
-            weigh(s0, s_at + 96), weigh(s1, s_at + 112);
-            tc_ld32(s0, s_at), tc_ld32(s1, s_at + 32);
-            tc_wait_ld(s0), tc_wait_ld(s1);
-            hide(s0, 0), hide(s1, 1);
-            weigh(s0, s_at + 64), weigh(s1, s_at + 80);
+            l += sum;
+            tc_st32(at, p);
             tc_wait_st();
             tc_fence_before();
-            mbar_arrive(smem_addr(&sh.p_full[i]));
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&sh.p_full[i]));  // 256 arrivals on one barrier would take their time
         }
         if (ok && blocks > 0) ok = __all_sync(0xffffffffu, wait(sh.o_full[i], 0));
         if (ok) {
             tc_fence_after();
+            sh.row[i][half][tr] = l;
+            pair_sync();
+            l += sh.row[i][half ^ 1][tr];
             const bool whole = t.parts == 1, row = r < t.rows;
             const float inv = whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
             const long long at = row ? out_at(a, t, r, a.out_token, a.out_head) : 0;
             float* rec = row && !whole ? part_row(a, t, t.part, r) : nullptr;
 #pragma unroll 1
-            for (int d = 0; d < DP; d += 32) {
+            for (int d0 = 0; d0 < DP / 2; d0 += 32) {
+                const int d = half * (DP / 2) + d0;
                 float o[32];
                 __syncwarp();
                 if (blocks > 0) {
-                    tc_ld32(o, o_at + d);
+                    tc_ld32(o, o_at + d0);
                     tc_wait_ld(o);
                 } else {
 #pragma unroll
@@ -392,8 +465,10 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) attn_tiles_kernel(const AttnA
                         if (d + e < a.dim) __stcg(reinterpret_cast<float2*>(rec + 2 + d + e), make_float2(o[e], o[e + 1]));
                 }
             }
-            if (row && whole) put_lse(a, t, r, m, l);
-            if (row && !whole) __stcg(reinterpret_cast<float2*>(rec), make_float2(m, l));
+            if (row && half == 0) {
+                if (whole) put_lse(a, t, r, m, l);
+                else __stcg(reinterpret_cast<float2*>(rec), make_float2(m, l));
+            }
         }
         tc_fence_before();
     }

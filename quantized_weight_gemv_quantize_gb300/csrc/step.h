@@ -50,6 +50,14 @@ struct AttnArgs {
     int parts;       // parts of a row tile in the grid
     int row_tiles;   // row tiles of a sequence and key/value head in the grid
     int rows_part;   // rows of a part's record
+    int box;         // tokens of one tensor-map copy (128-row kernel), 0: no tensor map, every row is copied by itself
+};
+
+// The 128-row kernel's arguments: the cache's two tensor maps, [head, page, token, dim] with boxes of `box` tokens by 64
+// elements in the 128-byte swizzle.
+struct AttnTileArgs {
+    alignas(64) unsigned long long k_map[16], v_map[16];
+    AttnArgs a;
 };
 
 struct AttnPlan {

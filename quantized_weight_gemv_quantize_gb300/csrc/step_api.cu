@@ -1,5 +1,6 @@
 // C ABI of the operators between the GEMVs: rotary positions, attention over the paged cache, sampling.  Every check
 // runs on the host before anything is enqueued.
+#include <cuda.h>
 #include <limits.h>
 #include <math.h>
 #include <mutex>
@@ -191,8 +192,9 @@ static int attn_plan(int seqs, int tokens, int heads, int kv_heads, int dim, int
     const long long most = p->tiles ? (max_kv + 1023) / 1024 : (max_kv + 127) / 128;
     if (parts > most) parts = most;
     if (parts < 1 || tiles > ATTN_MAX_COUNTERS) parts = 1;
-    const long long chunk = ((max_kv + parts - 1) / parts + 15) / 16 * 16;
-    p->chunk = static_cast<int>(chunk < 16 ? 16 : chunk > INT_MAX - 15 ? INT_MAX - 15 : chunk);
+    const long long unit = p->tiles ? 128 : 16;
+    const long long chunk = ((max_kv + parts - 1) / parts + unit - 1) / unit * unit;
+    p->chunk = static_cast<int>(chunk < unit ? unit : chunk > INT_MAX - 127 ? INT_MAX - 127 : chunk);
     p->parts = max_kv > 0 ? static_cast<int>((static_cast<long long>(max_kv) + p->chunk - 1) / p->chunk) : 1;
     p->grid = tiles * p->parts;
     if (p->grid > INT_MAX) return QGEMV_ERR_UNSUPPORTED;
@@ -218,6 +220,41 @@ static int allow_smem(const void* fn, unsigned smem) {
         return QGEMV_OK;
     }
     return QGEMV_ERR_UNSUPPORTED;
+}
+
+// Tensor map of one side of a cache for the 128-row kernel; false where the cache cannot be described by one (then the
+// kernel copies row by row).  Host arithmetic of the driver, about a microsecond.
+static bool cache_map(unsigned long long (&map)[16], const void* base, const qgemv_cache& c, long long page, long long token,
+                      long long head, int box) {
+    using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    static const Encode encode = [] {
+        void* fn = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess) {
+            (void)cudaGetLastError();
+            fn = nullptr;
+        }
+        return reinterpret_cast<Encode>(fn);
+    }();
+    if (!encode) return false;
+    static_assert(sizeof(CUtensorMap) == sizeof(map), "");
+    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(c.dim), static_cast<cuuint64_t>(c.page_size),
+                                static_cast<cuuint64_t>(c.num_pages), static_cast<cuuint64_t>(c.heads)};
+    // (a dimension of one element is never stepped over: any valid stride will do)
+    const long long s[3] = {c.page_size > 1 ? token : c.dim, c.num_pages > 1 ? page : c.dim, c.heads > 1 ? head : c.dim};
+    cuuint64_t strides[3];
+    for (int i = 0; i < 3; ++i) {
+        if (s[i] <= 0 || s[i] >= 1ll << 38) return false;
+        strides[i] = static_cast<cuuint64_t>(s[i]) * 2;
+    }
+    const cuuint32_t boxes[4] = {64, static_cast<cuuint32_t>(box), 1, 1}, ones[4] = {1, 1, 1, 1};
+    return encode(reinterpret_cast<CUtensorMap*>(map),
+                  c.kind == QGEMV_ACT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+                  const_cast<void*>(base), dims, strides, boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 static int run_attn(const qgemv_attn_args* a, unsigned flags, void* stream) {
@@ -283,8 +320,21 @@ static int run_attn(const qgemv_attn_args* a, unsigned flags, void* stream) {
     unsigned smem, threads;
     const void* fn = (p.tiles ? attn_tiles_kernel_ptr : attn_rows_kernel_ptr)(a->kind == QGEMV_ACT_BF16, c.dim, &smem, &threads);
     if ((st = allow_smem(fn, smem))) return st;
-    cudaError_t e = launch_step(fn, dim3(static_cast<unsigned>(p.grid)), threads, smem, 1, pdl,
-                                static_cast<cudaStream_t>(stream), k);
+    const dim3 grid(static_cast<unsigned>(p.grid));
+    cudaError_t e;
+    if (p.tiles) {
+        AttnTileArgs ta = {};
+        // The tokens of one copy: the largest power of two that divides the page and a key tile; 8 is the swizzle's period.
+        int box = 128;
+        while (c.page_size % box) box /= 2;
+        if (box >= 8 && cache_map(ta.k_map, c.k, c, c.k_page, c.k_token, c.k_head, box) &&
+            cache_map(ta.v_map, c.v, c, c.v_page, c.v_token, c.v_head, box))
+            k.box = box;
+        ta.a = k;
+        e = launch_step(fn, grid, threads, smem, 1, pdl, static_cast<cudaStream_t>(stream), ta);
+    } else {
+        e = launch_step(fn, grid, threads, smem, 1, pdl, static_cast<cudaStream_t>(stream), k);
+    }
     if (e != cudaSuccess) return api_cuda_fail(e);
     api_route(p.tiles ? QGEMV_ROUTE_ATTN_TILES : QGEMV_ROUTE_ATTN_ROWS, pdl);
     return QGEMV_OK;
