@@ -14,10 +14,11 @@ namespace qg {
 
 constexpr int TR = 128;          // rows of a row tile
 constexpr int TK = 128;          // keys of a key tile
-// Warps 0..15: softmax, two groups of four a row tile; 16, 17: copies of keys and of values; 18: products.  With at most five
-// warps a quarter of the SM a thread has 96 registers, enough for its 64 scores (spills would go past the small L1 that is left).
-constexpr int K_WARP = 16, V_WARP = 17, MMA_WARP = 18;
-constexpr int TILE_THREADS = 19 * 32;
+// Warps 0..15: softmax, two groups of four a row tile; 16, 17: copies of keys and of values; 18: products; 19: waits for the
+// copies in its place (a wait costs the issuing warp some 250 cycles, even for what is there).  With at most five warps a quarter of
+// the SM a thread has 96 registers, enough for its 64 scores (spills would go past the small L1 that is left).
+constexpr int K_WARP = 16, V_WARP = 17, MMA_WARP = 18, GATE_WARP = 19;
+constexpr int TILE_THREADS = 20 * 32;
 
 template <int DP>
 struct TilesShape {
@@ -148,7 +149,7 @@ __device__ __forceinline__ uint32_t elect() {
 }
 
 struct TilesShared {
-    unsigned long long q_full, k_full[2], v_full[2], k_empty[2], v_empty[2], s_full[2], p_full[2], o_full[2], drain;
+    unsigned long long q_full, k_first, k_full[2], v_full[2], k_empty[2], v_empty[2], s_full[2], p_full[2], o_full[2], drain;
     uint32_t live[4][TK / 32];  // which keys of a key tile are there, one bit each
     float row[2][2][TR];  // by row tile and half of the keys: a row's maximum, at the end its sum
     uint32_t tmem;
@@ -177,9 +178,10 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) attn_tiles_kernel(const __gri
             mbar_init(smem_addr(&sh.k_empty[i]), 1);
             mbar_init(smem_addr(&sh.v_empty[i]), 1);
             mbar_init(smem_addr(&sh.s_full[i]), 1);
-            mbar_init(smem_addr(&sh.p_full[i]), 8);
+            mbar_init(smem_addr(&sh.p_full[i]), i == 0 ? 9 : 8);  // a softmax warp each, and the gate
             mbar_init(smem_addr(&sh.o_full[i]), 1);
         }
+        mbar_init(smem_addr(&sh.k_first), 1);
         mbar_init(smem_addr(&sh.drain), 1);
         fence_mbar_init();
     }
@@ -290,15 +292,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) attn_tiles_kernel(const __gri
                 tc_commit(smem_addr(&sh.s_full[i]), one);
             };
             auto await = [&](unsigned long long& bar, int parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
-            // Tiles that were copied row by row came through the generic proxy, and the tensor cores read through the
-            // asynchronous one.
-            auto landed = [&](unsigned long long& bar, int j) {
-                if (!await(bar, (j / 2) & 1)) return false;
-                const uint32_t* lv = sh.live[j & 3];
-                if (!a.box || (lv[0] & lv[1] & lv[2] & lv[3]) != 0xffffffffu) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                return true;
-            };
-            bool ok = await(sh.q_full, 0) && landed(sh.k_full[0], 0);
+            bool ok = await(sh.q_full, 0) && await(sh.k_first, 0);
             if (ok) {
                 tc_fence_after();
                 for (int i = 0; i < tiles; ++i) scores(i, 0);
@@ -307,11 +301,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) attn_tiles_kernel(const __gri
             for (int j = 0; j < blocks && ok; ++j) {
                 const int st = j & 1;
                 for (int i = 0; i < tiles; ++i) {
-                    if (i == 0) {  // waited for while the softmax runs
-                        ok = landed(sh.v_full[st], j);
-                        if (ok && j + 1 < blocks) ok = landed(sh.k_full[st ^ 1], j + 1);
-                    }
-                    if (ok) ok = await(sh.p_full[i], j & 1);
+                    ok = await(sh.p_full[i], j & 1);  // for the first row tile also: V_j and K_j+1 are there
                     if (!ok) break;
                     tc_fence_after();
 #pragma unroll
@@ -332,6 +322,25 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) attn_tiles_kernel(const __gri
             (void)mbar_wait_bounded(smem_addr(&sh.drain), 0);
         }
         __syncwarp();
+    } else if (warp == GATE_WARP) {
+        // Tiles that were copied row by row came through the generic proxy, and the tensor cores read through the asynchronous
+        // one: a fence lies between.
+        auto landed = [&](unsigned long long& bar, int j) {
+            if (!__all_sync(0xffffffffu, wait(bar, (j / 2) & 1))) return false;
+            const uint32_t* lv = sh.live[j & 3];
+            if (!a.box || (lv[0] & lv[1] & lv[2] & lv[3]) != 0xffffffffu) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            return true;
+        };
+        if (blocks > 0 && landed(sh.k_full[0], 0)) {
+            if (lane == 0) mbar_arrive(smem_addr(&sh.k_first));
+            for (int j = 0; j < blocks; ++j) {
+                // (not before S_j is there: the barrier's round for the block before has ended then)
+                if (!__all_sync(0xffffffffu, wait(sh.s_full[0], j & 1)) || !landed(sh.v_full[j & 1], j) ||
+                    (j + 1 < blocks && !landed(sh.k_full[(j + 1) & 1], j + 1)))
+                    break;
+                if (lane == 0) mbar_arrive(smem_addr(&sh.p_full[0]));
+            }
+        }
     } else if (warp / 8 < tiles) {
         // ---- softmax: two threads a row, one for each half of the keys
         const int i = warp / 8, half = warp / 4 % 2, tr = threadIdx.x % TR, r = i * TR + tr;  // r: row of the two tiles
