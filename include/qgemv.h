@@ -508,8 +508,8 @@ QGEMV_API int qgemv_rope(const qgemv_rope_args* args, unsigned flags, void* stre
  *
  * kind (QGEMV_ACT_BF16 / QGEMV_ACT_F16): type of q and out, and the cache's.  q, out [tokens, heads, cache->dim], last
  * dimension contiguous, 16-byte aligned, strides multiples of 8 elements.  lse: fp32 [tokens, heads] or NULL.
- * max_q, max_kv: bounds of n_b and kv_len[b] over the batch, for the launch's shape (a loose bound costs idle blocks);
- * the values on the device must keep to them: tokens beyond max_q are left unwritten, context beyond max_kv or beyond the
+ * max_q, max_kv (at most 2^30): bounds of n_b and kv_len[b] over the batch, for the choice of kernel and its launch; the
+ * values on the device must keep to them: tokens beyond max_q are left unwritten, context beyond max_kv or beyond the
  * row of the page table (pages_stride * page_size) is not read.  A page number outside the cache reads as if its tokens
  * were masked and sets QGEMV_DEVERR_BAD_INDEX in the device error word.
  * What lies in the cache beyond kv_len is never used, whatever its bits.  Keys and values inside the context must be finite.

@@ -26,113 +26,107 @@ __device__ __forceinline__ uint32_t pack16(float a, float b) {
     return r;
 }
 
-// One row tile of the launch: which rows, which keys, which of its parts.
+// x / d for d with shift = log2(d), or -1 where d is no power of two (both the same for the whole launch).
+__device__ __forceinline__ int div_by(int x, int d, int shift) { return shift >= 0 ? x >> shift : x / d; }
+__device__ __forceinline__ long long div_wide(long long x, long long d) {
+    return ((x | d) >> 32) == 0 ? static_cast<long long>(static_cast<uint32_t>(x) / static_cast<uint32_t>(d)) : x / d;
+}
+
+// Rows of one key/value head, and the keys of them that a block takes.
 struct Tile {
-    int seq, kv_head, part, parts;  // parts: how many the tile has (its own count, at most the grid's)
+    int seq, kv_head, part, parts;  // parts: how many the row tile's keys are cut into
     int row0, rows;                 // first row, and rows in the tile
     int q0;                         // first new token of the sequence in q
     int first_pos;                  // position of the sequence's new token 0
     int k0, k1;                     // keys of this part
-    int kv_len;                     // keys that may be read
-    long long index;                // number of (seq, kv_head, row tile) in the grid
+    long long index;                // number of the row tile, for the records of its parts
 };
 
-// False: nothing to do for this block (past the sequence's rows or the tile's parts).  LAST_FIRST: the row tiles with the
-// most keys (the last ones, under a causal mask) of all sequences and heads come first, so that the grid ends with short ones.
-template <int ROWS, bool LAST_FIRST>
-__device__ __forceinline__ bool find_tile(const AttnArgs& a, long long block, Tile* t) {
-    t->part = static_cast<int>(block % a.parts);
-    t->index = block / a.parts;
-    const int pairs = a.kv_heads * a.seqs;
-    const int rt = static_cast<int>(LAST_FIRST ? a.row_tiles - 1 - t->index / pairs : t->index % a.row_tiles);
-    const int sh = static_cast<int>(LAST_FIRST ? t->index % pairs : t->index / a.row_tiles);
-    t->kv_head = static_cast<int>(sh % a.kv_heads);
-    t->seq = static_cast<int>(sh / a.kv_heads);
-    // the values on the device are held to the bounds that the launch was shaped for
-    const int q0 = max(0, min(a.q_start[t->seq], a.tokens));
-    const int n = max(0, min(a.q_start[t->seq + 1], a.tokens) - q0);
-    const int len = max(0, a.kv_len[t->seq]);
-    t->q0 = q0;
-    t->first_pos = len - n;
-    const long long table = a.pages_stride * a.page_size;
-    const int usable = static_cast<int>(min(static_cast<long long>(min(len, a.max_kv)), table));
-    t->kv_len = usable;
-    t->row0 = rt * ROWS;
-    t->rows = min(ROWS, min(n, a.max_q) * a.group - t->row0);
-    if (t->rows <= 0) return false;
-    const int pos_lo = t->first_pos + t->row0 / a.group;
-    const int pos_hi = t->first_pos + (t->row0 + t->rows - 1) / a.group;
-    int lo = 0, hi = usable;
-    if (a.window > 0) lo = max(0, pos_lo - a.window + 1);
-    if (a.causal) hi = min(hi, pos_hi + 1);
-    if (LAST_FIRST) lo = lo / 128 * 128;  // the 128-row kernel's key tiles start at multiples of their size
-    hi = max(hi, lo);
-    t->parts = max(1, (hi - lo + a.chunk - 1) / a.chunk);
-    if (t->part >= t->parts) return false;
-    t->k0 = lo + t->part * a.chunk;
-    t->k1 = min(hi, t->k0 + a.chunk);
-    return true;
+// A sequence, with the values on the device held to the bounds that the launch was shaped for.
+struct Seq {
+    int q0, n, first_pos, usable;  // first token in q, new tokens, position of the first of them, keys that may be read
+};
+__device__ __forceinline__ Seq find_seq(const AttnArgs& a, int b) {
+    Seq s;
+    s.q0 = max(0, min(a.q_start[b], a.tokens));
+    const int n = max(0, min(a.q_start[b + 1], a.tokens) - s.q0), len = max(0, a.kv_len[b]);
+    s.first_pos = len - n;
+    s.n = min(n, a.max_q);
+    s.usable = static_cast<int>(min(static_cast<long long>(min(len, a.max_kv)), a.pages_stride * a.page_size));
+    return s;
+}
+
+// The keys that some row of [row0, row0 + rows) sees.
+__device__ __forceinline__ void find_keys(const AttnArgs& a, const Seq& s, int row0, int rows, int* lo, int* hi) {
+    // (from a multiple of 16 on; the keys before the first are masked like any other)
+    *lo = a.window > 0 ? max(0, s.first_pos + div_by(row0, a.group, a.group_shift) - a.window + 1) / 16 * 16 : 0;
+    *hi = a.causal ? min(s.usable, s.first_pos + div_by(row0 + rows - 1, a.group, a.group_shift) + 1) : s.usable;
+    *hi = max(*hi, *lo);
 }
 
 // Positions of the keys that row `r` of the tile sees: first_key(r) <= t <= last_key(r).
 __device__ __forceinline__ int row_pos(const AttnArgs& a, const Tile& t, int r) {
-    return t.first_pos + (t.row0 + r) / a.group;
+    return t.first_pos + div_by(t.row0 + r, a.group, a.group_shift);
 }
 
 __device__ __forceinline__ long long out_at(const AttnArgs& a, const Tile& t, int r, long long token_stride,
                                             long long head_stride) {
-    const int row = t.row0 + r;
-    return (t.q0 + row / a.group) * token_stride + (t.kv_head * a.group + row % a.group) * head_stride;
+    const int row = t.row0 + r, token = div_by(row, a.group, a.group_shift);
+    return (t.q0 + token) * token_stride + (t.kv_head * a.group + row - token * a.group) * head_stride;
 }
 
 __device__ __forceinline__ void put_lse(const AttnArgs& a, const Tile& t, int r, float m2, float l) {
     if (!a.lse) return;
-    const int row = t.row0 + r;
-    const long long at = static_cast<long long>(t.q0 + row / a.group) * a.heads + t.kv_head * a.group + row % a.group;
-    a.lse[at] = l > 0.f ? (m2 + log2f(l)) * 0.693147180559945309f : NEG_INF;
+    a.lse[out_at(a, t, r, a.heads, 1)] = l > 0.f ? (m2 + log2f(l)) * 0.693147180559945309f : NEG_INF;
 }
 
-// Record of row r of a part: m (base 2), l, then dim unnormalised sums.
-__device__ __forceinline__ float* part_row(const AttnArgs& a, const Tile& t, int part, int r) {
-    return a.part + ((t.index * a.parts + part) * a.rows_part + r) * static_cast<long long>(a.dim + 2);
-}
-
-// Called by every thread of the block after its part's records are written.  The block that arrives last joins the parts
-// in their order (so the result does not depend on which one that is) and puts the counter back to zero.
-template <bool BF>
-__device__ __forceinline__ void join_parts(const AttnArgs& a, const Tile& t) {
-    __shared__ unsigned last;
-    __threadfence();
-    __syncthreads();
-    if (threadIdx.x == 0) last = atomicAdd(a.count + t.index, 1u) == static_cast<unsigned>(t.parts - 1);
-    __syncthreads();
-    if (!last) return;
-    __threadfence();
-    if (threadIdx.x == 0) a.count[t.index] = 0;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, warps = blockDim.x / 32;
-    for (int r = warp; r < t.rows; r += warps) {
-        float m = NEG_INF;
-        for (int p = 0; p < t.parts; ++p) m = fmaxf(m, __ldcg(part_row(a, t, p, r)));
-        const float base = m == NEG_INF ? 0.f : m;
-        float l = 0.f;
-        for (int p = 0; p < t.parts; ++p) {
-            const float* rec = part_row(a, t, p, r);
-            l += exp2_approx(__ldcg(rec) - base) * __ldcg(rec + 1);
-        }
-        const float inv = l > 0.f ? 1.f / l : 0.f;
-        const long long at = out_at(a, t, r, a.out_token, a.out_head);
-        for (int d = 2 * lane; d < a.dim; d += 64) {
-            float x = 0.f, y = 0.f;
-            for (int p = 0; p < t.parts; ++p) {
-                const float* rec = part_row(a, t, p, r);
-                const float w = exp2_approx(__ldcg(rec) - base);
-                const float2 v = __ldcg(reinterpret_cast<const float2*>(rec + 2 + d));
-                x += w * v.x, y += w * v.y;
+// A part's record of a row: the maximum in use (base 2) and the sum in part_stat[at], dim unnormalised sums of values in
+// part_sum[at * dim ..].  A warp joins the parts of one row, always in the same order, and writes the result; rec(p): the record of
+// part p.  Lane l takes elements 4 l .. 4 l + 3 (and + 128).  The first loads depend on nothing but rec, so that all are on their way at once.
+template <int N, bool BF, class Rec>
+__device__ __forceinline__ void join_row(const AttnArgs& a, const Tile& t, int r, Rec rec) {
+    const int lane = threadIdx.x % 32;
+    float m = NEG_INF, l = 0.f;
+    float4 acc[N];
+#pragma unroll
+    for (int n = 0; n < N; ++n) acc[n] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int p0 = 0; p0 < t.parts; p0 += 32) {  // 32 parts at a time, a lane each for the statistics
+        const int here = min(32, t.parts - p0);
+        const float2 s = lane < here ? __ldcg(a.part_stat + rec(p0 + lane)) : make_float2(NEG_INF, 0.f);
+        float top = s.x;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        top = fmaxf(top, m);
+        const float base = top == NEG_INF ? 0.f : top, keep = exp2_approx(m - base), w = exp2_approx(s.x - base);
+        m = top;
+        float sum = w * s.y;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        l = l * keep + sum;
+#pragma unroll
+        for (int n = 0; n < N; ++n) acc[n].x *= keep, acc[n].y *= keep, acc[n].z *= keep, acc[n].w *= keep;
+#pragma unroll 8
+        for (int p = 0; p < here; ++p) {
+            const float f = __shfl_sync(0xffffffffu, w, p);
+            const float* from = a.part_sum + rec(p0 + p) * a.dim;
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+                const int d = n * 128 + 4 * lane;
+                const float4 v = d < a.dim ? __ldcg(reinterpret_cast<const float4*>(from + d)) : make_float4(0.f, 0.f, 0.f, 0.f);
+                acc[n].x += f * v.x, acc[n].y += f * v.y, acc[n].z += f * v.z, acc[n].w += f * v.w;
             }
-            *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + at + d) = pack16<BF>(x * inv, y * inv);
         }
-        if (lane == 0) put_lse(a, t, r, m, l);
     }
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const long long at = out_at(a, t, r, a.out_token, a.out_head);
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        const int d = n * 128 + 4 * lane;
+        if (d < a.dim)
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at + d) =
+                make_uint2(pack16<BF>(acc[n].x * inv, acc[n].y * inv), pack16<BF>(acc[n].z * inv, acc[n].w * inv));
+    }
+    if (lane == 0) put_lse(a, t, r, m, l);
 }
 
 }  // namespace qg

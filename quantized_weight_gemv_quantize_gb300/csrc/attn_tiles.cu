@@ -155,6 +155,32 @@ struct TilesShared {
     uint32_t tmem;
 };
 
+// The row tiles with the most keys (the last ones, under a causal mask) of all sequences and heads come first, so that the grid ends
+// with short ones.  False: nothing to do (past the sequence's rows or the tile's parts).
+__device__ __forceinline__ bool find_tile(const AttnArgs& a, long long block, Tile* t) {
+    const int pairs = a.kv_heads * a.seqs;
+    t->part = static_cast<int>(block % a.parts);
+    t->index = block / a.parts;
+    const int pair = static_cast<int>(t->index % pairs), rt = static_cast<int>(a.row_tiles - 1 - t->index / pairs);
+    t->kv_head = pair % a.kv_heads;
+    t->seq = pair / a.kv_heads;
+    const Seq s = find_seq(a, t->seq);
+    t->q0 = s.q0, t->first_pos = s.first_pos;
+    t->row0 = rt * 2 * TR;
+    t->rows = min(2 * TR, s.n * a.group - t->row0);
+    if (t->rows <= 0) return false;
+    int lo, hi;
+    find_keys(a, s, t->row0, t->rows, &lo, &hi);
+    lo = lo / TK * TK;  // key tiles start at multiples of their size
+    t->parts = max(1, (hi - lo + a.chunk - 1) / a.chunk);
+    t->k0 = lo + t->part * a.chunk;
+    t->k1 = min(hi, t->k0 + a.chunk);
+    return t->part < t->parts;
+}
+__device__ __forceinline__ long long part_at(const AttnArgs& a, const Tile& t, int part, int r) {
+    return (t.index * a.parts + part) * a.rows_part + r;
+}
+
 template <int DP, bool BF>
 __global__ void __launch_bounds__(TILE_THREADS, 1) attn_tiles_kernel(const __grid_constant__ AttnTileArgs ta) {
     using S = TilesShape<DP>;
@@ -164,7 +190,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) attn_tiles_kernel(const __gri
     pdl_launch_dependents();
     pdl_wait();
     Tile t;
-    if (!find_tile<2 * TR, true>(a, blockIdx.x, &t)) return;
+    if (!find_tile(a, blockIdx.x, &t)) return;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t smem = (smem_addr(smem_raw) + 1023u) & ~1023u;
     const int blocks = (t.k1 - t.k0 + TK - 1) / TK;
@@ -221,7 +247,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) attn_tiles_kernel(const __gri
         auto look_up = [&](int j) {
 #pragma unroll
             for (int h = 0; h < 4; ++h) {
-                const int key = t.k0 + j * TK + h * 32 + lane, nth = key / a.page_size;
+                const int key = t.k0 + j * TK + h * 32 + lane, nth = div_by(key, a.page_size, a.page_shift);
                 token[h] = key - nth * a.page_size;
                 page[h] = key < t.k1 ? table[nth] : -1;
             }
@@ -448,7 +474,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) attn_tiles_kernel(const __gri
             const bool whole = t.parts == 1, row = r < t.rows;
             const float inv = whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
             const long long at = row ? out_at(a, t, r, a.out_token, a.out_head) : 0;
-            float* rec = row && !whole ? part_row(a, t, t.part, r) : nullptr;
+            float* rec = row && !whole ? a.part_sum + part_at(a, t, t.part, r) * a.dim : nullptr;
 #pragma unroll 1
             for (int d0 = 0; d0 < DP / 2; d0 += 32) {
                 const int d = half * (DP / 2) + d0;
@@ -470,13 +496,13 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) attn_tiles_kernel(const __gri
                                            pack16<BF>(o[e + 4] * inv, o[e + 5] * inv), pack16<BF>(o[e + 6] * inv, o[e + 7] * inv));
                 } else if (row) {
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2)
-                        if (d + e < a.dim) __stcg(reinterpret_cast<float2*>(rec + 2 + d + e), make_float2(o[e], o[e + 1]));
+                    for (int e = 0; e < 32; e += 4)
+                        if (d + e < a.dim) __stcg(reinterpret_cast<float4*>(rec + d + e), make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]));
                 }
             }
             if (row && half == 0) {
                 if (whole) put_lse(a, t, r, m, l);
-                else __stcg(reinterpret_cast<float2*>(rec), make_float2(m, l));
+                else __stcg(a.part_stat + part_at(a, t, t.part, r), make_float2(m, l));
             }
         }
         tc_fence_before();
@@ -486,7 +512,20 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) attn_tiles_kernel(const __gri
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
     }
-    if (t.parts > 1) join_parts<BF>(a, t);
+}
+
+// Joins the parts of the rows of split tiles, one warp a row.
+template <bool BF>
+__global__ void __launch_bounds__(JOIN_WARPS * 32) attn_join_kernel(const AttnArgs a) {
+    pdl_launch_dependents();
+    pdl_wait();
+    const long long w = static_cast<long long>(blockIdx.x) * JOIN_WARPS + threadIdx.x / 32;
+    const long long index = w / a.rows_part;
+    const int r = static_cast<int>(w % a.rows_part);
+    if (index >= static_cast<long long>(a.row_tiles) * a.kv_heads * a.seqs) return;
+    Tile t;
+    if (!find_tile(a, index * a.parts, &t) || t.parts == 1 || r >= t.rows) return;
+    join_row<1, BF>(a, t, r, [&](int p) { return part_at(a, t, p, r); });
 }
 
 template <int DP>
@@ -494,6 +533,10 @@ static const void* pick(bool bf16, unsigned* smem, unsigned* threads) {
     *smem = TilesShape<DP>::SMEM;
     *threads = TILE_THREADS;
     return bf16 ? (const void*)attn_tiles_kernel<DP, true> : (const void*)attn_tiles_kernel<DP, false>;
+}
+
+const void* attn_join_kernel_ptr(bool bf16) {
+    return bf16 ? (const void*)attn_join_kernel<true> : (const void*)attn_join_kernel<false>;
 }
 
 const void* attn_tiles_kernel_ptr(bool bf16, int dim, unsigned* smem, unsigned* threads) {

@@ -39,17 +39,18 @@ struct AttnArgs {
     const int* pages;
     long long pages_stride;
     const int *q_start, *kv_len;
-    unsigned* count;  // arrival counters, one per row tile; zero between calls
-    float* part;      // parts of split row tiles: [tile][part][rows_part][dim + 2] (m, l, then the unnormalised sums)
+    unsigned* count;    // 16-row kernel: arrival counters, one a block; zero between calls
+    float2* part_stat;  // records of the parts of split row tiles: maximum in use (base 2) and sum of each row,
+    float* part_sum;    // and dim unnormalised sums of values
     unsigned* err;
     int num_pages, page_size, kv_heads, dim;
     int tokens, heads, group, seqs, max_q, max_kv;
+    int group_shift, page_shift;  // log2 of group and page_size, -1 where they are no powers of two
     float scale_log2;   // scale * log2(e): the softmax runs in base 2
     int causal, window;
-    int chunk;       // context tokens per part
-    int parts;       // parts of a row tile in the grid
-    int row_tiles;   // row tiles of a sequence and key/value head in the grid
-    int rows_part;   // rows of a part's record
+    // 128-row kernel: keys of a part, parts of a row tile and row tiles of a sequence and key/value head in the grid, rows of a
+    // part's records
+    int chunk, parts, row_tiles, rows_part;
     int box;         // tokens of one tensor-map copy (128-row kernel), 0: no tensor map, every row is copied by itself
 };
 
@@ -64,14 +65,14 @@ struct AttnPlan {
     bool tiles;  // the 128-row tensor-memory kernel (else the 16-row one)
     int chunk, parts, row_tiles, rows_part;
     long long grid;
-    unsigned smem, threads;
-    size_t scratch;
+    size_t records, scratch;  // rows of parts' records, bytes of scratch
 };
 
-constexpr unsigned ATTN_MAX_COUNTERS = QGEMV_ATTN_SCRATCH_HEAD / 4;
 
 const void* attn_rows_kernel_ptr(bool bf16, int dim, unsigned* smem, unsigned* threads);
 const void* attn_tiles_kernel_ptr(bool bf16, int dim, unsigned* smem, unsigned* threads);
+const void* attn_join_kernel_ptr(bool bf16);
+constexpr int JOIN_WARPS = 8;  // rows of a block of the joining kernel
 
 struct SampleArgs {
     const void* x;

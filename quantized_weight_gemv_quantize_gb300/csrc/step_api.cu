@@ -168,6 +168,8 @@ static int run_rope(const qgemv_rope_args* a, unsigned flags, void* stream) {
 
 // ---------------------------------------------------------------------------------------------------- attention
 
+static size_t round16(size_t n) { return (n + 15) / 16 * 16; }
+
 static int attn_plan(int seqs, int tokens, int heads, int kv_heads, int dim, int max_q, int max_kv, AttnPlan* p) {
     if (seqs < 0 || tokens < 0 || heads < 1 || kv_heads < 1 || heads % kv_heads || dim < 8 || dim % 8 || max_q < 0 ||
         max_kv < 0)
@@ -179,26 +181,38 @@ static int attn_plan(int seqs, int tokens, int heads, int kv_heads, int dim, int
     constexpr int SMS = 152;
     if (max_q > tokens) max_q = tokens;
     const long long rows = static_cast<long long>(max_q) * (heads / kv_heads);
+    if (max_kv > 1 << 30 || (rows + 15) / 16 * kv_heads > INT_MAX || rows > INT_MAX) return QGEMV_ERR_UNSUPPORTED;
     // More than 32 rows go to the 128-row kernel (heads of up to 128).
     p->tiles = rows > 32 && dim <= 128;
-    const int tile = p->tiles ? 256 : 16;
-    const long long row_tiles = (rows + tile - 1) / tile;
-    const long long tiles = row_tiles * kv_heads * seqs;
-    if (row_tiles > INT_MAX || tiles > INT_MAX) return QGEMV_ERR_UNSUPPORTED;
-    p->row_tiles = static_cast<int>(row_tiles);
-    p->rows_part = static_cast<int>(rows < tile ? rows : tile);
-    // Parts: enough to give every SM four blocks, of at least 128 keys (16-row kernel; 1024 for the other).
-    long long parts = (4 * SMS + tiles - 1) / tiles;
-    const long long most = p->tiles ? (max_kv + 1023) / 1024 : (max_kv + 127) / 128;
-    if (parts > most) parts = most;
-    if (parts < 1 || tiles > ATTN_MAX_COUNTERS) parts = 1;
-    const long long unit = p->tiles ? 128 : 16;
-    const long long chunk = ((max_kv + parts - 1) / parts + unit - 1) / unit * unit;
-    p->chunk = static_cast<int>(chunk < unit ? unit : chunk > INT_MAX - 127 ? INT_MAX - 127 : chunk);
-    p->parts = max_kv > 0 ? static_cast<int>((static_cast<long long>(max_kv) + p->chunk - 1) / p->chunk) : 1;
-    p->grid = tiles * p->parts;
-    if (p->grid > INT_MAX) return QGEMV_ERR_UNSUPPORTED;
-    if (p->parts > 1) p->scratch += static_cast<size_t>(p->grid) * p->rows_part * (dim + 2) * sizeof(float);
+    size_t records = 0;
+    if (!p->tiles) {
+        // One wave of blocks, two an SM (one with the larger shared memory of long heads); each has records of 16 rows for two
+        // parts of split row tiles.
+        p->grid = dim <= 128 ? 2 * SMS : SMS;
+        records = static_cast<size_t>(p->grid) * 2 * 16;
+    } else {
+        const long long tiles = (rows + 255) / 256 * kv_heads * seqs;
+        if (tiles > INT_MAX) return QGEMV_ERR_UNSUPPORTED;
+        p->row_tiles = static_cast<int>((rows + 255) / 256);
+        p->rows_part = static_cast<int>(rows < 256 ? rows : 256);
+        // Parts of a row tile's context; one block an SM.  The time of a launch in key tiles: waves of blocks, each as long as its
+        // part, with about 3 key tiles for its start and end, and 4 more where parts have to be written out and joined (measured:
+        // 1.5 us a key tile).  At most 32 parts of at least 8 key tiles, and no more than 16 waves of them.
+        const long long blocks = (static_cast<long long>(max_kv) + 127) / 128;
+        long long best = 1, best_cost = LLONG_MAX;
+        for (long long n = 1; n <= 32 && (n == 1 || (n * 8 <= blocks && tiles * n <= 16 * SMS)); ++n) {
+            const long long cost = (tiles * n + SMS - 1) / SMS * ((blocks + n - 1) / n + 3 + (n > 1 ? 4 : 0));
+            if (cost < best_cost) best = n, best_cost = cost;
+        }
+        const long long chunk = ((max_kv + best - 1) / best + 127) / 128 * 128;
+        p->chunk = static_cast<int>(chunk < 128 ? 128 : chunk > INT_MAX - 127 ? INT_MAX - 127 : chunk);
+        p->parts = max_kv > 0 ? static_cast<int>((static_cast<long long>(max_kv) + p->chunk - 1) / p->chunk) : 1;
+        p->grid = tiles * p->parts;
+        if (p->grid > INT_MAX) return QGEMV_ERR_UNSUPPORTED;
+        if (p->parts > 1) records = static_cast<size_t>(p->grid) * p->rows_part;
+    }
+    p->records = records;
+    p->scratch += round16(records * sizeof(float2)) + records * dim * sizeof(float);
     return QGEMV_OK;
 }
 
@@ -309,10 +323,18 @@ static int run_attn(const qgemv_attn_args* a, unsigned flags, void* stream) {
     k.v_page = c.v_page, k.v_token = c.v_token, k.v_head = c.v_head;
     k.pages = a->pages, k.pages_stride = a->pages_stride, k.q_start = a->q_start, k.kv_len = a->kv_len;
     k.count = static_cast<unsigned*>(a->scratch);
-    k.part = reinterpret_cast<float*>(static_cast<uint8_t*>(a->scratch) + QGEMV_ATTN_SCRATCH_HEAD);
+    uint8_t* parts = static_cast<uint8_t*>(a->scratch) + QGEMV_ATTN_SCRATCH_HEAD;
+    k.part_stat = reinterpret_cast<float2*>(parts);
+    k.part_sum = reinterpret_cast<float*>(parts + round16(p.records * sizeof(float2)));
     k.err = err, k.num_pages = c.num_pages, k.page_size = c.page_size, k.kv_heads = c.heads, k.dim = c.dim;
     k.tokens = a->tokens, k.heads = a->heads, k.group = a->heads / c.heads, k.seqs = a->seqs;
     k.max_q = a->max_q, k.max_kv = a->max_kv;
+    auto log2_of = [](int v) {
+        int n = 0;
+        while (1 << n < v) ++n;
+        return 1 << n == v ? n : -1;
+    };
+    k.group_shift = log2_of(k.group), k.page_shift = log2_of(c.page_size);
     k.scale_log2 = a->scale * 1.44269504088896341f;
     k.window = a->window, k.causal = a->causal || a->window > 0;
     k.chunk = p.chunk, k.parts = p.parts, k.row_tiles = p.row_tiles, k.rows_part = p.rows_part;
@@ -332,6 +354,13 @@ static int run_attn(const qgemv_attn_args* a, unsigned flags, void* stream) {
             k.box = box;
         ta.a = k;
         e = launch_step(fn, grid, threads, smem, 1, pdl, static_cast<cudaStream_t>(stream), ta);
+        if (e == cudaSuccess && p.parts > 1) {
+            // starts with the tail of the kernel before it, and waits there
+            const long long rows = static_cast<long long>(p.row_tiles) * k.kv_heads * k.seqs * p.rows_part;
+            e = launch_step(attn_join_kernel_ptr(a->kind == QGEMV_ACT_BF16),
+                            dim3(static_cast<unsigned>((rows + JOIN_WARPS - 1) / JOIN_WARPS)), JOIN_WARPS * 32, 0, 1, true,
+                            static_cast<cudaStream_t>(stream), k);
+        }
     } else {
         e = launch_step(fn, grid, threads, smem, 1, pdl, static_cast<cudaStream_t>(stream), k);
     }
