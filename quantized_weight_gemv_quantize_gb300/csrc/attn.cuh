@@ -28,9 +28,6 @@ __device__ __forceinline__ uint32_t pack16(float a, float b) {
 
 // x / d for d with shift = log2(d), or -1 where d is no power of two (both the same for the whole launch).
 __device__ __forceinline__ int div_by(int x, int d, int shift) { return shift >= 0 ? x >> shift : x / d; }
-__device__ __forceinline__ long long div_wide(long long x, long long d) {
-    return ((x | d) >> 32) == 0 ? static_cast<long long>(static_cast<uint32_t>(x) / static_cast<uint32_t>(d)) : x / d;
-}
 
 // Rows of one key/value head, and the keys of them that a block takes.
 struct Tile {
@@ -80,6 +77,15 @@ __device__ __forceinline__ void put_lse(const AttnArgs& a, const Tile& t, int r,
     a.lse[out_at(a, t, r, a.heads, 1)] = l > 0.f ? (m2 + log2f(l)) * 0.693147180559945309f : NEG_INF;
 }
 
+// Elements d .. d + 3 of a row of the result from its unnormalised sums; with d = 0 its log-sum-exp.
+template <bool BF>
+__device__ __forceinline__ void put_row4(const AttnArgs& a, const Tile& t, int r, int d, float4 x, float m, float l) {
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + out_at(a, t, r, a.out_token, a.out_head) + d) =
+        make_uint2(pack16<BF>(x.x * inv, x.y * inv), pack16<BF>(x.z * inv, x.w * inv));
+    if (d == 0) put_lse(a, t, r, m, l);
+}
+
 // A part's record of a row: the maximum in use (base 2) and the sum in part_stat[at], dim unnormalised sums of values in
 // part_sum[at * dim ..].  A warp joins the parts of one row, always in the same order, and writes the result; rec(p): the record of
 // part p.  Lane l takes elements 4 l .. 4 l + 3 (and + 128).  The first loads depend on nothing but rec, so that all are on their way at once.
@@ -117,16 +123,9 @@ __device__ __forceinline__ void join_row(const AttnArgs& a, const Tile& t, int r
             }
         }
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    const long long at = out_at(a, t, r, a.out_token, a.out_head);
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-        const int d = n * 128 + 4 * lane;
-        if (d < a.dim)
-            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at + d) =
-                make_uint2(pack16<BF>(acc[n].x * inv, acc[n].y * inv), pack16<BF>(acc[n].z * inv, acc[n].w * inv));
-    }
-    if (lane == 0) put_lse(a, t, r, m, l);
+    for (int n = 0; n < N; ++n)
+        if (n * 128 + 4 * lane < a.dim) put_row4<BF>(a, t, r, n * 128 + 4 * lane, acc[n], m, l);
 }
 
 }  // namespace qg

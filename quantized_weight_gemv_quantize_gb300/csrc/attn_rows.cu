@@ -59,15 +59,6 @@ __device__ __forceinline__ uint32_t piece_at(int r, int c) {
     return static_cast<uint32_t>(r * DP * 2 + ((c ^ (r & 7)) << 4));
 }
 
-// What a sequence counts for in the division of the work: each of its row tiles as many keys as any of its rows may see, in
-// units of the block's 64 keys, at least one (a row that sees nothing has its zeros written).
-__device__ __forceinline__ int share_of(const AttnArgs& a, const Seq& s) {
-    int lo, hi;
-    find_keys(a, s, 0, s.n * a.group, &lo, &hi);
-    return max(64, (hi - lo + 63) / 64 * 64);
-}
-__device__ __forceinline__ int tiles_of(const AttnArgs& a, const Seq& s) { return (s.n * a.group + 15) / 16 * a.kv_heads; }
-
 // One row tile's part: into the result, or into its record.  Called by the whole block.
 template <int DP, bool BF>
 __device__ __forceinline__ void attend(const AttnArgs& a, const Tile& t, long long record, uint8_t* smem) {
@@ -82,53 +73,57 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Tile& t, long lo
     const uint16_t* const vh = a.v + t.kv_head * a.v_head;
     const bool one_page = a.page_size % 16 == 0;  // pieces start at multiples of 16: all keys of one lie on one page
 
-    // Page and token of key lane % 16 of this warp's piece i, read well before the piece is copied; page -1: no such key.
+    // Where this warp's pieces lie.  With one page a piece, lane n holds page and token of piece 32 * batch + n, read a batch ahead.
     struct Where {
-        int page, token;
+        int page, token;  // page -1: no such key
     };
-    auto look_up = [&](int i) {
-        const int key = t.k0 + (warp + i * S::WARPS) * 16 + (lane & 15), nth = div_by(key, a.page_size, a.page_shift);
+    auto look_up = [&](int key) {
+        const int nth = div_by(key, a.page_size, a.page_shift);
         Where w = {-1, key - nth * a.page_size};
-        if (i < mine && key < t.k1) {
+        if (key < t.k1) {
             w.page = table[nth];
             if (w.page < 0 || w.page >= a.num_pages) atomicOr(a.err, ERR_BAD_INDEX), w.page = -1;
         }
         return w;
     };
+    auto key_of = [&](int i) { return t.k0 + (warp + i * S::WARPS) * 16; };
+    Where batch = {-1, 0}, ahead = {-1, 0};
+    if (one_page) batch = look_up(key_of(lane)), ahead = look_up(key_of(32 + lane));
     // Copies piece i into a slot of the ring; returns which of its keys are there, one bit each.
-    auto issue = [&](const Where& w, int slot) -> unsigned {
-        const unsigned live = __ballot_sync(0xffffffffu, w.page >= 0) & 0xffffu;
+    auto issue = [&](int i, int slot) -> unsigned {
         const uint32_t kbase = ring + slot * S::STAGE, vbase = kbase + 16 * S::ROW;
-        const int c = lane % PER_ROW;
+        const int c = lane % PER_ROW, r_in = lane / PER_ROW;
+        constexpr int STEP = 32 / PER_ROW;
         const bool col = c * 8 < a.dim;
-        const int page0 = __shfl_sync(0xffffffffu, w.page, 0), token0 = __shfl_sync(0xffffffffu, w.token, 0);
+        unsigned live = 0;
         if (one_page) {
-            const uint16_t* k = kh + page0 * a.k_page + (token0 + lane / PER_ROW) * a.k_token + c * 8;
-            const uint16_t* v = vh + page0 * a.v_page + (token0 + lane / PER_ROW) * a.v_token + c * 8;
+            if (i && i % 32 == 0) batch = ahead, ahead = look_up(key_of(i + 32 + lane));
+            const int page = __shfl_sync(0xffffffffu, batch.page, i % 32), token = __shfl_sync(0xffffffffu, batch.token, i % 32) + r_in;
+            const int left = page < 0 ? 0 : t.k1 - key_of(i);
+            live = left <= 0 ? 0u : left >= 16 ? 0xffffu : (1u << left) - 1u;
+            const uint16_t* k = live ? kh + page * a.k_page + token * a.k_token + c * 8 : a.k;
+            const uint16_t* v = live ? vh + page * a.v_page + token * a.v_token + c * 8 : a.v;
+            const long long k_step = live ? STEP * a.k_token : 0, v_step = live ? STEP * a.v_token : 0;
 #pragma unroll
-            for (int j = 0; j < 16 * PER_ROW / 32; ++j) {
-                const int r = j * (32 / PER_ROW) + lane / PER_ROW;
-                const bool in = (live >> r & 1u) && col;
-                cp_async16(kbase + piece_at<DP>(r, c), in ? k + j * (32 / PER_ROW) * a.k_token : a.k, in);
-                cp_async16(vbase + piece_at<DP>(r, c), in ? v + j * (32 / PER_ROW) * a.v_token : a.v, in);
+            for (int r0 = 0; r0 < 16; r0 += STEP) {
+                const bool in = (live >> (r0 + r_in) & 1u) && col;
+                cp_async16(kbase + piece_at<DP>(r0 + r_in, c), k, in);
+                cp_async16(vbase + piece_at<DP>(r0 + r_in, c), v, in);
+                k += k_step, v += v_step;
             }
         } else {
-#pragma unroll
-            for (int j = 0; j < 16 * PER_ROW / 32; ++j) {
-                const int r = j * (32 / PER_ROW) + lane / PER_ROW;
-                const int page = __shfl_sync(0xffffffffu, w.page, r), token = __shfl_sync(0xffffffffu, w.token, r);
+            const Where w = look_up(key_of(i) + (lane & 15));
+            live = __ballot_sync(0xffffffffu, w.page >= 0) & 0xffffu;
+#pragma unroll 1
+            for (int r0 = 0; r0 < 16; r0 += STEP) {
+                const int page = __shfl_sync(0xffffffffu, w.page, r0 + r_in), token = __shfl_sync(0xffffffffu, w.token, r0 + r_in);
                 const bool in = page >= 0 && col;
-                cp_async16(kbase + piece_at<DP>(r, c), in ? kh + page * a.k_page + token * a.k_token + c * 8 : a.k, in);
-                cp_async16(vbase + piece_at<DP>(r, c), in ? vh + page * a.v_page + token * a.v_token + c * 8 : a.v, in);
+                cp_async16(kbase + piece_at<DP>(r0 + r_in, c), in ? kh + page * a.k_page + token * a.k_token + c * 8 : a.k, in);
+                cp_async16(vbase + piece_at<DP>(r0 + r_in, c), in ? vh + page * a.v_page + token * a.v_token + c * 8 : a.v, in);
             }
         }
         return live;
     };
-
-    Where first[S::STAGES - 1];
-#pragma unroll
-    for (int s = 0; s < S::STAGES - 1; ++s) first[s] = look_up(s);
-    Where next = look_up(S::STAGES - 1);
 
     // The query rows as operand fragments: lane holds rows lane/4 and lane/4 + 8, columns 2 (lane % 4) + {0, 1, 8, 9}.
     uint32_t qf[DP / 16][4];
@@ -147,13 +142,7 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Tile& t, long lo
                 }
         }
     }
-    unsigned live_ring[S::STAGES];  // which keys of a staged piece are there
-#pragma unroll
-    for (int s = 0; s < S::STAGES - 1; ++s) {
-        live_ring[s] = issue(first[s], s);
-        cp_commit();
-    }
-    live_ring[S::STAGES - 1] = 0u;
+    unsigned live_ring[S::STAGES] = {};  // which keys of a staged piece are there
     // keys that the lane's two rows see: lo <= key <= hi
     int lo[2], hi[2];
 #pragma unroll
@@ -168,16 +157,18 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Tile& t, long lo
     for (int i = 0; i < DP / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
     float m[2] = {NEG_INF, NEG_INF}, l[2] = {0.f, 0.f};
 
-    for (int i = 0; i < mine; ++i) {
-        const int slot = i % S::STAGES;
+    // (the first rounds only fill the ring)
+    for (int i = 1 - S::STAGES; i < mine; ++i) {
         cp_wait<S::STAGES - 2>();
-        __syncwarp();  // the piece is there, and the slot that is filled next was read in the iteration before
+        __syncwarp();  // piece i is there, and the slot that is filled next was read in the round before
         const unsigned live = live_ring[0];
 #pragma unroll
         for (int j = 0; j + 1 < S::STAGES; ++j) live_ring[j] = live_ring[j + 1];
-        live_ring[S::STAGES - 2] = issue(next, (i + S::STAGES - 1) % S::STAGES);
+        const int next = i + S::STAGES - 1;
+        live_ring[S::STAGES - 2] = next < mine ? issue(next, next % S::STAGES) : 0u;
         cp_commit();
-        next = look_up(i + S::STAGES);
+        if (i < 0) continue;
+        const int slot = i % S::STAGES;
         const uint32_t kbase = ring + slot * S::STAGE, vbase = kbase + 16 * S::ROW;
         float s[2][4] = {};
 #pragma unroll
@@ -272,16 +263,46 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Tile& t, long lo
             x.x += f * v.x, x.y += f * v.y, x.z += f * v.z, x.w += f * v.w;
         }
         if (t.parts == 1) {
-            const float inv = ll > 0.f ? 1.f / ll : 0.f;
-            const long long at = out_at(a, t, r, a.out_token, a.out_head);
-            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at + d) =
-                make_uint2(pack16<BF>(x.x * inv, x.y * inv), pack16<BF>(x.z * inv, x.w * inv));
-            if (d == 0) put_lse(a, t, r, mm, ll);
+            put_row4<BF>(a, t, r, d, x, mm, ll);
         } else {
             __stcg(reinterpret_cast<float4*>(a.part_sum + (record + r) * a.dim + d), x);
             if (d == 0) __stcg(a.part_stat + record + r, make_float2(mm, ll));
         }
     }
+}
+
+// Joins the parts of a row tile that begins in block t.index: four elements of some rows a thread, one pass over the parts with the
+// maxima and the sums running along.  Eight loads of each kind on their way at once: rows of one part, or parts of one row.
+template <int DP, bool BF, int ITEMS>
+__device__ __forceinline__ void join_rows(const AttnArgs& a, const Tile& t) {
+    constexpr int ROWS = RowsShape<DP>::WARPS * 32 / (DP / 4);
+    const int r0 = threadIdx.x / (DP / 4), d = threadIdx.x % (DP / 4) * 4;
+    if (d >= a.dim || r0 >= t.rows) return;
+    float m[ITEMS], l[ITEMS];
+    float4 x[ITEMS];
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k) m[k] = NEG_INF, l[k] = 0.f, x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int rec0 = 2 * static_cast<int>(t.index) * 16 + r0;
+#pragma unroll(8 / ITEMS)
+    for (int p = 0; p < t.parts; ++p) {
+        const int rec = rec0 + p * 32 + (p == 0 ? 16 : 0);
+#pragma unroll
+        for (int k = 0; k < ITEMS; ++k) {
+            // (rows past the tile's read its last one's record)
+            const int at = rec + min(k * ROWS, t.rows - 1 - r0);
+            const float2 s = __ldcg(a.part_stat + at);
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part_sum + static_cast<long long>(at) * a.dim + d));
+            const float top = fmaxf(m[k], s.x), base = top == NEG_INF ? 0.f : top;
+            const float keep = exp2_approx(m[k] - base), w = exp2_approx(s.x - base);
+            m[k] = top;
+            l[k] = l[k] * keep + w * s.y;
+            x[k].x = x[k].x * keep + w * v.x, x[k].y = x[k].y * keep + w * v.y;
+            x[k].z = x[k].z * keep + w * v.z, x[k].w = x[k].w * keep + w * v.w;
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k)
+        if (r0 + k * ROWS < t.rows) put_row4<BF>(a, t, r0 + k * ROWS, d, x[k], m[k], l[k]);
 }
 
 template <int DP, bool BF>
@@ -290,90 +311,118 @@ __global__ void __launch_bounds__(RowsShape<DP>::WARPS * 32) attn_rows_kernel(co
     __shared__ unsigned last;
     pdl_launch_dependents();
     pdl_wait();
-    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    // The whole work, and this block's share [start, end) of it: 32 sequences at a time, every warp for itself.
-    auto work_of = [&](int b) {
-        if (b >= a.seqs) return 0ll;
-        const Seq s = find_seq(a, b);
-        return static_cast<long long>(tiles_of(a, s)) * share_of(a, s);
+    const unsigned lane = threadIdx.x % 32, me = blockIdx.x, blocks = gridDim.x, seqs = a.seqs, unit = a.unit_shift;
+    // A sequence in the division of the work: its row tiles, each as many units of keys (64, or more where 32 bits would not
+    // hold the whole) as any of its rows may see, at least one (a row that sees nothing has its zeros written).
+    Seq sq = {};
+    unsigned sq_units = 1, sq_tiles = 0;
+    auto read_seq = [&](unsigned b) {
+        sq_units = 1, sq_tiles = 0;
+        if (b >= seqs) return;
+        sq = find_seq(a, static_cast<int>(b));
+        int lo, hi;
+        find_keys(a, sq, 0, sq.n * a.group, &lo, &hi);
+        sq_tiles = (sq.n * a.group + 15) / 16 * a.kv_heads;
+        sq_units = max(1u, (static_cast<unsigned>(hi - lo) + (1u << unit) - 1) >> unit);
     };
-    auto scan = [&](long long v) {  // inclusive
+    // Sum over all sequences, 32 at a time (a lane each), every warp for itself.
+    auto sum_of = [&](auto&& f) {
+        unsigned v = 0;
+        for (unsigned b0 = 0; b0 < seqs; b0 += 32) {
+            if (seqs > 32) read_seq(b0 + lane);
+            v += f();
+        }
+        return __reduce_add_sync(0xffffffffu, v);
+    };
+    if (seqs <= 32) read_seq(lane);
+    const unsigned least = max(1u, 128u >> unit);  // less than 128 keys are not worth a block
+    const unsigned units = sum_of([&] { return sq_tiles * sq_units; }), row_tiles = sum_of([&] { return sq_tiles; });
+    // A block's share.  Where there are no more row tiles than blocks, it is made as long as it takes for every block to have a part
+    // of one row tile only: a second part costs a block's start and end again, some 400 keys' time.  The row tiles' keys are then
+    // counted in whole shares.
+    const unsigned even = max(least, (units + blocks - 1) / blocks);
+    unsigned share = even;
+    bool whole = row_tiles <= blocks;
+    for (int n = 0; whole; ++n) {
+        const unsigned need = sum_of([&] { return sq_tiles * ((sq_units + share - 1) / share); });
+        if (need <= blocks) break;
+        if (n == 6) whole = false, share = even;
+        else share = max(share + 1, static_cast<unsigned>(static_cast<unsigned long long>(share) * need / blocks));
+    }
+    auto counted = [&] { return whole ? (sq_units + share - 1) / share * share : sq_units; };
+    // the sequence that holds this block's start, and where it begins
+    const unsigned start = me * share;
+    unsigned at = 0, b = seqs, per = 1;
+    for (unsigned b0 = 0; b0 < seqs; b0 += 32) {
+        if (seqs > 32) read_seq(b0 + lane);
+        per = counted();
+        const unsigned own = sq_tiles * per;
+        unsigned sum = own;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const long long u = __shfl_up_sync(0xffffffffu, v, o);
-            if (lane >= o) v += u;
+            const unsigned u = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += u;
         }
-        return v;
-    };
-    long long total = 0, own = 0, sum = 0;
-    for (int b0 = 0; b0 < a.seqs; b0 += 32) {
-        own = work_of(b0 + lane);
-        sum = scan(own);
-        total += __shfl_sync(0xffffffffu, sum, 31);
-    }
-    // (at least 128 keys: less is not worth a block)
-    const long long share = max(128ll, (div_wide(total + gridDim.x - 1, gridDim.x) + 63) / 64 * 64);
-    const long long start = blockIdx.x * share, end = min(total, start + share);
-    if (start >= total) return;
-    // the sequence that holds the start, and where it begins
-    int b = 0;
-    long long at = 0;
-    for (int b0 = 0; b0 < a.seqs; b0 += 32) {
-        if (a.seqs > 32) own = work_of(b0 + lane), sum = scan(own);  // (else from above)
         const unsigned holds = __ballot_sync(0xffffffffu, start < at + sum);
         if (holds) {
             const int l = __ffs(holds) - 1;
             b = b0 + l;
             at += __shfl_sync(0xffffffffu, sum - own, l);
+            sq.q0 = __shfl_sync(0xffffffffu, sq.q0, l), sq.n = __shfl_sync(0xffffffffu, sq.n, l);
+            sq.first_pos = __shfl_sync(0xffffffffu, sq.first_pos, l), sq.usable = __shfl_sync(0xffffffffu, sq.usable, l);
+            per = __shfl_sync(0xffffffffu, per, l), sq_tiles = __shfl_sync(0xffffffffu, sq_tiles, l);
             break;
         }
         at += __shfl_sync(0xffffffffu, sum, 31);
     }
-    Seq s = find_seq(a, b);
-    int per = share_of(a, s), tiles = tiles_of(a, s), nth = static_cast<int>(div_wide(start - at, per));
+    if (b == seqs) return;  // past the end of the work
+    unsigned nth = (start - at) / per;
 
-    for (long long pos = start; pos < end;) {
-        while (nth >= tiles) {  // the next sequence with rows
-            at += static_cast<long long>(tiles) * per;
-            s = find_seq(a, ++b);
-            per = share_of(a, s), tiles = tiles_of(a, s), nth = 0;
+    for (unsigned pos = start, end = start + share; pos < end;) {
+        while (nth >= sq_tiles) {  // the next sequence with rows
+            at += sq_tiles * per;
+            if (++b >= seqs) return;
+            read_seq(b);
+            per = counted(), nth = 0;
         }
-        const long long tile_at = at + static_cast<long long>(nth) * per;  // the row tile's first key in the whole work
-        const long long stop = min(end, tile_at + per);
+        const unsigned tile_at = at + nth * per;  // the row tile's first unit in the whole work
+        const unsigned stop = min(end, tile_at + per);
         Tile t;
-        t.seq = b;
-        t.q0 = s.q0, t.first_pos = s.first_pos;
-        if (s.n * a.group <= 16) {
-            t.kv_head = nth, t.row0 = 0;
+        t.seq = static_cast<int>(b);
+        t.q0 = sq.q0, t.first_pos = sq.first_pos;
+        if (sq.n * a.group <= 16) {
+            t.kv_head = static_cast<int>(nth), t.row0 = 0;
         } else {
-            const int row_tiles = tiles / a.kv_heads;
-            t.kv_head = nth / row_tiles, t.row0 = nth % row_tiles * 16;
+            const unsigned in_head = sq_tiles / a.kv_heads;
+            t.kv_head = static_cast<int>(nth / in_head), t.row0 = static_cast<int>(nth % in_head * 16);
         }
-        t.rows = min(16, s.n * a.group - t.row0);
+        t.rows = min(16, sq.n * a.group - t.row0);
         int lo, hi;
-        find_keys(a, s, t.row0, t.rows, &lo, &hi);
-        t.k0 = min(hi, lo + static_cast<int>(pos - tile_at));
-        t.k1 = min(hi, lo + static_cast<int>(stop - tile_at));
-        // the block with the row tile's first part: this one where the tile begins here
-        const int first = tile_at >= start ? static_cast<int>(blockIdx.x) : static_cast<int>(div_wide(tile_at, share));
-        t.part = static_cast<int>(blockIdx.x) - first;
-        t.parts = (tile_at + per <= end ? static_cast<int>(blockIdx.x) : static_cast<int>(div_wide(tile_at + per - 1, share))) - first + 1;
+        find_keys(a, sq, t.row0, t.rows, &lo, &hi);
+        t.k0 = lo + static_cast<int>(min(static_cast<unsigned long long>(hi - lo), static_cast<unsigned long long>(pos - tile_at) << unit));
+        t.k1 = lo + static_cast<int>(min(static_cast<unsigned long long>(hi - lo), static_cast<unsigned long long>(stop - tile_at) << unit));
+        // the blocks with the row tile's first and last part: this one where the tile begins or ends here
+        const unsigned first = tile_at >= start ? me : tile_at / share;
+        t.part = static_cast<int>(me - first);
+        t.parts = static_cast<int>((tile_at + per <= end ? me : (tile_at + per - 1) / share) - first + 1);
         t.index = first;
         // A block has at most two parts of split row tiles: one that another block began (record 2 b) and one that it begins
         // itself (record 2 b + 1).
-        attend<DP, BF>(a, t, (2ll * blockIdx.x + (t.part == 0 ? 1 : 0)) * 16, smem);
+        attend<DP, BF>(a, t, (2 * me + (t.part == 0 ? 1 : 0)) * 16, smem);
         if (t.parts > 1) {
             // The block that arrives last joins the parts (in their order, so the result does not depend on which one that
             // is) and puts the counter back to zero.
-            __threadfence();
             __syncthreads();
-            if (threadIdx.x == 0) last = atomicAdd(a.count + first, 1u) == static_cast<unsigned>(t.parts - 1);
+            if (threadIdx.x == 0) {  // (the block's writes before the barrier are released with this thread's)
+                unsigned before;
+                asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(before) : "l"(a.count + first) : "memory");
+                last = before == static_cast<unsigned>(t.parts - 1);
+                if (last) a.count[first] = 0;
+            }
             __syncthreads();
             if (last) {
-                __threadfence();
-                if (threadIdx.x == 0) a.count[first] = 0;
-                for (int r = warp; r < t.rows; r += RowsShape<DP>::WARPS)
-                    join_row<(DP + 127) / 128, BF>(a, t, r, [&](int p) { return (2ll * (first + p) + (p == 0 ? 1 : 0)) * 16 + r; });
+                if (t.rows <= RowsShape<DP>::WARPS * 32 / (DP / 4)) join_rows<DP, BF, 1>(a, t);
+                else join_rows<DP, BF, DP / 32>(a, t);
             }
         }
         __syncthreads();  // shared memory is free again

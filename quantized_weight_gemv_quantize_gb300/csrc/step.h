@@ -48,6 +48,7 @@ struct AttnArgs {
     int group_shift, page_shift;  // log2 of group and page_size, -1 where they are no powers of two
     float scale_log2;   // scale * log2(e): the softmax runs in base 2
     int causal, window;
+    int unit_shift;  // 16-row kernel: the work is divided in units of 2^unit_shift keys
     // 128-row kernel: keys of a part, parts of a row tile and row tiles of a sequence and key/value head in the grid, rows of a
     // part's records
     int chunk, parts, row_tiles, rows_part;
@@ -63,7 +64,7 @@ struct AttnTileArgs {
 
 struct AttnPlan {
     bool tiles;  // the 128-row tensor-memory kernel (else the 16-row one)
-    int chunk, parts, row_tiles, rows_part;
+    int chunk, parts, row_tiles, rows_part, unit_shift;
     long long grid;
     size_t records, scratch;  // rows of parts' records, bytes of scratch
 };

@@ -190,6 +190,11 @@ static int attn_plan(int seqs, int tokens, int heads, int kv_heads, int dim, int
         // parts of split row tiles.
         p->grid = dim <= 128 ? 2 * SMS : SMS;
         records = static_cast<size_t>(p->grid) * 2 * 16;
+        // Units of 64 keys, longer ones where the bounds alone would let the whole (twice over, for its rounding) pass 32 bits.
+        const double tiles = static_cast<double>((rows + 15) / 16) * kv_heads * seqs;
+        p->unit_shift = 6;
+        while (p->unit_shift < 30 && tiles * (static_cast<double>(max_kv >> p->unit_shift) + 1) > 1e9) ++p->unit_shift;
+        if (tiles > 1e9) return QGEMV_ERR_UNSUPPORTED;
     } else {
         const long long tiles = (rows + 255) / 256 * kv_heads * seqs;
         if (tiles > INT_MAX) return QGEMV_ERR_UNSUPPORTED;
@@ -338,6 +343,7 @@ static int run_attn(const qgemv_attn_args* a, unsigned flags, void* stream) {
     k.scale_log2 = a->scale * 1.44269504088896341f;
     k.window = a->window, k.causal = a->causal || a->window > 0;
     k.chunk = p.chunk, k.parts = p.parts, k.row_tiles = p.row_tiles, k.rows_part = p.rows_part;
+    k.unit_shift = p.unit_shift;
     const bool pdl = (flags & QGEMV_FLAG_PDL) != 0;
     unsigned smem, threads;
     const void* fn = (p.tiles ? attn_tiles_kernel_ptr : attn_rows_kernel_ptr)(a->kind == QGEMV_ACT_BF16, c.dim, &smem, &threads);
