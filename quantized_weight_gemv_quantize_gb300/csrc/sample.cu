@@ -3,12 +3,13 @@
 // Weights are whole numbers, w = floor(2^42 exp((x - max) / T)): their sums are exact in 64 bits whatever the order, so
 // the result is the same on every run and for every split of the work (and the blocks may sum with atomics).  Nothing is
 // sorted.  With c = (key bits of x, reversed index) as one number, the tokens that top-k and top-p keep are those with
-// c >= cut.  The cut is found from a histogram (counts for top-k, masses for top-p) of 1024 bins that are linear in
-// (max - x) / T: the bin in which the count or the mass reaches its bound is gathered, and each of its few tokens compares
-// itself with the others.  A bin with more than CAP tokens is first split again, by c, until one has at most CAP (c differs
-// for all tokens, so this ends even for a row of equal logits).
+// c >= cut.  A histogram of 1024 bins linear in (max - x) / T (counts for top-k, masses for top-p) tells the bin in which the count or
+// the mass reaches its bound.  Where the tokens up to and with that bin are few (at most CAP), they are gathered, and each compares
+// itself with the others: rank, mass before it, and the draw itself come from that list.  Else the bin's tokens alone are gathered
+// and give the cut, and the draw takes one more pass over the row; a bin of more than CAP tokens is split again, by c, until one has at
+// most CAP (c differs for all tokens, so this ends even for a row of equal logits).
 // Each block keeps its slice of the row in shared memory; the row is read once from global memory.  One row is bound by the
-// latency of its few passes and cluster barriers, many rows by the arithmetic a token (one expf, one or two shared atomics).
+// latency of its few passes and cluster barriers, many rows by the arithmetic a token.
 #include "common.cuh"
 #include "internal.h"
 #include "step.h"
@@ -18,9 +19,9 @@ namespace qg {
 using u64 = unsigned long long;
 
 constexpr int ST = SAMPLE_THREADS, SW = ST / 32;
-constexpr int BINS = 1024;
+constexpr int BINS = 1024, GROUP = 32, GROUPS = BINS / GROUP;
 constexpr int CAP = 512;  // one token a thread in the comparison
-static_assert(CAP <= ST, "");
+static_assert(CAP <= ST && BINS == 2 * ST && GROUPS == 32 && GROUP == 32, "");
 
 // ---- cluster: barrier, and the same shared-memory address in another block
 __device__ __forceinline__ void cluster_sync() {
@@ -37,26 +38,29 @@ __device__ __forceinline__ u64 peer_ld64(uint32_t a) {
     asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
     return v;
 }
-__device__ __forceinline__ uint32_t peer_ld32(uint32_t a) {
-    uint32_t v;
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-    return v;
-}
 __device__ __forceinline__ void peer_st64(uint32_t a, u64 v) {
     asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
 }
 
-// Unsigned key that orders as x does (both zeros alike).
+// Unsigned key that orders as x does (both zeros alike), and x from its key.
 __device__ __forceinline__ uint32_t key_of(float x) {
     const uint32_t b = __float_as_uint(x + 0.0f);
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
+__device__ __forceinline__ float x_of(uint32_t key) { return __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key); }
 __device__ __forceinline__ u64 place_of(uint32_t key, int i) { return static_cast<u64>(key) << 20 | (0xFFFFFu - i); }
 __device__ __forceinline__ float e_of(float x, float top, float rate) { return expf((x - top) * rate); }
-__device__ __forceinline__ u64 mass_of(float e) { return static_cast<u64>(__float2ull_rz(e * 0x1p42f)); }
+// floor(2^42 e) for 0 <= e <= 1, from the bits of e: the 24-bit significand shifted by exponent - 108.
+__device__ __forceinline__ u64 mass_of(float e) {
+    const uint32_t b = __float_as_uint(e);
+    const int shift = static_cast<int>(b >> 23) - 108;
+    const uint32_t sig = (b & 0x7fffffu) | 0x800000u;
+    return shift >= 0 ? static_cast<u64>(sig) << shift : static_cast<u64>(shift > -24 ? sig >> -shift : 0u);
+}
 // Monotone in x: 1024 bins over the 30 nats below the largest logit (2^-42 is 29.1), everything further in the last.
+constexpr float BIN_RATE = BINS / 30.0f;
 __device__ __forceinline__ int bin_of(float x, float top, float rate) {
-    return min(BINS - 1, static_cast<int>((top - x) * rate * (BINS / 30.0f)));
+    return min(BINS - 1, static_cast<int>((top - x) * rate * BIN_RATE));
 }
 
 template <int XK>
@@ -73,18 +77,27 @@ __device__ __forceinline__ float widen(typename Raw<XK>::type w) {
     else if constexpr (XK == ACT_BF16) return __uint_as_float(static_cast<uint32_t>(w) << 16);
     else return h2f(w);
 }
+template <int XK>
+__device__ __forceinline__ void widen_all(const uint4& w, float (&x)[16 / sizeof(typename Raw<XK>::type)]) {
+    const uint32_t p[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if constexpr (XK == ACT_F32) x[j] = __uint_as_float(p[j]);
+        else if constexpr (XK == ACT_BF16) x[2 * j] = __uint_as_float(p[j] << 16), x[2 * j + 1] = __uint_as_float(p[j] & 0xffff0000u);
+        else x[2 * j] = h2f(p[j]), x[2 * j + 1] = h2f(p[j] >> 16);
+    }
+}
 
 struct alignas(16) SampleShared {  // the slice follows it in shared memory, written 16 bytes at a time
     uint32_t lo[BINS], hi[BINS], count[BINS];  // masses as two words (hi takes the carries of lo), counts
-    u64 list_c[CAP], list_w[CAP];              // the tokens of this block in the bin that is split
-    u64 all_c[CAP], all_w[CAP];                // and of the whole cluster
+    u64 list_c[CAP], list_w[CAP];              // tokens of this block that were gathered (the whole cluster's take lo and hi)
+    u64 got_m[2][8][32], got_n[2][8][32];      // masses and counts of groups of bins, and of a group's bins, from each block
     u64 push[2][4][8];                         // what the blocks tell each other, by kind and block; two sets in turn
     u64 red[3][SW];
-    u64 bc[8];
     unsigned used;
+    uint8_t kept[CAP];
 };
-
-static_assert(sizeof(SampleShared) % 16 == 0, "");
+static_assert(sizeof(SampleShared) % 16 == 0 && sizeof(u64) * CAP <= sizeof(uint32_t) * BINS, "");
 
 template <class T, class Op>
 __device__ __forceinline__ T warp_reduce(T v, Op op) {
@@ -92,27 +105,76 @@ __device__ __forceinline__ T warp_reduce(T v, Op op) {
     for (int o = 16; o; o >>= 1) v = op(v, __shfl_xor_sync(0xffffffffu, v, o));
     return v;
 }
+__device__ __forceinline__ u64 warp_scan(u64 v, int lane) {  // inclusive
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const u64 u = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += u;
+    }
+    return v;
+}
 
 template <int XK>
-__global__ void __launch_bounds__(ST) sample_kernel(const SampleArgs a) {
+__global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleArgs a) {
     using raw = typename Raw<XK>::type;
+    constexpr int V = 16 / sizeof(raw);
     extern __shared__ __align__(16) uint8_t smem[];
     SampleShared& s = *reinterpret_cast<SampleShared*>(smem);
-    raw* stage = reinterpret_cast<raw*>(smem + sizeof(SampleShared));
+    uint4* const stage = reinterpret_cast<uint4*>(smem + sizeof(SampleShared));
+    u64 *const all_c = reinterpret_cast<u64*>(s.lo), *const all_w = reinterpret_cast<u64*>(s.hi);  // in use when the histogram is not
     pdl_launch_dependents();
     pdl_wait();
     const int CS = a.blocks, rank = static_cast<int>(blockIdx.x) % CS, row = static_cast<int>(blockIdx.x) / CS;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, N = a.N;
     const int first = rank * a.slice, n = max(0, min(a.slice, N - first));  // this block's tokens
-    const raw* src = static_cast<const raw*>(a.x) + row * a.row_stride + first;
-    auto at = [&](int i) { return widen<XK>(a.staged ? stage[i] : src[i]); };
+    const int vecs = (n + V - 1) / V;                                       // in 16-byte pieces, the last filled up with -inf
+    const raw* const src = static_cast<const raw*>(a.x) + row * a.row_stride + first;
+    const float NONE = __int_as_float(0xff800000);
+    // A piece from global memory: whole where it can be read so.
+    const bool wide = reinterpret_cast<uintptr_t>(src) % 16 == 0;
+    auto from_global = [&](int i, float (&x)[V]) {
+        if (wide && (i + 1) * V <= n) {
+            widen_all<XK>(reinterpret_cast<const uint4*>(src)[i], x);
+        } else {
+#pragma unroll
+            for (int q = 0; q < V; ++q) x[q] = i * V + q < n ? widen<XK>(src[i * V + q]) : NONE;
+        }
+    };
+    auto piece = [&](int i, float (&x)[V]) {
+        if (a.staged) widen_all<XK>(stage[i], x);
+        else from_global(i, x);
+    };
+    auto token = [&](int i) {  // i < vecs * V
+        if (a.staged) return widen<XK>(reinterpret_cast<const raw*>(stage)[i]);
+        return i < n ? widen<XK>(src[i]) : NONE;
+    };
+    // Every token of the slice: f(x, i), several pieces at a time.
+    auto for_all = [&](auto&& f) {
+        constexpr int U = V == 4 ? 4 : 2;
+        int i = tid;
+        for (; i + (U - 1) * ST < vecs; i += U * ST) {
+            float x[U][V];
+#pragma unroll
+            for (int j = 0; j < U; ++j) piece(i + j * ST, x[j]);
+#pragma unroll
+            for (int j = 0; j < U; ++j)
+#pragma unroll
+                for (int q = 0; q < V; ++q) f(x[j][q], (i + j * ST) * V + q);
+        }
+        for (; i < vecs; i += ST) {
+            float x[V];
+            piece(i, x);
+#pragma unroll
+            for (int q = 0; q < V; ++q) f(x[q], i * V + q);
+        }
+    };
     auto sync_all = [&] {
         if (CS > 1) cluster_sync();
         else __syncthreads();
     };
     int turn = 0;
-    // Every block gives up to 3 values (thread 0's) and gets all blocks': s.push[turn][kind][block].  Two sets in turn: a set
-    // is written again only after another exchange, whose barrier lies after every read of it.
+    // Every block gives up to 3 values (the same in all its threads) and gets all blocks': s.push[turn][kind][block].  Two sets in
+    // turn: a set is written again only after another exchange, whose barrier lies after every read of it.
     auto exchange = [&](u64 v0, u64 v1, u64 v2) {
         turn ^= 1;
         if (tid < CS) {
@@ -120,6 +182,18 @@ __global__ void __launch_bounds__(ST) sample_kernel(const SampleArgs a) {
             peer_st64(base, v0), peer_st64(base + 64, v1), peer_st64(base + 128, v2);
         }
         sync_all();
+    };
+    auto max64 = [](u64 p, u64 q) { return p > q ? p : q; };
+    auto min64 = [](u64 p, u64 q) { return p < q ? p : q; };
+    auto add64 = [](u64 p, u64 q) { return p + q; };
+    auto block_reduce = [&](u64 v, int set, auto&& op) {
+        v = warp_reduce(v, op);
+        __syncthreads();
+        if (lane == 0) s.red[set][warp] = v;
+        __syncthreads();
+        v = s.red[set][0];
+        for (int w = 1; w < SW; ++w) v = op(v, s.red[set][w]);
+        return v;
     };
 
     const float T = a.temperature ? a.temperature[row] : 1.f;
@@ -133,251 +207,307 @@ __global__ void __launch_bounds__(ST) sample_kernel(const SampleArgs a) {
     if (!(T > 0.f) || !(rate < 3e38f) || !(top_p > 0.f) || !(min_p <= 1.f)) k = 1;
     if (k <= 0 || k > N) k = N;
 
-    // ---- the slice into shared memory, and its largest token (NaN ranks above everything, as in torch.argmax)
-    u64 best = 0;
-    auto see = [&](raw w, int i) {
-        const float x = widen<XK>(w);
-        const u64 c = place_of(x != x ? 0xffffffffu : key_of(x), first + i);
-        best = c > best ? c : best;
-    };
-    constexpr int V = 16 / sizeof(raw);
-    const int vecs = reinterpret_cast<uintptr_t>(src) % 16 == 0 ? n / V : 0;
+    // ---- the slice into shared memory, and its largest logit (NaN ranks above everything, as in torch.argmax)
+    float largest = NONE;
+    bool nan = false;
     {
-        const uint4* sv = reinterpret_cast<const uint4*>(src);
-        constexpr int U = 4;
+        constexpr int U = 5;
         for (int i0 = tid; i0 < vecs; i0 += U * ST) {
             uint4 w[U];
 #pragma unroll
             for (int j = 0; j < U; ++j)
-                if (i0 + j * ST < vecs) w[j] = sv[i0 + j * ST];
+                if (wide && (i0 + j * ST + 1) * V <= n) w[j] = reinterpret_cast<const uint4*>(src)[i0 + j * ST];
 #pragma unroll
             for (int j = 0; j < U; ++j) {
                 const int i = i0 + j * ST;
                 if (i >= vecs) break;
-                if (a.staged) reinterpret_cast<uint4*>(stage)[i] = w[j];
-                const raw* e = reinterpret_cast<const raw*>(&w[j]);
+                if (!wide || (i + 1) * V > n) {
+                    alignas(16) raw p[V];
 #pragma unroll
-                for (int q = 0; q < V; ++q) see(e[q], i * V + q);
+                    for (int q = 0; q < V; ++q) {
+                        if (i * V + q < n) p[q] = src[i * V + q];
+                        else if constexpr (XK == ACT_F32) p[q] = NONE;
+                        else p[q] = XK == ACT_BF16 ? 0xff80 : 0xfc00;
+                    }
+                    w[j] = *reinterpret_cast<const uint4*>(p);
+                }
+                if (a.staged) stage[i] = w[j];
+                float x[V];
+                widen_all<XK>(w[j], x);
+#pragma unroll
+                for (int q = 0; q < V; ++q) largest = fmaxf(largest, x[q]), nan |= x[q] != x[q];
             }
         }
-        for (int i = vecs * V + tid; i < n; i += ST) {
-            const raw w = src[i];
-            if (a.staged) stage[i] = w;
-            see(w, i);
-        }
     }
-    auto max64 = [](u64 p, u64 q) { return p > q ? p : q; };
-    auto min64 = [](u64 p, u64 q) { return p < q ? p : q; };
-    auto add64 = [](u64 p, u64 q) { return p + q; };
-    best = warp_reduce(best, max64);
-    if (lane == 0) s.red[0][warp] = best;
-    __syncthreads();
-    best = s.red[0][0];
-    for (int w = 1; w < SW; ++w) best = max64(best, s.red[0][w]);
+    u64 best = block_reduce(nan ? 0xffffffffull : static_cast<u64>(key_of(largest)), 0, max64);
     exchange(best, 0, 0);
     for (int b = 0; b < CS; ++b) best = max64(best, s.push[turn][0][b]);
-    const uint32_t top_key = static_cast<uint32_t>(best >> 20);
-    const int top_at = static_cast<int>(0xFFFFFu - (best & 0xFFFFFu));
+    const uint32_t top_key = static_cast<uint32_t>(best);
+    const float top = x_of(top_key);
     // NaN or +inf; nothing but -inf; or rank 0 alone
     const bool broken = top_key >= 0xff800000u, none = top_key <= 0x007fffffu;
     if (broken || none || k == 1) {
+        u64 at = ~0ull;
+        if (!none) for_all([&](float x, int i) {
+            if (top_key == 0xffffffffu ? x != x : x == top) at = min64(at, static_cast<u64>(first + i));
+        });
+        at = block_reduce(at, 1, min64);
+        exchange(at, 0, 0);
+        for (int b = 0; b < CS; ++b) at = min64(at, s.push[turn][0][b]);
         if (tid == 0 && rank == 0) {
-            a.token[row] = none ? -1 : top_at;
+            a.token[row] = none ? -1 : static_cast<int>(at);
             if (a.prob) a.prob[row] = none ? 0.f : broken ? __int_as_float(0x7fc00000) : 1.f;
         }
         return;
     }
-    const float top = __uint_as_float(top_key & 0x80000000u ? top_key & 0x7fffffffu : ~top_key);
 
-    // ---- the smallest c that a filter keeps: by count (rank < k) or by mass (the mass before < reach)
-    // Returns the cut; *mass is the sum of w over c >= cut.  The reach is top_p of `of`, or of all mass where that is 0.
-    auto find_cut = [&](bool by_count, u64 of, u64* mass) {
-        const u64 bound_count = static_cast<u64>(k);
-        u64 lo = 0, hi = 0, above_count = 0, above_mass = 0;
-        double reach = 0.0;
-        bool linear = true;
-        int shift = 0;
-        for (;;) {
-            // the histogram of the undecided tokens (all, or lo <= c <= hi)
-            for (int b = tid; b < BINS; b += ST) s.lo[b] = s.hi[b] = s.count[b] = 0;
-            if (tid == 0) s.used = 0;
-            __syncthreads();
-            for (int i = tid; i < n; i += ST) {
-                const float x = at(i);
-                int b;
-                if (linear) {
-                    b = bin_of(x, top, rate);
-                } else {
-                    const u64 c = place_of(key_of(x), first + i);
-                    if (c < lo || c > hi) continue;
-                    b = static_cast<int>((hi - c) >> shift);
-                }
-                if (by_count) atomicAdd(&s.count[b], 1u);
-                const u64 w = mass_of(e_of(x, top, rate));
-                const uint32_t w0 = static_cast<uint32_t>(w);
-                uint32_t w1 = static_cast<uint32_t>(w >> 32);
-                if (w0) w1 += atomicAdd(&s.lo[b], w0) > ~w0;  // the carry of the lower word
-                if (w1) atomicAdd(&s.hi[b], w1);
+    // ---- histogram of the undecided tokens: all (linear), or lo <= c <= hi in bins of 2^shift
+    u64 lo = 0, hi = 0;
+    bool linear = true;
+    int shift = 0;
+    auto c_of = [&](float x, int i) { return place_of(key_of(x), first + i); };
+    auto fill = [&](bool counts, bool masses) {
+        for (int b = tid; b < BINS; b += ST) s.lo[b] = s.hi[b] = s.count[b] = 0;
+        __syncthreads();
+        auto add = [&](int b, float x) {
+            if (counts) atomicAdd(&s.count[b], 1u);
+            if (!masses) return;
+            const u64 w = mass_of(e_of(x, top, rate));
+            const uint32_t w0 = static_cast<uint32_t>(w);
+            uint32_t w1 = static_cast<uint32_t>(w >> 32);
+            if (w0) w1 += atomicAdd(&s.lo[b], w0) > ~w0;  // the carry of the lower word
+            if (w1) atomicAdd(&s.hi[b], w1);
+        };
+        if (linear) for_all([&](float x, int) { add(bin_of(x, top, rate), x); });
+        else for_all([&](float x, int i) {
+            const u64 c = c_of(x, i);
+            if (c >= lo && c <= hi) add(static_cast<int>((hi - c) >> shift), x);
+        });
+        __syncthreads();
+    };
+    // Adds up all blocks' bins, first in groups of 32, then in the group that reaches the bound; every warp of every block comes
+    // to the same bin.  above_*: before the bin, within_m: in it.  `all` receives the whole mass (first call).
+    u64 above_n = 0, above_m = 0, within_m = 0, all = 0;
+    auto find_bin = [&](auto&& reached) {
+        int group = 0;
+        u64 out_m = 0, out_n = 0;
+#pragma unroll 1
+        for (int level = 0; level < 2; ++level) {
+            u64 m, c;
+            if (level == 0) {
+                // thread t holds bins 2 t and 2 t + 1: a group is 16 threads
+                m = (static_cast<u64>(s.hi[2 * tid]) + s.hi[2 * tid + 1] << 32) + s.lo[2 * tid] + s.lo[2 * tid + 1];
+                c = s.count[2 * tid] + s.count[2 * tid + 1];
+#pragma unroll
+                for (int o = 8; o; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o), c += __shfl_xor_sync(0xffffffffu, c, o);
+                if (tid % 16 == 0)
+                    for (int b = 0; b < CS; ++b) {
+                        peer_st64(peer(smem_addr(&s.got_m[0][rank][tid / 16]), b), m);
+                        peer_st64(peer(smem_addr(&s.got_n[0][rank][tid / 16]), b), c);
+                    }
+            } else if (tid < 32 * CS) {
+                const int at = group * GROUP + lane;
+                m = (static_cast<u64>(s.hi[at]) << 32) + s.lo[at], c = s.count[at];
+                peer_st64(peer(smem_addr(&s.got_m[1][rank][lane]), warp), m);
+                peer_st64(peer(smem_addr(&s.got_n[1][rank][lane]), warp), c);
             }
             sync_all();
-            // all blocks sum all blocks' bins (two a thread) and look for the bin that reaches the bound
-            constexpr int PER = BINS / ST;
-            u64 bm[PER] = {}, bn[PER] = {};
-            for (int r = 0; r < CS; ++r) {
-                const uint32_t l = peer(smem_addr(s.lo), r), h = peer(smem_addr(s.hi), r), c = peer(smem_addr(s.count), r);
-#pragma unroll
-                for (int j = 0; j < PER; ++j) {
-                    const uint32_t off = 4u * (tid * PER + j);
-                    bm[j] += static_cast<u64>(peer_ld32(l + off)) + (static_cast<u64>(peer_ld32(h + off)) << 32);
-                    if (by_count) bn[j] += peer_ld32(c + off);
-                }
-            }
-            u64 m = 0, cnt = 0;
-#pragma unroll
-            for (int j = 0; j < PER; ++j) m += bm[j], cnt += bn[j];
-            const u64 own_m = m, own_c = cnt;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const u64 pm = __shfl_up_sync(0xffffffffu, m, o), pc = __shfl_up_sync(0xffffffffu, cnt, o);
-                if (lane >= o) m += pm, cnt += pc;
-            }
-            if (lane == 31) s.red[0][warp] = m, s.red[1][warp] = cnt;
-            __syncthreads();
-            u64 total = 0;
-            for (int w = 0; w < SW; ++w) {
-                if (w < warp) m += s.red[0][w], cnt += s.red[1][w];
-                total += s.red[0][w];
-            }
-            if (linear) reach = static_cast<double>(top_p) * static_cast<double>(of ? of : total);
-            // before this thread's bins
-            u64 pm = above_mass + m - own_m, pc = above_count + cnt - own_c;
-            auto reached = [&](u64 qc, u64 qm) { return by_count ? qc >= bound_count : static_cast<double>(qm) >= reach; };
-            if (!reached(pc, pm)) {
-#pragma unroll
-                for (int j = 0; j < PER; ++j) {
-                    if (!reached(pc, pm) && reached(pc + bn[j], pm + bm[j])) s.bc[0] = tid * PER + j, s.bc[1] = pc, s.bc[2] = pm;
-                    pm += bm[j], pc += bn[j];
-                }
-            }
-            __syncthreads();
-            const int bin = static_cast<int>(s.bc[0]);
-            above_count = s.bc[1], above_mass = s.bc[2];
-            // gather the bin's tokens
-            u64 cmin = ~0ull, cmax = 0;
-            for (int i = tid; i < n; i += ST) {
-                const float x = at(i);
-                if (linear && bin_of(x, top, rate) != bin) continue;
-                const u64 c = place_of(key_of(x), first + i);
-                if (!linear && (c < lo || c > hi || static_cast<int>((hi - c) >> shift) != bin)) continue;
-                cmin = min64(cmin, c), cmax = max64(cmax, c);
-                const unsigned p = atomicAdd(&s.used, 1u);
-                if (p < CAP) s.list_c[p] = c, s.list_w[p] = mass_of(e_of(x, top, rate));
-            }
-            cmin = warp_reduce(cmin, min64), cmax = warp_reduce(cmax, max64);
-            if (lane == 0) s.red[0][warp] = cmin, s.red[1][warp] = cmax;
-            __syncthreads();
-            for (int w = 0; w < SW; ++w) cmin = min64(cmin, s.red[0][w]), cmax = max64(cmax, s.red[1][w]);
-            exchange(s.used, cmin, cmax);
-            unsigned members = 0;
-            for (int b = 0; b < CS; ++b) {
-                members += static_cast<unsigned>(s.push[turn][0][b]);
-                cmin = min64(cmin, s.push[turn][1][b]), cmax = max64(cmax, s.push[turn][2][b]);
-            }
-            if (members > CAP) {  // split the bin by c
-                lo = cmin, hi = cmax, linear = false;
-                const int bits = 64 - __clzll(static_cast<long long>(hi - lo));
-                shift = max(0, bits - 10);
-                continue;
-            }
-            // each token of the bin against the others
-            unsigned base = 0;
-            for (int b = 0; b < CS; ++b) {
-                const unsigned nb = static_cast<unsigned>(s.push[turn][0][b]);
-                const uint32_t c = peer(smem_addr(s.list_c), b), w = peer(smem_addr(s.list_w), b);
-                for (unsigned i = tid; i < nb; i += ST) s.all_c[base + i] = peer_ld64(c + 8 * i), s.all_w[base + i] = peer_ld64(w + 8 * i);
-                base += nb;
-            }
-            __syncthreads();
-            u64 cut = ~0ull, kept = 0;
-            if (tid < members) {
-                const u64 c = s.all_c[tid];
-                u64 before = above_mass, place = above_count;
-                for (unsigned j = 0; j < members; ++j)
-                    if (s.all_c[j] > c) before += s.all_w[j], ++place;
-                if (!reached(place, before)) cut = c, kept = s.all_w[tid];  // rank < k, or mass before < reach
-            }
-            cut = warp_reduce(cut, min64), kept = warp_reduce(kept, add64);
-            if (lane == 0) s.red[0][warp] = cut, s.red[1][warp] = kept;
-            __syncthreads();
-            kept = above_mass;
-            for (int w = 0; w < SW; ++w) cut = min64(cut, s.red[0][w]), kept += s.red[1][w];
-            *mass = kept;
-            return cut;
+            m = c = 0;
+            for (int b = 0; b < CS; ++b) m += s.got_m[level][b][lane], c += s.got_n[level][b][lane];
+            const u64 sm = warp_scan(m, lane), sc = warp_scan(c, lane);
+            if (level == 0 && linear) all = __shfl_sync(0xffffffffu, sm, 31);
+            const unsigned hit = __ballot_sync(0xffffffffu, reached(above_n + sc, above_m + sm));
+            const int l = hit ? __ffs(hit) - 1 : 31;
+            out_m = __shfl_sync(0xffffffffu, sm - m, l), out_n = __shfl_sync(0xffffffffu, sc - c, l);
+            within_m = __shfl_sync(0xffffffffu, m, l);
+            above_m += out_m, above_n += out_n;
+            group = level == 0 ? l : group * GROUP + l;
+        }
+        return group;
+    };
+    // Gathers tokens into the block's list; tells all blocks how many there are and the range of their c.
+    unsigned members = 0;
+    u64 cmin = 0, cmax = 0;
+    auto gather = [&](auto&& take) {
+        if (tid == 0) s.used = 0;
+        __syncthreads();
+        cmin = ~0ull, cmax = 0;
+        for_all([&](float x, int i) {
+            if (!take(x, i)) return;
+            const u64 c = c_of(x, i);
+            cmin = min64(cmin, c), cmax = max64(cmax, c);
+            const unsigned p = atomicAdd(&s.used, 1u);
+            if (p < CAP) s.list_c[p] = c, s.list_w[p] = mass_of(e_of(x, top, rate));
+        });
+        cmin = warp_reduce(cmin, min64), cmax = warp_reduce(cmax, max64);
+        if (lane == 0) s.red[0][warp] = cmin, s.red[1][warp] = cmax;
+        __syncthreads();
+        for (int w = 0; w < SW; ++w) cmin = min64(cmin, s.red[0][w]), cmax = max64(cmax, s.red[1][w]);
+        exchange(s.used, cmin, cmax);
+        members = 0;
+        for (int b = 0; b < CS; ++b) {
+            members += static_cast<unsigned>(s.push[turn][0][b]);
+            cmin = min64(cmin, s.push[turn][1][b]), cmax = max64(cmax, s.push[turn][2][b]);
         }
     };
-    u64 cut = 0, kept = 0;
-    if (k < N) cut = find_cut(true, 0, &kept);
+    // All blocks' lists, at most CAP tokens, into this one.
+    auto collect = [&] {
+        unsigned base = 0;
+        for (int b = 0; b < CS; ++b) {
+            const unsigned nb = static_cast<unsigned>(s.push[turn][0][b]);
+            const uint32_t c = peer(smem_addr(s.list_c), b), w = peer(smem_addr(s.list_w), b);
+            if (tid >= base && tid < base + nb) {
+                all_c[tid] = peer_ld64(c + 8 * (tid - base));
+                all_w[tid] = peer_ld64(w + 8 * (tid - base));
+            }
+            base += nb;
+        }
+        __syncthreads();
+    };
+    // The draw from a list that holds every token that may be kept (thread t has token t of it); `of`: the mass that top-p
+    // is a share of, 0 for that of the tokens that top-k keeps.
+    auto draw_from_list = [&](u64 of) {
+        if (rank == 0) {
+            collect();
+            const bool mine = tid < members;
+            const u64 c = mine ? all_c[tid] : 0, w = mine ? all_w[tid] : 0;
+            u64 before = 0;
+            int place = 0;
+            for (unsigned j = 0; j < members; ++j)
+                if (all_c[j] > c) before += all_w[j], ++place;
+            bool keep = mine && place < k;
+            if (top_p < 1.f) {
+                if (!of) of = block_reduce(keep ? w : 0, 0, add64);
+                keep = keep && static_cast<double>(before) < static_cast<double>(top_p) * static_cast<double>(of);
+            }
+            const float e = e_of(x_of(static_cast<uint32_t>(c >> 20)), top, rate);
+            keep = keep && e >= min_p;
+            if (mine) s.kept[tid] = keep;
+            const u64 W = block_reduce(keep ? w : 0, 1, add64);  // (its barriers order the flags)
+            u64 target = static_cast<u64>(static_cast<double>(u) * static_cast<double>(W));
+            if (target >= W) target = W - 1;
+            // in index order: the lower bits of c fall as the index grows
+            u64 until = 0;
+            if (keep)
+                for (unsigned j = 0; j < members; ++j)
+                    if (s.kept[j] && (all_c[j] & 0xFFFFFu) > (c & 0xFFFFFu)) until += all_w[j];
+            if (keep && until <= target && target < until + w) {
+                a.token[row] = static_cast<int>(0xFFFFFu - (c & 0xFFFFFu));
+                if (a.prob) a.prob[row] = e / (static_cast<float>(W) * 0x1p-42f);
+            }
+        }
+        sync_all();  // no block ends while its list is read
+    };
+    // The smallest c that a filter keeps; *mass: the sum of w over c >= cut.
+    auto cut_of = [&](auto&& reached, u64* mass) {
+        for (;;) {
+            const int bin = find_bin(reached);
+            if (linear) gather([&](float x, int) { return bin_of(x, top, rate) == bin; });
+            else gather([&](float x, int i) {
+                const u64 c = c_of(x, i);
+                return c >= lo && c <= hi && static_cast<int>((hi - c) >> shift) == bin;
+            });
+            if (members <= CAP) break;
+            lo = cmin, hi = cmax, linear = false;
+            const int bits = 64 - __clzll(static_cast<long long>(hi - lo));
+            shift = max(0, bits - 10);
+            fill(true, true);
+        }
+        collect();
+        u64 cut = ~0ull, kept = 0;
+        if (tid < members) {
+            const u64 c = all_c[tid];
+            u64 before = above_m, place = above_n;
+            for (unsigned j = 0; j < members; ++j)
+                if (all_c[j] > c) before += all_w[j], ++place;
+            if (!reached(place, before)) cut = c, kept = all_w[tid];  // rank < k, or mass before < reach
+        }
+        cut = block_reduce(cut, 0, min64), kept = block_reduce(kept, 1, add64);
+        *mass = above_m + kept;
+        return cut;
+    };
+
+    u64 cut = 0, kept_mass = 0;
+    if (k < N) {
+        auto reached = [&](u64 qc, u64) { return qc >= static_cast<u64>(k); };
+        const bool few = k <= CAP / 2;
+        fill(true, !few);
+        if (few) {
+            const int bin = find_bin(reached);
+            gather([&](float x, int) { return bin_of(x, top, rate) <= bin; });
+            if (members <= CAP) {
+                draw_from_list(0);
+                return;
+            }
+            above_n = above_m = 0;
+            fill(true, true);
+        }
+        cut = cut_of(reached, &kept_mass);
+    }
     if (top_p < 1.f) {
+        above_n = above_m = 0, linear = true;
+        fill(false, true);
+        double reach = 0.0;
+        bool known = k < N;
+        if (known) reach = static_cast<double>(top_p) * static_cast<double>(kept_mass);
+        auto reached = [&](u64, u64 qm) {
+            // (the whole mass is known from the first level of the first search on)
+            return static_cast<double>(qm) >= (known ? reach : static_cast<double>(top_p) * static_cast<double>(all));
+        };
         u64 unused;
-        cut = max64(cut, find_cut(false, kept, &unused));
+        cut = max64(cut, cut_of(reached, &unused));
     }
 
-    // ---- the kept mass, by warp: each owns a contiguous piece of the slice
-    const int piece = (n + SW - 1) / SW, p0 = min(n, warp * piece), p1 = min(n, p0 + piece);
-    auto weight = [&](int i) {
-        const float x = at(i), e = e_of(x, top, rate);
-        return place_of(key_of(x), first + i) >= cut && e >= min_p ? mass_of(e) : 0ull;
+    // ---- the draw by a pass over the row: each thread owns a contiguous part of the slice (an odd number of pieces: the
+    // threads of a quarter warp then read different banks)
+    const int own_vecs = (vecs + ST - 1) / ST | 1, v0 = min(vecs, tid * own_vecs), v1 = min(vecs, v0 + own_vecs);
+    const uint32_t cut_key = static_cast<uint32_t>(cut >> 20);
+    auto weight = [&](float x, int i) -> u64 {
+        const uint32_t key = key_of(x);
+        if (key < cut_key || place_of(key, first + i) < cut) return 0;
+        const float e = e_of(x, top, rate);
+        return e >= min_p ? mass_of(e) : 0;
     };
-    u64 sum = 0;
-    for (int i = p0 + lane; i < p1; i += 32) sum += weight(i);
-    sum = warp_reduce(sum, add64);
+    u64 own = 0;
+#pragma unroll 2
+    for (int i = v0; i < v1; ++i) {
+        float x[V];
+        piece(i, x);
+#pragma unroll
+        for (int q = 0; q < V; ++q) own += weight(x[q], i * V + q);
+    }
+    const u64 run = warp_scan(own, lane);
     __syncthreads();
-    if (lane == 0) s.red[2][warp] = sum;
+    if (lane == 31) s.red[2][warp] = run;
     __syncthreads();
-    u64 mine = 0, before_warp = 0;
+    u64 mine = 0, start = run - own;
     for (int w = 0; w < SW; ++w) {
-        if (w < warp) before_warp += s.red[2][w];
+        if (w < warp) start += s.red[2][w];
         mine += s.red[2][w];
     }
     exchange(mine, 0, 0);
-    u64 W = 0, before = 0;
+    u64 W = 0;
     for (int b = 0; b < CS; ++b) {
-        if (b < rank) before += s.push[turn][0][b];
+        if (b < rank) start += s.push[turn][0][b];
         W += s.push[turn][0][b];
     }
     u64 target = static_cast<u64>(static_cast<double>(u) * static_cast<double>(W));
     if (target >= W) target = W - 1;
-    // ---- the warp whose piece holds the target: its lanes sum a contiguous part each, then share the part that holds it
-    const u64 start = before + before_warp;
-    if (target < start || target >= start + sum) return;
-    const int part = (p1 - p0 + 31) / 32, q0 = min(p1, p0 + lane * part), q1 = min(p1, q0 + part);
-    u64 own = 0;
-    for (int i = q0; i < q1; ++i) own += weight(i);
-    u64 run = own;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const u64 v = __shfl_up_sync(0xffffffffu, run, o);
-        if (lane >= o) run += v;
-    }
-    run += start;
-    const int owner = __ffs(__ballot_sync(0xffffffffu, run > target)) - 1;
-    u64 base = __shfl_sync(0xffffffffu, run - own, owner);
-    const int r0 = __shfl_sync(0xffffffffu, q0, owner), r1 = __shfl_sync(0xffffffffu, q1, owner);
-    for (int i0 = r0; i0 < r1; i0 += 32) {
-        const int i = i0 + lane;
-        u64 v = i < r1 ? weight(i) : 0ull;
-        const u64 w = v;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const u64 t = __shfl_up_sync(0xffffffffu, v, o);
-            if (lane >= o) v += t;
-        }
-        v += base;
-        if (v > target && v - w <= target) {
+    // the thread whose part holds the target; its warp shares the part
+    const unsigned holds = __ballot_sync(0xffffffffu, start <= target && target < start + own);
+    if (!holds) return;
+    const int owner = __ffs(holds) - 1;
+    u64 base = __shfl_sync(0xffffffffu, start, owner);
+    const int i0 = __shfl_sync(0xffffffffu, v0 * V, owner), i1 = __shfl_sync(0xffffffffu, v1 * V, owner);
+    for (int j = i0; j < i1; j += 32) {
+        const int i = j + lane;
+        const float x = i < i1 ? token(i) : NONE;
+        const u64 w = i < i1 ? weight(x, i) : 0, sum = warp_scan(w, lane) + base;
+        if (sum > target && sum - w <= target) {
             a.token[row] = first + i;
-            if (a.prob) a.prob[row] = e_of(at(i), top, rate) / (static_cast<float>(W) * 0x1p-42f);
+            if (a.prob) a.prob[row] = e_of(x, top, rate) / (static_cast<float>(W) * 0x1p-42f);
         }
-        base = __shfl_sync(0xffffffffu, v, 31);
+        base = __shfl_sync(0xffffffffu, sum, 31);
         if (base > target) break;
     }
 }
