@@ -3,11 +3,13 @@
 // Weights are whole numbers, w = floor(2^42 exp((x - max) / T)): their sums are exact in 64 bits whatever the order, so
 // the result is the same on every run and for every split of the work (and the blocks may sum with atomics).  Nothing is
 // sorted.  With c = (key bits of x, reversed index) as one number, the tokens that top-k and top-p keep are those with
-// c >= cut.  A histogram of 1024 bins linear in (max - x) / T (counts for top-k, masses for top-p) tells the bin in which the count or
-// the mass reaches its bound.  Where the tokens up to and with that bin are few (at most CAP), they are gathered, and each compares
-// itself with the others: rank, mass before it, and the draw itself come from that list.  Else the bin's tokens alone are gathered
-// and give the cut, and the draw takes one more pass over the row; a bin of more than CAP tokens is split again, by c, until one has at
-// most CAP (c differs for all tokens, so this ends even for a row of equal logits).
+// c >= cut.
+//  - Up to 512 tokens by top-k: the k-th largest of the threads' own largest logits is a bound that at least k tokens reach, and few
+//    more than k do.  Those are gathered and sorted: ranks, masses and the draw come from that list.
+//  - Else a histogram of 1024 bins linear in (max - x) / T (counts for top-k, masses for top-p) tells the bin in which the count or the
+//    mass reaches its bound.  Where the tokens up to that bin are surely few, the list is made of them.  Else the bin's tokens alone are
+//    gathered and give the cut, and the draw takes one more pass over the row; a bin of more than CAP tokens is split again, by c, until
+//    one has at most CAP (c differs for all tokens, so this ends even for a row of equal logits).
 // Each block keeps its slice of the row in shared memory; the row is read once from global memory.  One row is bound by the
 // latency of its few passes and cluster barriers, many rows by the arithmetic a token.
 #include "common.cuh"
@@ -20,8 +22,8 @@ using u64 = unsigned long long;
 
 constexpr int ST = SAMPLE_THREADS, SW = ST / 32;
 constexpr int BINS = 1024, GROUP = 32, GROUPS = BINS / GROUP;
-constexpr int CAP = 512;  // one token a thread in the comparison
-static_assert(CAP <= ST && BINS == 2 * ST && GROUPS == 32 && GROUP == 32, "");
+constexpr int CAP = ST;  // one token a thread
+static_assert( BINS == 2 * ST && GROUPS == 32 && GROUP == 32, "");
 
 // ---- cluster: barrier, and the same shared-memory address in another block
 __device__ __forceinline__ void cluster_sync() {
@@ -90,14 +92,14 @@ __device__ __forceinline__ void widen_all(const uint4& w, float (&x)[16 / sizeof
 
 struct alignas(16) SampleShared {  // the slice follows it in shared memory, written 16 bytes at a time
     uint32_t lo[BINS], hi[BINS], count[BINS];  // masses as two words (hi takes the carries of lo), counts
-    u64 list_c[CAP], list_w[CAP];              // tokens of this block that were gathered (the whole cluster's take lo and hi)
+    u64 list[CAP];                             // c of the tokens of this block that were gathered
+    u64 group_m[32], group_n[32];
     u64 got_m[2][8][32], got_n[2][8][32];      // masses and counts of groups of bins, and of a group's bins, from each block
     u64 push[2][4][8];                         // what the blocks tell each other, by kind and block; two sets in turn
     u64 red[3][SW];
     unsigned used;
-    uint8_t kept[CAP];
 };
-static_assert(sizeof(SampleShared) % 16 == 0 && sizeof(u64) * CAP <= sizeof(uint32_t) * BINS, "");
+static_assert(sizeof(SampleShared) % 16 == 0 && sizeof(u64) * ST <= sizeof(uint32_t) * BINS, "");
 
 template <class T, class Op>
 __device__ __forceinline__ T warp_reduce(T v, Op op) {
@@ -121,7 +123,7 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleArgs a) {
     extern __shared__ __align__(16) uint8_t smem[];
     SampleShared& s = *reinterpret_cast<SampleShared*>(smem);
     uint4* const stage = reinterpret_cast<uint4*>(smem + sizeof(SampleShared));
-    u64 *const all_c = reinterpret_cast<u64*>(s.lo), *const all_w = reinterpret_cast<u64*>(s.hi);  // in use when the histogram is not
+    u64* const line = reinterpret_cast<u64*>(s.lo);  // a word a thread, in use when the histogram is not
     pdl_launch_dependents();
     pdl_wait();
     const int CS = a.blocks, rank = static_cast<int>(blockIdx.x) % CS, row = static_cast<int>(blockIdx.x) / CS;
@@ -148,8 +150,8 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleArgs a) {
         if (a.staged) return widen<XK>(reinterpret_cast<const raw*>(stage)[i]);
         return i < n ? widen<XK>(src[i]) : NONE;
     };
-    // Every token of the slice: f(x, i), several pieces at a time.
-    auto for_all = [&](auto&& f) {
+    // Every piece of the slice, several at a time: f(x, i); every token: f(x, i).
+    auto for_pieces = [&](auto&& f) {
         constexpr int U = V == 4 ? 4 : 2;
         int i = tid;
         for (; i + (U - 1) * ST < vecs; i += U * ST) {
@@ -157,16 +159,19 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleArgs a) {
 #pragma unroll
             for (int j = 0; j < U; ++j) piece(i + j * ST, x[j]);
 #pragma unroll
-            for (int j = 0; j < U; ++j)
-#pragma unroll
-                for (int q = 0; q < V; ++q) f(x[j][q], (i + j * ST) * V + q);
+            for (int j = 0; j < U; ++j) f(x[j], i + j * ST);
         }
         for (; i < vecs; i += ST) {
             float x[V];
             piece(i, x);
+            f(x, i);
+        }
+    };
+    auto for_all = [&](auto&& f) {
+        for_pieces([&](const float (&x)[V], int i) {
 #pragma unroll
             for (int q = 0; q < V; ++q) f(x[q], i * V + q);
-        }
+        });
     };
     auto sync_all = [&] {
         if (CS > 1) cluster_sync();
@@ -300,11 +305,12 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleArgs a) {
                 c = s.count[2 * tid] + s.count[2 * tid + 1];
 #pragma unroll
                 for (int o = 8; o; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o), c += __shfl_xor_sync(0xffffffffu, c, o);
-                if (tid % 16 == 0)
-                    for (int b = 0; b < CS; ++b) {
-                        peer_st64(peer(smem_addr(&s.got_m[0][rank][tid / 16]), b), m);
-                        peer_st64(peer(smem_addr(&s.got_n[0][rank][tid / 16]), b), c);
-                    }
+                if (tid % 16 == 0) s.group_m[tid / 16] = m, s.group_n[tid / 16] = c;
+                __syncthreads();
+                if (tid < 32 * CS) {
+                    peer_st64(peer(smem_addr(&s.got_m[0][rank][lane]), warp), s.group_m[lane]);
+                    peer_st64(peer(smem_addr(&s.got_n[0][rank][lane]), warp), s.group_n[lane]);
+                }
             } else if (tid < 32 * CS) {
                 const int at = group * GROUP + lane;
                 m = (static_cast<u64>(s.hi[at]) << 32) + s.lo[at], c = s.count[at];
@@ -325,137 +331,187 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleArgs a) {
         }
         return group;
     };
-    // Gathers tokens into the block's list; tells all blocks how many there are and the range of their c.
+    // Gathers tokens into the block's list; tells all blocks how many there are.
     unsigned members = 0;
-    u64 cmin = 0, cmax = 0;
-    auto gather = [&](auto&& take) {
+    auto put = [&](float x, int i) {
+        const unsigned p = atomicAdd(&s.used, 1u);
+        if (p < CAP) s.list[p] = c_of(x, i);
+    };
+    auto gather = [&](auto&& all_of) {
         if (tid == 0) s.used = 0;
         __syncthreads();
-        cmin = ~0ull, cmax = 0;
-        for_all([&](float x, int i) {
-            if (!take(x, i)) return;
-            const u64 c = c_of(x, i);
-            cmin = min64(cmin, c), cmax = max64(cmax, c);
-            const unsigned p = atomicAdd(&s.used, 1u);
-            if (p < CAP) s.list_c[p] = c, s.list_w[p] = mass_of(e_of(x, top, rate));
-        });
-        cmin = warp_reduce(cmin, min64), cmax = warp_reduce(cmax, max64);
-        if (lane == 0) s.red[0][warp] = cmin, s.red[1][warp] = cmax;
+        all_of();
         __syncthreads();
-        for (int w = 0; w < SW; ++w) cmin = min64(cmin, s.red[0][w]), cmax = max64(cmax, s.red[1][w]);
-        exchange(s.used, cmin, cmax);
+        exchange(s.used, 0, 0);
         members = 0;
-        for (int b = 0; b < CS; ++b) {
-            members += static_cast<unsigned>(s.push[turn][0][b]);
-            cmin = min64(cmin, s.push[turn][1][b]), cmax = max64(cmax, s.push[turn][2][b]);
-        }
+        for (int b = 0; b < CS; ++b) members += static_cast<unsigned>(s.push[turn][0][b]);
     };
-    // All blocks' lists, at most CAP tokens, into this one.
+    // Logits of the bins up to `bin` are at least this (bin_of has three roundings, this two more: the margins are wider).
+    auto least_of = [&](int bin) {
+        const float x = top - (bin + 1) / (rate * BIN_RATE) * 1.000001f;
+        return bin >= BINS - 1 ? NONE : x - (fabsf(x) + fabsf(top)) * 4e-7f;
+    };
+    // the tokens from `least` on that take(x, i) wants
+    auto gather_from = [&](float least, auto&& take) {
+        gather([&] {
+            for_pieces([&](const float (&x)[V], int i) {
+                float m = x[0];
+#pragma unroll
+                for (int q = 1; q < V; ++q) m = fmaxf(m, x[q]);
+                if (m < least) return;
+#pragma unroll
+                for (int q = 0; q < V; ++q)
+                    if (x[q] >= least && take(x[q], i * V + q)) put(x[q], i * V + q);
+            });
+        });
+    };
+    // All blocks' lists, at most CAP tokens, sorted: thread t gets the c of rank t (0 past the last).
+    auto sorted = [&](u64 v, unsigned count) {  // descending, over the first threads; a bitonic network
+        int width = 1;
+        while (static_cast<unsigned>(width) < count) width <<= 1;
+#pragma unroll 1
+        for (int size = 2; size <= width; size <<= 1)
+#pragma unroll 1
+            for (int j = size >> 1; j; j >>= 1) {
+                u64 o;
+                if (j >= 32) {
+                    __syncthreads();
+                    line[tid] = v;
+                    __syncthreads();
+                    o = line[tid ^ j];
+                } else {
+                    o = __shfl_xor_sync(0xffffffffu, v, j);
+                }
+                v = ((tid & j) == 0) == ((tid & size) == 0) ? max64(v, o) : min64(v, o);
+            }
+        return v;
+    };
     auto collect = [&] {
         unsigned base = 0;
+        u64 c = 0;
         for (int b = 0; b < CS; ++b) {
             const unsigned nb = static_cast<unsigned>(s.push[turn][0][b]);
-            const uint32_t c = peer(smem_addr(s.list_c), b), w = peer(smem_addr(s.list_w), b);
-            if (tid >= base && tid < base + nb) {
-                all_c[tid] = peer_ld64(c + 8 * (tid - base));
-                all_w[tid] = peer_ld64(w + 8 * (tid - base));
-            }
+            if (tid >= base && tid < base + nb) c = peer_ld64(peer(smem_addr(s.list), b) + 8 * (tid - base));
             base += nb;
         }
-        __syncthreads();
+        return sorted(c, members);
     };
-    // The draw from a list that holds every token that may be kept (thread t has token t of it); `of`: the mass that top-p
-    // is a share of, 0 for that of the tokens that top-k keeps.
+    auto x_at = [&](u64 c) { return x_of(static_cast<uint32_t>(c >> 20)); };
+    // Sum over the threads up to this one, and over all of them.
+    auto block_scan = [&](u64 v, u64* total) {
+        const u64 run = warp_scan(v, lane);
+        __syncthreads();
+        if (lane == 31) s.red[2][warp] = run;
+        __syncthreads();
+        u64 before = 0, sum = 0;
+        for (int w = 0; w < SW; ++w) {
+            if (w < warp) before += s.red[2][w];
+            sum += s.red[2][w];
+        }
+        *total = sum;
+        return before + run;
+    };
+    // The draw from a list that holds every token that may be kept; `of`: the mass that top-p is a share of, 0 for that of the tokens that
+    // top-k keeps.
     auto draw_from_list = [&](u64 of) {
         if (rank == 0) {
-            collect();
-            const bool mine = tid < members;
-            const u64 c = mine ? all_c[tid] : 0, w = mine ? all_w[tid] : 0;
-            u64 before = 0;
-            int place = 0;
-            for (unsigned j = 0; j < members; ++j)
-                if (all_c[j] > c) before += all_w[j], ++place;
-            bool keep = mine && place < k;
-            if (top_p < 1.f) {
-                if (!of) of = block_reduce(keep ? w : 0, 0, add64);
-                keep = keep && static_cast<double>(before) < static_cast<double>(top_p) * static_cast<double>(of);
-            }
-            const float e = e_of(x_of(static_cast<uint32_t>(c >> 20)), top, rate);
-            keep = keep && e >= min_p;
-            if (mine) s.kept[tid] = keep;
-            const u64 W = block_reduce(keep ? w : 0, 1, add64);  // (its barriers order the flags)
+            const u64 c = collect();
+            const float e = e_of(x_at(c), top, rate);
+            const u64 w = tid < members ? mass_of(e) : 0;
+            u64 among;
+            const u64 before = block_scan(tid < k ? w : 0, &among) - w;  // (of use where tid < k)
+            bool keep = tid < members && tid < k && e >= min_p;
+            if (top_p < 1.f) keep = keep && static_cast<double>(before) < static_cast<double>(top_p) * static_cast<double>(of ? of : among);
+            // in index order: the lower bits of c fall as the index grows
+            const u64 next = sorted(keep ? 1ull << 62 | (c & 0xFFFFFu) << 32 | static_cast<unsigned>(tid) : 0, members);
+            __syncthreads();
+            line[tid] = c;
+            __syncthreads();
+            const bool kept = next != 0;
+            const u64 its = kept ? line[next & (ST - 1)] : 0;
+            const float its_e = e_of(x_at(its), top, rate);
+            const u64 its_w = kept ? mass_of(its_e) : 0;
+            u64 W;
+            const u64 until = block_scan(its_w, &W);
             u64 target = static_cast<u64>(static_cast<double>(u) * static_cast<double>(W));
             if (target >= W) target = W - 1;
-            // in index order: the lower bits of c fall as the index grows
-            u64 until = 0;
-            if (keep)
-                for (unsigned j = 0; j < members; ++j)
-                    if (s.kept[j] && (all_c[j] & 0xFFFFFu) > (c & 0xFFFFFu)) until += all_w[j];
-            if (keep && until <= target && target < until + w) {
-                a.token[row] = static_cast<int>(0xFFFFFu - (c & 0xFFFFFu));
-                if (a.prob) a.prob[row] = e / (static_cast<float>(W) * 0x1p-42f);
+            if (until > target && until - its_w <= target) {
+                a.token[row] = static_cast<int>(0xFFFFFu - (its & 0xFFFFFu));
+                if (a.prob) a.prob[row] = its_e / (static_cast<float>(W) * 0x1p-42f);
             }
         }
         sync_all();  // no block ends while its list is read
     };
-    // The smallest c that a filter keeps; *mass: the sum of w over c >= cut.
-    auto cut_of = [&](auto&& reached, u64* mass) {
+    // The smallest c that a filter keeps, from the histogram's bin on; *mass: the sum of w over c >= cut.
+    auto cut_of = [&](int bin, auto&& reached, u64* mass) {
         for (;;) {
-            const int bin = find_bin(reached);
-            if (linear) gather([&](float x, int) { return bin_of(x, top, rate) == bin; });
-            else gather([&](float x, int i) {
+            auto in_bin = [&](float x, int i) {
+                if (linear) return bin_of(x, top, rate) == bin;
                 const u64 c = c_of(x, i);
                 return c >= lo && c <= hi && static_cast<int>((hi - c) >> shift) == bin;
-            });
+            };
+            gather_from(linear ? least_of(bin) : NONE, in_bin);
             if (members <= CAP) break;
+            // too many: split the bin by c
+            u64 cmin = ~0ull, cmax = 0;
+            for_all([&](float x, int i) {
+                if (in_bin(x, i)) cmin = min64(cmin, c_of(x, i)), cmax = max64(cmax, c_of(x, i));
+            });
+            cmin = block_reduce(cmin, 0, min64), cmax = block_reduce(cmax, 1, max64);
+            exchange(cmin, cmax, 0);
+            for (int b = 0; b < CS; ++b) cmin = min64(cmin, s.push[turn][0][b]), cmax = max64(cmax, s.push[turn][1][b]);
             lo = cmin, hi = cmax, linear = false;
             const int bits = 64 - __clzll(static_cast<long long>(hi - lo));
             shift = max(0, bits - 10);
             fill(true, true);
+            bin = find_bin(reached);
         }
-        collect();
-        u64 cut = ~0ull, kept = 0;
-        if (tid < members) {
-            const u64 c = all_c[tid];
-            u64 before = above_m, place = above_n;
-            for (unsigned j = 0; j < members; ++j)
-                if (all_c[j] > c) before += all_w[j], ++place;
-            if (!reached(place, before)) cut = c, kept = all_w[tid];  // rank < k, or mass before < reach
-        }
-        cut = block_reduce(cut, 0, min64), kept = block_reduce(kept, 1, add64);
-        *mass = above_m + kept;
-        return cut;
+        const u64 c = collect();
+        const u64 w = tid < members ? mass_of(e_of(x_at(c), top, rate)) : 0;
+        u64 unused;
+        const u64 until = block_scan(w, &unused);
+        const bool keep = tid < members && !reached(above_n + tid, above_m + until - w);  // rank < k, or mass before < reach
+        *mass = above_m + block_reduce(keep ? w : 0, 1, add64);
+        return block_reduce(keep ? c : ~0ull, 0, min64);
     };
 
     u64 cut = 0, kept_mass = 0;
     if (k < N) {
         auto reached = [&](u64 qc, u64) { return qc >= static_cast<u64>(k); };
-        const bool few = k <= CAP / 2;
-        fill(true, !few);
-        if (few) {
-            const int bin = find_bin(reached);
-            gather([&](float x, int) { return bin_of(x, top, rate) <= bin; });
+        if (k <= CAP) {
+            for (int b = tid; b < BINS; b += ST) s.lo[b] = s.hi[b] = s.count[b] = 0;
+            __syncthreads();
+            if (tid < vecs) atomicAdd(&s.count[bin_of(largest, top, rate)], 1u);
+            __syncthreads();
+            gather_from(least_of(find_bin(reached)), [](float, int) { return true; });
             if (members <= CAP) {
                 draw_from_list(0);
                 return;
             }
             above_n = above_m = 0;
-            fill(true, true);
         }
-        cut = cut_of(reached, &kept_mass);
+        fill(true, true);
+        cut = cut_of(find_bin(reached), reached, &kept_mass);
     }
     if (top_p < 1.f) {
         above_n = above_m = 0, linear = true;
         fill(false, true);
-        double reach = 0.0;
-        bool known = k < N;
-        if (known) reach = static_cast<double>(top_p) * static_cast<double>(kept_mass);
+        // (the whole mass is known from the first level of the search on)
         auto reached = [&](u64, u64 qm) {
-            // (the whole mass is known from the first level of the first search on)
-            return static_cast<double>(qm) >= (known ? reach : static_cast<double>(top_p) * static_cast<double>(all));
+            return static_cast<double>(qm) >= static_cast<double>(top_p) * static_cast<double>(k < N ? kept_mass : all);
         };
+        const int bin = find_bin(reached);
+        // a token of the bins up to this one weighs at least so much (with a margin for the roundings)
+        const u64 least = mass_of(expf(-(bin + 1) / BIN_RATE) * 0.999f);
+        if (k == N && (above_m + within_m) / 4 < least * (CAP / 4)) {
+            gather_from(least_of(bin), [](float, int) { return true; });
+            if (members <= CAP) {
+                draw_from_list(all);
+                return;
+            }
+        }
         u64 unused;
-        cut = max64(cut, cut_of(reached, &unused));
+        cut = max64(cut, cut_of(bin, reached, &unused));
     }
 
     // ---- the draw by a pass over the row: each thread owns a contiguous part of the slice (an odd number of pieces: the
@@ -476,15 +532,7 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleArgs a) {
 #pragma unroll
         for (int q = 0; q < V; ++q) own += weight(x[q], i * V + q);
     }
-    const u64 run = warp_scan(own, lane);
-    __syncthreads();
-    if (lane == 31) s.red[2][warp] = run;
-    __syncthreads();
-    u64 mine = 0, start = run - own;
-    for (int w = 0; w < SW; ++w) {
-        if (w < warp) start += s.red[2][w];
-        mine += s.red[2][w];
-    }
+    u64 mine, start = block_scan(own, &mine) - own;
     exchange(mine, 0, 0);
     u64 W = 0;
     for (int b = 0; b < CS; ++b) {
