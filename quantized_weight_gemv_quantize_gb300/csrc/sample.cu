@@ -4,7 +4,7 @@
 // the result is the same on every run and for every split of the work (and the blocks may sum with atomics).  Nothing is
 // sorted.  With c = (key bits of x, reversed index) as one number, the tokens that top-k and top-p keep are those with
 // c >= cut.
-//  - Up to 512 tokens by top-k: the k-th largest of the threads' own largest logits is a bound that at least k tokens reach, and few
+//  - Few tokens by top-k (up to one a thread): the k-th largest of the threads' own largest logits is a bound that at least k tokens reach, and few
 //    more than k do.  Those are gathered and sorted: ranks, masses and the draw come from that list.
 //  - Else a histogram of 1024 bins linear in (max - x) / T (counts for top-k, masses for top-p) tells the bin in which the count or the
 //    mass reaches its bound.  Where the tokens up to that bin are surely few, the list is made of them.  Else the bin's tokens alone are
@@ -20,10 +20,10 @@ namespace qg {
 
 using u64 = unsigned long long;
 
-constexpr int ST = SAMPLE_THREADS, SW = ST / 32;
-constexpr int BINS = 1024, GROUP = 32, GROUPS = BINS / GROUP;
-constexpr int CAP = ST;  // one token a thread
-static_assert( BINS == 2 * ST && GROUPS == 32 && GROUP == 32, "");
+constexpr int ST = SAMPLE_THREADS, SW = ST / 32;  // threads and warps of a block
+constexpr int CAP = ST;                           // tokens of a list: one a thread
+constexpr int BINS = 1024, GROUP = 32;            // 32 groups of 32 bins: a warp's width each
+constexpr int PER = BINS / ST;                    // bins of a thread
 
 // ---- cluster: barrier, and the same shared-memory address in another block
 __device__ __forceinline__ void cluster_sync() {
@@ -52,17 +52,23 @@ __device__ __forceinline__ uint32_t key_of(float x) {
 __device__ __forceinline__ float x_of(uint32_t key) { return __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key); }
 __device__ __forceinline__ u64 place_of(uint32_t key, int i) { return static_cast<u64>(key) << 20 | (0xFFFFFu - i); }
 __device__ __forceinline__ float e_of(float x, float top, float rate) { return expf((x - top) * rate); }
-// floor(2^42 e) for 0 <= e <= 1, from the bits of e: the 24-bit significand shifted by exponent - 108.
+// floor(2^42 e) for 0 <= e <= 1, from the bits of e: the 24-bit significand, as 2^42 for e = 1, shifted down by the exponent.
 __device__ __forceinline__ u64 mass_of(float e) {
     const uint32_t b = __float_as_uint(e);
-    const int shift = static_cast<int>(b >> 23) - 108;
-    const uint32_t sig = (b & 0x7fffffu) | 0x800000u;
-    return shift >= 0 ? static_cast<u64>(sig) << shift : static_cast<u64>(shift > -24 ? sig >> -shift : 0u);
+    const u64 one = static_cast<u64>((b & 0x7fffffu) | 0x800000u) << 19;
+    u64 w;
+    asm("shr.u64 %0, %1, %2;" : "=l"(w) : "l"(one), "r"(127u - (b >> 23)));  // (a shift of 64 or more gives 0)
+    return w;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
 }
 // Monotone in x: 1024 bins over the 30 nats below the largest logit (2^-42 is 29.1), everything further in the last.
 constexpr float BIN_RATE = BINS / 30.0f;
 __device__ __forceinline__ int bin_of(float x, float top, float rate) {
-    return min(BINS - 1, static_cast<int>((top - x) * rate * BIN_RATE));
+    return min(BINS - 1, static_cast<int>((x - top) * rate * -BIN_RATE));  // (the first product is e_of's)
 }
 
 template <int XK>
@@ -92,14 +98,16 @@ __device__ __forceinline__ void widen_all(const uint4& w, float (&x)[16 / sizeof
 
 struct alignas(16) SampleShared {  // the slice follows it in shared memory, written 16 bytes at a time
     uint32_t lo[BINS], hi[BINS], count[BINS];  // masses as two words (hi takes the carries of lo), counts
-    u64 list[CAP];                             // c of the tokens of this block that were gathered
+    u64 list[ST];                             // c of the tokens of this block that were gathered
+    u64 line[2 * ST];                          // two words a thread, for the lists
     u64 group_m[32], group_n[32];
+    u64 found[2][5];                           // by level: which, count and mass before it, mass in it, the whole mass
     u64 got_m[2][8][32], got_n[2][8][32];      // masses and counts of groups of bins, and of a group's bins, from each block
     u64 push[2][4][8];                         // what the blocks tell each other, by kind and block; two sets in turn
-    u64 red[3][SW];
+    u64 red[3][ST / 32];
     unsigned used;
 };
-static_assert(sizeof(SampleShared) % 16 == 0 && sizeof(u64) * ST <= sizeof(uint32_t) * BINS, "");
+static_assert(sizeof(SampleShared) % 16 == 0, "");
 
 template <class T, class Op>
 __device__ __forceinline__ T warp_reduce(T v, Op op) {
@@ -123,7 +131,7 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleArgs a) {
     extern __shared__ __align__(16) uint8_t smem[];
     SampleShared& s = *reinterpret_cast<SampleShared*>(smem);
     uint4* const stage = reinterpret_cast<uint4*>(smem + sizeof(SampleShared));
-    u64* const line = reinterpret_cast<u64*>(s.lo);  // a word a thread, in use when the histogram is not
+    u64* const line = s.line;
     pdl_launch_dependents();
     pdl_wait();
     const int CS = a.blocks, rank = static_cast<int>(blockIdx.x) % CS, row = static_cast<int>(blockIdx.x) / CS;
@@ -214,7 +222,6 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleArgs a) {
 
     // ---- the slice into shared memory, and its largest logit (NaN ranks above everything, as in torch.argmax)
     float largest = NONE;
-    bool nan = false;
     {
         constexpr int U = 5;
         for (int i0 = tid; i0 < vecs; i0 += U * ST) {
@@ -240,11 +247,11 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleArgs a) {
                 float x[V];
                 widen_all<XK>(w[j], x);
 #pragma unroll
-                for (int q = 0; q < V; ++q) largest = fmaxf(largest, x[q]), nan |= x[q] != x[q];
+                for (int q = 0; q < V; ++q) largest = max_nan(largest, x[q]);
             }
         }
     }
-    u64 best = block_reduce(nan ? 0xffffffffull : static_cast<u64>(key_of(largest)), 0, max64);
+    u64 best = block_reduce(largest != largest ? 0xffffffffull : static_cast<u64>(key_of(largest)), 0, max64);
     exchange(best, 0, 0);
     for (int b = 0; b < CS; ++b) best = max64(best, s.push[turn][0][b]);
     const uint32_t top_key = static_cast<uint32_t>(best);
@@ -280,7 +287,7 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleArgs a) {
             const u64 w = mass_of(e_of(x, top, rate));
             const uint32_t w0 = static_cast<uint32_t>(w);
             uint32_t w1 = static_cast<uint32_t>(w >> 32);
-            if (w0) w1 += atomicAdd(&s.lo[b], w0) > ~w0;  // the carry of the lower word
+            w1 += atomicAdd(&s.lo[b], w0) > ~w0;  // the carry of the lower word
             if (w1) atomicAdd(&s.hi[b], w1);
         };
         if (linear) for_all([&](float x, int) { add(bin_of(x, top, rate), x); });
@@ -290,22 +297,22 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleArgs a) {
         });
         __syncthreads();
     };
-    // Adds up all blocks' bins, first in groups of 32, then in the group that reaches the bound; every warp of every block comes
-    // to the same bin.  above_*: before the bin, within_m: in it.  `all` receives the whole mass (first call).
+    // Adds up all blocks' bins, first in groups of 32, then in the group that reaches the bound; every block comes to the same bin.  above_*: before the bin, within_m: in it.  `all` receives the whole mass (first call).
     u64 above_n = 0, above_m = 0, within_m = 0, all = 0;
     auto find_bin = [&](auto&& reached) {
         int group = 0;
-        u64 out_m = 0, out_n = 0;
 #pragma unroll 1
         for (int level = 0; level < 2; ++level) {
             u64 m, c;
             if (level == 0) {
-                // thread t holds bins 2 t and 2 t + 1: a group is 16 threads
-                m = (static_cast<u64>(s.hi[2 * tid]) + s.hi[2 * tid + 1] << 32) + s.lo[2 * tid] + s.lo[2 * tid + 1];
-                c = s.count[2 * tid] + s.count[2 * tid + 1];
+                // a group is 32 / PER threads
+                m = c = 0;
 #pragma unroll
-                for (int o = 8; o; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o), c += __shfl_xor_sync(0xffffffffu, c, o);
-                if (tid % 16 == 0) s.group_m[tid / 16] = m, s.group_n[tid / 16] = c;
+                for (int j = 0; j < PER; ++j)
+                    m += (static_cast<u64>(s.hi[PER * tid + j]) << 32) + s.lo[PER * tid + j], c += s.count[PER * tid + j];
+#pragma unroll
+                for (int o = GROUP / PER / 2; o; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o), c += __shfl_xor_sync(0xffffffffu, c, o);
+                if (tid % (GROUP / PER) == 0) s.group_m[tid / (GROUP / PER)] = m, s.group_n[tid / (GROUP / PER)] = c;
                 __syncthreads();
                 if (tid < 32 * CS) {
                     peer_st64(peer(smem_addr(&s.got_m[0][rank][lane]), warp), s.group_m[lane]);
@@ -318,15 +325,19 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleArgs a) {
                 peer_st64(peer(smem_addr(&s.got_n[1][rank][lane]), warp), c);
             }
             sync_all();
-            m = c = 0;
-            for (int b = 0; b < CS; ++b) m += s.got_m[level][b][lane], c += s.got_n[level][b][lane];
-            const u64 sm = warp_scan(m, lane), sc = warp_scan(c, lane);
-            if (level == 0 && linear) all = __shfl_sync(0xffffffffu, sm, 31);
-            const unsigned hit = __ballot_sync(0xffffffffu, reached(above_n + sc, above_m + sm));
-            const int l = hit ? __ffs(hit) - 1 : 31;
-            out_m = __shfl_sync(0xffffffffu, sm - m, l), out_n = __shfl_sync(0xffffffffu, sc - c, l);
-            within_m = __shfl_sync(0xffffffffu, m, l);
-            above_m += out_m, above_n += out_n;
+            if (warp == 0) {
+                m = c = 0;
+                for (int b = 0; b < CS; ++b) m += s.got_m[level][b][lane], c += s.got_n[level][b][lane];
+                const u64 sm = warp_scan(m, lane), sc = warp_scan(c, lane);
+                if (level == 0 && linear) all = __shfl_sync(0xffffffffu, sm, 31);
+                const unsigned hit = __ballot_sync(0xffffffffu, reached(above_n + sc, above_m + sm));
+                const int l = hit ? __ffs(hit) - 1 : 31;
+                if (lane == l) s.found[level][0] = l, s.found[level][1] = above_n + sc - c, s.found[level][2] = above_m + sm - m, s.found[level][3] = m;
+                if (lane == 0) s.found[level][4] = all;
+            }
+            __syncthreads();
+            const int l = static_cast<int>(s.found[level][0]);
+            above_n = s.found[level][1], above_m = s.found[level][2], within_m = s.found[level][3], all = s.found[level][4];
             group = level == 0 ? l : group * GROUP + l;
         }
         return group;
@@ -346,22 +357,26 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleArgs a) {
         members = 0;
         for (int b = 0; b < CS; ++b) members += static_cast<unsigned>(s.push[turn][0][b]);
     };
-    // Logits of the bins up to `bin` are at least this (bin_of has three roundings, this two more: the margins are wider).
-    auto least_of = [&](int bin) {
-        const float x = top - (bin + 1) / (rate * BIN_RATE) * 1.000001f;
-        return bin >= BINS - 1 ? NONE : x - (fabsf(x) + fabsf(top)) * 4e-7f;
+    // Logits of the bins up to `bin` are at least least_of, those of the bins from `bin` on at most most_of (bin_of has three
+    // roundings, these two more: the margins are wider).
+    const float INF = __int_as_float(0x7f800000);
+    auto edge = [&](float bins, float margin) {
+        const float x = top - bins / (rate * BIN_RATE) * (1.f + margin);
+        return x - (fabsf(x) + fabsf(top)) * (0.4f * margin);
     };
-    // the tokens from `least` on that take(x, i) wants
-    auto gather_from = [&](float least, auto&& take) {
+    auto least_of = [&](int bin) { return bin >= BINS - 1 ? NONE : edge(static_cast<float>(bin + 1), 1e-6f); };
+    auto most_of = [&](int bin) { return bin == 0 ? INF : edge(static_cast<float>(bin), -1e-6f); };
+    // the tokens from `least` to `most` that take(x, i) wants
+    auto gather_range = [&](float least, float most, auto&& take) {
         gather([&] {
             for_pieces([&](const float (&x)[V], int i) {
-                float m = x[0];
+                bool any = false;
 #pragma unroll
-                for (int q = 1; q < V; ++q) m = fmaxf(m, x[q]);
-                if (m < least) return;
+                for (int q = 0; q < V; ++q) any |= x[q] >= least && x[q] <= most;
+                if (!any) return;
 #pragma unroll
                 for (int q = 0; q < V; ++q)
-                    if (x[q] >= least && take(x[q], i * V + q)) put(x[q], i * V + q);
+                    if (x[q] >= least && x[q] <= most && take(x[q], i * V + q)) put(x[q], i * V + q);
             });
         });
     };
@@ -369,21 +384,25 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleArgs a) {
     auto sorted = [&](u64 v, unsigned count) {  // descending, over the first threads; a bitonic network
         int width = 1;
         while (static_cast<unsigned>(width) < count) width <<= 1;
+        const bool in = warp * 32 < width;  // (the other warps would only take turns from these)
+        auto turn_with = [&](u64 o, int j, int size) {
+            const bool larger = ((tid & j) == 0) == ((tid & size) == 0);
+            v = (v > o) == larger ? v : o;
+        };
 #pragma unroll 1
-        for (int size = 2; size <= width; size <<= 1)
+        for (int size = 2; size <= width; size <<= 1) {
 #pragma unroll 1
-            for (int j = size >> 1; j; j >>= 1) {
-                u64 o;
-                if (j >= 32) {
-                    __syncthreads();
-                    line[tid] = v;
-                    __syncthreads();
-                    o = line[tid ^ j];
-                } else {
-                    o = __shfl_xor_sync(0xffffffffu, v, j);
-                }
-                v = ((tid & j) == 0) == ((tid & size) == 0) ? max64(v, o) : min64(v, o);
+            for (int j = size >> 1; j >= 32; j >>= 1) {
+                __syncthreads();
+                if (in) line[tid] = v;
+                __syncthreads();
+                if (in) turn_with(line[tid ^ j], j, size);
             }
+            if (!in) continue;
+#pragma unroll
+            for (int j = 16; j; j >>= 1)
+                if (j < size) turn_with(__shfl_xor_sync(0xffffffffu, v, j), j, size);
+        }
         return v;
     };
     auto collect = [&] {
@@ -422,17 +441,39 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleArgs a) {
             const u64 before = block_scan(tid < k ? w : 0, &among) - w;  // (of use where tid < k)
             bool keep = tid < members && tid < k && e >= min_p;
             if (top_p < 1.f) keep = keep && static_cast<double>(before) < static_cast<double>(top_p) * static_cast<double>(of ? of : among);
-            // in index order: the lower bits of c fall as the index grows
-            const u64 next = sorted(keep ? 1ull << 62 | (c & 0xFFFFFu) << 32 | static_cast<unsigned>(tid) : 0, members);
-            __syncthreads();
-            line[tid] = c;
-            __syncthreads();
-            const bool kept = next != 0;
-            const u64 its = kept ? line[next & (ST - 1)] : 0;
-            const float its_e = e_of(x_at(its), top, rate);
-            const u64 its_w = kept ? mass_of(its_e) : 0;
-            u64 W;
-            const u64 until = block_scan(its_w, &W);
+            // in index order (the lower bits of c fall as the index grows): a short list by comparing each token with all, with as many
+            // threads a token as there are; a long one by sorting once more
+            u64 W, until, its = c, its_w = keep ? w : 0;
+            float its_e = e;
+            if (members <= 128) {
+                __syncthreads();
+                line[tid] = c, line[ST + tid] = its_w;
+                __syncthreads();
+                int bits = 2;
+                while (members << (bits + 1) <= ST && bits < 5) ++bits;
+                const int which = tid >> bits, part = tid & ((1 << bits) - 1);
+                its = line[which], its_w = line[ST + which], its_e = e_of(x_at(its), top, rate);
+                u64 sum = 0, upto = 0;
+#pragma unroll 4
+                for (int j = part; j < static_cast<int>(members); j += 1 << bits) {
+                    const u64 v = line[ST + j];
+                    sum += v;
+                    if ((line[j] & 0xFFFFFu) >= (its & 0xFFFFFu)) upto += v;
+                }
+                for (int o = 1 << bits >> 1; o; o >>= 1)
+                    sum += __shfl_xor_sync(0xffffffffu, sum, o), upto += __shfl_xor_sync(0xffffffffu, upto, o);
+                W = sum, until = upto;
+                if (which >= static_cast<int>(members) || part) until = 0;  // (one thread a token tells)
+            } else {
+                const u64 next = sorted(keep ? 1ull << 62 | (c & 0xFFFFFu) << 32 | static_cast<unsigned>(tid) : 0, members);
+                __syncthreads();
+                line[tid] = c;
+                __syncthreads();
+                its = next ? line[next & (ST - 1)] : 0;
+                its_e = e_of(x_at(its), top, rate);
+                its_w = next ? mass_of(its_e) : 0;
+                until = block_scan(its_w, &W);
+            }
             u64 target = static_cast<u64>(static_cast<double>(u) * static_cast<double>(W));
             if (target >= W) target = W - 1;
             if (until > target && until - its_w <= target) {
@@ -442,15 +483,23 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleArgs a) {
         }
         sync_all();  // no block ends while its list is read
     };
-    // The smallest c that a filter keeps, from the histogram's bin on; *mass: the sum of w over c >= cut.
-    auto cut_of = [&](int bin, auto&& reached, u64* mass) {
+    // The smallest c that a filter keeps, from the histogram's bin on; *mass: the sum of w over c >= cut, *own: of this block's.
+    auto cut_of = [&](int bin, auto&& reached, u64* mass, u64* own) {
+        auto own_above = [&] {  // this block's mass in the bins before
+            u64 m = 0;
+#pragma unroll
+            for (int j = 0; j < PER; ++j)
+                if (PER * tid + j < bin) m += (static_cast<u64>(s.hi[PER * tid + j]) << 32) + s.lo[PER * tid + j];
+            return block_reduce(m, 0, add64);
+        };
+        *own = own_above();
         for (;;) {
             auto in_bin = [&](float x, int i) {
                 if (linear) return bin_of(x, top, rate) == bin;
                 const u64 c = c_of(x, i);
                 return c >= lo && c <= hi && static_cast<int>((hi - c) >> shift) == bin;
             };
-            gather_from(linear ? least_of(bin) : NONE, in_bin);
+            gather_range(linear ? least_of(bin) : NONE, linear ? most_of(bin) : INF, in_bin);
             if (members <= CAP) break;
             // too many: split the bin by c
             u64 cmin = ~0ull, cmax = 0;
@@ -465,17 +514,28 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleArgs a) {
             shift = max(0, bits - 10);
             fill(true, true);
             bin = find_bin(reached);
+            *own += own_above();
         }
-        const u64 c = collect();
-        const u64 w = tid < members ? mass_of(e_of(x_at(c), top, rate)) : 0;
-        u64 unused;
-        const u64 until = block_scan(w, &unused);
-        const bool keep = tid < members && !reached(above_n + tid, above_m + until - w);  // rank < k, or mass before < reach
-        *mass = above_m + block_reduce(keep ? w : 0, 1, add64);
-        return block_reduce(keep ? c : ~0ull, 0, min64);
+        // the first block decides on the list, and tells the others the cut and the mass
+        u64 cut = 0, kept = 0;
+        if (rank == 0) {
+            const u64 c = collect();
+            const u64 w = tid < members ? mass_of(e_of(x_at(c), top, rate)) : 0;
+            u64 unused;
+            const u64 until = block_scan(w, &unused);
+            const bool keep = tid < members && !reached(above_n + tid, above_m + until - w);  // rank < k, or mass before < reach
+            kept = above_m + block_reduce(keep ? w : 0, 1, add64);
+            cut = block_reduce(keep ? c : ~0ull, 0, min64);
+        }
+        const unsigned listed = min(s.used, static_cast<unsigned>(CAP));
+        exchange(cut, kept, 0);
+        cut = s.push[turn][0][0], *mass = s.push[turn][1][0];
+        const u64 c = tid < listed ? s.list[tid] : 0;
+        *own += block_reduce(c >= cut ? mass_of(e_of(x_at(c), top, rate)) : 0, 0, add64);
+        return cut;
     };
 
-    u64 cut = 0, kept_mass = 0;
+    u64 cut = 0, kept_mass = 0, own_mass = 0;
     if (k < N) {
         auto reached = [&](u64 qc, u64) { return qc >= static_cast<u64>(k); };
         if (k <= CAP) {
@@ -483,7 +543,7 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleArgs a) {
             __syncthreads();
             if (tid < vecs) atomicAdd(&s.count[bin_of(largest, top, rate)], 1u);
             __syncthreads();
-            gather_from(least_of(find_bin(reached)), [](float, int) { return true; });
+            gather_range(least_of(find_bin(reached)), INF, [](float, int) { return true; });
             if (members <= CAP) {
                 draw_from_list(0);
                 return;
@@ -491,11 +551,12 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleArgs a) {
             above_n = above_m = 0;
         }
         fill(true, true);
-        cut = cut_of(find_bin(reached), reached, &kept_mass);
+        cut = cut_of(find_bin(reached), reached, &kept_mass, &own_mass);
     }
     if (top_p < 1.f) {
-        above_n = above_m = 0, linear = true;
-        fill(false, true);
+        // (top-k's histogram still holds unless it was split)
+        above_n = above_m = 0;
+        if (k == N || !linear) linear = true, fill(false, true);
         // (the whole mass is known from the first level of the search on)
         auto reached = [&](u64, u64 qm) {
             return static_cast<double>(qm) >= static_cast<double>(top_p) * static_cast<double>(k < N ? kept_mass : all);
@@ -504,43 +565,52 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleArgs a) {
         // a token of the bins up to this one weighs at least so much (with a margin for the roundings)
         const u64 least = mass_of(expf(-(bin + 1) / BIN_RATE) * 0.999f);
         if (k == N && (above_m + within_m) / 4 < least * (CAP / 4)) {
-            gather_from(least_of(bin), [](float, int) { return true; });
+            gather_range(least_of(bin), INF, [](float, int) { return true; });
             if (members <= CAP) {
                 draw_from_list(all);
                 return;
             }
         }
-        u64 unused;
-        cut = max64(cut, cut_of(bin, reached, &unused));
+        u64 mass, own;
+        const u64 c = cut_of(bin, reached, &mass, &own);
+        if (c >= cut) cut = c, own_mass = own;
     }
 
     // ---- the draw by a pass over the row: each thread owns a contiguous part of the slice (an odd number of pieces: the
-    // threads of a quarter warp then read different banks)
+    // threads of a quarter warp then read different banks).  With a cut and no min-p the blocks' masses are known, and only the block
+    // that holds the target makes the pass.
     const int own_vecs = (vecs + ST - 1) / ST | 1, v0 = min(vecs, tid * own_vecs), v1 = min(vecs, v0 + own_vecs);
     const uint32_t cut_key = static_cast<uint32_t>(cut >> 20);
     auto weight = [&](float x, int i) -> u64 {
         const uint32_t key = key_of(x);
-        if (key < cut_key || place_of(key, first + i) < cut) return 0;
         const float e = e_of(x, top, rate);
-        return e >= min_p ? mass_of(e) : 0;
+        const bool in = (key > cut_key || (key == cut_key && place_of(key, first + i) >= cut)) && e >= min_p;
+        return in ? mass_of(e) : 0;
     };
-    u64 own = 0;
+    u64 own = 0, mine = own_mass, start = 0;
+    auto pass = [&] {
 #pragma unroll 2
-    for (int i = v0; i < v1; ++i) {
-        float x[V];
-        piece(i, x);
+        for (int i = v0; i < v1; ++i) {
+            float x[V];
+            piece(i, x);
 #pragma unroll
-        for (int q = 0; q < V; ++q) own += weight(x[q], i * V + q);
-    }
-    u64 mine, start = block_scan(own, &mine) - own;
+            for (int q = 0; q < V; ++q) own += weight(x[q], i * V + q);
+        }
+        start = block_scan(own, &mine) - own;
+    };
+    const bool known = cut != 0 && !(min_p > 0.f);
+    if (!known) pass();
     exchange(mine, 0, 0);
-    u64 W = 0;
+    u64 W = 0, block_start = 0;
     for (int b = 0; b < CS; ++b) {
-        if (b < rank) start += s.push[turn][0][b];
+        if (b < rank) block_start += s.push[turn][0][b];
         W += s.push[turn][0][b];
     }
     u64 target = static_cast<u64>(static_cast<double>(u) * static_cast<double>(W));
     if (target >= W) target = W - 1;
+    if (target < block_start || target >= block_start + mine) return;
+    if (known) pass();
+    start += block_start;
     // the thread whose part holds the target; its warp shares the part
     const unsigned holds = __ballot_sync(0xffffffffu, start <= target && target < start + own);
     if (!holds) return;

@@ -89,8 +89,8 @@ struct SampleArgs {
     int staged;  // the slice is kept in shared memory
 };
 
-constexpr int SAMPLE_THREADS = 512;
-unsigned sample_smem_base();  // shared memory beside the slice
+constexpr int SAMPLE_THREADS = 512;  // (1024: one row 16.4 -> 20.5 us, 320 rows 224 -> 306 us)
+unsigned sample_smem_base();         // shared memory beside the slice
 const void* sample_kernel_ptr(int kind);
 
 }  // namespace qg
