@@ -26,6 +26,7 @@ struct RopeArgs {
     float mscale;
 };
 
+constexpr int ROPE_THREADS = 64;
 // vec: heads are handled in 8-element pieces (the rotated part splits into whole pieces); half: the pairing.
 const void* rope_kernel_ptr(int x_kind, bool half, bool vec);
 

@@ -155,12 +155,12 @@ static int run_rope(const qgemv_rope_args* a, unsigned flags, void* stream) {
     // Blocks of a token: as many as its pieces fill once, until the tokens alone fill the GPU.
     const int w = vec ? 8 : 1;
     const long long per_token = static_cast<long long>(a->heads + 2 * a->kv_heads) * a->dim / w;
-    long long y = (per_token + 127) / 128;
-    const long long enough = (16ll * sms + T - 1) / T;
+    long long y = (per_token + ROPE_THREADS - 1) / ROPE_THREADS;
+    const long long enough = (32ll * sms + T - 1) / T;
     if (y > enough) y = enough;
     const bool pdl = (flags & QGEMV_FLAG_PDL) != 0;
     cudaError_t e = launch_step(rope_kernel_ptr(a->x_kind, half, vec), dim3(static_cast<unsigned>(T), static_cast<unsigned>(y)),
-                                128, 0, 1, pdl, static_cast<cudaStream_t>(stream), r);
+                                ROPE_THREADS, 0, 1, pdl, static_cast<cudaStream_t>(stream), r);
     if (e != cudaSuccess) return api_cuda_fail(e);
     api_route(QGEMV_ROUTE_ROPE, pdl);
     return QGEMV_OK;
