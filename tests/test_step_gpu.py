@@ -262,6 +262,50 @@ def test_attention(case, mask):
     assert int(s.scratch[:qg.QGEMV_ATTN_SCRATCH_HEAD].sum()) == 0
 
 
+@pytest.mark.parametrize("case", ["few tiles", "more tiles than blocks", "idle", "long heads", "no context"])
+def test_attention_many_sequences(case):
+    """The division of the work over one wave of blocks: more sequences than a warp's 32, with and without rows, idle ones, more row
+    tiles than blocks (a block then has the end of one, whole ones and the start of another)."""
+    rng = np.random.default_rng(99)
+    if case == "few tiles":
+        new, ctx, H, KH, D = [1] * 40, rng.integers(1, 900, 40).tolist(), 4, 2, 64
+    elif case == "more tiles than blocks":
+        new, ctx, H, KH, D = rng.integers(0, 6, 90).tolist(), rng.integers(5, 700, 90).tolist(), 8, 8, 64
+    elif case == "idle":
+        new, ctx, H, KH, D = [1] * 70, [0] * 33 + [100] + [0] * 35 + [1], 8, 2, 64
+    elif case == "long heads":
+        new, ctx, H, KH, D = [3, 0, 50, 1], [2000, 10, 60, 1], 4, 2, 192
+    else:
+        new, ctx, H, KH, D = [150, 33, 2], [0, 20, 0], 4, 1, 64  # the 128-row kernel, row tiles that see nothing
+    s = Step(40, new, ctx, H, KH, D, 16, B16)
+    for mask in (dict(), dict(window=64)):
+        qg.qgemv_attn(s.args(**mask))
+        s.check(**mask)
+        first = s.out.clone()
+        qg.qgemv_attn(s.args(**mask))
+        assert torch.equal(first, s.out)
+        assert int(s.scratch[:qg.QGEMV_ATTN_SCRATCH_HEAD].sum()) == 0
+
+
+@pytest.mark.parametrize("flags", [0, qg.QGEMV_FLAG_PDL])
+def test_attention_of_a_chunk_in_a_graph(flags):
+    s = Step(41, [200], [5000], 4, 1, 128, 64, B16)  # parts, joined by the second kernel
+    a = s.args()
+    qg.qgemv_route_reset()
+    qg.qgemv_attn(a)
+    assert qg.qgemv_route_counts()[qg.ROUTE_ATTN_TILES] == 1
+    s.check()
+    want = (s.out.clone(), s.lse.clone())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for _ in range(3):
+            qg.qgemv_attn(a, flags)
+    s.out.fill_(0), s.lse.fill_(0)
+    g.replay(), g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(s.out, want[0]) and torch.equal(s.lse, want[1])
+
+
 @pytest.mark.parametrize("new,ctx", [([1], [3000]), ([4, 200], [900, 700])])
 def test_attention_orders_and_strides(new, ctx):
     s = Step(21, new, ctx, 8, 2, 128, 16, B16, order="head-token")
@@ -421,6 +465,19 @@ def test_sampling(m, n, dtype):
     run_sample(x, T=np.full(m, 0.7), p=rng.uniform(0.2, 0.999, m), u=u)
     run_sample(x, mp=rng.uniform(0.0, 0.3, m), u=u)
     run_sample(x, T=rng.uniform(0.3, 2.0, m), k=rng.integers(1, 2 * n, m), p=rng.uniform(0.5, 1.1, m), mp=rng.uniform(0.0, 0.01, m), u=u)
+
+
+@pytest.mark.parametrize("dtype", [B16, torch.float32])
+def test_sampling_many_rows(dtype):
+    # more rows than fill the GPU with short slices
+    rng = np.random.default_rng(12)
+    m, n = 90, 151936
+    x = rnd(rng, (m, n), dtype, 2.0)
+    x[::7, rng.integers(0, n, 100000)] = -float("inf")
+    u = rng.random(m, dtype=np.float32)
+    a = run_sample(x, T=rng.uniform(0.5, 1.5, m), k=rng.choice([0, 1, 40, 512, 513, 3000], m), p=rng.choice([0.5, 0.95, 1.0], m), u=u)
+    b = run_sample(x, T=rng.uniform(0.5, 1.5, m), p=np.full(m, 0.9), mp=rng.choice([0.0, 0.01], m), u=u)
+    assert a[0].shape == b[0].shape == (m,)
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, B16, H16])
