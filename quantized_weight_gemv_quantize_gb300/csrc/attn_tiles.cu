@@ -7,7 +7,15 @@
 // true one has grown by more than 2^8: then O_i and l are rescaled; p stays below 2^8, so nothing is lost by the delay.
 // The keys of a tile lie on pages anywhere: four warps look the rows up and copy them 16 bytes at a time into the
 // 128-byte-swizzled layout that the tensor cores read (K as the K-major, V as the MN-major operand: no transpose is made).
-// 4 D flops a pair of row and key against one exponential: at D = 128 the tensor cores bound it.
+// A key tile whose keys are all there comes by tensor-map copies, one a page (or 128 tokens) and 64 columns.
+//
+// Work a pair of row tiles and a key tile at D = 128: 2048 cycles of the tensor cores, 1024 of the exponential units; measured about 2900, the
+// time of one row tile's round: softmax 1250, its products 1024, some 600 of barriers and of the products' latency.  Only two row
+// tiles fit tensor memory (2 x (128 scores + 128 sums) = 512 columns), so that no third round hides those.  A chunk of 2000 tokens over
+// 24000 (32 and 8 heads): 620 us, 1.21 PFLOP/s; two prompts of 6000: 434 us, 1.22 PFLOP/s; tensor pipe active 64% (cuBLAS bf16: 1.72 sustained).
+// What the steps gave, for the chunk: 1302 us with one softmax thread a row, row-by-row copies and a wait for each of them; 1062 with
+// copies that announce themselves; 777 with tensor-map copies, two threads a row and exponentials ahead of the maximum; 694 with a
+// warp that waits in the issuing warp's place; 623 with parts by cost and a kernel that joins them.
 #include "attn.cuh"
 
 namespace qg {
