@@ -364,6 +364,10 @@ QGEMV_API int qgemv_plan_info_chunk(int fmt, int m, int N, int Kc, int num_sms, 
  * 1 = whenever they fit, 2 = never.  Rows are bit-identical either way. */
 QGEMV_API void qgemv_tune_pairs(int mode);
 
+/* Tuning hook: qgemv_attn's kernel, 0 = planner decides, 1 = the 16-row kernel, 2 = the 128-row kernel (heads of up to 128).  It
+ * also decides what qgemv_attn_scratch_bytes says. */
+QGEMV_API void qgemv_tune_attn(int kernel);
+
 QGEMV_API void qgemv_tune_override(int ctas_per_sm, int lanes_log2, int rows_per_tile, int stages,
                                    int kernel_build);
 

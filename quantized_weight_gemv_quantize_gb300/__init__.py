@@ -144,6 +144,8 @@ def lib():
         L.qgemv_rope.restype = i32
         L.qgemv_attn.argtypes = [ctypes.POINTER(QgemvAttnArgs), ctypes.c_uint, vp]
         L.qgemv_attn.restype = i32
+        L.qgemv_tune_attn.argtypes = [i32]
+        L.qgemv_tune_attn.restype = None
         L.qgemv_attn_scratch_bytes.argtypes = [i32] * 7
         L.qgemv_attn_scratch_bytes.restype = sz
         L.qgemv_sample.argtypes = [i32, vp, ctypes.c_longlong, i32, i32, vp, vp, vp, vp, vp, vp, vp, ctypes.c_uint, vp]
@@ -505,6 +507,11 @@ def qgemv_plan_info_chunk(fmt, m: int, N: int, Kc: int, num_sms: int = 152, ctas
 def qgemv_tune_pairs(mode: int = 0) -> None:
     """Tuning only: row pairs 0 = planner decides, 1 = whenever they fit, 2 = never."""
     lib().qgemv_tune_pairs(mode)
+
+
+def qgemv_tune_attn(kernel: int = 0) -> None:
+    """Tuning only: attention's kernel 0 = planner decides, 1 = the 16-row kernel, 2 = the 128-row kernel."""
+    lib().qgemv_tune_attn(kernel)
 
 
 def qgemv_tune_override(ctas_per_sm: int = 0, lanes_log2: int = -1, rows_per_tile: int = 0, stages: int = 0,

@@ -1,6 +1,7 @@
 // C ABI of the operators between the GEMVs: rotary positions, attention over the paged cache, sampling.  Every check
 // runs on the host before anything is enqueued.
 #include <cuda.h>
+#include <atomic>
 #include <limits.h>
 #include <math.h>
 #include <mutex>
@@ -168,6 +169,8 @@ static int run_rope(const qgemv_rope_args* a, unsigned flags, void* stream) {
 
 // ---------------------------------------------------------------------------------------------------- attention
 
+static std::atomic<int> g_attn_kernel{0};
+
 static size_t round16(size_t n) { return (n + 15) / 16 * 16; }
 
 static int attn_plan(int seqs, int tokens, int heads, int kv_heads, int dim, int max_q, int max_kv, AttnPlan* p) {
@@ -182,8 +185,24 @@ static int attn_plan(int seqs, int tokens, int heads, int kv_heads, int dim, int
     if (max_q > tokens) max_q = tokens;
     const long long rows = static_cast<long long>(max_q) * (heads / kv_heads);
     if (max_kv > 1 << 30 || (rows + 15) / 16 * kv_heads > INT_MAX || rows > INT_MAX) return QGEMV_ERR_UNSUPPORTED;
-    // More than 32 rows go to the 128-row kernel (heads of up to 128).
-    p->tiles = rows > 32 && dim <= 128;
+    // The 128-row kernel: 256 rows a block, one block an SM, the row tiles' contexts in parts.  The time of a launch in key tiles: waves of
+    // blocks, each as long as its part, with about 3 key tiles for its start and end, and 4 more where parts have to be written out and
+    // joined.  At most 32 parts of at least 8 key tiles, and no more than 16 waves of them.
+    const long long tiles = (rows + 255) / 256 * kv_heads * seqs, blocks = (static_cast<long long>(max_kv) + 127) / 128;
+    long long best = 1, best_cost = LLONG_MAX;
+    for (long long n = 1; n <= 32 && (n == 1 || (n * 8 <= blocks && tiles * n <= 16 * SMS)); ++n) {
+        const long long cost = (tiles * n + SMS - 1) / SMS * ((blocks + n - 1) / n + 3 + (n > 1 ? 4 : 0));
+        if (cost < best_cost) best = n, best_cost = cost;
+    }
+    // Which kernel, for more than 32 rows (and heads of up to 128, which the 128-row kernel is built for): by what both would take, in us.  The
+    // 16-row kernel goes over the keys once for 16 rows, 19 row tiles and keys a ns; over sequences of uneven length its time is their sum's, the
+    // other's the longest's.  Measured, 8 key/value heads, 16-row against 128-row kernel in us: 64 rows over 4000 keys 18.4 / 26.6, 128 rows 24.6 / 28.4,
+    // 256 rows 38.9 / 33.0; over 50000 keys 32 rows 51.2 / 52.4, 64 rows 84.5 / 53.7; 16 sequences of up to 8000: 32 rows 63.5 / 93.8, 48 rows
+    // 78.7 / 94.0, 64 rows 139 / 94; 4 sequences of 300 with 64 rows 10.6 / 14.4; 64 tokens alone 8.2 / 18.5.
+    const double keys16 = static_cast<double>((rows + 15) / 16) * kv_heads * seqs * max_kv;
+    const double rows_us = 8 + keys16 / 19000 * (seqs > 1 ? 0.75 : 1.0), tiles_us = 11 + 1.3 * static_cast<double>(best_cost);
+    const int forced = g_attn_kernel.load(std::memory_order_relaxed);
+    p->tiles = dim <= 128 && (forced ? forced == 2 : rows > 32 && tiles_us < rows_us);
     size_t records = 0;
     if (!p->tiles) {
         // One wave of blocks, two an SM (one with the larger shared memory of long heads); each has records of 16 rows for two
@@ -191,24 +210,14 @@ static int attn_plan(int seqs, int tokens, int heads, int kv_heads, int dim, int
         p->grid = dim <= 128 ? 2 * SMS : SMS;
         records = static_cast<size_t>(p->grid) * 2 * 16;
         // Units of 64 keys, longer ones where the bounds alone would let the whole (twice over, for its rounding) pass 32 bits.
-        const double tiles = static_cast<double>((rows + 15) / 16) * kv_heads * seqs;
+        const double row_tiles = static_cast<double>((rows + 15) / 16) * kv_heads * seqs;
         p->unit_shift = 6;
-        while (p->unit_shift < 30 && tiles * (static_cast<double>(max_kv >> p->unit_shift) + 1) > 1e9) ++p->unit_shift;
-        if (tiles > 1e9) return QGEMV_ERR_UNSUPPORTED;
+        while (p->unit_shift < 30 && row_tiles * (static_cast<double>(max_kv >> p->unit_shift) + 1) > 1e9) ++p->unit_shift;
+        if (row_tiles > 1e9) return QGEMV_ERR_UNSUPPORTED;
     } else {
-        const long long tiles = (rows + 255) / 256 * kv_heads * seqs;
         if (tiles > INT_MAX) return QGEMV_ERR_UNSUPPORTED;
         p->row_tiles = static_cast<int>((rows + 255) / 256);
         p->rows_part = static_cast<int>(rows < 256 ? rows : 256);
-        // Parts of a row tile's context; one block an SM.  The time of a launch in key tiles: waves of blocks, each as long as its
-        // part, with about 3 key tiles for its start and end, and 4 more where parts have to be written out and joined (measured:
-        // 1.5 us a key tile).  At most 32 parts of at least 8 key tiles, and no more than 16 waves of them.
-        const long long blocks = (static_cast<long long>(max_kv) + 127) / 128;
-        long long best = 1, best_cost = LLONG_MAX;
-        for (long long n = 1; n <= 32 && (n == 1 || (n * 8 <= blocks && tiles * n <= 16 * SMS)); ++n) {
-            const long long cost = (tiles * n + SMS - 1) / SMS * ((blocks + n - 1) / n + 3 + (n > 1 ? 4 : 0));
-            if (cost < best_cost) best = n, best_cost = cost;
-        }
         const long long chunk = ((max_kv + best - 1) / best + 127) / 128 * 128;
         p->chunk = static_cast<int>(chunk < 128 ? 128 : chunk > INT_MAX - 127 ? INT_MAX - 127 : chunk);
         p->parts = max_kv > 0 ? static_cast<int>((static_cast<long long>(max_kv) + p->chunk - 1) / p->chunk) : 1;
@@ -482,6 +491,8 @@ int qgemv_rope(const qgemv_rope_args* args, unsigned flags, void* stream) {
     if (api_injected(&st)) return st;
     return run_rope(args, flags, stream);
 }
+
+void qgemv_tune_attn(int kernel) { g_attn_kernel.store(kernel == 1 || kernel == 2 ? kernel : 0); }
 
 size_t qgemv_attn_scratch_bytes(int seqs, int tokens, int heads, int kv_heads, int dim, int max_q, int max_kv) {
     AttnPlan p;

@@ -33,6 +33,14 @@ def _lib():
     assert qg.qgemv_device_error() == 0
 
 
+@pytest.fixture(params=["16-row", "128-row"])
+def kernel(request):
+    """Attention by one kernel or the other, whatever the planner would take (heads beyond 128 go to the first)."""
+    qg.qgemv_tune_attn(1 if request.param == "16-row" else 2)
+    yield request.param
+    qg.qgemv_tune_attn(0)
+
+
 def rnd(rng, shape, dtype, scale=1.0):
     return (torch.from_numpy(rng.standard_normal(shape, dtype=np.float32)) * scale).to(dtype).cuda()
 
@@ -254,7 +262,7 @@ ATTN = [
 
 @pytest.mark.parametrize("mask", [dict(), dict(window=100), dict(window=1), dict(causal=False)], ids=str)
 @pytest.mark.parametrize("case", range(len(ATTN)))
-def test_attention(case, mask):
+def test_attention(case, mask, kernel):
     new, ctx, H, KH, D, page, dtype = ATTN[case]
     s = Step(case, new, ctx, H, KH, D, page, dtype)
     qg.qgemv_attn(s.args(**mask))
@@ -263,7 +271,7 @@ def test_attention(case, mask):
 
 
 @pytest.mark.parametrize("case", ["few tiles", "more tiles than blocks", "idle", "long heads", "no context"])
-def test_attention_many_sequences(case):
+def test_attention_many_sequences(case, kernel):
     """The division of the work over one wave of blocks: more sequences than a warp's 32, with and without rows, idle ones, more row
     tiles than blocks (a block then has the end of one, whole ones and the start of another)."""
     rng = np.random.default_rng(99)
@@ -288,8 +296,19 @@ def test_attention_many_sequences(case):
 
 
 @pytest.mark.parametrize("flags", [0, qg.QGEMV_FLAG_PDL])
+def test_attention_takes_the_kernel_that_the_sizes_ask_for(flags):
+    for new, ctx, route in ((1, 9000, qg.ROUTE_ATTN_ROWS), (8, 9000, qg.ROUTE_ATTN_ROWS), (40, 40, qg.ROUTE_ATTN_ROWS), (500, 9000, qg.ROUTE_ATTN_TILES)):
+        s = Step(42, [new], [ctx], 8, 2, 128, 64, B16)
+        a = s.args(lse=False)
+        qg.qgemv_route_reset()
+        qg.qgemv_attn(a, flags)
+        assert qg.qgemv_route_counts()[route] == 1
+        s.check()
+
+
+@pytest.mark.parametrize("flags", [0, qg.QGEMV_FLAG_PDL])
 def test_attention_of_a_chunk_in_a_graph(flags):
-    s = Step(41, [200], [5000], 4, 1, 128, 64, B16)  # parts, joined by the second kernel
+    s = Step(41, [500], [9000], 8, 2, 128, 64, B16)  # parts, joined by the second kernel
     a = s.args()
     qg.qgemv_route_reset()
     qg.qgemv_attn(a)
@@ -307,7 +326,7 @@ def test_attention_of_a_chunk_in_a_graph(flags):
 
 
 @pytest.mark.parametrize("new,ctx", [([1], [3000]), ([4, 200], [900, 700])])
-def test_attention_orders_and_strides(new, ctx):
+def test_attention_orders_and_strides(new, ctx, kernel):
     s = Step(21, new, ctx, 8, 2, 128, 16, B16, order="head-token")
     wide = torch.full((s.q.shape[0], 3, 8, 128 + 8), float("nan"), dtype=B16, device="cuda")
     wide[:, 1, :, :128] = s.q
@@ -317,7 +336,7 @@ def test_attention_orders_and_strides(new, ctx):
 
 
 @pytest.mark.parametrize("new,ctx,loose", [([1, 1], [900, 40], 40000), ([150, 20], [900, 40], 5000)])
-def test_attention_loose_bounds_shared_scratch_and_repeats(new, ctx, loose):
+def test_attention_loose_bounds_shared_scratch_and_repeats(new, ctx, loose, kernel):
     s = Step(22, new, ctx, 8, 2, 128, 16, B16)
     n = max(qg.qgemv_attn_scratch_bytes(2, sum(new), 8, 2, 128, a, b) for a, b in ((max(new), loose), (max(new) + 70, max(ctx))))
     scratch = torch.full((n,), 0x5A, dtype=torch.uint8, device="cuda")  # only the head has to start as zeros
@@ -332,7 +351,7 @@ def test_attention_loose_bounds_shared_scratch_and_repeats(new, ctx, loose):
 
 
 @pytest.mark.parametrize("new", [1, 200])
-def test_attention_large_scores_and_softmax_range(new):
+def test_attention_large_scores_and_softmax_range(new, kernel):
     # scores of hundreds: the running maximum moves far, most probabilities vanish
     s = Step(23, [new], [1500], 8, 2, 128, 16, B16, scale=2.0)
     s.check_args = s.args()
@@ -348,7 +367,7 @@ def test_attention_large_scores_and_softmax_range(new):
     s.check()
 
 
-def test_attention_bad_page_is_masked_and_reported():
+def test_attention_bad_page_is_masked_and_reported(kernel):
     for new in (1, 150):
         s = Step(25, [new], [400], 4, 2, 128, 16, B16)
         s.table[0, 3], s.table[0, 7] = -1, 2 ** 30
@@ -360,7 +379,7 @@ def test_attention_bad_page_is_masked_and_reported():
         s.check(causal=False)
 
 
-def test_attention_tokens_beyond_the_bounds_are_left_alone():
+def test_attention_tokens_beyond_the_bounds_are_left_alone(kernel):
     s = Step(26, [3, 2], [50, 60], 4, 2, 64, 16, B16)
     qg.qgemv_attn(s.args(max_q=2, causal=False))
     assert bool((s.out[2] == 7.0).all()) and bool((s.lse[2] == 7.0).all()) and not bool((s.out[[0, 1, 3, 4]] == 7.0).any())
@@ -373,7 +392,7 @@ def test_attention_tokens_beyond_the_bounds_are_left_alone():
 
 
 @pytest.mark.parametrize("new", [1, 140])
-def test_attention_offsets_past_32_bits(new):
+def test_attention_offsets_past_32_bits(new, kernel):
     # pages 2^31 elements apart in one allocation: element offsets to 2^33
     free = torch.cuda.mem_get_info()[0]
     assert free > 40 << 30

@@ -153,6 +153,17 @@ def test_attn_scratch_stays_small(L):
         assert 0 < qg.qgemv_attn_scratch_bytes(seqs, seqs * new, 32, 8, 128, new, ctx) <= 512 << 20
 
 
+def test_tuning_hook_changes_the_plan_and_back(L):
+    sizes = (4, 400, 8, 2, 128, 100, 300)
+    plain = qg.qgemv_attn_scratch_bytes(*sizes)
+    seen = set()
+    for k in (1, 2):
+        qg.qgemv_tune_attn(k)
+        seen.add(qg.qgemv_attn_scratch_bytes(*sizes))
+    qg.qgemv_tune_attn(0)
+    assert plain in seen and len(seen) == 2 and qg.qgemv_attn_scratch_bytes(*sizes) == plain
+
+
 def sample(L, **kw):
     a = dict(kind=F32, x=Q, stride=1000, m=4, n=1000, t=K, k=V, p=QO, mp=KO, u=LEN, token=TAB, prob=ST, flags=0)
     a.update(kw)
