@@ -60,13 +60,13 @@ __device__ __forceinline__ void store8(int kind, void* y, long long i, const flo
 
 // 16000 tokens of 32 and 8 heads of 128, bf16: 68.1 us, 5.78 TB/s, 85% of what a plain copy reaches.  Small blocks suit it: 64 threads 68.1 us,
 // 128 69.3, 256 77.9, 448 (one piece a thread) 101; two pieces a thread on their way before the table is ready cost registers and
-// took 89.4, streaming loads changed nothing (69.7).  24 blocks an SM (40 registers): with more registers 81.8 us, with 32 spilled ones 70.0.
+// took 89.4, streaming loads changed nothing (69.7).  24 blocks an SM (40 registers): with more registers 81.8 us, with 32 spilled ones 70.0; interleaved pairs need no more than 32.
 //
 // One block serves one token (blockIdx.x) and every gridDim.y-th group of its pieces.  A piece of a query or key head is
 // 8 pairs (half layout: 8 elements and their 8 partners), 4 pairs (interleaved: 8 elements) or 8 elements that are copied;
 // without VEC it is one pair or one element.  Pieces of the value heads are copied.
 template <int XK, bool HALF, bool VEC>
-__global__ void __launch_bounds__(ROPE_THREADS, 24) rope_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(ROPE_THREADS, HALF && VEC ? 24 : 32) rope_kernel(const RopeArgs a) {
     __shared__ float2 cs[128];
     pdl_launch_dependents();
     pdl_wait();
