@@ -40,7 +40,7 @@ struct AttnArgs {
     const int* pages;
     long long pages_stride;
     const int *q_start, *kv_len;
-    unsigned* count;    // 16-row kernel: arrival counters, one a block; zero between calls
+    unsigned* count;    // zero between calls: 16-row kernel, arrival counters, one a block; 128-row kernel, next part and blocks done
     float2* part_stat;  // records of the parts of split row tiles: maximum in use (base 2) and sum of each row,
     float* part_sum;    // and dim unnormalised sums of values
     unsigned* err;
@@ -53,13 +53,15 @@ struct AttnArgs {
     // 128-row kernel: keys of a part, parts of a row tile and row tiles of a sequence and key/value head in the grid, rows of a
     // part's records
     int chunk, parts, row_tiles, rows_part;
-    int box;         // tokens of one tensor-map copy (128-row kernel), 0: no tensor map, every row is copied by itself
+    int wide;        // out's and the records' rows begin at multiples of 32 bytes and are as long: the 128-row kernel writes 32 at a time
+    int box;         // tokens of one tensor-map copy of the cache (128-row kernel), 0: no tensor map, every row is copied by itself
+    int q_map;       // the queries too come by tensor map: a row tile is a box of 128 / group tokens by group heads
 };
 
 // The 128-row kernel's arguments: the cache's two tensor maps, [head, page, token, dim] with boxes of `box` tokens by 64
-// elements in the 128-byte swizzle.
+// elements in the 128-byte swizzle, and that of the queries, [1, token, head, dim].
 struct AttnTileArgs {
-    alignas(64) unsigned long long k_map[16], v_map[16];
+    alignas(64) unsigned long long k_map[16], v_map[16], q_map[16];
     AttnArgs a;
 };
 

@@ -171,7 +171,7 @@ static int run_rope(const qgemv_rope_args* a, unsigned flags, void* stream) {
 
 static std::atomic<int> g_attn_kernel{0};
 
-static size_t round16(size_t n) { return (n + 15) / 16 * 16; }
+static size_t round32(size_t n) { return (n + 31) / 32 * 32; }
 
 static int attn_plan(int seqs, int tokens, int heads, int kv_heads, int dim, int max_q, int max_kv, AttnPlan* p) {
     if (seqs < 0 || tokens < 0 || heads < 1 || kv_heads < 1 || heads % kv_heads || dim < 8 || dim % 8 || max_q < 0 ||
@@ -226,7 +226,7 @@ static int attn_plan(int seqs, int tokens, int heads, int kv_heads, int dim, int
         if (p->parts > 1) records = static_cast<size_t>(p->grid) * p->rows_part;
     }
     p->records = records;
-    p->scratch += round16(records * sizeof(float2)) + records * dim * sizeof(float);
+    p->scratch += round32(records * sizeof(float2)) + records * dim * sizeof(float);
     return QGEMV_OK;
 }
 
@@ -250,10 +250,10 @@ static int allow_smem(const void* fn, unsigned smem) {
     return QGEMV_ERR_UNSUPPORTED;
 }
 
-// Tensor map of one side of a cache for the 128-row kernel; false where the cache cannot be described by one (then the
-// kernel copies row by row).  Host arithmetic of the driver, about a microsecond.
-static bool cache_map(unsigned long long (&map)[16], const void* base, const qgemv_cache& c, long long page, long long token,
-                      long long head, int box) {
+// Tensor map of 16-bit elements with 64 of them to a row of a box, in the 128-byte swizzle; strides in elements.  False where the
+// tensor cannot be described by one (then the kernel copies row by row).  Host arithmetic of the driver, about a microsecond.
+static bool tensor_map(unsigned long long (&map)[16], const void* base, int kind, const long long (&size)[4], const long long (&stride)[3],
+                       const int (&box)[4]) {
     using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -269,18 +269,18 @@ static bool cache_map(unsigned long long (&map)[16], const void* base, const qge
     }();
     if (!encode) return false;
     static_assert(sizeof(CUtensorMap) == sizeof(map), "");
-    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(c.dim), static_cast<cuuint64_t>(c.page_size),
-                                static_cast<cuuint64_t>(c.num_pages), static_cast<cuuint64_t>(c.heads)};
-    // (a dimension of one element is never stepped over: any valid stride will do)
-    const long long s[3] = {c.page_size > 1 ? token : c.dim, c.num_pages > 1 ? page : c.dim, c.heads > 1 ? head : c.dim};
-    cuuint64_t strides[3];
+    cuuint64_t dims[4], strides[3];
+    cuuint32_t boxes[4];
+    for (int i = 0; i < 4; ++i) dims[i] = static_cast<cuuint64_t>(size[i]), boxes[i] = static_cast<cuuint32_t>(box[i]);
     for (int i = 0; i < 3; ++i) {
-        if (s[i] <= 0 || s[i] >= 1ll << 38) return false;
-        strides[i] = static_cast<cuuint64_t>(s[i]) * 2;
+        // (a dimension of one element is never stepped over: any valid stride will do)
+        const long long s = size[i + 1] > 1 ? stride[i] : size[0];
+        if (s <= 0 || s >= 1ll << 38 || s % 8) return false;
+        strides[i] = static_cast<cuuint64_t>(s) * 2;
     }
-    const cuuint32_t boxes[4] = {64, static_cast<cuuint32_t>(box), 1, 1}, ones[4] = {1, 1, 1, 1};
+    const cuuint32_t ones[4] = {1, 1, 1, 1};
     return encode(reinterpret_cast<CUtensorMap*>(map),
-                  c.kind == QGEMV_ACT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+                  kind == QGEMV_ACT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
                   const_cast<void*>(base), dims, strides, boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -339,7 +339,7 @@ static int run_attn(const qgemv_attn_args* a, unsigned flags, void* stream) {
     k.count = static_cast<unsigned*>(a->scratch);
     uint8_t* parts = static_cast<uint8_t*>(a->scratch) + QGEMV_ATTN_SCRATCH_HEAD;
     k.part_stat = reinterpret_cast<float2*>(parts);
-    k.part_sum = reinterpret_cast<float*>(parts + round16(p.records * sizeof(float2)));
+    k.part_sum = reinterpret_cast<float*>(parts + round32(p.records * sizeof(float2)));
     k.err = err, k.num_pages = c.num_pages, k.page_size = c.page_size, k.kv_heads = c.heads, k.dim = c.dim;
     k.tokens = a->tokens, k.heads = a->heads, k.group = a->heads / c.heads, k.seqs = a->seqs;
     k.max_q = a->max_q, k.max_kv = a->max_kv;
@@ -357,18 +357,21 @@ static int run_attn(const qgemv_attn_args* a, unsigned flags, void* stream) {
     unsigned smem, threads;
     const void* fn = (p.tiles ? attn_tiles_kernel_ptr : attn_rows_kernel_ptr)(a->kind == QGEMV_ACT_BF16, c.dim, &smem, &threads);
     if ((st = allow_smem(fn, smem))) return st;
-    const dim3 grid(static_cast<unsigned>(p.grid));
     cudaError_t e;
     if (p.tiles) {
         AttnTileArgs ta = {};
         // The tokens of one copy: the largest power of two that divides the page and a key tile; 8 is the swizzle's period.
         int box = 128;
         while (c.page_size % box) box /= 2;
-        if (box >= 8 && cache_map(ta.k_map, c.k, c, c.k_page, c.k_token, c.k_head, box) &&
-            cache_map(ta.v_map, c.v, c, c.v_page, c.v_token, c.v_head, box))
+        const long long cache[4] = {c.dim, c.page_size, c.num_pages, c.heads};
+        if (box >= 8 && tensor_map(ta.k_map, c.k, c.kind, cache, {c.k_token, c.k_page, c.k_head}, {64, box, 1, 1}) &&
+            tensor_map(ta.v_map, c.v, c.kind, cache, {c.v_token, c.v_page, c.v_head}, {64, box, 1, 1}))
             k.box = box;
+        k.q_map = 128 % k.group == 0 && tensor_map(ta.q_map, a->q, c.kind, {c.dim, a->heads, a->tokens, 1},
+                                                   {a->q_head, a->q_token, c.dim}, {64, k.group, 128 / k.group, 1});
+        k.wide = api_aligned(a->out, 32) && api_aligned(k.part_sum, 32) && a->out_token % 16 == 0 && a->out_head % 16 == 0 && c.dim % 16 == 0;
         ta.a = k;
-        e = launch_step(fn, grid, threads, smem, 1, pdl, static_cast<cudaStream_t>(stream), ta);
+        e = launch_step(fn, dim3(static_cast<unsigned>(p.grid < sms ? p.grid : sms)), threads, smem, 1, pdl, static_cast<cudaStream_t>(stream), ta);
         if (e == cudaSuccess && p.parts > 1) {
             // starts with the tail of the kernel before it, and waits there
             const long long rows = static_cast<long long>(p.row_tiles) * k.kv_heads * k.seqs * p.rows_part;
@@ -377,7 +380,7 @@ static int run_attn(const qgemv_attn_args* a, unsigned flags, void* stream) {
                             static_cast<cudaStream_t>(stream), k);
         }
     } else {
-        e = launch_step(fn, grid, threads, smem, 1, pdl, static_cast<cudaStream_t>(stream), k);
+        e = launch_step(fn, dim3(static_cast<unsigned>(p.grid)), threads, smem, 1, pdl, static_cast<cudaStream_t>(stream), k);
     }
     if (e != cudaSuccess) return api_cuda_fail(e);
     api_route(p.tiles ? QGEMV_ROUTE_ATTN_TILES : QGEMV_ROUTE_ATTN_ROWS, pdl);

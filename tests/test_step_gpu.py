@@ -295,6 +295,24 @@ def test_attention_many_sequences(case, kernel):
         assert int(s.scratch[:qg.QGEMV_ATTN_SCRATCH_HEAD].sum()) == 0
 
 
+@pytest.mark.parametrize("D,page,dtype", [(128, 64, B16), (64, 5, H16)])
+def test_attention_blocks_that_take_many_parts(D, page, dtype, kernel):
+    """More parts of row tiles than blocks: ones with one row and with two full tiles, without rows, without keys, with a few keys and with
+    many, after one another in a block; three times with one scratch."""
+    rng = np.random.default_rng(7)
+    new = [int(x) for x in rng.choice([0, 1, 20, 100, 130, 300], 60)]
+    ctx = [int(x) for x in rng.choice([0, 1, 60, 128, 400, 700, 1500], 60)]
+    s = Step(61, new, ctx, 8, 4, D, page, dtype)
+    for mask in (dict(), dict(causal=False), dict(window=150)):
+        qg.qgemv_attn(s.args(**mask))
+        s.check(**mask)
+        first, scratch = s.out.clone(), s.scratch
+        for _ in range(3):
+            qg.qgemv_attn(s.args(scratch=scratch, **mask), qg.QGEMV_FLAG_PDL)
+            assert torch.equal(first, s.out)
+        assert int(s.scratch[:qg.QGEMV_ATTN_SCRATCH_HEAD].sum()) == 0
+
+
 @pytest.mark.parametrize("flags", [0, qg.QGEMV_FLAG_PDL])
 def test_attention_takes_the_kernel_that_the_sizes_ask_for(flags):
     for new, ctx, route in ((1, 9000, qg.ROUTE_ATTN_ROWS), (8, 9000, qg.ROUTE_ATTN_ROWS), (40, 40, qg.ROUTE_ATTN_ROWS), (500, 9000, qg.ROUTE_ATTN_TILES)):
