@@ -12,12 +12,13 @@
 // Work a pair of row tiles and a key tile at D = 128: 2048 cycles of the tensor cores, 1024 of the exponential units; measured about 2720, the
 // time of one row tile's round: softmax 1200, its products 1024, some 500 of barriers and of the products' latency.  Only two row
 // tiles fit tensor memory (2 x (128 scores + 128 sums) = 512 columns), so that no third round hides those.  A chunk of 2000 tokens over
-// 24000 (32 and 8 heads): 580 us, 1.30 PFLOP/s; two prompts of 6000: 397 us, 1.33 PFLOP/s (cuBLAS bf16: 1.72 sustained).
+// 24000 (32 and 8 heads): 541 us, 1.39 PFLOP/s; two prompts of 6000: 397 us, 1.33 PFLOP/s (cuBLAS bf16: 1.72 sustained).
 // What the steps gave, for the chunk: 1302 us with one softmax thread a row, row-by-row copies and a wait for each of them; 1062 with
 // copies that announce themselves; 777 with tensor-map copies, two threads a row and exponentials ahead of the maximum; 694 with a
 // warp that waits in the issuing warp's place; 612 with parts by cost and a kernel that joins them; 580 with blocks that stay (prompts:
 // 435 to 397): the next part's keys and queries come under the end of the last one, and the warps' numbers and loop bounds
-// are uniform for the compiler, which took 400 to 180 cycles from a probability's arrival to its product.  Stores of 32 bytes (a whole
+// are uniform for the compiler, which took 400 to 180 cycles from a probability's arrival to its product; 541 with the parts' records and
+// launch in their cost.  Stores of 32 bytes (a whole
 // sector) a thread in place of 16: prompts 429 to 420, chunks that are split 76 to 74.
 #include "attn.cuh"
 

@@ -185,22 +185,28 @@ static int attn_plan(int seqs, int tokens, int heads, int kv_heads, int dim, int
     if (max_q > tokens) max_q = tokens;
     const long long rows = static_cast<long long>(max_q) * (heads / kv_heads);
     if (max_kv > 1 << 30 || (rows + 15) / 16 * kv_heads > INT_MAX || rows > INT_MAX) return QGEMV_ERR_UNSUPPORTED;
-    // The 128-row kernel: 256 rows a block, one block an SM, the row tiles' contexts in parts.  The time of a launch in key tiles: waves of
-    // blocks, each as long as its part, with about 3 key tiles for its start and end, and 4 more where parts have to be written out and
-    // joined.  At most 32 parts of at least 8 key tiles, and no more than 16 waves of them.
+    // The 128-row kernel: 256 rows a block, one block an SM, the row tiles' contexts in n parts.  Its time in us: 9 for the launch, start and
+    // end; waves of blocks, each as long as its part and about 3 key tiles for its start and end, at 1.4 a key tile; where parts are joined, 4
+    // for the second kernel and their records, written and read at 5 TB/s.  Measured and by this rule: 32 and 8 heads of 128, 2000 tokens over 24000,
+    // n = 1: 542 / 544, n = 2: 591 / 583, 4: 578 / 557, 8: 640 / 650; 1000 over 30000, n = 1: 346 / 342, 2: 375 / 365, 8: 405 / 390; 256 over 16000,
+    // n = 1: 182 / 188, 4: 64 / 69, 8: 74 / 80; 64 over 4000, n = 1: 56 / 58, 4: 30 / 30.  At most 32 parts of at least 8 key tiles, and no more
+    // than 16 waves of them.
     const long long tiles = (rows + 255) / 256 * kv_heads * seqs, blocks = (static_cast<long long>(max_kv) + 127) / 128;
-    long long best = 1, best_cost = LLONG_MAX;
+    long long best = 1;
+    double tiles_us = 0;
     for (long long n = 1; n <= 32 && (n == 1 || (n * 8 <= blocks && tiles * n <= 16 * SMS)); ++n) {
-        const long long cost = (tiles * n + SMS - 1) / SMS * ((blocks + n - 1) / n + 3 + (n > 1 ? 4 : 0));
-        if (cost < best_cost) best = n, best_cost = cost;
+        const double waves = static_cast<double>((tiles * n + SMS - 1) / SMS), part = static_cast<double>((blocks + n - 1) / n);
+        const double records = n > 1 ? 8e-6 / 5 * static_cast<double>(tiles * n * (rows < 256 ? rows : 256) * dim) : 0;
+        const double us = 9 + 1.4 * waves * (part + 3) + (n > 1 ? 4 + records : 0);
+        if (n == 1 || us < tiles_us) best = n, tiles_us = us;
     }
     // Which kernel, for more than 32 rows (and heads of up to 128, which the 128-row kernel is built for): by what both would take, in us.  The
     // 16-row kernel goes over the keys once for 16 rows, 19 row tiles and keys a ns; over sequences of uneven length its time is their sum's, the
-    // other's the longest's.  Measured, 8 key/value heads, 16-row against 128-row kernel in us: 64 rows over 4000 keys 18.4 / 26.6, 128 rows 24.6 / 28.4,
-    // 256 rows 38.9 / 33.0; over 50000 keys 32 rows 51.2 / 52.4, 64 rows 84.5 / 53.7; 16 sequences of up to 8000: 32 rows 63.5 / 93.8, 48 rows
-    // 78.7 / 94.0, 64 rows 139 / 94; 4 sequences of 300 with 64 rows 10.6 / 14.4; 64 tokens alone 8.2 / 18.5.
+    // other's the longest's.  Measured, 8 key/value heads, 16-row against 128-row kernel in us: 64 rows over 4000 keys 18.5 / 26.7, 128 rows 24.6 / 27.9,
+    // 256 rows 39.0 / 32.8; over 50000 keys 32 rows 51.2 / 52.4, 64 rows 84.5 / 53.0; 16 sequences of up to 8000: 32 rows 63.5 / 93.8, 48 rows
+    // 78.7 / 94.4, 64 rows 141 / 94; 4 sequences of 300 with 64 tokens 18.5 / 18.5; 128 tokens alone 9.0 / 18.5, 256 over 1000 37.2 / 26.7.
     const double keys16 = static_cast<double>((rows + 15) / 16) * kv_heads * seqs * max_kv;
-    const double rows_us = 8 + keys16 / 19000 * (seqs > 1 ? 0.75 : 1.0), tiles_us = 11 + 1.3 * static_cast<double>(best_cost);
+    const double rows_us = 8 + keys16 / 19000 * (seqs > 1 ? 0.75 : 1.0);
     const int forced = g_attn_kernel.load(std::memory_order_relaxed);
     p->tiles = dim <= 128 && (forced ? forced == 2 : rows > 32 && tiles_us < rows_us);
     size_t records = 0;
