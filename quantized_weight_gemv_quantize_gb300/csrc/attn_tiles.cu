@@ -16,10 +16,9 @@
 // What the steps gave, for the chunk: 1302 us with one softmax thread a row, row-by-row copies and a wait for each of them; 1062 with
 // copies that announce themselves; 777 with tensor-map copies, two threads a row and exponentials ahead of the maximum; 694 with a
 // warp that waits in the issuing warp's place; 612 with parts by cost and a kernel that joins them; 580 with blocks that stay (prompts:
-// 435 to 397): the next part's keys and queries come under the end of the last one, and the warps' numbers and loop bounds
-// are uniform for the compiler, which took 400 to 180 cycles from a probability's arrival to its product; 541 with the parts' records and
-// launch in their cost.  Stores of 32 bytes (a whole
-// sector) a thread in place of 16: prompts 429 to 420, chunks that are split 76 to 74.
+// 435 to 397): the next part's keys and queries come under the end of the last one, and the warps' numbers and loop bounds are
+// uniform for the compiler, which took 400 to 180 cycles from a probability's arrival to its product; 541 with the parts' records and
+// launch in their cost.  Stores of 32 bytes (a whole sector) a thread in place of 16: prompts 429 to 420, chunks in parts 76 to 74.
 #include "attn.cuh"
 
 namespace qg {
