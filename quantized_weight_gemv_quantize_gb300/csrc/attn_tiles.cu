@@ -12,13 +12,13 @@
 // Work a pair of row tiles and a key tile at D = 128: 2048 cycles of the tensor cores, 1024 of the exponential units; measured about 2720, the
 // time of one row tile's round: softmax 1200, its products 1024, some 500 of barriers and of the products' latency.  Only two row
 // tiles fit tensor memory (2 x (128 scores + 128 sums) = 512 columns), so that no third round hides those.  A chunk of 2000 tokens over
-// 24000 (32 and 8 heads): 541 us, 1.39 PFLOP/s; two prompts of 6000: 397 us, 1.33 PFLOP/s (cuBLAS bf16: 1.72 sustained).
+// 24000 (32 and 8 heads): 525 us, 1.43 PFLOP/s; two prompts of 6000: 397 us, 1.33 PFLOP/s (cuBLAS bf16: 1.72 sustained).
 // What the steps gave, for the chunk: 1302 us with one softmax thread a row, row-by-row copies and a wait for each of them; 1062 with
 // copies that announce themselves; 777 with tensor-map copies, two threads a row and exponentials ahead of the maximum; 694 with a
 // warp that waits in the issuing warp's place; 612 with parts by cost and a kernel that joins them; 580 with blocks that stay (prompts:
 // 435 to 397): the next part's keys and queries come under the end of the last one, and the warps' numbers and loop bounds are
 // uniform for the compiler, which took 400 to 180 cycles from a probability's arrival to its product; 541 with the parts' records and
-// launch in their cost.  Stores of 32 bytes (a whole sector) a thread in place of 16: prompts 429 to 420, chunks in parts 76 to 74.
+// launch in their cost; 525 where only the row tiles that do not fill a wave are cut.  Stores of 32 bytes (a whole sector) a thread in place of 16: prompts 429 to 420, chunks in parts 76 to 74.
 #include "attn.cuh"
 
 namespace qg {
@@ -179,8 +179,9 @@ struct TilesShared {
 // with short ones.  False: nothing to do (past the sequence's rows or the tile's parts).
 __device__ __forceinline__ bool find_tile(const AttnArgs& a, long long block, Tile* t) {
     const int pairs = a.kv_heads * a.seqs;
-    t->part = static_cast<int>(block % a.parts);
-    t->index = block / a.parts;
+    const long long of_parts = block - a.whole;
+    t->part = of_parts < 0 ? 0 : static_cast<int>(of_parts % a.parts);
+    t->index = of_parts < 0 ? block : a.whole + of_parts / a.parts;
     const int pair = static_cast<int>(t->index % pairs), rt = static_cast<int>(a.row_tiles - 1 - t->index / pairs);
     t->kv_head = pair % a.kv_heads;
     t->seq = pair / a.kv_heads;
@@ -192,13 +193,14 @@ __device__ __forceinline__ bool find_tile(const AttnArgs& a, long long block, Ti
     int lo, hi;
     find_keys(a, s, t->row0, t->rows, &lo, &hi);
     lo = lo / TK * TK;  // key tiles start at multiples of their size
-    t->parts = max(1, (hi - lo + a.chunk - 1) / a.chunk);
-    t->k0 = lo + t->part * a.chunk;
-    t->k1 = min(hi, t->k0 + a.chunk);
+    const int chunk = of_parts < 0 ? max(hi - lo, 1) : a.chunk;
+    t->parts = max(1, (hi - lo + chunk - 1) / chunk);
+    t->k0 = lo + t->part * chunk;
+    t->k1 = min(hi, t->k0 + chunk);
     return t->part < t->parts;
 }
 __device__ __forceinline__ long long part_at(const AttnArgs& a, const Tile& t, int part, int r) {
-    return (t.index * a.parts + part) * a.rows_part + r;
+    return ((t.index - a.whole) * a.parts + part) * a.rows_part + r;
 }
 
 // A block takes parts of row tiles one after the other, the next one's number from a counter (the first from its own), until there
@@ -219,7 +221,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) attn_tiles_kernel(const __gri
     const uint32_t smem = (smem_addr(smem_raw) + 1023u) & ~1023u;
     constexpr int PER_ROW = DP / 8;  // 16-byte pieces of a row
 
-    const unsigned all = static_cast<unsigned>(a.parts) * a.row_tiles * (a.kv_heads * a.seqs);
+    const unsigned all = a.whole + static_cast<unsigned>(a.parts) * (a.row_tiles * (a.kv_heads * a.seqs) - a.whole);
     // The n-th part that this block takes, the first from its own number.
     auto next_part = [&](unsigned n) {
         Tile* t = &sh.item[n % ITEMS];
@@ -661,11 +663,11 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) attn_join_kernel(const AttnAr
     pdl_launch_dependents();
     pdl_wait();
     const long long w = static_cast<long long>(blockIdx.x) * JOIN_WARPS + threadIdx.x / 32;
-    const long long index = w / a.rows_part;
+    const long long index = w / a.rows_part;  // among the row tiles that are cut
     const int r = static_cast<int>(w % a.rows_part);
-    if (index >= static_cast<long long>(a.row_tiles) * a.kv_heads * a.seqs) return;
+    if (index >= static_cast<long long>(a.row_tiles) * a.kv_heads * a.seqs - a.whole) return;
     Tile t;
-    if (!find_tile(a, index * a.parts, &t) || t.parts == 1 || r >= t.rows) return;
+    if (!find_tile(a, a.whole + index * a.parts, &t) || t.parts == 1 || r >= t.rows) return;
     join_row<1, BF>(a, t, r, [&](int p) { return part_at(a, t, p, r); });
 }
 

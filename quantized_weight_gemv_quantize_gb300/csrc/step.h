@@ -53,6 +53,7 @@ struct AttnArgs {
     // 128-row kernel: keys of a part, parts of a row tile and row tiles of a sequence and key/value head in the grid, rows of a
     // part's records
     int chunk, parts, row_tiles, rows_part;
+    int whole;       // the first row tiles, whole waves of blocks, that are not cut into parts
     int wide;        // out's and the records' rows begin at multiples of 32 bytes and are as long: the 128-row kernel writes 32 at a time
     int box;         // tokens of one tensor-map copy of the cache (128-row kernel), 0: no tensor map, every row is copied by itself
     int q_map;       // the queries too come by tensor map: a row tile is a box of 128 / group tokens by group heads
@@ -67,7 +68,7 @@ struct AttnTileArgs {
 
 struct AttnPlan {
     bool tiles;  // the 128-row tensor-memory kernel (else the 16-row one)
-    int chunk, parts, row_tiles, rows_part, unit_shift;
+    int chunk, parts, row_tiles, rows_part, whole, unit_shift;
     long long grid;
     size_t records, scratch;  // rows of parts' records, bytes of scratch
 };

@@ -192,14 +192,21 @@ static int attn_plan(int seqs, int tokens, int heads, int kv_heads, int dim, int
     // n = 1: 182 / 188, 4: 64 / 69, 8: 74 / 80; 64 over 4000, n = 1: 56 / 58, 4: 30 / 30.  At most 32 parts of at least 8 key tiles, and no more
     // than 16 waves of them.
     const long long tiles = (rows + 255) / 256 * kv_heads * seqs, blocks = (static_cast<long long>(max_kv) + 127) / 128;
-    long long best = 1;
+    // Or the row tiles that fill whole waves stay whole and only the rest is cut (1300 tokens over
+    // 30000: 492 us with all cut alike, 419; 1500 over 20000: 368, 331; 2000 over 24000: 532 with none cut, 525).
+    const long long full = tiles / SMS * SMS;
+    long long best = 1, best_whole = 0;
     double tiles_us = 0;
-    for (long long n = 1; n <= 32 && (n == 1 || (n * 8 <= blocks && tiles * n <= 16 * SMS)); ++n) {
-        const double waves = static_cast<double>((tiles * n + SMS - 1) / SMS), part = static_cast<double>((blocks + n - 1) / n);
-        const double records = n > 1 ? 8e-6 / 5 * static_cast<double>(tiles * n * (rows < 256 ? rows : 256) * dim) : 0;
-        const double us = 9 + 1.4 * waves * (part + 3) + (n > 1 ? 4 + records : 0);
-        if (n == 1 || us < tiles_us) best = n, tiles_us = us;
-    }
+    for (long long n = 1; n <= 32 && (n == 1 || n * 8 <= blocks); ++n)
+        for (const long long whole : {0ll, full}) {
+            if (whole > 0 && (n == 1 || whole == tiles)) continue;
+            if (n > 1 && (tiles - whole) * n > 16 * SMS) continue;
+            const double part = static_cast<double>((blocks + n - 1) / n);
+            const double waves = static_cast<double>(((tiles - whole) * n + SMS - 1) / SMS);
+            const double records = n > 1 ? 8e-6 / 5 * static_cast<double>((tiles - whole) * n * (rows < 256 ? rows : 256) * dim) : 0;
+            const double us = 9 + 1.4 * (waves * (part + 3) + static_cast<double>(whole / SMS * (blocks + 3))) + (n > 1 ? 4 + records : 0);
+            if (n == 1 || us < tiles_us) best = n, best_whole = whole, tiles_us = us;
+        }
     // Which kernel, for more than 32 rows (and heads of up to 128, which the 128-row kernel is built for): by what both would take, in us.  The
     // 16-row kernel goes over the keys once for 16 rows, 19 row tiles and keys a ns; over sequences of uneven length its time is their sum's, the
     // other's the longest's.  Measured, 8 key/value heads, 16-row against 128-row kernel in us: 64 rows over 4000 keys 18.5 / 26.7, 128 rows 24.6 / 27.9,
@@ -227,9 +234,10 @@ static int attn_plan(int seqs, int tokens, int heads, int kv_heads, int dim, int
         const long long chunk = ((max_kv + best - 1) / best + 127) / 128 * 128;
         p->chunk = static_cast<int>(chunk < 128 ? 128 : chunk > INT_MAX - 127 ? INT_MAX - 127 : chunk);
         p->parts = max_kv > 0 ? static_cast<int>((static_cast<long long>(max_kv) + p->chunk - 1) / p->chunk) : 1;
-        p->grid = tiles * p->parts;
+        p->whole = p->parts > 1 ? static_cast<int>(best_whole) : 0;
+        p->grid = p->whole + (tiles - p->whole) * p->parts;
         if (p->grid > INT_MAX) return QGEMV_ERR_UNSUPPORTED;
-        if (p->parts > 1) records = static_cast<size_t>(p->grid) * p->rows_part;
+        if (p->parts > 1) records = static_cast<size_t>(p->grid - p->whole) * p->rows_part;
     }
     p->records = records;
     p->scratch += round32(records * sizeof(float2)) + records * dim * sizeof(float);
@@ -357,7 +365,7 @@ static int run_attn(const qgemv_attn_args* a, unsigned flags, void* stream) {
     k.group_shift = log2_of(k.group), k.page_shift = log2_of(c.page_size);
     k.scale_log2 = a->scale * 1.44269504088896341f;
     k.window = a->window, k.causal = a->causal || a->window > 0;
-    k.chunk = p.chunk, k.parts = p.parts, k.row_tiles = p.row_tiles, k.rows_part = p.rows_part;
+    k.chunk = p.chunk, k.parts = p.parts, k.row_tiles = p.row_tiles, k.rows_part = p.rows_part, k.whole = p.whole;
     k.unit_shift = p.unit_shift;
     const bool pdl = (flags & QGEMV_FLAG_PDL) != 0;
     unsigned smem, threads;
@@ -380,7 +388,7 @@ static int run_attn(const qgemv_attn_args* a, unsigned flags, void* stream) {
         e = launch_step(fn, dim3(static_cast<unsigned>(p.grid < sms ? p.grid : sms)), threads, smem, 1, pdl, static_cast<cudaStream_t>(stream), ta);
         if (e == cudaSuccess && p.parts > 1) {
             // starts with the tail of the kernel before it, and waits there
-            const long long rows = static_cast<long long>(p.row_tiles) * k.kv_heads * k.seqs * p.rows_part;
+            const long long rows = (static_cast<long long>(p.row_tiles) * k.kv_heads * k.seqs - p.whole) * p.rows_part;
             e = launch_step(attn_join_kernel_ptr(a->kind == QGEMV_ACT_BF16),
                             dim3(static_cast<unsigned>((rows + JOIN_WARPS - 1) / JOIN_WARPS)), JOIN_WARPS * 32, 0, 1, true,
                             static_cast<cudaStream_t>(stream), k);

@@ -313,6 +313,17 @@ def test_attention_blocks_that_take_many_parts(D, page, dtype, kernel):
         assert int(s.scratch[:qg.QGEMV_ATTN_SCRATCH_HEAD].sum()) == 0
 
 
+@pytest.mark.parametrize("mask", [dict(), dict(window=1100)], ids=str)
+def test_attention_whole_row_tiles_before_cut_ones(mask):
+    """160 row tiles: the 152 that fill a wave of blocks are left whole, the others' contexts are cut into parts."""
+    s = Step(62, [1250], [2100], 32, 32, 64, 16, B16)
+    qg.qgemv_route_reset()
+    qg.qgemv_attn(s.args(**mask))
+    assert qg.qgemv_route_counts()[qg.ROUTE_ATTN_TILES] == 1
+    s.check(**mask)
+    assert int(s.scratch[:qg.QGEMV_ATTN_SCRATCH_HEAD].sum()) == 0
+
+
 @pytest.mark.parametrize("flags", [0, qg.QGEMV_FLAG_PDL])
 def test_attention_takes_the_kernel_that_the_sizes_ask_for(flags):
     for new, ctx, route in ((1, 9000, qg.ROUTE_ATTN_ROWS), (8, 9000, qg.ROUTE_ATTN_ROWS), (40, 40, qg.ROUTE_ATTN_ROWS), (500, 9000, qg.ROUTE_ATTN_TILES)):
