@@ -18,7 +18,8 @@
 // warp that waits in the issuing warp's place; 612 with parts by cost and a kernel that joins them; 580 with blocks that stay (prompts:
 // 435 to 397): the next part's keys and queries come under the end of the last one, and the warps' numbers and loop bounds are
 // uniform for the compiler, which took 400 to 180 cycles from a probability's arrival to its product; 541 with the parts' records and
-// launch in their cost; 525 where only the row tiles that do not fill a wave are cut.  Stores of 32 bytes (a whole sector) a thread in place of 16: prompts 429 to 420, chunks in parts 76 to 74.
+// launch in their cost; 525 where only the row tiles that do not fill a wave are cut.  Stores of 32 bytes (a whole sector) a thread in
+// place of 16: prompts 429 to 420, chunks in parts 76 to 74.
 #include "attn.cuh"
 
 namespace qg {
@@ -282,6 +283,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) attn_tiles_kernel(const __gri
         return base + (c / 8) * S::HALF_BYTES + r * 128 + (((c % 8) ^ (r & 7)) << 4);
     };
 
+    // 512 x 104 + 128 x 64 registers: the launch's 640 x 96.  The softmax then keeps its scores without spills in its loop.
     if (warp >= K_WARP) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
         if (warp == K_WARP || warp == V_WARP) {
