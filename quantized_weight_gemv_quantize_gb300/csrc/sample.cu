@@ -29,9 +29,17 @@ constexpr int BINS = 1024, GROUP = 32;            // 32 groups of 32 bins: a war
 constexpr int PER = BINS / ST;                    // bins of a thread
 
 // ---- cluster: barrier, and the same shared-memory address in another block
-__device__ __forceinline__ void cluster_sync() {
+__device__ __forceinline__ void cluster_arrive() {
     __syncwarp();
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    __syncwarp();
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+    cluster_arrive();
+    cluster_wait();
 }
 __device__ __forceinline__ uint32_t peer(uint32_t addr, int rank) {
     uint32_t r;
@@ -135,6 +143,9 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleArgs a) {
     SampleShared& s = *reinterpret_cast<SampleShared*>(smem);
     uint4* const stage = reinterpret_cast<uint4*>(smem + sizeof(SampleShared));
     u64* const line = s.line;
+    // Another block's shared memory may be written only once that block runs: every block says so here, and waits for the
+    // others before the first exchange, when the slice's load has long covered it.
+    if (a.blocks > 1) cluster_arrive();
     pdl_launch_dependents();
     pdl_wait();
     const int CS = a.blocks, rank = static_cast<int>(blockIdx.x) % CS, row = static_cast<int>(blockIdx.x) / CS;
@@ -255,6 +266,7 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleArgs a) {
         }
     }
     u64 best = block_reduce(largest != largest ? 0xffffffffull : static_cast<u64>(key_of(largest)), 0, max64);
+    if (CS > 1) cluster_wait();  // the other blocks run
     exchange(best, 0, 0);
     for (int b = 0; b < CS; ++b) best = max64(best, s.push[turn][0][b]);
     const uint32_t top_key = static_cast<uint32_t>(best);

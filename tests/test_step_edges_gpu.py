@@ -1,0 +1,77 @@
+"""Edges of the operators between the GEMVs on the GPU: rows of logits over several blocks, masks and bounds at the ends of pages
+and of the page table, kernels by their route.  Formulas and tolerances are those of test_step_gpu."""
+import numpy as np
+import pytest
+
+import quantized_weight_gemv_quantize_gb300 as qg
+
+torch = pytest.importorskip("torch")
+
+from tests.test_step_gpu import B16, H16, f64, rnd, run_sample  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    qg.build()
+    qg.lib()
+    qg.qgemv_device_error(reset=True)
+    yield
+    assert qg.qgemv_device_error() == 0
+
+
+# --------------------------------------------------------------------------------------------------------- sampling
+
+# rows of two, four and eight blocks, the last of them with and without an odd end
+@pytest.mark.parametrize("dtype", [torch.float32, B16, H16])
+@pytest.mark.parametrize("n", [20481, 65541, 151936, 163843])
+def test_sampling_special_rows_over_several_blocks(n, dtype):
+    rng = np.random.default_rng(n)
+    x = rnd(rng, (13, n), dtype, 2.0)
+    inf, end = float("inf"), n - 1
+    x[0] = -inf
+    x[1, end] = float("nan")   # in the last block; an infinity in the first
+    x[1, 17] = inf
+    x[2, end] = inf            # the first of two infinities, in different blocks
+    x[2, n // 2] = inf
+    x[3] = -inf
+    x[3, end] = -3.0           # one token is left
+    x[4, ::2] = -inf
+    x[5] = 0.25                # one tie of the whole row
+    x[6] = -0.0
+    x[6, ::3] = 0.0            # both zeros are one value
+    x[7, 100:n - 100] = x[7].max()
+    x[8, end] = 3e38 if dtype is not H16 else 6e4
+    x[9] *= 1e-4
+    x[10, end] = float("nan")
+    x[10, end - 1] = float("nan")
+    x[11] = -6e4
+    x[12, :n - 40] = -inf      # only the last block has tokens
+    u = rng.random(13, dtype=np.float32)
+    for kw in (dict(), dict(k=np.full(13, 7)), dict(p=np.full(13, 0.5)), dict(mp=np.full(13, 0.1)), dict(T=np.zeros(13)),
+               dict(k=np.full(13, 1000), p=np.full(13, 0.9), mp=np.full(13, 0.05)), dict(k=np.ones(13)),
+               dict(T=np.full(13, 1e-3)), dict(p=np.full(13, 0.999))):
+        a = run_sample(x, u=u, **kw)
+        b = run_sample(x, u=u, flags=qg.QGEMV_FLAG_PDL, check=False, **kw)
+        assert np.array_equal(a[0], b[0]) and np.array_equal(a[1], b[1], equal_nan=True)
+    for edge in (0.0, np.float32(1 - 2.0 ** -24)):
+        run_sample(x, u=np.full(13, edge), k=np.full(13, 50))
+    # rank 0 alone: the first of the largest, whichever block it lies in
+    token, prob = run_sample(x, u=u, check=False, T=np.full(13, -1.0))
+    ok = [3, 4, 5, 6, 7, 8, 9, 11, 12]
+    assert np.array_equal(token[ok], f64(x).argmax(1)[ok]) and np.all(prob[ok] == 1)
+
+
+@pytest.mark.parametrize("dtype,n", [(torch.float32, 40963), (B16, 151931), (H16, 81925)])
+def test_sampling_unaligned_rows_over_several_blocks(dtype, n):
+    rng = np.random.default_rng(n)
+    wide = rnd(rng, (5, n + 6), dtype, 2.0)
+    x = wide[:, :n]
+    assert x.stride(0) * x.element_size() % 16
+    u = rng.random(5, dtype=np.float32)
+    for kw in (dict(k=np.full(5, 50), p=np.full(5, 0.8)), dict(p=np.full(5, 0.9)), dict(), dict(k=np.full(5, 2000)), dict(T=np.zeros(5))):
+        a = run_sample(x, u=u, **kw)
+        b = run_sample(x.contiguous(), u=u, **kw)
+        assert np.array_equal(a[0], b[0]) and np.array_equal(a[1], b[1])
