@@ -53,10 +53,10 @@ __device__ __forceinline__ Seq find_seq(const AttnArgs& a, int b) {
     return s;
 }
 
-// The keys that some row of [row0, row0 + rows) sees.
-__device__ __forceinline__ void find_keys(const AttnArgs& a, const Seq& s, int row0, int rows, int* lo, int* hi) {
-    // (from a multiple of 16 on; the keys before the first are masked like any other)
-    *lo = a.window > 0 ? max(0, s.first_pos + div_by(row0, a.group, a.group_shift) - a.window + 1) / 16 * 16 : 0;
+// The keys that some row of [row0, row0 + rows) sees, from a multiple of `step` on (the keys before the first are masked like any
+// other).  Where there are none, hi = lo: the rounding comes first, so that nothing beyond the keys that may be read is in the range.
+__device__ __forceinline__ void find_keys(const AttnArgs& a, const Seq& s, int row0, int rows, int step, int* lo, int* hi) {
+    *lo = a.window > 0 ? max(0, s.first_pos + div_by(row0, a.group, a.group_shift) - a.window + 1) / step * step : 0;
     *hi = a.causal ? min(s.usable, s.first_pos + div_by(row0 + rows - 1, a.group, a.group_shift) + 1) : s.usable;
     *hi = max(*hi, *lo);
 }

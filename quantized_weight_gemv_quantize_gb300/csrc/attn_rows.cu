@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(RowsShape<DP>::WARPS * 32) attn_rows_kernel(co
         if (b >= seqs) return;
         sq = find_seq(a, static_cast<int>(b));
         int lo, hi;
-        find_keys(a, sq, 0, sq.n * a.group, &lo, &hi);
+        find_keys(a, sq, 0, sq.n * a.group, 16, &lo, &hi);
         sq_tiles = (sq.n * a.group + 15) / 16 * a.kv_heads;
         sq_units = max(1u, (static_cast<unsigned>(hi - lo) + (1u << unit) - 1) >> unit);
     };
@@ -402,7 +402,7 @@ __global__ void __launch_bounds__(RowsShape<DP>::WARPS * 32) attn_rows_kernel(co
         }
         t.rows = min(16, sq.n * a.group - t.row0);
         int lo, hi;
-        find_keys(a, sq, t.row0, t.rows, &lo, &hi);
+        find_keys(a, sq, t.row0, t.rows, 16, &lo, &hi);
         t.k0 = lo + static_cast<int>(min(static_cast<unsigned long long>(hi - lo), static_cast<unsigned long long>(pos - tile_at) << unit));
         t.k1 = lo + static_cast<int>(min(static_cast<unsigned long long>(hi - lo), static_cast<unsigned long long>(stop - tile_at) << unit));
         // the blocks with the row tile's first and last part: this one where the tile begins or ends here

@@ -192,8 +192,7 @@ __device__ __forceinline__ bool find_tile(const AttnArgs& a, long long block, Ti
     t->rows = min(2 * TR, s.n * a.group - t->row0);
     if (t->rows <= 0) return false;
     int lo, hi;
-    find_keys(a, s, t->row0, t->rows, &lo, &hi);
-    lo = lo / TK * TK;  // key tiles start at multiples of their size
+    find_keys(a, s, t->row0, t->rows, TK, &lo, &hi);  // key tiles start at multiples of their size
     const int chunk = of_parts < 0 ? max(hi - lo, 1) : a.chunk;
     t->parts = max(1, (hi - lo + chunk - 1) / chunk);
     t->k0 = lo + t->part * chunk;

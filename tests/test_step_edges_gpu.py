@@ -7,7 +7,7 @@ import quantized_weight_gemv_quantize_gb300 as qg
 
 torch = pytest.importorskip("torch")
 
-from tests.test_step_gpu import B16, H16, f64, rnd, run_sample  # noqa: E402
+from tests.test_step_gpu import B16, H16, TINY, U, Step, f64, kernel, rnd, run_sample  # noqa: E402,F401
 
 pytestmark = pytest.mark.gpu
 
@@ -20,6 +20,56 @@ def _lib():
     qg.qgemv_device_error(reset=True)
     yield
     assert qg.qgemv_device_error() == 0
+
+
+# -------------------------------------------------------------------------------------------------------- attention
+
+def check_seen(s, sees):
+    """The result of a step of one sequence against the formula in 64 bits, its tokens seeing the keys `sees` [tokens, context]."""
+    out, lse, u = f64(s.out), f64(s.lse), U[s.dtype]
+    q, k, v = f64(s.q), f64(s.k[0]), f64(s.v[0])
+    for h in range(s.H):
+        kh, vh, qh = k[:, h // (s.H // s.KH)], v[:, h // (s.H // s.KH)], q[:, h]
+        some = sees.any(0)  # (what no token sees may be anything)
+        kh, vh = np.where(some[:, None], kh, 0.0), np.where(some[:, None], vh, 0.0)
+        x = np.where(sees, s.scale * (qh @ kh.T), -np.inf)
+        top = x.max(1, initial=-np.inf, keepdims=True)
+        top = np.where(np.isinf(top), 0.0, top)
+        p = np.exp(x - top)
+        l = p.sum(1, keepdims=True)
+        p = p / np.where(l == 0, 1, l)
+        ref, A = p @ vh, p @ np.abs(vh)
+        off = 2.0 ** -20 * s.scale * (np.linalg.norm(qh, axis=1) * np.linalg.norm(kh, axis=1).max(initial=0.0))[:, None]
+        err = np.abs(out[:, h] - ref)
+        assert np.all(err <= u * np.abs(ref) + (u + 4 * off + 2.0 ** -18) * A + TINY[s.dtype]), (h, np.nanmax(err))
+        empty = l[:, 0] == 0
+        assert np.array_equal(np.isneginf(lse[:, h]), empty)
+        got, want = lse[~empty, h], (top[:, 0] + np.log(np.where(empty, 1.0, l[:, 0])))[~empty]
+        assert np.all(np.abs(got - want) <= off[~empty, 0] + 2.0 ** -20 * np.maximum(1, np.abs(want)))
+
+
+def window_sees(n, kv_len, window, readable):
+    pos, t = kv_len - n + np.arange(n), np.arange(max(kv_len, 1))
+    return (t[None] <= pos[:, None]) & (t[None] > pos[:, None] - window) & (t[None] < readable)
+
+
+# context, window; a context of 1000 lies wholly past the 256 tokens that may be read, one of 700 starts among them
+@pytest.mark.parametrize("new", [3, 100])
+@pytest.mark.parametrize("kv_len,window", [(1000, 500), (1000, 130), (700, 500), (700, 440), (360, 1), (355, 99)])
+@pytest.mark.parametrize("limit", ["table", "max_kv"])
+def test_window_past_the_keys_that_may_be_read(new, kv_len, window, limit, kernel):  # noqa: F811
+    """The row of the page table, or max_kv, ends at 256 tokens; what follows the row in memory is no page number, so an entry
+    read there would show in the device error word."""
+    s = Step(70 + new, [new], [kv_len], 8, 2, 64, 16, B16)
+    cols = 16
+    memory = torch.full((1 << 14,), 2 ** 30, dtype=torch.int32, device="cuda")
+    memory[:cols] = s.table[0, :cols]
+    s.table = memory[:cols].view(1, cols) if limit == "table" else memory[:kv_len // 16 + 1].view(1, -1)
+    qg.qgemv_device_error(reset=True)
+    qg.qgemv_attn(s.args(window=window, max_kv=kv_len if limit == "table" else 16 * cols))
+    check_seen(s, window_sees(new, kv_len, window, 16 * cols))
+    assert qg.qgemv_device_error() == 0
+    assert int(s.scratch[:qg.QGEMV_ATTN_SCRATCH_HEAD].sum()) == 0
 
 
 # --------------------------------------------------------------------------------------------------------- sampling
