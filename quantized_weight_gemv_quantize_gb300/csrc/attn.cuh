@@ -53,15 +53,20 @@ __device__ __forceinline__ Seq find_seq(const AttnArgs& a, int b) {
     return s;
 }
 
+// The first key that a token at position `pos` sees (any window: no difference leaves 32 bits).
+__device__ __forceinline__ int first_key(const AttnArgs& a, int pos) {
+    return a.window > 0 && pos >= a.window ? pos - a.window + 1 : 0;
+}
+
 // The keys that some row of [row0, row0 + rows) sees, from a multiple of `step` on (the keys before the first are masked like any
 // other).  Where there are none, hi = lo: the rounding comes first, so that nothing beyond the keys that may be read is in the range.
 __device__ __forceinline__ void find_keys(const AttnArgs& a, const Seq& s, int row0, int rows, int step, int* lo, int* hi) {
-    *lo = a.window > 0 ? max(0, s.first_pos + div_by(row0, a.group, a.group_shift) - a.window + 1) / step * step : 0;
+    *lo = first_key(a, s.first_pos + div_by(row0, a.group, a.group_shift)) / step * step;
     *hi = a.causal ? min(s.usable, s.first_pos + div_by(row0 + rows - 1, a.group, a.group_shift) + 1) : s.usable;
     *hi = max(*hi, *lo);
 }
 
-// Positions of the keys that row `r` of the tile sees: first_key(r) <= t <= last_key(r).
+// Position of row `r` of the tile: it sees the keys from first_key to (under a causal mask) its own position.
 __device__ __forceinline__ int row_pos(const AttnArgs& a, const Tile& t, int r) {
     return t.first_pos + div_by(t.row0 + r, a.group, a.group_shift);
 }

@@ -153,7 +153,7 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Tile& t, long lo
     for (int hh = 0; hh < 2; ++hh) {
         const int pos = row_pos(a, t, lane / 4 + 8 * hh);
         hi[hh] = a.causal ? min(t.k1 - 1, pos) : t.k1 - 1;
-        lo[hh] = a.window > 0 ? pos - a.window + 1 : 0;
+        lo[hh] = first_key(a, pos);
     }
 
     float o[DP / 8][4];

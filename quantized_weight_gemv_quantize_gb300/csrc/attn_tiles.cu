@@ -520,7 +520,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) attn_tiles_kernel(const __gri
                 continue;
             }
             const int pos = row_pos(a, t, r);
-            const int hi = a.causal ? min(t.k1 - 1, pos) : t.k1 - 1, lo = a.window > 0 ? pos - a.window + 1 : 0;
+            const int hi = a.causal ? min(t.k1 - 1, pos) : t.k1 - 1, lo = first_key(a, pos);
             float m = NEG_INF, l = 0.f;  // m: the maximum in use, in units of the scaled scores (base 2)
             for (int j = 0; j < blocks; ++j, ++g) {
                 if (!(ok = await(sh.s_full[i], round++))) break;

@@ -49,7 +49,7 @@ def check_seen(s, sees):
 
 
 def window_sees(n, kv_len, window, readable):
-    pos, t = kv_len - n + np.arange(n), np.arange(max(kv_len, 1))
+    pos, t = kv_len - n + np.arange(n, dtype=np.int64), np.arange(kv_len)
     return (t[None] <= pos[:, None]) & (t[None] > pos[:, None] - window) & (t[None] < readable)
 
 
@@ -70,6 +70,19 @@ def test_window_past_the_keys_that_may_be_read(new, kv_len, window, limit, kerne
     check_seen(s, window_sees(new, kv_len, window, 16 * cols))
     assert qg.qgemv_device_error() == 0
     assert int(s.scratch[:qg.QGEMV_ATTN_SCRATCH_HEAD].sum()) == 0
+
+
+@pytest.mark.parametrize("new,kv_len", [(3, 1), (20, 2), (20, 0), (200, 90), (300, 300), (5, 700)])
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 2, 2 ** 30, 90, 91])
+def test_window_of_any_size(new, kv_len, window, kernel):  # noqa: F811
+    """A window longer than any context masks nothing, also where tokens sit at positions below 0."""
+    s = Step(80 + new, [new], [kv_len], 8, 2, 64, 16, B16)
+    qg.qgemv_attn(s.args(window=window))
+    check_seen(s, window_sees(new, kv_len, window, kv_len))
+    if window >= 2 ** 30:
+        plain = (s.out.clone(), s.lse.clone())
+        qg.qgemv_attn(s.args())
+        assert torch.equal(plain[0], s.out) and torch.equal(plain[1], s.lse)
 
 
 # --------------------------------------------------------------------------------------------------------- sampling
