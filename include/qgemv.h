@@ -516,7 +516,9 @@ QGEMV_API int qgemv_rope(const qgemv_rope_args* args, unsigned flags, void* stre
  * values on the device must keep to them: tokens beyond max_q are left unwritten, context beyond max_kv or beyond the
  * row of the page table (pages_stride * page_size) is not read.  A page number outside the cache reads as if its tokens
  * were masked and sets QGEMV_DEVERR_BAD_INDEX in the device error word.
- * What lies in the cache beyond kv_len is never used, whatever its bits.  Keys and values inside the context must be finite.
+ * What lies in the cache beyond kv_len, or before the window of a sequence's first new token, is never used, whatever its bits, and the
+ * pages that lie there wholly are not looked up (their entries may be anything).  Keys and values that some token of the call sees must
+ * be finite.
  * scratch: at least qgemv_attn_scratch_bytes(...) bytes, 16-byte aligned, whose first QGEMV_ATTN_SCRATCH_HEAD bytes must be
  * zero before the first call (e.g. cudaMemset once); each call leaves them zero again, so calls of any sizes may share one
  * scratch that is large enough for each.  Calls that share a scratch must be ordered.

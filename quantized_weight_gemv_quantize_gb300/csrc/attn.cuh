@@ -35,6 +35,7 @@ struct Tile {
     int row0, rows;                 // first row, and rows in the tile
     int q0;                         // first new token of the sequence in q
     int first_pos;                  // position of the sequence's new token 0
+    int first;                      // the first key that a row of the tile sees: those of its key tile before it are as if missing
     int k0, k1;                     // keys of this part
     long long index;                // number of the row tile, for the records of its parts
 };
@@ -58,12 +59,14 @@ __device__ __forceinline__ int first_key(const AttnArgs& a, int pos) {
     return a.window > 0 && pos >= a.window ? pos - a.window + 1 : 0;
 }
 
-// The keys that some row of [row0, row0 + rows) sees, from a multiple of `step` on (the keys before the first are masked like any
-// other).  Where there are none, hi = lo: the rounding comes first, so that nothing beyond the keys that may be read is in the range.
-__device__ __forceinline__ void find_keys(const AttnArgs& a, const Seq& s, int row0, int rows, int step, int* lo, int* hi) {
-    *lo = first_key(a, s.first_pos + div_by(row0, a.group, a.group_shift)) / step * step;
+// The keys that some row of [row0, row0 + rows) sees, from a multiple of `step` on; returns the first one seen.  Where there are
+// none, hi = lo: the rounding comes first, so that nothing beyond the keys that may be read is in the range.
+__device__ __forceinline__ int find_keys(const AttnArgs& a, const Seq& s, int row0, int rows, int step, int* lo, int* hi) {
+    const int first = first_key(a, s.first_pos + div_by(row0, a.group, a.group_shift));
+    *lo = first / step * step;
     *hi = a.causal ? min(s.usable, s.first_pos + div_by(row0 + rows - 1, a.group, a.group_shift) + 1) : s.usable;
     *hi = max(*hi, *lo);
+    return first;
 }
 
 // Position of row `r` of the tile: it sees the keys from first_key to (under a causal mask) its own position.

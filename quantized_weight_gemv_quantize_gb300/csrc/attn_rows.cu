@@ -84,7 +84,7 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Tile& t, long lo
     auto look_up = [&](int key) {
         const int nth = div_by(key, a.page_size, a.page_shift);
         Where w = {-1, key - nth * a.page_size};
-        if (key < t.k1) {
+        if (key < t.k1 && (one_page || key >= t.first)) {  // (with one page a piece, that of the piece's first key holds all others)
             w.page = table[nth];
             if (w.page < 0 || w.page >= a.num_pages) atomicOr(a.err, ERR_BAD_INDEX), w.page = -1;
         }
@@ -105,6 +105,7 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Tile& t, long lo
             const int page = __shfl_sync(0xffffffffu, batch.page, i % 32), token = __shfl_sync(0xffffffffu, batch.token, i % 32) + r_in;
             const int left = page < 0 ? 0 : t.k1 - key_of(i);
             live = left <= 0 ? 0u : left >= 16 ? 0xffffu : (1u << left) - 1u;
+            live &= 0xffffu << max(0, t.first - key_of(i));  // (pieces start at most 15 keys before the first)
             const uint16_t* k = live ? kh + page * a.k_page + token * a.k_token + c * 8 : a.k;
             const uint16_t* v = live ? vh + page * a.v_page + token * a.v_token + c * 8 : a.v;
             const long long k_step = live ? STEP * a.k_token : 0, v_step = live ? STEP * a.v_token : 0;
@@ -402,7 +403,7 @@ __global__ void __launch_bounds__(RowsShape<DP>::WARPS * 32) attn_rows_kernel(co
         }
         t.rows = min(16, sq.n * a.group - t.row0);
         int lo, hi;
-        find_keys(a, sq, t.row0, t.rows, 16, &lo, &hi);
+        t.first = find_keys(a, sq, t.row0, t.rows, 16, &lo, &hi);
         t.k0 = lo + static_cast<int>(min(static_cast<unsigned long long>(hi - lo), static_cast<unsigned long long>(pos - tile_at) << unit));
         t.k1 = lo + static_cast<int>(min(static_cast<unsigned long long>(hi - lo), static_cast<unsigned long long>(stop - tile_at) << unit));
         // the blocks with the row tile's first and last part: this one where the tile begins or ends here

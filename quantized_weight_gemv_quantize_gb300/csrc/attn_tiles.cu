@@ -192,7 +192,7 @@ __device__ __forceinline__ bool find_tile(const AttnArgs& a, long long block, Ti
     t->rows = min(2 * TR, s.n * a.group - t->row0);
     if (t->rows <= 0) return false;
     int lo, hi;
-    find_keys(a, s, t->row0, t->rows, TK, &lo, &hi);  // key tiles start at multiples of their size
+    t->first = find_keys(a, s, t->row0, t->rows, TK, &lo, &hi);  // key tiles start at multiples of their size
     const int chunk = of_parts < 0 ? max(hi - lo, 1) : a.chunk;
     t->parts = max(1, (hi - lo + chunk - 1) / chunk);
     t->k0 = lo + t->part * chunk;
@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) attn_tiles_kernel(const __gri
                     for (int h = 0; h < 4; ++h) {
                         const int key = t.k0 + j * TK + h * 32 + lane, nth = div_by(key, a.page_size, a.page_shift);
                         token[h] = key - nth * a.page_size;
-                        page[h] = key < t.k1 ? table[nth] : -1;
+                        page[h] = key >= t.first && key < t.k1 ? table[nth] : -1;
                     }
                 };
                 auto of_row = [&](const int (&v)[4], int row) {
@@ -335,7 +335,8 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) attn_tiles_kernel(const __gri
 #pragma unroll
                     for (int h = 0; h < 4; ++h) {
                         const bool live = page[h] >= 0 && page[h] < a.num_pages;
-                        if (!live && !side && t.k0 + j * TK + h * 32 + lane < t.k1) atomicOr(a.err, ERR_BAD_INDEX);
+                        const int key = t.k0 + j * TK + h * 32 + lane;
+                        if (!live && !side && key >= t.first && key < t.k1) atomicOr(a.err, ERR_BAD_INDEX);
                         if (!live) page[h] = -1;
                         const uint32_t mask = __ballot_sync(0xffffffffu, live);
                         if (!side && lane == 0) sh.live[g & 3][h] = mask;
@@ -354,17 +355,16 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) attn_tiles_kernel(const __gri
                         }
                     } else {  // row by row, the missing ones as zeros
                         const int c = lane % PER_ROW;
-#pragma unroll 8
-                        for (int r0 = 0; r0 < TK; r0 += 32 / PER_ROW) {
-                            const int r = r0 + lane / PER_ROW;
-                            int pg = 0, tk = 0;
 #pragma unroll
-                            for (int h = 0; h < 32 / PER_ROW; ++h) {
-                                const int p = of_row(page, r0 + h), k = of_row(token, r0 + h);
-                                if (h == lane / PER_ROW) pg = p, tk = k;
+                        for (int h = 0; h < 4; ++h) {
+                            // where this lane's key lies; its row's lanes ask for it
+                            const long long at = page[h] < 0 ? -1 : page[h] * page_stride + token[h] * token_stride;
+#pragma unroll 4
+                            for (int r0 = 0; r0 < 32; r0 += 32 / PER_ROW) {
+                                const long long off = __shfl_sync(0xffffffffu, at, r0 + lane / PER_ROW);
+                                const bool in = off >= 0 && c * 8 < a.dim;
+                                cp16(place(to, h * 32 + r0 + lane / PER_ROW, c), src + (in ? off + c * 8 : 0), in);
                             }
-                            const bool in = pg >= 0 && c * 8 < a.dim;
-                            cp16(place(to, r, c), src + (in ? pg * page_stride + tk * token_stride + c * 8 : 0), in);
                         }
                         // the barrier counts this lane's arrival when its copies have landed; the lane itself goes on
                         asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");

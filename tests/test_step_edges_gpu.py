@@ -85,6 +85,23 @@ def test_window_of_any_size(new, kv_len, window, kernel):  # noqa: F811
         assert torch.equal(plain[0], s.out) and torch.equal(plain[1], s.lse)
 
 
+@pytest.mark.parametrize("page", [1, 7, 16, 64])
+@pytest.mark.parametrize("new,kv_len,window", [(1, 1000, 100), (3, 999, 333), (40, 1000, 129), (150, 1500, 201), (300, 700, 37)])
+def test_window_leaves_what_lies_before_it_alone(new, kv_len, window, page, kernel):  # noqa: F811
+    """Keys and values before the first token's window may be anything, and their pages given back (a table entry of -1)."""
+    s = Step(90 + page, [new], [kv_len], 8, 2, 128, page, B16)
+    sees = window_sees(new, kv_len, window, kv_len)
+    first = int(sees.any(0).argmax())
+    t = torch.arange(first, device="cuda")
+    for x in (s.kc, s.vc):
+        x[s.table[0, t // page].long(), t % page] = float("nan")
+    s.table[0, :first // page] = -1
+    qg.qgemv_device_error(reset=True)
+    qg.qgemv_attn(s.args(window=window))
+    assert qg.qgemv_device_error(reset=True) == 0
+    check_seen(s, sees)
+
+
 # --------------------------------------------------------------------------------------------------------- sampling
 
 # rows of two, four and eight blocks, the last of them with and without an odd end
