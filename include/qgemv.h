@@ -409,6 +409,7 @@ QGEMV_API int qgemv_trace_read(unsigned long long* host, size_t bytes, int* laun
  * attention of new tokens over that cache, and sampling from the lm_head's logits.  They follow the common
  * rules above (caller-owned device memory, host-side checks before anything is enqueued, results in stream
  * order, QGEMV_FLAG_PDL) and serve any number of tokens, not only 1..16.  They serve inference: no gradients.
+ * Strides go up to 2^40 elements; a tensor, cache or page table that spans more than 9e15 elements is refused as unsupported.
  */
 
 /*

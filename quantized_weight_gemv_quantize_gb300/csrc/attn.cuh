@@ -50,7 +50,7 @@ __device__ __forceinline__ Seq find_seq(const AttnArgs& a, int b) {
     const int n = max(0, min(a.q_start[b + 1], a.tokens) - s.q0), len = max(0, a.kv_len[b]);
     s.first_pos = len - n;
     s.n = min(n, a.max_q);
-    s.usable = static_cast<int>(min(static_cast<long long>(min(len, a.max_kv)), a.pages_stride * a.page_size));
+    s.usable = min(len, a.max_kv);
     return s;
 }
 

@@ -45,7 +45,8 @@ struct AttnArgs {
     float* part_sum;    // and dim unnormalised sums of values
     unsigned* err;
     int num_pages, page_size, kv_heads, dim;
-    int tokens, heads, group, seqs, max_q, max_kv;
+    int tokens, heads, group, seqs, max_q;
+    int max_kv;  // bound of the keys that may be read: the caller's, or what a row of the page table reaches
     int group_shift, page_shift;  // log2 of group and page_size, -1 where they are no powers of two
     float scale_log2;   // scale * log2(e): the softmax runs in base 2
     int causal, window;

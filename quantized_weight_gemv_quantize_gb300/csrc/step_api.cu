@@ -17,6 +17,9 @@ static int elem_size(int kind) {
     return kind == QGEMV_ACT_F32 ? 4 : kind == QGEMV_ACT_BF16 || kind == QGEMV_ACT_F16 ? 2 : 0;
 }
 
+// Elements that a tensor may span: beyond any memory, and its bytes and addresses stay within 64 bits.
+constexpr double SPAN_MAX = 9e15;
+
 // A tensor [n0, n1, dim] with strides s0, s1 (elements of `size` bytes), as the memory it covers.
 struct Region {
     const void* p;
@@ -26,8 +29,13 @@ struct Region {
         if (n0 < 1 || n1 < 1) return 0;
         return static_cast<size_t>((n0 - 1) * s0 + (n1 - 1) * s1 + dim) * size;
     }
-    bool ok() const {  // strides in range, and no product below overflows
-        return s0 >= 0 && s1 >= 0 && s0 <= (1ll << 40) && s1 <= (1ll << 40) && (s0 * size) % 16 == 0 && (s1 * size) % 16 == 0;
+    // Strides in range (each up to 2^40, and the span that they and the sizes make), rows at multiples of 16 bytes and `step` elements.
+    int check(int step) const {
+        if (s0 < 0 || s1 < 0 || s0 > (1ll << 40) || s1 > (1ll << 40)) return QGEMV_ERR_INVALID_ARG;
+        if ((s0 * size) % 16 || (s1 * size) % 16 || s0 % step || s1 % step || !api_aligned(p, 16)) return QGEMV_ERR_MISALIGNED;
+        if (static_cast<double>(n0) * static_cast<double>(s0) + static_cast<double>(n1) * static_cast<double>(s1) > SPAN_MAX)
+            return QGEMV_ERR_UNSUPPORTED;
+        return QGEMV_OK;
     }
 };
 
@@ -67,10 +75,10 @@ static int check_cache(const qgemv_cache* c) {
         if (v < 0 || v > (1ll << 40)) return QGEMV_ERR_INVALID_ARG;
         if (v % 8) return QGEMV_ERR_MISALIGNED;
     }
-    // no product of the kernels' offset arithmetic leaves 64 bits: 2^31 pages of strides below 2^31 elements or fewer
-    // pages of larger ones
-    const double span = static_cast<double>(c->num_pages) * (c->k_page > c->v_page ? c->k_page : c->v_page);
-    if (span > 9e15) return QGEMV_ERR_UNSUPPORTED;
+    for (int i = 0; i < 6; i += 3)  // no offset of the kernels' arithmetic leaves 64 bits
+        if (static_cast<double>(c->num_pages) * static_cast<double>(s[i]) + static_cast<double>(c->page_size) * static_cast<double>(s[i + 1]) +
+                static_cast<double>(c->heads) * static_cast<double>(s[i + 2]) > SPAN_MAX)
+            return QGEMV_ERR_UNSUPPORTED;
     if (!api_aligned(c->k, 16) || !api_aligned(c->v, 16)) return QGEMV_ERR_MISALIGNED;
     return QGEMV_OK;
 }
@@ -105,8 +113,7 @@ static int run_rope(const qgemv_rope_args* a, unsigned flags, void* stream) {
     const Region* all[5] = {&q, &k, &v, &qo, &ko};
     for (const Region* r : all) {
         if (!r->p) continue;
-        if (r->s0 < 0 || r->s1 < 0 || r->s0 > (1ll << 40) || r->s1 > (1ll << 40)) return QGEMV_ERR_INVALID_ARG;
-        if (!r->ok() || r->s0 % 8 || r->s1 % 8 || !api_aligned(r->p, 16)) return QGEMV_ERR_MISALIGNED;
+        if ((st = r->check(8))) return st;
     }
     if (!api_aligned(a->positions, 4) || !api_aligned(a->freqs, 8) || (a->slots && !api_aligned(a->slots, 8)))
         return QGEMV_ERR_MISALIGNED;
@@ -197,7 +204,7 @@ static int attn_plan(int seqs, int tokens, int heads, int kv_heads, int dim, int
     const long long full = tiles / SMS * SMS;
     long long best = 1, best_whole = 0;
     double tiles_us = 0;
-    for (long long n = 1; n <= 32 && (n == 1 || n * 8 <= blocks); ++n)
+    for (long long n = 1; n <= 32 && (n == 1 || (n * 8 <= blocks && tiles <= INT_MAX)); ++n)
         for (const long long whole : {0ll, full}) {
             if (whole > 0 && (n == 1 || whole == tiles)) continue;
             if (n > 1 && (tiles - whole) * n > 16 * SMS) continue;
@@ -310,14 +317,17 @@ static int run_attn(const qgemv_attn_args* a, unsigned flags, void* stream) {
     if (!(a->scale > 0.f && a->scale <= 1e30f)) return QGEMV_ERR_INVALID_ARG;  // NaN too
     AttnPlan p;
     if ((st = attn_plan(a->seqs, a->tokens, a->heads, c.heads, c.dim, a->max_q, a->max_kv, &p))) return st;
-    if (a->pages_stride > (1ll << 40)) return QGEMV_ERR_UNSUPPORTED;
+    if (a->pages_stride > (1ll << 40) || static_cast<double>(a->seqs) * static_cast<double>(a->pages_stride) > SPAN_MAX)
+        return QGEMV_ERR_UNSUPPORTED;
+    // The keys that a row of the page table reaches, and the entries of a row that may be read.
+    const long long pages = (static_cast<long long>(a->max_kv) + c.page_size - 1) / c.page_size;
+    const int reach = a->pages_stride < pages ? static_cast<int>(a->pages_stride * c.page_size) : a->max_kv;
+    const long long entries = a->pages_stride < pages ? a->pages_stride : pages;
     if (a->scratch_bytes < p.scratch) return QGEMV_ERR_INVALID_ARG;
     const Region q = {a->q, a->tokens, a->q_token, a->heads, a->q_head, c.dim, 2};
     const Region o = {a->out, a->tokens, a->out_token, a->heads, a->out_head, c.dim, 2};
-    for (const Region* r : {&q, &o}) {
-        if (r->s0 < 0 || r->s1 < 0 || r->s0 > (1ll << 40) || r->s1 > (1ll << 40)) return QGEMV_ERR_INVALID_ARG;
-        if (!r->ok() || !api_aligned(r->p, 16)) return QGEMV_ERR_MISALIGNED;
-    }
+    for (const Region* r : {&q, &o})
+        if ((st = r->check(1))) return st;
     if (!api_aligned(a->scratch, 16) || !api_aligned(a->pages, 4) || !api_aligned(a->q_start, 4) || !api_aligned(a->kv_len, 4) ||
         (a->lse && !api_aligned(a->lse, 4)))
         return QGEMV_ERR_MISALIGNED;
@@ -326,7 +336,7 @@ static int run_attn(const qgemv_attn_args* a, unsigned flags, void* stream) {
     struct Span { const void* p; size_t n; };
     const Span in[] = {{c.k, cache_bytes(c, c.k_page, c.k_token, c.k_head)},
                        {c.v, cache_bytes(c, c.v_page, c.v_token, c.v_head)},
-                       {a->pages, (static_cast<size_t>(a->seqs) * a->pages_stride) * 4},
+                       {a->pages, static_cast<size_t>((a->seqs - 1) * a->pages_stride + entries) * 4},
                        {a->q_start, (static_cast<size_t>(a->seqs) + 1) * 4},
                        {a->kv_len, static_cast<size_t>(a->seqs) * 4}};
     const size_t lse_bytes = a->lse ? static_cast<size_t>(a->tokens) * a->heads * 4 : 0;
@@ -356,7 +366,7 @@ static int run_attn(const qgemv_attn_args* a, unsigned flags, void* stream) {
     k.part_sum = reinterpret_cast<float*>(parts + round32(p.records * sizeof(float2)));
     k.err = err, k.num_pages = c.num_pages, k.page_size = c.page_size, k.kv_heads = c.heads, k.dim = c.dim;
     k.tokens = a->tokens, k.heads = a->heads, k.group = a->heads / c.heads, k.seqs = a->seqs;
-    k.max_q = a->max_q, k.max_kv = a->max_kv;
+    k.max_q = a->max_q, k.max_kv = reach;
     auto log2_of = [](int v) {
         int n = 0;
         while (1 << n < v) ++n;
@@ -409,7 +419,8 @@ static int run_sample(const SampleArgs& s, int kind, unsigned flags, void* strea
     const int size = elem_size(kind);
     if (!size || (flags & ~QGEMV_FLAG_PDL)) return QGEMV_ERR_INVALID_ARG;
     if (s.m < 0 || s.N < 1 || s.row_stride < s.N || !s.x || !s.u || !s.token) return QGEMV_ERR_INVALID_ARG;
-    if (s.N > 1 << 20 || s.row_stride > (1ll << 40)) return QGEMV_ERR_UNSUPPORTED;
+    if (s.N > 1 << 20 || s.row_stride > (1ll << 40) || static_cast<double>(s.m) * static_cast<double>(s.row_stride) > SPAN_MAX)
+        return QGEMV_ERR_UNSUPPORTED;
     if (!api_aligned(s.x, 16)) return QGEMV_ERR_MISALIGNED;
     const void* words[] = {s.temperature, s.top_k, s.top_p, s.min_p, s.u, s.token, s.prob};
     for (const void* w : words)

@@ -72,6 +72,17 @@ def test_window_past_the_keys_that_may_be_read(new, kv_len, window, limit, kerne
     assert int(s.scratch[:qg.QGEMV_ATTN_SCRATCH_HEAD].sum()) == 0
 
 
+@pytest.mark.parametrize("new", [2, 100])
+def test_a_table_row_and_a_page_whose_product_leaves_64_bits(new, kernel):  # noqa: F811
+    """One page of 2^24 tokens, and rows of the table 2^40 entries apart: a row reaches further than any context."""
+    page, kv_len = 1 << 24, 1200
+    s = Step(75, [new], [kv_len], 4, 1, 8, page, B16)
+    a = s.args()
+    a.pages_stride = 1 << 40
+    qg.qgemv_attn(a)
+    s.check()
+
+
 @pytest.mark.parametrize("new,kv_len", [(3, 1), (20, 2), (20, 0), (200, 90), (300, 300), (5, 700)])
 @pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 2, 2 ** 30, 90, 91])
 def test_window_of_any_size(new, kv_len, window, kernel):  # noqa: F811
