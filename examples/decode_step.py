@@ -42,7 +42,7 @@ class Decoder:
         freqs, self.mscale = qg.qgemv_rope_freqs(DIM, 1e6)
         self.freqs = freqs.cuda()
         self.kv_len = torch.zeros(seqs, dtype=torch.int32, device="cuda")
-        need = max(qg.qgemv_attn_scratch_bytes(seqs, seqs * n, HEADS, KV_HEADS, DIM, n, longest) for n in (1, 16 // seqs))
+        need = qg.qgemv_attn_scratch_bytes(seqs, 16, HEADS, KV_HEADS, DIM, 16 // seqs, longest)  # of every smaller call too
         self.scratch = torch.zeros(need, dtype=torch.uint8, device="cuda")
         self.buffers = {}
 

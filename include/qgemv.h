@@ -522,7 +522,7 @@ QGEMV_API int qgemv_rope(const qgemv_rope_args* args, unsigned flags, void* stre
  * be finite.
  * scratch: at least qgemv_attn_scratch_bytes(...) bytes, 16-byte aligned, whose first QGEMV_ATTN_SCRATCH_HEAD bytes must be
  * zero before the first call (e.g. cudaMemset once); each call leaves them zero again, so calls of any sizes may share one
- * scratch that is large enough for each.  Calls that share a scratch must be ordered.
+ * scratch that is large enough for each: that of the largest sizes is (see below).  Calls that share a scratch must be ordered.
  * The result does not depend on timing: parts of a long context are joined in a fixed order.
  * heads a multiple of cache->heads; 0 < scale <= 1e30.  tokens = 0 or seqs = 0 does nothing.
  */
@@ -546,7 +546,8 @@ typedef struct {
 } qgemv_attn_args;
 
 QGEMV_API int qgemv_attn(const qgemv_attn_args* args, unsigned flags, void* stream);
-/* Scratch of a call with these sizes (0 for invalid sizes).  No device needed. */
+/* Scratch that serves every call of these sizes or smaller seqs, tokens, max_q and max_kv, with these heads and any window (0 for invalid
+ * sizes).  It never falls as a size grows.  No device needed. */
 #define QGEMV_ATTN_SCRATCH_HEAD 65536
 QGEMV_API size_t qgemv_attn_scratch_bytes(int seqs, int tokens, int heads, int kv_heads, int dim, int max_q, int max_kv);
 

@@ -387,7 +387,7 @@ def qgemv_rope(args: QgemvRopeArgs, flags: int = 0, stream=None) -> None:
 
 
 def qgemv_attn_scratch_bytes(seqs: int, tokens: int, heads: int, kv_heads: int, dim: int, max_q: int, max_kv: int) -> int:
-    """Scratch of a qgemv_attn call with these sizes; its first QGEMV_ATTN_SCRATCH_HEAD bytes must start as zeros."""
+    """Scratch of every qgemv_attn call with these sizes or smaller seqs, tokens, max_q and max_kv; its first QGEMV_ATTN_SCRATCH_HEAD bytes must start as zeros."""
     return int(lib().qgemv_attn_scratch_bytes(seqs, tokens, heads, kv_heads, dim, max_q, max_kv))
 
 

@@ -72,8 +72,8 @@ struct AttnPlan {
     int chunk, parts, row_tiles, rows_part, whole, unit_shift;
     long long grid;
     size_t records, scratch;  // rows of parts' records, bytes of scratch
+    size_t scratch_most;      // scratch that serves every call of these sizes or smaller ones
 };
-
 
 const void* attn_rows_kernel_ptr(bool bf16, int dim, unsigned* smem, unsigned* threads);
 const void* attn_tiles_kernel_ptr(bool bf16, int dim, unsigned* smem, unsigned* threads);

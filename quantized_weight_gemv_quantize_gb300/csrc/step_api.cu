@@ -180,15 +180,30 @@ static std::atomic<int> g_attn_kernel{0};
 
 static size_t round32(size_t n) { return (n + 31) / 32 * 32; }
 
+constexpr int SMS = 152;
+
+// Parts that row tiles may be cut into, all together: as many waves of blocks as half the square root of the context's key tiles, at most
+// 16.  A wave costs its start and end, some 3 key tiles, so that more of them win nothing by the estimate below (the limit moves
+// nothing by more than 0.01 us, for 1 to 4000 row tiles over 8 to 2^23 key tiles); it bounds the scratch.
+static long long parts_max(long long blocks) {
+    const long long waves = static_cast<long long>(ceil(sqrt(static_cast<double>(blocks)) / 2));
+    return (waves < 16 ? waves : 16) * SMS;
+}
+// Blocks of the 16-row kernel: one wave, two an SM (one with the larger shared memory of long heads); each has records of 16 rows for two
+// parts of split row tiles.
+static int rows_grid(int dim) { return dim <= 128 ? 2 * SMS : SMS; }
+static size_t scratch_of(size_t records, int dim) {
+    return QGEMV_ATTN_SCRATCH_HEAD + round32(records * sizeof(float2)) + records * dim * sizeof(float);
+}
+
 static int attn_plan(int seqs, int tokens, int heads, int kv_heads, int dim, int max_q, int max_kv, AttnPlan* p) {
     if (seqs < 0 || tokens < 0 || heads < 1 || kv_heads < 1 || heads % kv_heads || dim < 8 || dim % 8 || max_q < 0 ||
         max_kv < 0)
         return QGEMV_ERR_INVALID_ARG;
     if (dim > 256 || heads > 65536) return QGEMV_ERR_UNSUPPORTED;
     *p = AttnPlan{};
-    p->scratch = QGEMV_ATTN_SCRATCH_HEAD;
+    p->scratch = p->scratch_most = QGEMV_ATTN_SCRATCH_HEAD;
     if (seqs == 0 || tokens == 0 || max_q == 0) return QGEMV_OK;
-    constexpr int SMS = 152;
     if (max_q > tokens) max_q = tokens;
     const long long rows = static_cast<long long>(max_q) * (heads / kv_heads);
     if (max_kv > 1 << 30 || (rows + 15) / 16 * kv_heads > INT_MAX || rows > INT_MAX) return QGEMV_ERR_UNSUPPORTED;
@@ -196,8 +211,7 @@ static int attn_plan(int seqs, int tokens, int heads, int kv_heads, int dim, int
     // end; waves of blocks, each as long as its part and about 3 key tiles for its start and end, at 1.4 a key tile; where parts are joined, 4
     // for the second kernel and their records, written and read at 5 TB/s.  Measured and by this rule: 32 and 8 heads of 128, 2000 tokens over 24000,
     // n = 1: 542 / 544, n = 2: 591 / 583, 4: 578 / 557, 8: 640 / 650; 1000 over 30000, n = 1: 346 / 342, 2: 375 / 365, 8: 405 / 390; 256 over 16000,
-    // n = 1: 182 / 188, 4: 64 / 69, 8: 74 / 80; 64 over 4000, n = 1: 56 / 58, 4: 30 / 30.  At most 32 parts of at least 8 key tiles, and no more
-    // than 16 waves of them.
+    // n = 1: 182 / 188, 4: 64 / 69, 8: 74 / 80; 64 over 4000, n = 1: 56 / 58, 4: 30 / 30.  At most 32 parts of at least 8 key tiles.
     const long long tiles = (rows + 255) / 256 * kv_heads * seqs, blocks = (static_cast<long long>(max_kv) + 127) / 128;
     // Or the row tiles that fill whole waves stay whole and only the rest is cut (1300 tokens over
     // 30000: 492 us with all cut alike, 419; 1500 over 20000: 368, 331; 2000 over 24000: 532 with none cut, 525).
@@ -207,7 +221,7 @@ static int attn_plan(int seqs, int tokens, int heads, int kv_heads, int dim, int
     for (long long n = 1; n <= 32 && (n == 1 || (n * 8 <= blocks && tiles <= INT_MAX)); ++n)
         for (const long long whole : {0ll, full}) {
             if (whole > 0 && (n == 1 || whole == tiles)) continue;
-            if (n > 1 && (tiles - whole) * n > 16 * SMS) continue;
+            if (n > 1 && (tiles - whole) * n > parts_max(blocks)) continue;
             const double part = static_cast<double>((blocks + n - 1) / n);
             const double waves = static_cast<double>(((tiles - whole) * n + SMS - 1) / SMS);
             const double records = n > 1 ? 8e-6 / 5 * static_cast<double>((tiles - whole) * n * (rows < 256 ? rows : 256) * dim) : 0;
@@ -225,9 +239,7 @@ static int attn_plan(int seqs, int tokens, int heads, int kv_heads, int dim, int
     p->tiles = dim <= 128 && (forced ? forced == 2 : rows > 32 && tiles_us < rows_us);
     size_t records = 0;
     if (!p->tiles) {
-        // One wave of blocks, two an SM (one with the larger shared memory of long heads); each has records of 16 rows for two
-        // parts of split row tiles.
-        p->grid = dim <= 128 ? 2 * SMS : SMS;
+        p->grid = rows_grid(dim);
         records = static_cast<size_t>(p->grid) * 2 * 16;
         // Units of 64 keys, longer ones where the bounds alone would let the whole (twice over, for its rounding) pass 32 bits.
         const double row_tiles = static_cast<double>((rows + 15) / 16) * kv_heads * seqs;
@@ -247,7 +259,16 @@ static int attn_plan(int seqs, int tokens, int heads, int kv_heads, int dim, int
         if (p->parts > 1) records = static_cast<size_t>(p->grid - p->whole) * p->rows_part;
     }
     p->records = records;
-    p->scratch += round32(records * sizeof(float2)) + records * dim * sizeof(float);
+    p->scratch = scratch_of(records, dim);
+    // What every call of these sizes or smaller ones is content with: the choices above do not grow with the sizes, these bounds do.
+    size_t most = dim <= 128 && forced == 2 ? 0 : static_cast<size_t>(rows_grid(dim)) * 2 * 16;
+    if (dim <= 128 && (forced ? forced == 2 : rows > 32) && blocks >= 16) {
+        const long long n = blocks / 8 < 32 ? blocks / 8 : 32, limit = parts_max(blocks);
+        const long long parts = tiles < limit && tiles * n < limit ? tiles * n : limit;
+        const size_t cut = static_cast<size_t>(parts) * (rows < 256 ? rows : 256);
+        if (cut > most) most = cut;
+    }
+    p->scratch_most = scratch_of(most, dim);
     return QGEMV_OK;
 }
 
@@ -524,7 +545,7 @@ void qgemv_tune_attn(int kernel) { g_attn_kernel.store(kernel == 1 || kernel == 
 
 size_t qgemv_attn_scratch_bytes(int seqs, int tokens, int heads, int kv_heads, int dim, int max_q, int max_kv) {
     AttnPlan p;
-    return attn_plan(seqs, tokens, heads, kv_heads, dim, max_q, max_kv, &p) ? 0 : (p.scratch + 255) / 256 * 256;
+    return attn_plan(seqs, tokens, heads, kv_heads, dim, max_q, max_kv, &p) ? 0 : (p.scratch_most + 255) / 256 * 256;
 }
 
 int qgemv_attn(const qgemv_attn_args* args, unsigned flags, void* stream) {

@@ -1,5 +1,7 @@
 """Edges of the operators between the GEMVs without a GPU: sizes at the ends of the arithmetic, the scratch over all sizes, what
 the binding takes."""
+import itertools
+
 import pytest
 
 import quantized_weight_gemv_quantize_gb300 as qg
@@ -43,3 +45,54 @@ def test_large_strides_of_small_tensors_are_taken(L):  # noqa: F811
     assert L.qgemv_attn(attn(pages=KC + (1 << 29), pages_stride=1 << 26, seqs=1, max_kv=600), 0, None) in (4, 5)
     assert L.qgemv_attn(attn(pages=QO - 256, pages_stride=1 << 26, seqs=1, max_kv=600), 0, None) in (4, 5)
     assert L.qgemv_attn(attn(pages=QO - 148, pages_stride=1 << 26, seqs=1, max_kv=600), 0, None) == 6
+
+
+# ------------------------------------------------------------------------------------------------------- the scratch
+
+SEQS, NEW, CONTEXT = (1, 2, 7, 48, 300), (1, 2, 8, 9, 16, 64, 250, 1056, 2000, 8192), (0, 1, 600, 4096, 24000, 32768, 131072, 1 << 20)
+
+
+@pytest.fixture(params=[0, 1, 2], ids=["planned", "16-row", "128-row"])
+def hook(request):
+    qg.qgemv_tune_attn(request.param)
+    yield
+    qg.qgemv_tune_attn(0)
+
+
+@pytest.mark.parametrize("heads,kv_heads,dim", [(32, 8, 128), (16, 8, 64), (8, 1, 96), (4, 4, 256)])
+def test_scratch_never_falls_as_a_size_grows(L, hook, heads, kv_heads, dim):  # noqa: F811
+    size = {(s, n, c): qg.qgemv_attn_scratch_bytes(s, s * n, heads, kv_heads, dim, n, c)
+            for s, n, c in itertools.product(SEQS, NEW, CONTEXT)}
+    assert min(size.values()) >= qg.QGEMV_ATTN_SCRATCH_HEAD
+    for (s, n, c), v in size.items():
+        for axis, steps in enumerate((SEQS, NEW, CONTEXT)):
+            at = (s, n, c)[axis]
+            if at != steps[-1]:
+                up = [s, n, c]
+                up[axis] = steps[steps.index(at) + 1]
+                assert size[tuple(up)] >= v, (s, n, c, up)
+
+
+def test_scratch_never_falls_from_one_length_to_the_next(L):  # noqa: F811
+    for new in (9, 40, 64, 500, 1000, 1056, 1250, 2000):
+        sizes = [qg.qgemv_attn_scratch_bytes(1, new, 32, 8, 128, new, c) for c in range(0, 1 << 19, 512)]
+        assert sizes == sorted(sizes)
+    for context in (3000, 24000, 131072):
+        sizes = [qg.qgemv_attn_scratch_bytes(1, n, 32, 8, 128, n, context) for n in range(1, 3000)]
+        assert sizes == sorted(sizes)
+        sizes = [qg.qgemv_attn_scratch_bytes(b, b * 40, 32, 8, 128, 40, context) for b in range(1, 400)]
+        assert sizes == sorted(sizes)
+
+
+@pytest.mark.skipif(HAS_GPU_NODE, reason="checks the no-GPU path only (fake addresses must never reach a GPU)")
+@pytest.mark.parametrize("dim", [64, 128])
+def test_scratch_of_the_largest_call_serves_the_smaller_ones(L, hook, dim):  # noqa: F811
+    one = cache(dim=dim, num_pages=1000)
+    for seqs, new, context in ((4, 8192, 131072), (1, 4864, 32768), (48, 16, 16384), (1, 2000, 24000)):
+        n = qg.qgemv_attn_scratch_bytes(seqs, seqs * new, 32, 8, dim, new, context)
+        for s, q, c in itertools.product(SEQS, (1, 2, 9, 17, 100, 130, 257, 1024, 1056, 2048, 4864, 8192), (1, 300, 2048, 9999, 24000, 32768, 131072)):
+            if s <= seqs and q <= new and c <= context:
+                for tokens in {s * q, s + q - 1}:  # every sequence's, and one long one beside single tokens
+                    call = attn(cache=one, tokens=tokens, seqs=s, max_q=q, max_kv=c, pages_stride=8192, scratch_bytes=n,
+                                q_token=32 * dim, q_head=dim, out_token=32 * dim, out_head=dim, scratch=1 << 45)
+                    assert L.qgemv_attn(call, 0, None) in (4, 5), (seqs, new, context, s, q, c)
