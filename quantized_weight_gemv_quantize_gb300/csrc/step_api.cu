@@ -196,7 +196,8 @@ static size_t scratch_of(size_t records, int dim) {
     return QGEMV_ATTN_SCRATCH_HEAD + round32(records * sizeof(float2)) + records * dim * sizeof(float);
 }
 
-static int attn_plan(int seqs, int tokens, int heads, int kv_heads, int dim, int max_q, int max_kv, AttnPlan* p) {
+static int attn_plan(int seqs, int tokens, int heads, int kv_heads, int dim, int max_q, int max_kv, int window,
+                     AttnPlan* p) {
     if (seqs < 0 || tokens < 0 || heads < 1 || kv_heads < 1 || heads % kv_heads || dim < 8 || dim % 8 || max_q < 0 ||
         max_kv < 0)
         return QGEMV_ERR_INVALID_ARG;
@@ -207,12 +208,20 @@ static int attn_plan(int seqs, int tokens, int heads, int kv_heads, int dim, int
     if (max_q > tokens) max_q = tokens;
     const long long rows = static_cast<long long>(max_q) * (heads / kv_heads);
     if (max_kv > 1 << 30 || (rows + 15) / 16 * kv_heads > INT_MAX || rows > INT_MAX) return QGEMV_ERR_UNSUPPORTED;
+    // Keys that a row tile goes over: the context, or with a window that of its first token to that of its last and what the rounding of the
+    // range adds.  (The 128-row kernel's parts rely on it.)
+    auto keys_of = [&](int tile, int step) {
+        const int group = heads / kv_heads, later = (tile - 1) / group + 1, span = max_q - 1 < later ? max_q - 1 : later;
+        const long long keys = static_cast<long long>(window) + span + step - 1;
+        return window > 0 && keys < max_kv ? static_cast<int>(keys) : max_kv;
+    };
+    const int keys = keys_of(256, 128);
     // The 128-row kernel: 256 rows a block, one block an SM, the row tiles' contexts in n parts.  Its time in us: 9 for the launch, start and
     // end; waves of blocks, each as long as its part and about 3 key tiles for its start and end, at 1.4 a key tile; where parts are joined, 4
     // for the second kernel and their records, written and read at 5 TB/s.  Measured and by this rule: 32 and 8 heads of 128, 2000 tokens over 24000,
     // n = 1: 542 / 544, n = 2: 591 / 583, 4: 578 / 557, 8: 640 / 650; 1000 over 30000, n = 1: 346 / 342, 2: 375 / 365, 8: 405 / 390; 256 over 16000,
     // n = 1: 182 / 188, 4: 64 / 69, 8: 74 / 80; 64 over 4000, n = 1: 56 / 58, 4: 30 / 30.  At most 32 parts of at least 8 key tiles.
-    const long long tiles = (rows + 255) / 256 * kv_heads * seqs, blocks = (static_cast<long long>(max_kv) + 127) / 128;
+    const long long tiles = (rows + 255) / 256 * kv_heads * seqs, blocks = (static_cast<long long>(keys) + 127) / 128;
     // Or the row tiles that fill whole waves stay whole and only the rest is cut (1300 tokens over
     // 30000: 492 us with all cut alike, 419; 1500 over 20000: 368, 331; 2000 over 24000: 532 with none cut, 525).
     const long long full = tiles / SMS * SMS;
@@ -233,7 +242,8 @@ static int attn_plan(int seqs, int tokens, int heads, int kv_heads, int dim, int
     // other's the longest's.  Measured, 8 key/value heads, 16-row against 128-row kernel in us: 64 rows over 4000 keys 18.5 / 26.7, 128 rows 24.6 / 27.9,
     // 256 rows 39.0 / 32.8; over 50000 keys 32 rows 51.2 / 52.4, 64 rows 84.5 / 53.0; 16 sequences of up to 8000: 32 rows 63.5 / 93.8, 48 rows
     // 78.7 / 94.4, 64 rows 141 / 94; 4 sequences of 300 with 64 tokens 18.5 / 18.5; 128 tokens alone 9.0 / 18.5, 256 over 1000 37.2 / 26.7.
-    const double keys16 = static_cast<double>((rows + 15) / 16) * kv_heads * seqs * max_kv;
+    // With a window of 1024 over 24000 keys 24 tokens 11.7 / 22.6, 128 tokens 20.5 / 26.7, 500 tokens 65.2 / 31.0.
+    const double keys16 = static_cast<double>((rows + 15) / 16) * kv_heads * seqs * keys_of(16, 16);
     const double rows_us = 8 + keys16 / 19000 * (seqs > 1 ? 0.75 : 1.0);
     const int forced = g_attn_kernel.load(std::memory_order_relaxed);
     p->tiles = dim <= 128 && (forced ? forced == 2 : rows > 32 && tiles_us < rows_us);
@@ -250,9 +260,9 @@ static int attn_plan(int seqs, int tokens, int heads, int kv_heads, int dim, int
         if (tiles > INT_MAX) return QGEMV_ERR_UNSUPPORTED;
         p->row_tiles = static_cast<int>((rows + 255) / 256);
         p->rows_part = static_cast<int>(rows < 256 ? rows : 256);
-        const long long chunk = ((max_kv + best - 1) / best + 127) / 128 * 128;
-        p->chunk = static_cast<int>(chunk < 128 ? 128 : chunk > INT_MAX - 127 ? INT_MAX - 127 : chunk);
-        p->parts = max_kv > 0 ? static_cast<int>((static_cast<long long>(max_kv) + p->chunk - 1) / p->chunk) : 1;
+        const long long chunk = ((keys + best - 1) / best + 127) / 128 * 128;
+        p->chunk = static_cast<int>(chunk < 128 ? 128 : chunk);
+        p->parts = keys > 0 ? static_cast<int>((static_cast<long long>(keys) + p->chunk - 1) / p->chunk) : 1;
         p->whole = p->parts > 1 ? static_cast<int>(best_whole) : 0;
         p->grid = p->whole + (tiles - p->whole) * p->parts;
         if (p->grid > INT_MAX) return QGEMV_ERR_UNSUPPORTED;
@@ -337,7 +347,7 @@ static int run_attn(const qgemv_attn_args* a, unsigned flags, void* stream) {
     if (c.kind != a->kind || a->tokens < 0 || a->seqs < 0 || a->pages_stride < 0 || a->window < 0) return QGEMV_ERR_INVALID_ARG;
     if (!(a->scale > 0.f && a->scale <= 1e30f)) return QGEMV_ERR_INVALID_ARG;  // NaN too
     AttnPlan p;
-    if ((st = attn_plan(a->seqs, a->tokens, a->heads, c.heads, c.dim, a->max_q, a->max_kv, &p))) return st;
+    if ((st = attn_plan(a->seqs, a->tokens, a->heads, c.heads, c.dim, a->max_q, a->max_kv, a->window, &p))) return st;
     if (a->pages_stride > (1ll << 40) || static_cast<double>(a->seqs) * static_cast<double>(a->pages_stride) > SPAN_MAX)
         return QGEMV_ERR_UNSUPPORTED;
     // The keys that a row of the page table reaches, and the entries of a row that may be read.
@@ -545,7 +555,7 @@ void qgemv_tune_attn(int kernel) { g_attn_kernel.store(kernel == 1 || kernel == 
 
 size_t qgemv_attn_scratch_bytes(int seqs, int tokens, int heads, int kv_heads, int dim, int max_q, int max_kv) {
     AttnPlan p;
-    return attn_plan(seqs, tokens, heads, kv_heads, dim, max_q, max_kv, &p) ? 0 : (p.scratch_most + 255) / 256 * 256;
+    return attn_plan(seqs, tokens, heads, kv_heads, dim, max_q, max_kv, 0, &p) ? 0 : (p.scratch_most + 255) / 256 * 256;
 }
 
 int qgemv_attn(const qgemv_attn_args* args, unsigned flags, void* stream) {

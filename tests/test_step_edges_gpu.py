@@ -113,6 +113,36 @@ def test_window_leaves_what_lies_before_it_alone(new, kv_len, window, page, kern
     check_seen(s, sees)
 
 
+@pytest.mark.parametrize("new,kv_len,window,route", [
+    (24, 24000, 1024, "rows"), (100, 24000, 300, "rows"), (16, 24000, 4000, "rows"),  # few keys a token: without the window, all take the other
+    (64, 24000, 15000, "tiles"), (500, 9000, 1024, "tiles"), (1300, 3000, 600, "tiles")])
+def test_window_decides_the_kernel_and_the_parts(new, kv_len, window, route):
+    s = Step(95, [new], [kv_len], 32, 8, 128, 64, B16)
+    if route == "rows":
+        qg.qgemv_route_reset()
+        qg.qgemv_attn(s.args())
+        assert qg.qgemv_route_counts()[qg.ROUTE_ATTN_TILES] == 1
+    qg.qgemv_route_reset()
+    qg.qgemv_attn(s.args(window=window))
+    assert qg.qgemv_route_counts()[{"rows": qg.ROUTE_ATTN_ROWS, "tiles": qg.ROUTE_ATTN_TILES}[route]] == 1
+    s.check(window=window)
+
+
+@pytest.mark.parametrize("H,KH", [(8, 8), (6, 2), (4, 1), (20, 1)])
+@pytest.mark.parametrize("new", [40, 333])
+@pytest.mark.parametrize("window", [900, 1900, 2047, 2500, 6000])
+def test_windows_whose_keys_are_cut_into_parts(new, window, H, KH):
+    """The 128-row kernel at windows around the lengths where a row tile's keys make one part more: tokens at every offset in a key tile."""
+    qg.qgemv_tune_attn(2)
+    try:
+        s = Step(96, [new, new // 3, 1], [6300, 2090 + new, 3001], H, KH, 64, 16, B16)
+        qg.qgemv_attn(s.args(window=window))
+        s.check(window=window)
+        assert int(s.scratch[:qg.QGEMV_ATTN_SCRATCH_HEAD].sum()) == 0
+    finally:
+        qg.qgemv_tune_attn(0)
+
+
 # --------------------------------------------------------------------------------------------------------- sampling
 
 # rows of two, four and eight blocks, the last of them with and without an odd end
