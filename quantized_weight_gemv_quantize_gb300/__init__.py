@@ -393,8 +393,8 @@ def qgemv_attn_scratch_bytes(seqs: int, tokens: int, heads: int, kv_heads: int, 
 
 def attn_args(q, cache: QgemvCache, pages, q_start, kv_len, out, scratch, max_q: int, max_kv: int, scale: float,
               causal: bool = True, window: int = 0, lse=None) -> QgemvAttnArgs:
-    """Arguments of qgemv_attn from tensors: q and out [tokens, heads, dim], pages int32 [seqs, pages of a row],
-    q_start int32 [seqs + 1], kv_len int32 [seqs], scratch uint8, lse fp32 [tokens, heads] or None.  The result holds the
+    """Arguments of qgemv_attn from tensors: q and out [tokens, heads, dim], pages int32 [seqs, pages of a row] (a view of longer
+    rows too, such as ``table[:, :n]``: context beyond its columns is not read), q_start int32 [seqs + 1], kv_len int32 [seqs], scratch uint8, lse fp32 [tokens, heads] or None.  The result holds the
     tensors' addresses and keeps the tensors alive; it may be used for many calls."""
     a = QgemvAttnArgs()
     a.q_token, a.q_head = _heads_first(q, "attn_args: q")
@@ -405,9 +405,11 @@ def attn_args(q, cache: QgemvCache, pages, q_start, kv_len, out, scratch, max_q:
     a.q, a.out, a.lse = _ptr(q), _ptr(out), _ptr(_typed(lse, "float32", "lse"))
     a.cache = ctypes.pointer(cache)
     a.seqs = pages.shape[0]
-    # the table's row: its stride when rows are apart, and no more of it than there is
-    _need(a.seqs <= 1 or pages.stride(0) == pages.shape[1], "attn_args: pages contiguous")
-    a.pages, a.pages_stride = _ptr(pages), pages.shape[1]
+    # the record's stride is also the length of a row: max_kv holds it to the columns there are
+    columns = pages.shape[1]
+    _need(a.seqs <= 1 or pages.stride(0) >= columns, "attn_args: rows of pages overlap")
+    a.pages, a.pages_stride = _ptr(pages), columns if a.seqs <= 1 or columns == 0 else pages.stride(0)
+    max_kv = min(max_kv, columns * cache.page_size)
     a.q_start, a.kv_len = _ptr(_typed(q_start, "int32", "q_start")), _ptr(_typed(kv_len, "int32", "kv_len"))
     _need(isinstance(q_start, int) or q_start.numel() == a.seqs + 1, "attn_args: q_start has seqs + 1 values")
     _need(isinstance(kv_len, int) or kv_len.numel() == a.seqs, "attn_args: kv_len has seqs values")

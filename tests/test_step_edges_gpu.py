@@ -72,6 +72,16 @@ def test_window_past_the_keys_that_may_be_read(new, kv_len, window, limit, kerne
     assert int(s.scratch[:qg.QGEMV_ATTN_SCRATCH_HEAD].sum()) == 0
 
 
+@pytest.mark.parametrize("new,ctx", [([1, 1, 3], [900, 40, 500]), ([150, 20, 1], [900, 40, 700])])
+def test_a_view_of_a_longer_page_table(new, ctx, kernel):  # noqa: F811
+    s = Step(76, new, ctx, 8, 2, 128, 16, B16)
+    whole = torch.full((3, 500), 2 ** 30, dtype=torch.int32, device="cuda")  # a fixed table; this step needs a few of its columns
+    whole[:, 2:2 + s.table.shape[1]] = s.table
+    s.table = whole[:, 2:2 + s.table.shape[1]]
+    qg.qgemv_attn(s.args(max_kv=5000))
+    s.check()
+
+
 @pytest.mark.parametrize("new", [2, 100])
 def test_a_table_row_and_a_page_whose_product_leaves_64_bits(new, kernel):  # noqa: F811
     """One page of 2^24 tokens, and rows of the table 2^40 entries apart: a row reaches further than any context."""

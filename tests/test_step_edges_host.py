@@ -96,3 +96,29 @@ def test_scratch_of_the_largest_call_serves_the_smaller_ones(L, hook, dim):  # n
                     call = attn(cache=one, tokens=tokens, seqs=s, max_q=q, max_kv=c, pages_stride=8192, scratch_bytes=n,
                                 q_token=32 * dim, q_head=dim, out_token=32 * dim, out_head=dim, scratch=1 << 45)
                     assert L.qgemv_attn(call, 0, None) in (4, 5), (seqs, new, context, s, q, c)
+
+
+# ------------------------------------------------------------------------------------------------------- the binding
+
+def record(pages, max_kv, scratch=None):
+    q = torch.zeros(5, 4, 64, dtype=torch.bfloat16)
+    kv = qg.kv_cache(*(torch.zeros(30, 16, 2, 64, dtype=torch.bfloat16) for _ in range(2)))
+    scratch = torch.zeros(1 << 20, dtype=torch.uint8) if scratch is None else scratch
+    return qg.attn_args(q, kv, pages, torch.zeros(pages.shape[0] + 1, dtype=torch.int32), torch.zeros(pages.shape[0], dtype=torch.int32),
+                        torch.empty_like(q), scratch, 1, max_kv, 0.1)
+
+
+def test_binding_takes_a_view_of_a_longer_page_table():
+    table = torch.zeros(5, 64, dtype=torch.int32)
+    a = record(table[:, 3:13], 1000)
+    assert (a.pages, a.pages_stride, a.seqs, a.max_kv) == (table.data_ptr() + 12, 64, 5, 160)
+    assert record(table[:, :13], 100).max_kv == 100
+    a = record(table, 2000)
+    assert (a.pages_stride, a.max_kv) == (64, 1024)
+    a = record(table[2:3, :7], 2000)  # a single row: no stride is needed
+    assert (a.pages_stride, a.max_kv) == (7, 112)
+    a = record(table[:, :0], 2000)
+    assert (a.pages_stride, a.max_kv) == (0, 0)
+    for bad in (table.t(), table[0].expand(5, 64), table.long(), table[0]):
+        with pytest.raises(qg.QgemvError):
+            record(bad, 100)
