@@ -414,6 +414,7 @@ def attn_args(q, cache: QgemvCache, pages, q_start, kv_len, out, scratch, max_q:
     _need(isinstance(q_start, int) or q_start.numel() == a.seqs + 1, "attn_args: q_start has seqs + 1 values")
     _need(isinstance(kv_len, int) or kv_len.numel() == a.seqs, "attn_args: kv_len has seqs values")
     _need(lse is None or isinstance(lse, int) or lse.shape == q.shape[:2], "attn_args: lse [tokens, heads]")
+    _need(scratch.is_contiguous(), "attn_args: scratch contiguous")
     a.scratch, a.scratch_bytes = _ptr(scratch), scratch.numel() * scratch.element_size()
     a.kind, a.tokens, a.heads = _kind(q), q.shape[0], q.shape[1]
     a.max_q, a.max_kv, a.scale, a.causal, a.window = max_q, max_kv, scale, 1 if causal else 0, window

@@ -122,3 +122,10 @@ def test_binding_takes_a_view_of_a_longer_page_table():
     for bad in (table.t(), table[0].expand(5, 64), table.long(), table[0]):
         with pytest.raises(qg.QgemvError):
             record(bad, 100)
+
+
+def test_binding_wants_a_contiguous_scratch():
+    with pytest.raises(qg.QgemvError):
+        record(torch.zeros(5, 64, dtype=torch.int32), 100, torch.zeros(1, dtype=torch.uint8).expand(1 << 20))
+    with pytest.raises(qg.QgemvError):
+        record(torch.zeros(5, 64, dtype=torch.int32), 100, torch.zeros(1 << 21, dtype=torch.uint8)[::2])
