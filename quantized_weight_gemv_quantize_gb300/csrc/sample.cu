@@ -380,7 +380,11 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleArgs a) {
         return x - (fabsf(x) + fabsf(top)) * (0.4f * margin);
     };
     auto least_of = [&](int bin) { return bin >= BINS - 1 ? NONE : edge(static_cast<float>(bin + 1), 1e-6f); };
-    auto most_of = [&](int bin) { return bin == 0 ? INF : edge(static_cast<float>(bin), -1e-6f); };
+    auto most_of = [&](int bin) {
+        if (bin == 0) return INF;
+        const float x = edge(static_cast<float>(bin), -1e-6f);
+        return x == x ? x : INF;  // (NaN where the edge lies below every fp32: a temperature above 1e37)
+    };
     // the tokens from `least` to `most` that take(x, i) wants
     auto gather_range = [&](float least, float most, auto&& take) {
         gather([&] {

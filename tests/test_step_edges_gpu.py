@@ -206,3 +206,21 @@ def test_sampling_unaligned_rows_over_several_blocks(dtype, n):
         a = run_sample(x, u=u, **kw)
         b = run_sample(x.contiguous(), u=u, **kw)
         assert np.array_equal(a[0], b[0]) and np.array_equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, B16])
+@pytest.mark.parametrize("n", [2003, 30011])
+def test_sampling_at_the_largest_temperatures(n, dtype):
+    """So flat that the edges of the histogram's bins lie beyond fp32, with fewer tokens left by a mask than top-k asks for."""
+    rng = np.random.default_rng(n)
+    x = rnd(rng, (6, n), dtype, 3.0)
+    for i, left in enumerate((n, 1500, 900, 300, 20, 1)):
+        x[i, torch.from_numpy(rng.permutation(n)[left:]).cuda()] = -float("inf")
+    u = rng.random(6, dtype=np.float32)
+    for k in (5, 400, 600, 1600):
+        for p in (1.0, 0.7):
+            kw = dict(k=np.full(6, k), p=np.full(6, p), u=u)
+            a = run_sample(x, T=np.full(6, 1e38), **kw)
+            b = run_sample(x, T=np.full(6, np.inf), check=False, **kw)
+            assert np.array_equal(a[0], b[0]) and np.array_equal(a[1], b[1])
+            run_sample(x, T=np.full(6, 2e36), **kw)
