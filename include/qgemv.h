@@ -507,7 +507,7 @@ QGEMV_API int qgemv_rope(const qgemv_rope_args* args, unsigned flags, void* stre
  *     s_t = scale * <q, k_t>,  out = sum_t softmax(s)_t v_t,  lse = ln sum_t exp(s_t)
  * over the context tokens t that the new token sees: all of them, or with causal != 0 those up to its own position, and
  * with window > 0 only the `window` tokens that end at its position.  A token that sees nothing (a context of length 0, or
- * a position below 0) gets out = 0 and lse = -inf.
+ * a position below 0) gets out = 0 and lse = -inf.  A query with a NaN gives NaN, in its own row only.
  * Scores, softmax statistics and sums are fp32; the probabilities meet the values in the 16-bit type of q (each rounded
  * once, unnormalised, their sum taken before the rounding); out is rounded once.
  *

@@ -82,13 +82,14 @@ __device__ __forceinline__ long long out_at(const AttnArgs& a, const Tile& t, in
 
 __device__ __forceinline__ void put_lse(const AttnArgs& a, const Tile& t, int r, float m2, float l) {
     if (!a.lse) return;
-    a.lse[out_at(a, t, r, a.heads, 1)] = l > 0.f ? (m2 + log2f(l)) * 0.693147180559945309f : NEG_INF;
+    // (l is 0 where the row sees nothing; NaN, of a query that is no number, goes on as NaN)
+    a.lse[out_at(a, t, r, a.heads, 1)] = l == 0.f ? NEG_INF : (m2 + log2f(l)) * 0.693147180559945309f;
 }
 
 // Elements d .. d + 3 of a row of the result from its unnormalised sums; with d = 0 its log-sum-exp.
 template <bool BF>
 __device__ __forceinline__ void put_row4(const AttnArgs& a, const Tile& t, int r, int d, float4 x, float m, float l) {
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
     *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + out_at(a, t, r, a.out_token, a.out_head) + d) =
         make_uint2(pack16<BF>(x.x * inv, x.y * inv), pack16<BF>(x.z * inv, x.w * inv));
     if (d == 0) put_lse(a, t, r, m, l);

@@ -599,7 +599,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) attn_tiles_kernel(const __gri
                 l += sh.sum[i][half ^ 1][tr];
             }
             const bool whole = t.parts == 1, row = r < t.rows;
-            const float inv = whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
+            const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
             const long long to = row ? out_at(a, t, r, a.out_token, a.out_head) + half * (DP / 2) : 0;
             float* rec = row && !whole ? a.part_sum + part_at(a, t, t.part, r) * a.dim + half * (DP / 2) : nullptr;
             const int dims = a.dim - half * (DP / 2);  // of this half

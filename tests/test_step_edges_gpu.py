@@ -153,6 +153,18 @@ def test_windows_whose_keys_are_cut_into_parts(new, window, H, KH):
         qg.qgemv_tune_attn(0)
 
 
+@pytest.mark.parametrize("new,ctx", [([3, 2], [700, 40]), ([150, 20], [900, 40]), ([40, 1], [9000, 9000])])
+def test_a_query_of_nan_shows_in_its_own_row_only(new, ctx, kernel):  # noqa: F811
+    s = Step(97, new, ctx, 8, 2, 128, 16, B16)
+    qg.qgemv_attn(s.args())
+    out, lse = s.out.clone(), s.lse.clone()
+    s.q[1, 5, 100] = float("nan")
+    qg.qgemv_attn(s.args())
+    assert bool(torch.isnan(s.out[1, 5]).all()) and bool(torch.isnan(s.lse[1, 5]))
+    s.out[1, 5], s.lse[1, 5] = out[1, 5], lse[1, 5]
+    assert torch.equal(s.out, out) and torch.equal(s.lse, lse)
+
+
 # --------------------------------------------------------------------------------------------------------- sampling
 
 # rows of two, four and eight blocks, the last of them with and without an odd end
