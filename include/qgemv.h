@@ -477,7 +477,8 @@ QGEMV_API int qgemv_rope_freqs(int rot_dim, double theta, int scaling, double fa
  * q_out may be q itself and k_out k itself (same kind and strides); other overlaps of an output with an input, or of
  * outputs, are refused.  positions: int[tokens] (any 32-bit value; negative positions turn backwards).
  * freqs: device copy of qgemv_rope_freqs' output, 8-byte aligned.  rot_dim even, 2..dim; dim a multiple of 8, 8..256.
- * Pointers 16-byte aligned; strides multiples of 16 bytes (of 8 elements for fp32).  tokens = 0 is valid and does nothing.
+ * Pointers 16-byte aligned; strides multiples of 16 bytes (of 8 elements for fp32).  tokens = 0 is valid and does nothing (the
+ * tensors' addresses may then be NULL, here and below).
  */
 typedef struct {
     const void* q;

@@ -94,6 +94,7 @@ static int run_rope(const qgemv_rope_args* a, unsigned flags, void* stream) {
         return QGEMV_ERR_INVALID_ARG;
     if (a->dim < 8 || a->dim % 8 || a->rot_dim < 2 || a->rot_dim % 2 || a->rot_dim > a->dim) return QGEMV_ERR_INVALID_ARG;
     if (a->dim > 256 || a->heads > 65536 || a->kv_heads > 65536) return QGEMV_ERR_UNSUPPORTED;
+    if (a->tokens == 0) return QGEMV_OK;  // (empty tensors may have no address)
     if (!a->positions || !a->freqs) return QGEMV_ERR_INVALID_ARG;
     const bool has_q = a->heads > 0, has_k = a->kv_heads > 0, has_c = a->cache != nullptr;
     if (has_q != (a->q != nullptr) || has_q != (a->q_out != nullptr) || has_k != (a->k != nullptr)) return QGEMV_ERR_INVALID_ARG;
@@ -117,7 +118,6 @@ static int run_rope(const qgemv_rope_args* a, unsigned flags, void* stream) {
     }
     if (!api_aligned(a->positions, 4) || !api_aligned(a->freqs, 8) || (a->slots && !api_aligned(a->slots, 8)))
         return QGEMV_ERR_MISALIGNED;
-    if (T == 0) return QGEMV_OK;
     const size_t nf = static_cast<size_t>(a->rot_dim / 2) * 8, np = static_cast<size_t>(T) * 4, ns = static_cast<size_t>(T) * 8;
     const Region* outs[2] = {&qo, &ko};
     for (const Region* o : outs) {
@@ -340,7 +340,11 @@ static bool tensor_map(unsigned long long (&map)[16], const void* base, int kind
 static int run_attn(const qgemv_attn_args* a, unsigned flags, void* stream) {
     if (!a || (flags & ~QGEMV_FLAG_PDL)) return QGEMV_ERR_INVALID_ARG;
     if (a->kind != QGEMV_ACT_BF16 && a->kind != QGEMV_ACT_F16) return QGEMV_ERR_INVALID_ARG;
-    if (!a->cache || !a->q || !a->out || !a->pages || !a->q_start || !a->kv_len || !a->scratch) return QGEMV_ERR_INVALID_ARG;
+    if (!a->cache || !a->scratch) return QGEMV_ERR_INVALID_ARG;
+    if (a->tokens != 0 && a->seqs != 0) {  // (empty tensors may have no address)
+        if (!a->q || !a->out || !a->q_start || !a->kv_len) return QGEMV_ERR_INVALID_ARG;
+        if (!a->pages && a->pages_stride != 0) return QGEMV_ERR_INVALID_ARG;
+    }
     int st;
     if ((st = check_cache(a->cache))) return st;
     const qgemv_cache& c = *a->cache;
@@ -449,14 +453,15 @@ constexpr unsigned SAMPLE_SMEM_MAX = 220 * 1024;
 static int run_sample(const SampleArgs& s, int kind, unsigned flags, void* stream) {
     const int size = elem_size(kind);
     if (!size || (flags & ~QGEMV_FLAG_PDL)) return QGEMV_ERR_INVALID_ARG;
-    if (s.m < 0 || s.N < 1 || s.row_stride < s.N || !s.x || !s.u || !s.token) return QGEMV_ERR_INVALID_ARG;
+    if (s.m < 0 || s.N < 1 || s.row_stride < s.N) return QGEMV_ERR_INVALID_ARG;
+    if (s.m == 0) return QGEMV_OK;  // (empty tensors may have no address)
+    if (!s.x || !s.u || !s.token) return QGEMV_ERR_INVALID_ARG;
     if (s.N > 1 << 20 || s.row_stride > (1ll << 40) || static_cast<double>(s.m) * static_cast<double>(s.row_stride) > SPAN_MAX)
         return QGEMV_ERR_UNSUPPORTED;
     if (!api_aligned(s.x, 16)) return QGEMV_ERR_MISALIGNED;
     const void* words[] = {s.temperature, s.top_k, s.top_p, s.min_p, s.u, s.token, s.prob};
     for (const void* w : words)
         if (w && !api_aligned(w, 4)) return QGEMV_ERR_MISALIGNED;
-    if (s.m == 0) return QGEMV_OK;
     const size_t n = static_cast<size_t>(s.m) * 4;
     const size_t xb = (static_cast<size_t>(s.m - 1) * s.row_stride + s.N) * size;
     const void* outs[] = {s.token, s.prob};

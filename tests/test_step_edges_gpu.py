@@ -82,6 +82,13 @@ def test_a_view_of_a_longer_page_table(new, ctx, kernel):  # noqa: F811
     s.check()
 
 
+def test_a_page_table_without_columns(kernel):  # noqa: F811
+    s = Step(77, [3, 150], [0, 0], 4, 2, 64, 16, B16)
+    s.table = torch.empty(2, 0, dtype=torch.int32, device="cuda")
+    qg.qgemv_attn(s.args())
+    s.check()
+
+
 @pytest.mark.parametrize("new", [2, 100])
 def test_a_table_row_and_a_page_whose_product_leaves_64_bits(new, kernel):  # noqa: F811
     """One page of 2^24 tokens, and rows of the table 2^40 entries apart: a row reaches further than any context."""

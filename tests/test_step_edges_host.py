@@ -129,3 +129,37 @@ def test_binding_wants_a_contiguous_scratch():
         record(torch.zeros(5, 64, dtype=torch.int32), 100, torch.zeros(1, dtype=torch.uint8).expand(1 << 20))
     with pytest.raises(qg.QgemvError):
         record(torch.zeros(5, 64, dtype=torch.int32), 100, torch.zeros(1 << 21, dtype=torch.uint8)[::2])
+
+
+def test_binding_does_nothing_for_empty_tensors():
+    """A step without tokens: empty tensors have no address."""
+    none = lambda *n, dtype=torch.bfloat16: torch.empty(*n, dtype=dtype)  # noqa: E731
+    i32 = lambda *n: torch.zeros(*n, dtype=torch.int32)  # noqa: E731
+    kv = qg.kv_cache(*(torch.zeros(30, 16, 2, 64, dtype=torch.bfloat16) for _ in range(2)))
+    q, k = none(0, 4, 64), none(0, 2, 64)
+    assert q.data_ptr() == 0
+    freqs = torch.zeros(32, dtype=torch.int64)
+    qg.qgemv_rope(qg.rope_args(q, k, k, i32(0), freqs, none(0, 4, 64), none(0, 2, 64), kv, torch.zeros(0, dtype=torch.int64)), stream=0)
+    qg.qgemv_rope(qg.rope_args(q, None, None, i32(0), freqs, none(0, 4, 64)), stream=0)
+    scratch = torch.zeros(qg.qgemv_attn_scratch_bytes(3, 0, 4, 2, 64, 0, 100), dtype=torch.uint8)
+    args = lambda table, starts, lens: qg.attn_args(q, kv, table, starts, lens, none(0, 4, 64), scratch, 0, 100, 0.1, lse=none(0, 4, dtype=torch.float32))  # noqa: E731
+    qg.qgemv_attn(args(i32(3, 7), i32(4), i32(3)), stream=0)  # sequences, but no new tokens
+    qg.qgemv_attn(args(i32(0, 7), i32(1), i32(0)), stream=0)  # no sequences
+    f32 = none(0, dtype=torch.float32)
+    qg.qgemv_sample(none(0, 1000), f32, i32(0), f32, f32, f32, i32(0), f32, stream=0)
+    with pytest.raises(qg.QgemvError):
+        qg.qgemv_sample(none(0, 0), f32, i32(0), f32, f32, f32, i32(0), f32, stream=0)
+
+
+@pytest.mark.skipif(HAS_GPU_NODE, reason="checks the no-GPU path only (fake addresses must never reach a GPU)")
+def test_a_page_table_without_columns_needs_no_address(L):  # noqa: F811
+    assert L.qgemv_attn(attn(pages=None, pages_stride=0), 0, None) in (4, 5)  # tokens that see nothing
+    assert L.qgemv_attn(attn(pages=None, pages_stride=0, tokens=0), 0, None) == 0
+
+
+def test_empty_calls_are_checked_as_far_as_they_go(L):  # noqa: F811
+    assert L.qgemv_rope(rope(tokens=0, q=None, k=None, v=None, q_out=None, k_out=None, positions=None, slots=None), 0, None) == 0
+    assert L.qgemv_rope(rope(tokens=0, rot_dim=3), 0, None) == 1 and L.qgemv_rope(rope(tokens=0, layout=5), 0, None) == 1
+    assert L.qgemv_attn(attn(tokens=0, scratch=None), 0, None) == 1 and L.qgemv_attn(attn(seqs=0, scale=0.0), 0, None) == 1
+    assert L.qgemv_attn(attn(tokens=0, cache=None), 0, None) == 1
+    assert sample(L, m=0, kind=0) == 1 and sample(L, m=0, x=None, u=None, token=None) == 0 and sample(L, m=0, stride=999) == 1
