@@ -510,7 +510,8 @@ QGEMV_API int qgemv_rope(const qgemv_rope_args* args, unsigned flags, void* stre
  * with window > 0 only the `window` tokens that end at its position.  A token that sees nothing (a context of length 0, or
  * a position below 0) gets out = 0 and lse = -inf.  A query with a NaN gives NaN, in its own row only.
  * Scores, softmax statistics and sums are fp32; the probabilities meet the values in the 16-bit type of q (each rounded
- * once, unnormalised, their sum taken before the rounding); out is rounded once.
+ * once, unnormalised, their sum taken before the rounding; with f16, those below 2^-29 of the row's largest, or 2^-21 in the 128-row
+ * kernel, have fewer bits, and none below 2^-40 or 2^-32); out is rounded once.
  *
  * kind (QGEMV_ACT_BF16 / QGEMV_ACT_F16): type of q and out, and the cache's.  q, out [tokens, heads, cache->dim], last
  * dimension contiguous, 16-byte aligned, strides multiples of 8 elements.  lse: fp32 [tokens, heads] or NULL.

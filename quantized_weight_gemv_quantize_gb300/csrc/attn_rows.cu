@@ -199,7 +199,7 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Tile& t, long lo
         for (int hh = 0; hh < 2; ++hh) {
             top[hh] = fmaxf(top[hh], __shfl_xor_sync(0xffffffffu, top[hh], 1));
             top[hh] = fmaxf(top[hh], __shfl_xor_sync(0xffffffffu, top[hh], 2));
-            const float mn = fmaxf(m[hh], top[hh]);
+            const float mn = fmaxf(m[hh], top[hh] - Lift<BF>::ROWS);
             const float base = mn == NEG_INF ? 0.f : mn;  // a row that has seen nothing yet: 2^(-inf - 0) = 0
             keep[hh] = exp2_approx(m[hh] - base);
             m[hh] = mn;

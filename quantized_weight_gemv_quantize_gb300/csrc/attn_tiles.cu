@@ -521,7 +521,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) attn_tiles_kernel(const __gri
             }
             const int pos = row_pos(a, t, r);
             const int hi = a.causal ? min(t.k1 - 1, pos) : t.k1 - 1, lo = first_key(a, pos);
-            float m = NEG_INF, l = 0.f;  // m: the maximum in use, in units of the scaled scores (base 2)
+            float m = NEG_INF, l = 0.f;  // m: the maximum in use (less the lift), in units of the scaled scores (base 2)
             for (int j = 0; j < blocks; ++j, ++g) {
                 if (!(ok = await(sh.s_full[i], round++))) break;
                 tc_fence_after();
@@ -559,15 +559,15 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) attn_tiles_kernel(const __gri
                     sum = (sums[0] + sums[1]) + (sums[2] + sums[3]);
                 };
                 // The exponentials are taken against the maximum in use while the new one is being found; only where that turns
-                // out to be larger by more than 2^8 (and for the first keys that a row sees) are they taken again.
+                // out to be larger by more than 2^LAG (and for the first keys that a row sees) are they taken again.
                 weigh(m == NEG_INF ? 0.f : m);
                 sh.top[i][half][tr] = top;
                 pair_sync();
                 top = fmaxf(top, sh.top[i][half ^ 1][tr]) * a.scale_log2;
-                const bool move = top > m + 8.f;
+                const bool move = top > m + (Lift<BF>::TILES + Lift<BF>::LAG);
                 if (__any_sync(0xffffffffu, move)) {
-                    const float f = move ? exp2_approx(m - top) : 1.f;  // 0 for the first keys that the row sees
-                    if (move) m = top;
+                    const float to = top - Lift<BF>::TILES, f = move ? exp2_approx(m - to) : 1.f;  // 0 for the first keys that the row sees
+                    if (move) m = to;
                     l *= f;
                     if (j > 0) {
                         // S_j is there, so the product before it, into O, has ended

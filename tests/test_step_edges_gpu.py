@@ -172,6 +172,31 @@ def test_a_query_of_nan_shows_in_its_own_row_only(new, ctx, kernel):  # noqa: F8
     assert torch.equal(s.out, out) and torch.equal(s.lse, lse)
 
 
+@pytest.mark.parametrize("gap", [6.0, 10.0, 12.0, 14.0, 16.0, 17.5])
+@pytest.mark.parametrize("dtype", [B16, H16])
+@pytest.mark.parametrize("new,ctx", [(1, 40000), (100, 3000), (100, 20000)])
+def test_many_keys_far_below_one(new, ctx, dtype, gap, kernel):  # noqa: F811
+    """A first token that takes nearly all of the attention and has no value, as trained models have it: the result is what many keys
+    `gap` nats below it add up to, and their probabilities must not lose bits for being small."""
+    rng = np.random.default_rng(98)
+    s = Step(98, [new], [ctx], 4, 2, 64, 64, dtype, scale=1.0)
+    q = torch.zeros(new, 4, 64, dtype=dtype, device="cuda")
+    q[..., 0] = 1.0
+    q[..., 1:] = rnd(rng, (new, 4, 63), dtype, 0.1)
+    s.q = q
+    k, v = rnd(rng, (ctx, 2, 64), dtype, 0.1), rnd(rng, (ctx, 2, 64), dtype, 0.25) + 1.0
+    k[:, :, 0] = 0.0
+    k[0] = 0.0
+    k[0, :, 0] = gap
+    v[0] = 0.0
+    s.k[0], s.v[0] = k, v
+    t = torch.arange(ctx, device="cuda")
+    at = s.table[0, t // 64].long(), t % 64
+    s.kc[at], s.vc[at] = k, v
+    qg.qgemv_attn(s.args())
+    s.check()
+
+
 # --------------------------------------------------------------------------------------------------------- sampling
 
 # rows of two, four and eight blocks, the last of them with and without an odd end
