@@ -109,45 +109,28 @@ __device__ __forceinline__ void put_row4(const AttnArgs& a, const Tile& t, int r
 }
 
 // A part's record of a row: the maximum in use (base 2) and the sum in part_stat[at], dim unnormalised sums of values in
-// part_sum[at * dim ..].  A warp joins the parts of one row, always in the same order, and writes the result; rec(p): the record of
-// part p.  Lane l takes elements 4 l .. 4 l + 3 (and + 128).  The first loads depend on nothing but rec, so that all are on their way at once.
-template <int N, bool BF, class Rec>
+// part_sum[at * dim ..].  A warp joins the parts of one row (at most 32, of heads of up to 128), always in the same order, and writes the
+// result; rec(p): the record of part p.  Lane l takes elements 4 l .. 4 l + 3.  The first loads depend on nothing but rec, so that all are
+// on their way at once.
+template <bool BF, class Rec>
 __device__ __forceinline__ void join_row(const AttnArgs& a, const Tile& t, int r, Rec rec) {
-    const int lane = threadIdx.x % 32;
-    float m = NEG_INF, l = 0.f;
-    float4 acc[N];
+    const int lane = threadIdx.x % 32, d = 4 * lane;
+    const float2 s = lane < t.parts ? __ldcg(a.part_stat + rec(lane)) : make_float2(NEG_INF, 0.f);  // a lane a part
+    float m = s.x;
 #pragma unroll
-    for (int n = 0; n < N; ++n) acc[n] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int p0 = 0; p0 < t.parts; p0 += 32) {  // 32 parts at a time, a lane each for the statistics
-        const int here = min(32, t.parts - p0);
-        const float2 s = lane < here ? __ldcg(a.part_stat + rec(p0 + lane)) : make_float2(NEG_INF, 0.f);
-        float top = s.x;
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float w = exp2_approx(s.x - (m == NEG_INF ? 0.f : m));
+    float l = w * s.y;
 #pragma unroll
-        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        top = fmaxf(top, m);
-        const float base = top == NEG_INF ? 0.f : top, keep = exp2_approx(m - base), w = exp2_approx(s.x - base);
-        m = top;
-        float sum = w * s.y;
-#pragma unroll
-        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        l = l * keep + sum;
-#pragma unroll
-        for (int n = 0; n < N; ++n) acc[n].x *= keep, acc[n].y *= keep, acc[n].z *= keep, acc[n].w *= keep;
+    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-        for (int p = 0; p < here; ++p) {
-            const float f = __shfl_sync(0xffffffffu, w, p);
-            const float* from = a.part_sum + rec(p0 + p) * a.dim;
-#pragma unroll
-            for (int n = 0; n < N; ++n) {
-                const int d = n * 128 + 4 * lane;
-                const float4 v = d < a.dim ? __ldcg(reinterpret_cast<const float4*>(from + d)) : make_float4(0.f, 0.f, 0.f, 0.f);
-                acc[n].x += f * v.x, acc[n].y += f * v.y, acc[n].z += f * v.z, acc[n].w += f * v.w;
-            }
-        }
+    for (int p = 0; p < t.parts; ++p) {
+        const float f = __shfl_sync(0xffffffffu, w, p);
+        const float4 v = d < a.dim ? __ldcg(reinterpret_cast<const float4*>(a.part_sum + rec(p) * a.dim + d)) : make_float4(0.f, 0.f, 0.f, 0.f);
+        acc.x += f * v.x, acc.y += f * v.y, acc.z += f * v.z, acc.w += f * v.w;
     }
-#pragma unroll
-    for (int n = 0; n < N; ++n)
-        if (n * 128 + 4 * lane < a.dim) put_row4<BF>(a, t, r, n * 128 + 4 * lane, acc[n], m, l);
+    if (d < a.dim) put_row4<BF>(a, t, r, d, acc, m, l);
 }
 
 }  // namespace qg

@@ -173,7 +173,7 @@ struct TilesShared {
     Tile item[ITEMS];           // the parts that the block works on, in a ring; seq -1: no more
     uint32_t live[4][TK / 32];  // which keys of a key tile are there, one bit each
     float top[2][2][TR], sum[2][2][TR];  // by row tile and half of the keys: a row's maximum, at a part's end its sum
-    uint32_t tmem;
+    uint32_t tmem;  // the allocation's answer, always column 0 (all 512 are asked for)
 };
 
 // The row tiles with the most keys (the last ones, under a causal mask) of all sequences and heads come first, so that the grid ends
@@ -669,7 +669,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) attn_join_kernel(const AttnAr
     if (index >= static_cast<long long>(a.row_tiles) * a.kv_heads * a.seqs - a.whole) return;
     Tile t;
     if (!find_tile(a, a.whole + index * a.parts, &t) || t.parts == 1 || r >= t.rows) return;
-    join_row<1, BF>(a, t, r, [&](int p) { return part_at(a, t, p, r); });
+    join_row<BF>(a, t, r, [&](int p) { return part_at(a, t, p, r); });
 }
 
 template <int DP>

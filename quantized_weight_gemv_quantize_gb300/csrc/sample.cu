@@ -114,7 +114,7 @@ struct alignas(16) SampleShared {  // the slice follows it in shared memory, wri
     u64 group_m[32], group_n[32];
     u64 found[2][5];                           // by level: which, count and mass before it, mass in it, the whole mass
     u64 got_m[2][8][32], got_n[2][8][32];      // masses and counts of groups of bins, and of a group's bins, from each block
-    u64 push[2][4][8];                         // what the blocks tell each other, by kind and block; two sets in turn
+    u64 push[2][2][8];                         // what the blocks tell each other, by kind and block; two sets in turn
     u64 red[3][ST / 32];
     unsigned used;
 };
@@ -200,13 +200,13 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleArgs a) {
         else __syncthreads();
     };
     int turn = 0;
-    // Every block gives up to 3 values (the same in all its threads) and gets all blocks': s.push[turn][kind][block].  Two sets in
+    // Every block gives two values (the same in all its threads) and gets all blocks': s.push[turn][kind][block].  Two sets in
     // turn: a set is written again only after another exchange, whose barrier lies after every read of it.
-    auto exchange = [&](u64 v0, u64 v1, u64 v2) {
+    auto exchange = [&](u64 v0, u64 v1) {
         turn ^= 1;
         if (tid < CS) {
             const uint32_t base = peer(smem_addr(&s.push[turn][0][rank]), tid);
-            peer_st64(base, v0), peer_st64(base + 64, v1), peer_st64(base + 128, v2);
+            peer_st64(base, v0), peer_st64(base + 64, v1);
         }
         sync_all();
     };
@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleArgs a) {
     }
     u64 best = block_reduce(largest != largest ? 0xffffffffull : static_cast<u64>(key_of(largest)), 0, max64);
     if (CS > 1) cluster_wait();  // the other blocks run
-    exchange(best, 0, 0);
+    exchange(best, 0);
     for (int b = 0; b < CS; ++b) best = max64(best, s.push[turn][0][b]);
     const uint32_t top_key = static_cast<uint32_t>(best);
     const float top = x_of(top_key);
@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleArgs a) {
             if (top_key == 0xffffffffu ? x != x : x == top) at = min64(at, static_cast<u64>(first + i));
         });
         at = block_reduce(at, 1, min64);
-        exchange(at, 0, 0);
+        exchange(at, 0);
         for (int b = 0; b < CS; ++b) at = min64(at, s.push[turn][0][b]);
         if (tid == 0 && rank == 0) {
             a.token[row] = none ? -1 : static_cast<int>(at);
@@ -368,7 +368,7 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleArgs a) {
         __syncthreads();
         all_of();
         __syncthreads();
-        exchange(s.used, 0, 0);
+        exchange(s.used, 0);
         members = 0;
         for (int b = 0; b < CS; ++b) members += static_cast<unsigned>(s.push[turn][0][b]);
     };
@@ -526,7 +526,7 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleArgs a) {
                 if (in_bin(x, i)) cmin = min64(cmin, c_of(x, i)), cmax = max64(cmax, c_of(x, i));
             });
             cmin = block_reduce(cmin, 0, min64), cmax = block_reduce(cmax, 1, max64);
-            exchange(cmin, cmax, 0);
+            exchange(cmin, cmax);
             for (int b = 0; b < CS; ++b) cmin = min64(cmin, s.push[turn][0][b]), cmax = max64(cmax, s.push[turn][1][b]);
             lo = cmin, hi = cmax, linear = false;
             const int bits = 64 - __clzll(static_cast<long long>(hi - lo));
@@ -547,7 +547,7 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleArgs a) {
             cut = block_reduce(keep ? c : ~0ull, 0, min64);
         }
         const unsigned listed = min(s.used, static_cast<unsigned>(CAP));
-        exchange(cut, kept, 0);
+        exchange(cut, kept);
         cut = s.push[turn][0][0], *mass = s.push[turn][1][0];
         const u64 c = tid < listed ? s.list[tid] : 0;
         *own += block_reduce(c >= cut ? mass_of(e_of(x_at(c), top, rate)) : 0, 0, add64);
@@ -619,7 +619,7 @@ __global__ void __launch_bounds__(ST, 2) sample_kernel(const SampleArgs a) {
     };
     const bool known = cut != 0 && !(min_p > 0.f);
     if (!known) pass();
-    exchange(mine, 0, 0);
+    exchange(mine, 0);
     u64 W = 0, block_start = 0;
     for (int b = 0; b < CS; ++b) {
         if (b < rank) block_start += s.push[turn][0][b];
