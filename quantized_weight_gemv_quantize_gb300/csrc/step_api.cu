@@ -478,7 +478,7 @@ static int run_sample(const SampleArgs& s, int kind, unsigned flags, void* strea
     // Blocks of a row: slices of at most 20480 tokens, up to the 8 blocks of a portable cluster.  Where the rows make more than two
     // waves of two blocks an SM, slices of twice that as long as two of them still fit (320 rows of 151936 bf16 logits: 273 -> 222 us;
     // 16 rows: 43 -> 54 us): each block's passes then carry fewer barriers.  A slice stays in shared memory where it fits
-    // (always up to 388,000 fp32 or 777,000 16-bit logits); longer ones are read again from L2.
+    // (up to 382528 fp32 or 765056 16-bit logits a row); longer ones are read again from L2.
     SampleArgs k = s;
     auto blocks_of = [&](int most) {
         int n = 1;
@@ -488,7 +488,7 @@ static int run_sample(const SampleArgs& s, int kind, unsigned flags, void* strea
     k.blocks = blocks_of(20480);
     if (static_cast<long long>(s.m) * k.blocks > 4ll * sms && size == 2) k.blocks = blocks_of(40960);
     k.slice = ((s.N + k.blocks - 1) / k.blocks + 7) / 8 * 8;
-    const unsigned base = sample_smem_base(), room = SAMPLE_SMEM_MAX - base;
+    const unsigned base = sample_smem_base(), room = SAMPLE_SMEM_MAX - base;  // 34016 of 225280 bytes
     k.staged = static_cast<unsigned>(k.slice) * size <= room;
     if (static_cast<long long>(s.m) * k.blocks > INT_MAX) return QGEMV_ERR_UNSUPPORTED;
     const void* fn = sample_kernel_ptr(kind);

@@ -268,3 +268,15 @@ def test_sampling_at_the_largest_temperatures(n, dtype):
             b = run_sample(x, T=np.full(6, np.inf), check=False, **kw)
             assert np.array_equal(a[0], b[0]) and np.array_equal(a[1], b[1])
             run_sample(x, T=np.full(6, 2e36), **kw)
+
+
+# the last length whose slices (an eighth each) stay in shared memory beside the rest, and the next one, which is read again from L2
+@pytest.mark.parametrize("dtype,n", [(torch.float32, 382528), (torch.float32, 382529), (B16, 765056), (B16, 765057), (H16, 765056), (H16, 765064)])
+def test_sampling_around_the_longest_slices_in_shared_memory(dtype, n):
+    rng = np.random.default_rng(n)
+    x = rnd(rng, (3, n), dtype, 2.0)
+    x[1, ::3] = -float("inf")
+    u = rng.random(3, dtype=np.float32)
+    for kw in (dict(), dict(k=np.full(3, 50), p=np.full(3, 0.9)), dict(k=np.full(3, 3000)), dict(p=np.full(3, 0.8)), dict(mp=np.full(3, 0.01)),
+               dict(T=np.zeros(3))):
+        run_sample(x, u=u, **kw)
