@@ -467,7 +467,9 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) attn_tiles_kernel(const __gri
             (void)mbar_wait_bounded(smem_addr(&sh.drain), 0);
             __syncwarp();
         } else if (warp == GATE_WARP) {
-            // ---- the waits for the copies
+            // ---- the waits for the copies.  Rows that were copied one by one were written through the generic proxy, and the products read
+            // through the asynchronous one: the fence between them lies on the path from the copies' arrival, which every lane here has
+            // waited for, to lane 0's arrival, which the issuing thread waits for.  (The copying lanes do not wait for their copies.)
             auto landed = [&](unsigned long long& bar, unsigned g) {
                 if (!await(bar, g / 2)) return false;
                 const uint32_t* lv = sh.live[g & 3];

@@ -7,7 +7,7 @@ import quantized_weight_gemv_quantize_gb300 as qg
 
 torch = pytest.importorskip("torch")
 
-from tests.test_step_gpu import B16, H16, TINY, U, Step, f64, kernel, rnd, run_sample  # noqa: E402,F401
+from tests.test_step_gpu import ATTN, B16, H16, TINY, U, Step, f64, kernel, rnd, run_sample  # noqa: E402,F401
 
 pytestmark = pytest.mark.gpu
 
@@ -51,6 +51,21 @@ def check_seen(s, sees):
 def window_sees(n, kv_len, window, readable):
     pos, t = kv_len - n + np.arange(n, dtype=np.int64), np.arange(kv_len)
     return (t[None] <= pos[:, None]) & (t[None] > pos[:, None] - window) & (t[None] < readable)
+
+
+# heads that fit, groups that do and do not divide 128 (queries by tensor map, row by row), pages of multiples of 8 tokens and others
+# (keys by tensor map, row by row)
+@pytest.mark.parametrize("shape", ATTN + [([130, 3], [500, 300], 6, 2, 128, 5, H16), ([70], [333], 10, 2, 64, 24, B16),
+                                          ([20, 40], [90, 1100], 9, 1, 96, 33, B16), ([3, 3], [40, 200], 64, 1, 64, 12, H16),
+                                          ([150], [2000], 130, 1, 64, 8, B16), ([60], [700], 3, 3, 72, 64, H16)], ids=str)
+def test_the_forced_kernel_is_the_one_that_runs(shape, kernel):  # noqa: F811
+    new, ctx, H, KH, D, page, dtype = shape
+    s = Step(60, new, ctx, H, KH, D, page, dtype)
+    qg.qgemv_route_reset()
+    qg.qgemv_attn(s.args())
+    counts = qg.qgemv_route_counts()
+    assert (counts[qg.ROUTE_ATTN_ROWS], counts[qg.ROUTE_ATTN_TILES]) == ((1, 0) if kernel == "16-row" or D > 128 else (0, 1))
+    s.check()
 
 
 # context, window; a context of 1000 lies wholly past the 256 tokens that may be read, one of 700 starts among them
