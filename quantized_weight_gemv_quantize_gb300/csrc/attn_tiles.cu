@@ -651,6 +651,9 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) attn_tiles_kernel(const __gri
                 else __stcg(a.part_stat + part_at(a, t, t.part, r), make_float2(m, l));
             }
         }
+        // A warp whose wait ran out (it cannot in a correct run) may have a partner that got past the same wait and stands in pair_sync: it
+        // leaves one arrival there.  The partner's next wait then runs out too, for want of this warp's arrivals.
+        asm volatile("bar.arrive %0, 64;" ::"r"(2 + i * 4 + warp % 4) : "memory");
         tc_fence_before();
     }
     __syncthreads();
