@@ -9,9 +9,9 @@
 // are blocks (from the lengths on the device: uneven contexts and loose bounds cost nothing); a block takes its share, which may
 // be the end of one row tile, some whole ones and the start of another.  The parts of a row tile are joined through the scratch.
 //
-// 48 sequences of 2000 to 16384 tokens, 32 and 8 heads of 128: 210-217 us, 6.3 to 6.5 TB/s, 93 to 97% of a plain copy's rate (a grid of parts of
-// 2048 keys: 264 us).  One sequence of 100003: 72 us, 5.7 TB/s; the rest is the one wave's start (3 us) and the joining of 38
-// parts.  One of 777: 10.2 us, all latency: launch, lengths, page table, keys, a counter, the parts.
+// 48 sequences of 2000 to 16384 tokens, 32 and 8 heads of 128: 208-214 us, 6.4 to 6.6 TB/s, 94 to 97% of a plain copy's rate (a grid of parts of
+// 2048 keys: 264 us).  One sequence of 100003: 72 to 73 us, 5.6 to 5.7 TB/s; the rest is the one wave's start (3 us) and the joining of 38
+// parts.  One of 777: 10.2 us call after call, 8.2 in a graph, all latency: launch, lengths, page table, keys, a counter, the parts.
 #include "attn.cuh"
 
 namespace qg {

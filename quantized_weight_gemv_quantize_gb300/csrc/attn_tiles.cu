@@ -10,16 +10,18 @@
 // 128-byte-swizzled layout that the tensor cores read (K as the K-major, V as the MN-major operand: no transpose is made).
 //
 // Work a pair of row tiles and a key tile at D = 128: 2048 cycles of the tensor cores, 1024 of the exponential units; measured about 2720, the
-// time of one row tile's round: softmax 1200, its products 1024, some 500 of barriers and of the products' latency.  Only two row
-// tiles fit tensor memory (2 x (128 scores + 128 sums) = 512 columns), so that no third round hides those.  A chunk of 2000 tokens over
-// 24000 (32 and 8 heads): 525 us, 1.43 PFLOP/s; two prompts of 6000: 397 us, 1.33 PFLOP/s (cuBLAS bf16: 1.72 sustained).
+// time of one row tile's round: softmax 1200, its products 1024, some 500 of barriers and of the products' latency.  The scores of the
+// next keys wait for P V, because P lies in their columns; two row tiles' scores and sums (2 x (128 + 128) columns) are all of tensor
+// memory, so that no third round hides the wait.  A chunk of 2000 tokens over 24000 (32 and 8 heads): 531 to 539 us over four GPUs,
+// 1.40 to 1.42 PFLOP/s; two prompts of 6000: 384 to 387 us, 1.37 PFLOP/s (cuBLAS bf16: 1.72 sustained).
 // What the steps gave, for the chunk: 1302 us with one softmax thread a row, row-by-row copies and a wait for each of them; 1062 with
 // copies that announce themselves; 777 with tensor-map copies, two threads a row and exponentials ahead of the maximum; 694 with a
 // warp that waits in the issuing warp's place; 612 with parts by cost and a kernel that joins them; 580 with blocks that stay (prompts:
 // 435 to 397): the next part's keys and queries come under the end of the last one, and the warps' numbers and loop bounds are
 // uniform for the compiler, which took 400 to 180 cycles from a probability's arrival to its product; 541 with the parts' records and
-// launch in their cost; 525 where only the row tiles that do not fill a wave are cut.  Stores of 32 bytes (a whole sector) a thread in
-// place of 16: prompts 429 to 420, chunks in parts 76 to 74.
+// launch in their cost.  Stores of 32 bytes (a whole sector) a thread in place of 16: prompts 429 to 420, chunks in parts 76 to 74.  Key
+// tiles with gaps (a row tile's last keys, a window's first) copied with one shuffle a row in place of two rows' pages and tokens: prompts of
+// 6001 and 4000 tokens 314 to 305, 2000 tokens over 24000 with a window of 1024 76 to 65.
 #include "attn.cuh"
 
 namespace qg {

@@ -11,8 +11,9 @@
 //    gathered and give the cut, and the draw takes one more pass over the row; a bin of more than CAP tokens is split again, by c, until
 //    one has at most CAP (c differs for all tokens, so this ends even for a row of equal logits).
 // Each block keeps its slice of the row in shared memory; the row is read once from global memory.  At 151936 logits: one row with top-k and
-// top-p 15 us, four cluster barriers and the passes between them one after the other (load 1.5 us, maximum 1.4, bound 2.8, gathering 1.8, list 5);
-// 16 rows of mixed settings 39 us, set by the slowest, a top-k beyond the list and then top-p; 320 rows of bf16 logits, top-p alone, 216 us:
+// top-p 12.2 us in a graph (15 to 17 call after call, with the caller's part): four cluster barriers and the passes between them one after
+// the other (load 1.5 us, maximum 1.4, bound 2.8, gathering 1.8, list 5);
+// 16 rows of mixed settings 39 us, set by the slowest, a top-k beyond the list and then top-p; 320 rows of bf16 logits, top-p alone, 215 to 221 us:
 // 44 us of them the histogram's arithmetic (some 30 instructions a token, of which the exponential is 8), the rest barriers and lists
 // that two blocks an SM do not hide (issue slots 53% busy).  One block a row with a radix sort's passes took 4108, 4816 and 7278 us.
 #include "common.cuh"

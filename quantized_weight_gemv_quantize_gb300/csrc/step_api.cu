@@ -222,8 +222,10 @@ static int attn_plan(int seqs, int tokens, int heads, int kv_heads, int dim, int
     // n = 1: 542 / 544, n = 2: 591 / 583, 4: 578 / 557, 8: 640 / 650; 1000 over 30000, n = 1: 346 / 342, 2: 375 / 365, 8: 405 / 390; 256 over 16000,
     // n = 1: 182 / 188, 4: 64 / 69, 8: 74 / 80; 64 over 4000, n = 1: 56 / 58, 4: 30 / 30.  At most 32 parts of at least 8 key tiles.
     const long long tiles = (rows + 255) / 256 * kv_heads * seqs, blocks = (static_cast<long long>(keys) + 127) / 128;
-    // Or the row tiles that fill whole waves stay whole and only the rest is cut (1300 tokens over
-    // 30000: 492 us with all cut alike, 419; 1500 over 20000: 368, 331; 2000 over 24000: 532 with none cut, 525).
+    // Or the row tiles that fill whole waves stay whole and only the rest is cut (1300 tokens over 30000: 492 us with all cut alike, 419;
+    // 1500 over 20000: 368, 331; 2000 over 24000: no difference beyond that between GPUs).
+    // All of these, and the choice of kernel below, were fitted at heads of 128 and 152 SMs; heads of 64 and 96 take much the same time in
+    // the 128-row kernel (2000 over 8000: 164, 171 and 174 us at 64, 96 and 128), where the softmax sets the pace.
     const long long full = tiles / SMS * SMS;
     long long best = 1, best_whole = 0;
     double tiles_us = 0;
