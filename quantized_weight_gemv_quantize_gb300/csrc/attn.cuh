@@ -73,12 +73,12 @@ __device__ __forceinline__ int first_key(const AttnArgs& a, int pos) {
 }
 
 // The keys that some row of [row0, row0 + rows) sees, from a multiple of `step` on; returns the first one seen.  Where there are
-// none, hi = lo: the rounding comes first, so that nothing beyond the keys that may be read is in the range.
+// none, hi = lo: nothing before that first one, and nothing beyond the keys that may be read, is then in the range.
 __device__ __forceinline__ int find_keys(const AttnArgs& a, const Seq& s, int row0, int rows, int step, int* lo, int* hi) {
     const int first = first_key(a, s.first_pos + div_by(row0, a.group, a.group_shift));
     *lo = first / step * step;
     *hi = a.causal ? min(s.usable, s.first_pos + div_by(row0 + rows - 1, a.group, a.group_shift) + 1) : s.usable;
-    *hi = max(*hi, *lo);
+    if (*hi <= first) *hi = *lo;
     return first;
 }
 

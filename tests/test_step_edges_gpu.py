@@ -115,6 +115,17 @@ def test_a_table_row_and_a_page_whose_product_leaves_64_bits(new, kernel):  # no
     s.check()
 
 
+@pytest.mark.parametrize("max_kv,window", [(72, 22), (70, 22), (64, 30), (79, 10)])
+def test_a_window_past_the_keys_looks_no_page_up(max_kv, window, kernel):  # noqa: F811
+    """The page that holds max_kv ends before the window begins: it is not the tokens' affair, and may be given back."""
+    s = Step(78, [3], [96], 8, 8, 128, 16, B16)
+    s.table[0, :max_kv // 16 + 1] = -1
+    qg.qgemv_device_error(reset=True)
+    qg.qgemv_attn(s.args(window=window, max_kv=max_kv))
+    assert qg.qgemv_device_error(reset=True) == 0
+    check_seen(s, window_sees(3, 96, window, max_kv))
+
+
 @pytest.mark.parametrize("new,kv_len", [(3, 1), (20, 2), (20, 0), (200, 90), (300, 300), (5, 700)])
 @pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 2, 2 ** 30, 90, 91])
 def test_window_of_any_size(new, kv_len, window, kernel):  # noqa: F811
