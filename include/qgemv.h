@@ -314,7 +314,8 @@ QGEMV_API int qgemv_last_cuda_error(void);
  * (m = 9..16, any format); 52 launches with the fused argmax; 33 launches that quantized fp32
  * activations in-kernel, 34 launches over >= 2 matrices, 35 launches with programmatic dependent launch
  * (quantizer included), 54 launches that covered one K-chunk of long rows; 55 rotary positions, 56 and 57
- * attention (which kernel ran), 58 sampling.
+ * attention (which kernel ran), 58 sampling, 59 and 60 writes into and reads of a packed cache, 61 attention by the packed cache's own
+ * kernel (over an unpacked copy it counts as 56 or 57).
  */
 #define QGEMV_ROUTE_FUSED 33
 #define QGEMV_ROUTE_GROUPED 34
@@ -328,7 +329,10 @@ QGEMV_API int qgemv_last_cuda_error(void);
 #define QGEMV_ROUTE_ATTN_ROWS 56   /* qgemv_attn launches of the 16-row kernel (decode, drafts) */
 #define QGEMV_ROUTE_ATTN_TILES 57  /* qgemv_attn launches of the 128-row tensor-memory kernel (chunks, prompts) */
 #define QGEMV_ROUTE_SAMPLE 58      /* qgemv_sample launches */
-#define QGEMV_NUM_ROUTES 59
+#define QGEMV_ROUTE_CACHE_WRITE 59 /* qgemv_cache_write launches */
+#define QGEMV_ROUTE_CACHE_READ 60  /* qgemv_cache_read launches */
+#define QGEMV_ROUTE_ATTN_PACKED 61 /* qgemv_attn launches of the packed cache's own kernel */
+#define QGEMV_NUM_ROUTES 62
 QGEMV_API int qgemv_route_counts(unsigned long long* out, int n);
 QGEMV_API void qgemv_route_reset(void);
 
@@ -429,6 +433,25 @@ typedef struct {
     int num_pages, page_size, heads, dim;
 } qgemv_cache;
 
+/*
+ * Packed caches: `kind` QGEMV_CACHE_Q4 or QGEMV_CACHE_Q8.  A row (one token, one key/value head) is `dim` codes c of 4 or 8 bits, and for
+ * every block of 32 of them a step d >= 0 and a base m in fp16; a value stands as d * c + m:
+ *     [0 .. dim*bits/8)   codes: Q8 byte e is element e's; Q4 byte j is element 2j's in its low half, element 2j+1's in its high half
+ *     then dim/32 fp16    d of the blocks in their order
+ *     then dim/32 fp16    m of the blocks in their order
+ * qgemv_cache_row_bytes bytes, which is that rounded up to a multiple of 16 (the rest is not used): 80 and 144 for heads of 128.
+ * The strides of such a cache are in BYTES, positive multiples of 16 below 2^31 for tokens and heads and at most 2^39 for pages (a
+ * stride over a dimension of one element is not looked at); dim is a multiple of 32, 32..256; everything else is as above.
+ * A block of values x, each clamped to +-65504 first, is written as follows, with L = 15 or 255, every operation rounded to fp32:
+ *     m = the largest fp16 <= min x;   d = the smallest fp16 >= (max x - m) / L;   r = 1 / d;
+ *     c = min(L, rint((x - m) * r))   (ties to even; 0 where d = 0)
+ * so a value is off by at most d/2 (1 + 2^-12).  A block with a NaN is written as m = NaN, d = 0.
+ */
+#define QGEMV_CACHE_Q4 4
+#define QGEMV_CACHE_Q8 8
+/* Bytes of a row of a packed cache, 0 for an invalid kind or dim. */
+QGEMV_API size_t qgemv_cache_row_bytes(int kind, int dim);
+
 /* Pairing of the rotated elements of a head. */
 typedef enum {
     QGEMV_ROPE_HALF = 0,       /* element i with element i + rot_dim/2 */
@@ -499,6 +522,48 @@ typedef struct {
 } qgemv_rope_args;
 
 QGEMV_API int qgemv_rope(const qgemv_rope_args* args, unsigned flags, void* stream);
+
+/*
+ * Writes new tokens' keys and values into a packed cache as they are (qgemv_rope does it with their rotary positions):
+ * k, v [tokens, cache->heads, cache->dim] of kind x_kind (QGEMV_ACT_F32 / BF16 / F16), last dimension contiguous, 16-byte aligned,
+ * strides multiples of 8 elements and 16 bytes.  Token t goes to slot slots[t]; a negative slot writes nothing, one beyond the cache writes
+ * nothing and sets QGEMV_DEVERR_BAD_INDEX in the device error word.  Slots that are >= 0 must differ.  tokens = 0 does nothing.
+ */
+typedef struct {
+    const void* k;
+    const void* v;
+    long long k_token, k_head, v_token, v_head; /* strides, elements */
+    const qgemv_cache* cache;
+    const long long* slots;
+    int x_kind, tokens;
+} qgemv_cache_write_args;
+
+QGEMV_API int qgemv_cache_write(const qgemv_cache_write_args* args, unsigned flags, void* stream);
+
+/*
+ * Reads keys and values back from a packed cache.  Sequence b (b < seqs) has the rows out_start[b] .. out_start[b+1] - 1 of
+ * k_out and v_out [tokens, cache->heads, cache->dim] (either may be NULL): row out_start[b] + j receives its context token first[b] + j
+ * (first NULL: token j), which is token t % page_size of page pages[b * pages_stride + t / page_size], as in qgemv_attn.  The value
+ * d * c + m is computed in fp32 with one rounding (d * c is exact) and rounded to out_kind (QGEMV_ACT_F32 / BF16 / F16).
+ * Rows outside every sequence are left as they are.  A token before 0, at max_kv or beyond it, beyond the row of the page
+ * table (pages_stride * page_size), or on a page outside the cache, is read as zeros and sets QGEMV_DEVERR_BAD_INDEX.  out_start ascends; values outside 0..tokens are held to it.
+ * Outputs: last dimension contiguous, 16-byte aligned, strides multiples of 8 elements and 16 bytes, apart from each other and the inputs.
+ * tokens = 0 or seqs = 0 does nothing.
+ */
+typedef struct {
+    const qgemv_cache* cache;
+    const int* pages;
+    long long pages_stride;
+    const int* out_start; /* [seqs + 1] */
+    const int* first;     /* [seqs] or NULL */
+    void* k_out;
+    void* v_out;
+    long long k_token, k_head, v_token, v_head; /* strides, elements */
+    int out_kind, tokens, seqs;
+    int max_kv; /* context tokens that may be read */
+} qgemv_cache_read_args;
+
+QGEMV_API int qgemv_cache_read(const qgemv_cache_read_args* args, unsigned flags, void* stream);
 
 /*
  * Attention of new tokens over a paged cache.  Sequence b (b < seqs) has the new tokens q_start[b] .. q_start[b+1] - 1 of

@@ -24,15 +24,18 @@ QGEMV_ARGMAX_STATIC_SCRATCH_BYTES = 16384
 QGEMV_ROPE_HALF, QGEMV_ROPE_INTERLEAVED = 0, 1
 ROPE_LAYOUT = {"half": QGEMV_ROPE_HALF, "interleaved": QGEMV_ROPE_INTERLEAVED}
 ROPE_SCALING = {"none": 0, "linear": 1, "base": 2, "parts": 3, "bands": 4}
+QGEMV_CACHE_Q4, QGEMV_CACHE_Q8 = 4, 8
+PACKED = {"Q4": QGEMV_CACHE_Q4, "Q8": QGEMV_CACHE_Q8}
 QGEMV_ATTN_SCRATCH_HEAD = 65536
 QGEMV_DEVERR_BAD_INDEX = 4
 ROUTE_FUSED, ROUTE_GROUPED, ROUTE_PDL, ROUTE_Q5_K_M1, ROUTE_W8A16_CHANNEL_M1, ROUTE_ARGMAX, ROUTE_M16 = (
     33, 34, 35, 36, 44, 52, 53)
 ROUTE_CHUNKED = 54
 ROUTE_ROPE, ROUTE_ATTN_ROWS, ROUTE_ATTN_TILES, ROUTE_SAMPLE = 55, 56, 57, 58
+ROUTE_CACHE_WRITE, ROUTE_CACHE_READ, ROUTE_ATTN_PACKED = 59, 60, 61
 STATUS = {0: "QGEMV_OK", 1: "QGEMV_ERR_INVALID_ARG", 2: "QGEMV_ERR_UNSUPPORTED", 3: "QGEMV_ERR_MISALIGNED",
           4: "QGEMV_ERR_CUDA", 5: "QGEMV_ERR_DEVICE", 6: "QGEMV_ERR_OVERLAP"}
-NUM_ROUTES = 59
+NUM_ROUTES = 62
 
 _lib = None
 
@@ -57,6 +60,17 @@ class QgemvRopeArgs(ctypes.Structure):
                 ("positions", _vp), ("freqs", _vp), ("cache", ctypes.POINTER(QgemvCache)), ("slots", _vp),
                 ("x_kind", _i32), ("out_kind", _i32), ("tokens", _i32), ("heads", _i32), ("kv_heads", _i32),
                 ("dim", _i32), ("rot_dim", _i32), ("layout", _i32), ("mscale", _f32)]
+
+
+class QgemvCacheWriteArgs(ctypes.Structure):
+    _fields_ = [("k", _vp), ("v", _vp), ("k_token", _i64), ("k_head", _i64), ("v_token", _i64), ("v_head", _i64),
+                ("cache", ctypes.POINTER(QgemvCache)), ("slots", _vp), ("x_kind", _i32), ("tokens", _i32)]
+
+
+class QgemvCacheReadArgs(ctypes.Structure):
+    _fields_ = [("cache", ctypes.POINTER(QgemvCache)), ("pages", _vp), ("pages_stride", _i64), ("out_start", _vp), ("first", _vp),
+                ("k_out", _vp), ("v_out", _vp), ("k_token", _i64), ("k_head", _i64), ("v_token", _i64), ("v_head", _i64),
+                ("out_kind", _i32), ("tokens", _i32), ("seqs", _i32), ("max_kv", _i32)]
 
 
 class QgemvAttnArgs(ctypes.Structure):
@@ -142,6 +156,12 @@ def lib():
         L.qgemv_rope_freqs.restype = i32
         L.qgemv_rope.argtypes = [ctypes.POINTER(QgemvRopeArgs), ctypes.c_uint, vp]
         L.qgemv_rope.restype = i32
+        L.qgemv_cache_row_bytes.argtypes = [i32, i32]
+        L.qgemv_cache_row_bytes.restype = sz
+        L.qgemv_cache_write.argtypes = [ctypes.POINTER(QgemvCacheWriteArgs), ctypes.c_uint, vp]
+        L.qgemv_cache_write.restype = i32
+        L.qgemv_cache_read.argtypes = [ctypes.POINTER(QgemvCacheReadArgs), ctypes.c_uint, vp]
+        L.qgemv_cache_read.restype = i32
         L.qgemv_attn.argtypes = [ctypes.POINTER(QgemvAttnArgs), ctypes.c_uint, vp]
         L.qgemv_attn.restype = i32
         L.qgemv_tune_attn.argtypes = [i32]
@@ -328,6 +348,25 @@ def kv_cache(k, v) -> QgemvCache:
     return c
 
 
+def qgemv_cache_row_bytes(kind, dim: int) -> int:
+    """Bytes of a row (one token, one key/value head) of a packed cache; kind "Q4" or "Q8"."""
+    return int(lib().qgemv_cache_row_bytes(PACKED[kind] if isinstance(kind, str) else int(kind), dim))
+
+
+def packed_cache(kind, k, v, dim: int) -> QgemvCache:
+    """The packed cache ("Q4" or "Q8") of two uint8 tensors [pages, page_size, heads, qgemv_cache_row_bytes(kind, dim)], views with any
+    strides as in kv_cache.  Keep the tensors alive as long as the result."""
+    code = PACKED[kind] if isinstance(kind, str) else int(kind)
+    row = qgemv_cache_row_bytes(code, dim)
+    _need(row > 0, "packed_cache: kind Q4 or Q8, dim a multiple of 32 up to 256")
+    _need(k.dim() == 4 and k.shape == v.shape and str(k.dtype) == str(v.dtype) == "torch.uint8" and k.shape[3] == row,
+          f"packed_cache: k and v alike, uint8 of four dimensions, rows of {row} bytes")
+    _need(k.stride(3) == 1 and v.stride(3) == 1, "packed_cache: the last dimension contiguous")
+    c = QgemvCache(_ptr(k), _ptr(v), *k.stride()[:3], *v.stride()[:3], code, *k.shape[:3], dim)
+    c.tensors = (k, v)
+    return c
+
+
 def _heads_first(t, what):
     _need(t.dim() == 3 and t.stride(2) == 1, f"{what}: [tokens, heads, dim], the last dimension contiguous")
     return t.stride(0), t.stride(1)
@@ -386,6 +425,65 @@ def qgemv_rope(args: QgemvRopeArgs, flags: int = 0, stream=None) -> None:
     _check(lib().qgemv_rope(args, flags, _stream(stream)), "qgemv_rope")
 
 
+def cache_write_args(k, v, cache: QgemvCache, slots) -> QgemvCacheWriteArgs:
+    """Arguments of qgemv_cache_write from tensors: k and v [tokens, heads, dim], slots int64 [tokens].  The result holds the tensors'
+    addresses and keeps the tensors alive; it may be used for many calls."""
+    a = QgemvCacheWriteArgs()
+    a.k_token, a.k_head = _heads_first(k, "cache_write_args: k")
+    a.v_token, a.v_head = _heads_first(v, "cache_write_args: v")
+    _need(k.shape == v.shape and k.dtype == v.dtype and tuple(k.shape[1:]) == (cache.heads, cache.dim),
+          "cache_write_args: k, v and the cache unlike")
+    _need(isinstance(slots, int) or slots.numel() >= k.shape[0], "cache_write_args: slots too short")
+    a.k, a.v, a.slots = _ptr(k), _ptr(v), _ptr(_typed(slots, "int64", "slots"))
+    a.cache = ctypes.pointer(cache)
+    a.x_kind, a.tokens = _kind(k), k.shape[0]
+    a.tensors = (k, v, cache, slots)
+    return a
+
+
+def qgemv_cache_write(args: QgemvCacheWriteArgs, flags: int = 0, stream=None) -> None:
+    """Writes keys and values into a packed cache; args from cache_write_args()."""
+    _check(lib().qgemv_cache_write(args, flags, _stream(stream)), "qgemv_cache_write")
+
+
+def _page_rows(pages, what):
+    """(address, stride of the record, columns) of a page table: the record's stride is also the length of a row, as far as it may be read."""
+    _need(pages.dim() == 2 and str(pages.dtype) == "torch.int32" and (pages.shape[1] <= 1 or pages.stride(1) == 1),
+          f"{what}: pages int32 [seqs, pages]")
+    seqs, columns = pages.shape
+    _need(seqs <= 1 or pages.stride(0) >= columns, f"{what}: rows of pages overlap")
+    return _ptr(pages), columns if seqs <= 1 or columns == 0 else pages.stride(0), columns
+
+
+def cache_read_args(cache: QgemvCache, pages, out_start, k_out=None, v_out=None, first=None) -> QgemvCacheReadArgs:
+    """Arguments of qgemv_cache_read from tensors: pages int32 [seqs, pages of a row] (a view of longer rows
+    too: context beyond its columns is not read), out_start int32 [seqs + 1], first int32 [seqs] or None, k_out and v_out [tokens, heads, dim], either or both.  The result holds the
+    tensors' addresses and keeps the tensors alive; it may be used for many calls."""
+    a = QgemvCacheReadArgs()
+    out = k_out if k_out is not None else v_out
+    _need(out is not None, "cache_read_args: k_out or v_out")
+    for t, name in ((k_out, "k"), (v_out, "v")):
+        if t is not None:
+            token, head = _heads_first(t, f"cache_read_args: {name}_out")
+            _need(t.shape == out.shape and t.dtype == out.dtype and tuple(t.shape[1:]) == (cache.heads, cache.dim),
+                  f"cache_read_args: {name}_out unlike the cache or the other")
+            setattr(a, name + "_out", _ptr(t)), setattr(a, name + "_token", token), setattr(a, name + "_head", head)
+    a.pages, a.pages_stride, columns = _page_rows(pages, "cache_read_args")
+    a.seqs, a.max_kv = pages.shape[0], min(columns * cache.page_size, 2 ** 31 - 1)
+    a.out_start, a.first = _ptr(_typed(out_start, "int32", "out_start")), _ptr(_typed(first, "int32", "first"))
+    _need(isinstance(out_start, int) or out_start.numel() == a.seqs + 1, "cache_read_args: out_start has seqs + 1 values")
+    _need(first is None or isinstance(first, int) or first.numel() == a.seqs, "cache_read_args: first has seqs values")
+    a.cache = ctypes.pointer(cache)
+    a.out_kind, a.tokens = _kind(out), out.shape[0]
+    a.tensors = (cache, pages, out_start, k_out, v_out, first)
+    return a
+
+
+def qgemv_cache_read(args: QgemvCacheReadArgs, flags: int = 0, stream=None) -> None:
+    """Reads keys and values back from a packed cache; args from cache_read_args()."""
+    _check(lib().qgemv_cache_read(args, flags, _stream(stream)), "qgemv_cache_read")
+
+
 def qgemv_attn_scratch_bytes(seqs: int, tokens: int, heads: int, kv_heads: int, dim: int, max_q: int, max_kv: int) -> int:
     """Scratch of every qgemv_attn call with these sizes or smaller seqs, tokens, max_q and max_kv; its first QGEMV_ATTN_SCRATCH_HEAD bytes must start as zeros."""
     return int(lib().qgemv_attn_scratch_bytes(seqs, tokens, heads, kv_heads, dim, max_q, max_kv))
@@ -400,15 +498,10 @@ def attn_args(q, cache: QgemvCache, pages, q_start, kv_len, out, scratch, max_q:
     a.q_token, a.q_head = _heads_first(q, "attn_args: q")
     a.out_token, a.out_head = _heads_first(out, "attn_args: out")
     _need(q.shape == out.shape and q.dtype == out.dtype and q.shape[2] == cache.dim, "attn_args: q, out and the cache unlike")
-    _need(pages.dim() == 2 and str(pages.dtype) == "torch.int32" and (pages.shape[1] == 0 or pages.stride(1) == 1),
-          "attn_args: pages int32 [seqs, pages]")
+    a.pages, a.pages_stride, columns = _page_rows(pages, "attn_args")
     a.q, a.out, a.lse = _ptr(q), _ptr(out), _ptr(_typed(lse, "float32", "lse"))
     a.cache = ctypes.pointer(cache)
     a.seqs = pages.shape[0]
-    # the record's stride is also the length of a row: max_kv holds it to the columns there are
-    columns = pages.shape[1]
-    _need(a.seqs <= 1 or pages.stride(0) >= columns, "attn_args: rows of pages overlap")
-    a.pages, a.pages_stride = _ptr(pages), columns if a.seqs <= 1 or columns == 0 else pages.stride(0)
     max_kv = min(max_kv, columns * cache.page_size)
     a.q_start, a.kv_len = _ptr(_typed(q_start, "int32", "q_start")), _ptr(_typed(kv_len, "int32", "kv_len"))
     _need(isinstance(q_start, int) or q_start.numel() == a.seqs + 1, "attn_args: q_start has seqs + 1 values")

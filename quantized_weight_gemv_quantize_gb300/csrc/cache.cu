@@ -1,0 +1,137 @@
+// Writing into and reading from a packed cache.
+//
+// Both move a token's pieces of 8 elements, keys' heads first, then values': a piece's place within the token is worked out once a thread and
+// kept over the tokens of a block; the tokens' places in the cache are looked up once a block, into shared memory.
+#include "cache_rows.cuh"
+
+namespace qg {
+
+// Threads of a block over a token's pieces: `wide` of them side by side, and as many tokens at a time as there is room for.  (Pieces a
+// token are a multiple of 8, so that a block of 32 elements stays with four neighbouring lanes.)
+struct Lay {
+    int wide, at, deep, row;  // this thread: pieces at, at + wide, ... of the block's tokens row, row + deep, ...
+    __device__ __forceinline__ Lay(int pieces) {
+        wide = min(pieces, CACHE_THREADS);
+        deep = CACHE_THREADS / wide;
+        at = threadIdx.x % wide, row = threadIdx.x / wide;
+    }
+};
+
+// Four tokens' loads of a thread are on their way at once.
+constexpr int AHEAD = 4;
+
+template <int BITS, int XK>
+__global__ void __launch_bounds__(CACHE_THREADS) cache_write_kernel(const CacheWriteArgs a) {
+    __shared__ long long ks[CACHE_TOKENS], vs[CACHE_TOKENS];
+    pdl_launch_dependents();
+    pdl_wait();
+    const long long first = static_cast<long long>(blockIdx.x) * a.block_tokens;
+    const int n = static_cast<int>(min(static_cast<long long>(a.block_tokens), a.tokens - first));
+    if (threadIdx.x < n) {
+        const long long slot = a.slots[first + threadIdx.x];
+        long long k = -1, v = -1;
+        if (slot >= a.num_slots) {
+            atomicOr(a.err, ERR_BAD_INDEX);
+        } else if (slot >= 0) {
+            const long long page = a.page_shift >= 0 ? slot >> a.page_shift : slot / a.page_size, token = slot - page * a.page_size;
+            k = page * a.kc_page + token * a.kc_token, v = page * a.vc_page + token * a.vc_token;
+        }
+        ks[threadIdx.x] = k, vs[threadIdx.x] = v;
+    }
+    __syncthreads();
+    const int per_head = a.dim / 8, half = a.heads * per_head;
+    const Lay lay(2 * half);
+    if (lay.row >= lay.deep) return;  // (threads beyond the last whole token)
+    for (int p = lay.at; p < 2 * half; p += lay.wide) {
+        const bool is_v = p >= half;
+        const int h = (is_v ? p - half : p) / per_head, e = (p - (is_v ? half : 0) - h * per_head) * 8;
+        const long long src = (is_v ? a.v_head : a.k_head) * h + e, token_step = is_v ? a.v_token : a.k_token;
+        const void* x = is_v ? a.v : a.k;
+        uint8_t* rows = static_cast<uint8_t*>(is_v ? a.v_cache : a.k_cache) + (is_v ? a.vc_head : a.kc_head) * h;
+        const long long* place = is_v ? vs : ks;
+        for (int t0 = lay.row; t0 < n; t0 += lay.deep * AHEAD) {
+            float v[AHEAD][8];
+#pragma unroll
+            for (int j = 0; j < AHEAD; ++j) {
+                const int t = t0 + j * lay.deep;
+                if (t < n && place[t] >= 0) load8<XK>(x, (first + t) * token_step + src, v[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < AHEAD; ++j) {
+                const int t = t0 + j * lay.deep;
+                if (t < n && place[t] >= 0) put8<BITS>(rows + place[t], a.dim, e, v[j]);
+            }
+        }
+    }
+}
+
+template <int BITS>
+__global__ void __launch_bounds__(CACHE_THREADS) cache_read_kernel(const CacheReadArgs a) {
+    __shared__ long long ks[CACHE_TOKENS], vs[CACHE_TOKENS];  // place of a row in the cache, -1: zeros, -2: not a row of any sequence
+    pdl_launch_dependents();
+    pdl_wait();
+    const long long first = static_cast<long long>(blockIdx.x) * a.block_tokens;
+    const int n = static_cast<int>(min(static_cast<long long>(a.block_tokens), a.tokens - first));
+    if (threadIdx.x < n) {
+        const int r = static_cast<int>(first) + threadIdx.x;
+        // the last sequence that starts at or before the row
+        int lo = 0, hi = a.seqs;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            if (a.out_start[mid] <= r) lo = mid;
+            else hi = mid;
+        }
+        long long k = -2, v = -2;
+        const int start = max(0, a.out_start[lo]);
+        if (r >= start && r < a.out_start[lo + 1]) {
+            const long long t = static_cast<long long>(a.first ? a.first[lo] : 0) + (r - start);
+            k = v = -1;
+            if (t >= 0 && t < a.reach) {
+                const long long nth = a.page_shift >= 0 ? t >> a.page_shift : t / a.page_size, token = t - nth * a.page_size;
+                const int page = a.pages[lo * a.pages_stride + nth];
+                if (page >= 0 && page < a.num_pages) k = page * a.kc_page + token * a.kc_token, v = page * a.vc_page + token * a.vc_token;
+            }
+            if (k < 0) atomicOr(a.err, ERR_BAD_INDEX);
+        }
+        ks[threadIdx.x] = k, vs[threadIdx.x] = v;
+    }
+    __syncthreads();
+    const int per_head = a.dim / 8, half = a.heads * per_head;
+    const int pieces = half * ((a.k_out ? 1 : 0) + (a.v_out ? 1 : 0));
+    const Lay lay(pieces);
+    if (lay.row >= lay.deep) return;
+    for (int p = lay.at; p < pieces; p += lay.wide) {
+        const bool is_v = !a.k_out || p >= half;
+        const int in = p >= half ? p - half : p, h = in / per_head, e = (in - h * per_head) * 8;
+        const long long dst = (is_v ? a.v_head : a.k_head) * h + e, token_step = is_v ? a.v_token : a.k_token;
+        void* y = is_v ? a.v_out : a.k_out;
+        const uint8_t* rows = (is_v ? a.v_cache : a.k_cache) + (is_v ? a.vc_head : a.kc_head) * h;
+        const long long* place = is_v ? vs : ks;
+        for (int t0 = lay.row; t0 < n; t0 += lay.deep * AHEAD) {
+            float v[AHEAD][8];
+#pragma unroll
+            for (int j = 0; j < AHEAD; ++j) {
+                const int t = t0 + j * lay.deep;
+#pragma unroll
+                for (float& w : v[j]) w = 0.f;
+                if (t < n && place[t] >= 0) get8<BITS>(rows + place[t], a.dim, e, v[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < AHEAD; ++j) {
+                const int t = t0 + j * lay.deep;
+                if (t < n && place[t] >= -1) store8(a.out_kind, y, (first + t) * token_step + dst, v[j]);
+            }
+        }
+    }
+}
+
+template <int BITS>
+static const void* pick_write(int x_kind) {
+    if (x_kind == ACT_F32) return (const void*)cache_write_kernel<BITS, ACT_F32>;
+    return x_kind == ACT_BF16 ? (const void*)cache_write_kernel<BITS, ACT_BF16> : (const void*)cache_write_kernel<BITS, ACT_F16>;
+}
+
+const void* cache_write_kernel_ptr(int bits, int x_kind) { return bits == 4 ? pick_write<4>(x_kind) : pick_write<8>(x_kind); }
+const void* cache_read_kernel_ptr(int bits) { return bits == 4 ? (const void*)cache_read_kernel<4> : (const void*)cache_read_kernel<8>; }
+
+}  // namespace qg

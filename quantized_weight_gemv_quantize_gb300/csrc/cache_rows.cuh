@@ -1,0 +1,128 @@
+// Rows of a packed cache: codes of 4 or 8 bits, a step and a base in fp16 for every 32 of them (the layout is in qgemv.h).
+#pragma once
+#include "common.cuh"
+#include "internal.h"
+#include "step.h"
+
+namespace qg {
+
+template <int XK>
+__device__ __forceinline__ float load1(const void* x, long long i) {
+    if constexpr (XK == ACT_F32) return static_cast<const float*>(x)[i];
+    const uint16_t w = static_cast<const uint16_t*>(x)[i];
+    if constexpr (XK == ACT_BF16) return __uint_as_float(static_cast<uint32_t>(w) << 16);
+    return h2f(w);
+}
+
+// Eight consecutive values, 16-byte aligned, widened exactly.
+template <int XK>
+__device__ __forceinline__ void load8(const void* x, long long i, float (&v)[8]) {
+    if constexpr (XK == ACT_F32) {
+        const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(x) + i);
+        const float4 a = p[0], b = p[1];
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    } else {
+        const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + i);
+        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v[2 * j] = XK == ACT_BF16 ? __uint_as_float(w[j] << 16) : h2f(w[j]);
+            v[2 * j + 1] = XK == ACT_BF16 ? __uint_as_float(w[j] & 0xFFFF0000u) : h2f(w[j] >> 16);
+        }
+    }
+}
+
+__device__ __forceinline__ uint32_t pack2(int kind, float a, float b) {
+    uint32_t r;  // the first operand of the conversion goes to the upper half
+    if (kind == ACT_BF16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    return r;
+}
+
+__device__ __forceinline__ void store1(int kind, void* y, long long i, float v) {
+    if (kind == ACT_F32) static_cast<float*>(y)[i] = v;
+    else static_cast<uint16_t*>(y)[i] = static_cast<uint16_t>(pack2(kind, v, v));
+}
+
+__device__ __forceinline__ void store8(int kind, void* y, long long i, const float (&v)[8]) {
+    if (kind == ACT_F32) {
+        float4* p = reinterpret_cast<float4*>(static_cast<float*>(y) + i);
+        p[0] = make_float4(v[0], v[1], v[2], v[3]);
+        p[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(y) + i) =
+            make_uint4(pack2(kind, v[0], v[1]), pack2(kind, v[2], v[3]), pack2(kind, v[4], v[5]), pack2(kind, v[6], v[7]));
+    }
+}
+
+// Elements e .. e + 7 (e a multiple of 8) of a row of `dim`.  Four consecutive lanes, the first at a multiple of 4, hold a block: they
+// find its least and largest value together, and each writes its own codes.  All four call this, with the same `row`.
+//
+// The base is rounded down and the step up, so that every value lies within the codes: none is cut off by more than the rounding of
+// the fp32 arithmetic.  The product with 1 / d stands for the quotient (one instruction an element instead of eight); it moves a code by
+// one only where the value lies within 2^-14 steps of the middle of two.
+template <int BITS>
+__device__ __forceinline__ void put8(uint8_t* row, int dim, int e, float (&x)[8]) {
+    constexpr float TOP = (1 << BITS) - 1;
+    const unsigned team = 0xFu << (threadIdx.x & 28);
+    float lo = x[0], hi = x[0];
+    bool nan = false;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        nan |= x[j] != x[j];
+        x[j] = fminf(fmaxf(x[j], -65504.f), 65504.f);
+    }
+    lo = x[0], hi = x[0];
+#pragma unroll
+    for (int j = 1; j < 8; ++j) lo = fminf(lo, x[j]), hi = fmaxf(hi, x[j]);
+#pragma unroll
+    for (int o = 1; o < 4; o *= 2) {
+        lo = fminf(lo, __shfl_xor_sync(team, lo, o));
+        hi = fmaxf(hi, __shfl_xor_sync(team, hi, o));
+    }
+    nan = __any_sync(team, nan);
+    __half m = __float2half_rd(lo);
+    const float mf = __half2float(m);
+    __half d = __float2half_ru(__fdiv_rn(__fsub_rn(hi, mf), TOP));
+    if (nan) d = __ushort_as_half(0);
+    const float df = __half2float(d), rate = df == 0.f ? 0.f : __frcp_rn(df);
+    uint32_t c[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) c[j] = __float2uint_rn(fminf(__fmul_rn(__fsub_rn(x[j], mf), rate), TOP));
+    if constexpr (BITS == 4) {
+        uint32_t w = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w |= c[j] << (4 * j);
+        *reinterpret_cast<uint32_t*>(row + e / 2) = w;
+    } else {
+        *reinterpret_cast<uint2*>(row + e) =
+            make_uint2(c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24, c[4] | c[5] << 8 | c[6] << 16 | c[7] << 24);
+    }
+    if (e % 32 == 0) {
+        __half* scale = reinterpret_cast<__half*>(row + dim * BITS / 8);
+        scale[e / 32] = d;
+        scale[dim / 32 + e / 32] = nan ? __ushort_as_half(0x7E00) : m;
+    }
+}
+
+// The values of elements e .. e + 7 of a row.
+template <int BITS>
+__device__ __forceinline__ void get8(const uint8_t* row, int dim, int e, float (&x)[8]) {
+    const __half* scale = reinterpret_cast<const __half*>(row + dim * BITS / 8);
+    uint32_t w[BITS / 4];
+    if constexpr (BITS == 4) {
+        w[0] = *reinterpret_cast<const uint32_t*>(row + e / 2);
+    } else {
+        const uint2 u = *reinterpret_cast<const uint2*>(row + e);
+        w[0] = u.x, w[1] = u.y;
+    }
+    const float d = __half2float(scale[e / 32]), m = __half2float(scale[dim / 32 + e / 32]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const uint32_t c = w[j * BITS / 32] >> (j * BITS % 32) & ((1u << BITS) - 1u);
+        // (d c is exact in fp32, so that this rounds once)
+        x[j] = __fmaf_rn(d, i2f_small(static_cast<int>(c)), m);
+    }
+}
+
+}  // namespace qg

@@ -3,70 +3,72 @@
 // A pair (a, b) of a head turns by t = 2 pi frac(p F / 2^64): p F wraps in 64-bit integer arithmetic, its upper 32
 // bits are the signed fraction of a turn, and sincospif takes them without a range reduction.  The kernel reads q, k and
 // v once and writes each result once; it is bound by those bytes, and by the launch for a few tokens.
-#include "common.cuh"
-#include "internal.h"
-#include "step.h"
+#include "cache_rows.cuh"
 
 namespace qg {
-
-template <int XK>
-__device__ __forceinline__ float load1(const void* x, long long i) {
-    if constexpr (XK == ACT_F32) return static_cast<const float*>(x)[i];
-    const uint16_t w = static_cast<const uint16_t*>(x)[i];
-    if constexpr (XK == ACT_BF16) return __uint_as_float(static_cast<uint32_t>(w) << 16);
-    return h2f(w);
-}
-
-// Eight consecutive values, 16-byte aligned, widened exactly.
-template <int XK>
-__device__ __forceinline__ void load8(const void* x, long long i, float (&v)[8]) {
-    if constexpr (XK == ACT_F32) {
-        const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(x) + i);
-        const float4 a = p[0], b = p[1];
-        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-    } else {
-        const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + i);
-        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            v[2 * j] = XK == ACT_BF16 ? __uint_as_float(w[j] << 16) : h2f(w[j]);
-            v[2 * j + 1] = XK == ACT_BF16 ? __uint_as_float(w[j] & 0xFFFF0000u) : h2f(w[j] >> 16);
-        }
-    }
-}
-
-__device__ __forceinline__ uint32_t pack2(int kind, float a, float b) {
-    uint32_t r;  // the first operand of the conversion goes to the upper half
-    if (kind == ACT_BF16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
-    else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
-    return r;
-}
-
-__device__ __forceinline__ void store1(int kind, void* y, long long i, float v) {
-    if (kind == ACT_F32) static_cast<float*>(y)[i] = v;
-    else static_cast<uint16_t*>(y)[i] = static_cast<uint16_t>(pack2(kind, v, v));
-}
-
-__device__ __forceinline__ void store8(int kind, void* y, long long i, const float (&v)[8]) {
-    if (kind == ACT_F32) {
-        float4* p = reinterpret_cast<float4*>(static_cast<float*>(y) + i);
-        p[0] = make_float4(v[0], v[1], v[2], v[3]);
-        p[1] = make_float4(v[4], v[5], v[6], v[7]);
-    } else {
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(y) + i) =
-            make_uint4(pack2(kind, v[0], v[1]), pack2(kind, v[2], v[3]), pack2(kind, v[4], v[5]), pack2(kind, v[6], v[7]));
-    }
-}
 
 // 16000 tokens of 32 and 8 heads of 128, bf16: 68.1 us, 5.78 TB/s, 85% of what a plain copy reaches.  Small blocks suit it: 64 threads 68.1 us,
 // 128 69.3, 256 77.9, 448 (one piece a thread) 101; two pieces a thread on their way before the table is ready cost registers and
 // took 89.4, streaming loads changed nothing (69.7).  24 blocks an SM (40 registers): with more registers 81.8 us, with 32 spilled ones 70.0; interleaved pairs need no more than 32.
 //
+// With a packed cache (PACKED) the block takes its keys and values in a pass of their own, by blocks of 32 elements: four lanes turn 8 elements each
+// (a key's partner elements are read again, from L1) and pack them together.
+//
 // One block serves one token (blockIdx.x) and every gridDim.y-th group of its pieces.  A piece of a query or key head is
 // 8 pairs (half layout: 8 elements and their 8 partners), 4 pairs (interleaved: 8 elements) or 8 elements that are copied;
 // without VEC it is one pair or one element.  Pieces of the value heads are copied.
+// Elements e .. e + 7 of a head at `src`, turned where they lie in the rotated part.
 template <int XK, bool HALF, bool VEC>
-__global__ void __launch_bounds__(ROPE_THREADS, HALF && VEC ? 24 : 32) rope_kernel(const RopeArgs a) {
+__device__ __forceinline__ void turned8(const RopeArgs& a, const float2* cs, const void* x, long long src, int e, float (&y)[8]) {
+    const int half = a.rot / 2;
+    load8<XK>(x, src + e, y);
+    if (e >= a.rot) return;
+    if constexpr (VEC && HALF) {  // (pieces lie wholly in one half of the rotated part)
+        const bool upper = e >= half;
+        const int at = upper ? e - half : e;
+        float z[8];
+        load8<XK>(x, src + (upper ? at : e + half), z);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float2 t = cs[at + j];
+            y[j] = upper ? y[j] * t.x + z[j] * t.y : y[j] * t.x - z[j] * t.y;
+        }
+    } else if constexpr (VEC) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 t = cs[e / 2 + j];
+            const float u = y[2 * j], v = y[2 * j + 1];
+            y[2 * j] = u * t.x - v * t.y, y[2 * j + 1] = v * t.x + u * t.y;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int i = e + j;
+            if (i >= a.rot) continue;
+            const bool second = HALF ? i >= half : i % 2;
+            const int other = HALF ? (second ? i - half : i + half) : i ^ 1;
+            const float2 t = cs[HALF ? (second ? other : i) : i / 2];
+            const float z = load1<XK>(x, src + other);
+            y[j] = second ? y[j] * t.x + z * t.y : y[j] * t.x - z * t.y;
+        }
+    }
+}
+
+template <int XK, bool HALF, bool VEC, int BITS>
+__device__ __forceinline__ void pack_token(const RopeArgs& a, const float2* cs, long long tok, long long kslot, long long vslot) {
+    const int per_head = a.dim / 8, half = a.kv_heads * per_head;
+    for (int p = blockIdx.y * blockDim.x + threadIdx.x; p < 2 * half; p += blockDim.x * gridDim.y) {
+        const bool is_v = p >= half;
+        const int in = is_v ? p - half : p, h = in / per_head, e = (in - h * per_head) * 8;
+        float y[8];
+        if (is_v) load8<XK>(a.v, tok * a.v_token + h * a.v_head + e, y);
+        else turned8<XK, HALF, VEC>(a, cs, a.k, tok * a.k_token + h * a.k_head, e, y);
+        put8<BITS>(static_cast<uint8_t*>(is_v ? a.v_cache : a.k_cache) + (is_v ? vslot + h * a.vc_head : kslot + h * a.kc_head), a.dim, e, y);
+    }
+}
+
+template <int XK, bool HALF, bool VEC, bool PACKED>
+__global__ void __launch_bounds__(ROPE_THREADS, HALF && VEC && !PACKED ? 24 : PACKED ? 16 : 32) rope_kernel(const RopeArgs a) {
     __shared__ float2 cs[128];
     pdl_launch_dependents();
     pdl_wait();
@@ -91,14 +93,22 @@ __global__ void __launch_bounds__(ROPE_THREADS, HALF && VEC ? 24 : 32) rope_kern
         }
     }
     __syncthreads();
+    if constexpr (PACKED) {
+        if (kslot >= 0) {
+            if (a.cache_kind == QGEMV_CACHE_Q4) pack_token<XK, HALF, VEC, 4>(a, cs, tok, kslot, vslot);
+            else pack_token<XK, HALF, VEC, 8>(a, cs, tok, kslot, vslot);
+        }
+        __syncthreads();  // (keys that are turned in place have been read: one block takes the whole token then)
+    }
     constexpr int W = VEC ? 8 : 1;
     const int turned = VEC && !HALF ? a.rot / 8 : half / W;  // pieces that turn, then those that are copied
     const int per_head = turned + (a.dim - a.rot) / W;
-    const int copied = a.v ? a.dim / W : 0;  // pieces of a value head
-    const int total = (a.heads + a.kv_heads) * per_head + a.kv_heads * copied;
+    const int copied = a.v && !PACKED ? a.dim / W : 0;  // pieces of a value head
+    const int turning = a.heads + (PACKED && !a.k_out ? 0 : a.kv_heads);
+    const int total = turning * per_head + a.kv_heads * copied;
     for (int i = blockIdx.y * blockDim.x + threadIdx.x; i < total; i += blockDim.x * gridDim.y) {
-        if (i >= (a.heads + a.kv_heads) * per_head) {
-            const int j = i - (a.heads + a.kv_heads) * per_head;
+        if (i >= turning * per_head) {
+            const int j = i - turning * per_head;
             const int h = j / copied, e = j % copied * W;
             if (vslot < 0) continue;
             const long long src = tok * a.v_token + h * a.v_head + e, dst = vslot + h * a.vc_head + e;
@@ -118,7 +128,7 @@ __global__ void __launch_bounds__(ROPE_THREADS, HALF && VEC ? 24 : 32) rope_kern
         const long long src = is_q ? tok * a.q_token + h * a.q_head : tok * a.k_token + hk * a.k_head;
         void* y = is_q ? a.q_out : a.k_out;
         const long long dst = is_q ? tok * a.q_out_token + h * a.q_out_head : tok * a.k_out_token + hk * a.k_out_head;
-        const long long cdst = !is_q && kslot >= 0 ? kslot + hk * a.kc_head : -1;
+        const long long cdst = !PACKED && !is_q && kslot >= 0 ? kslot + hk * a.kc_head : -1;
         if (piece < turned) {
             if constexpr (VEC && HALF) {
                 const int e = piece * 8;
@@ -171,15 +181,16 @@ __global__ void __launch_bounds__(ROPE_THREADS, HALF && VEC ? 24 : 32) rope_kern
     }
 }
 
-template <int XK>
+template <int XK, bool PACKED>
 static const void* pick(bool half, bool vec) {
-    if (half) return vec ? (const void*)rope_kernel<XK, true, true> : (const void*)rope_kernel<XK, true, false>;
-    return vec ? (const void*)rope_kernel<XK, false, true> : (const void*)rope_kernel<XK, false, false>;
+    if (half) return vec ? (const void*)rope_kernel<XK, true, true, PACKED> : (const void*)rope_kernel<XK, true, false, PACKED>;
+    return vec ? (const void*)rope_kernel<XK, false, true, PACKED> : (const void*)rope_kernel<XK, false, false, PACKED>;
 }
 
-const void* rope_kernel_ptr(int x_kind, bool half, bool vec) {
-    if (x_kind == ACT_F32) return pick<ACT_F32>(half, vec);
-    return x_kind == ACT_BF16 ? pick<ACT_BF16>(half, vec) : pick<ACT_F16>(half, vec);
+const void* rope_kernel_ptr(int x_kind, bool half, bool vec, bool packed) {
+    if (x_kind == ACT_F32) return packed ? pick<ACT_F32, true>(half, vec) : pick<ACT_F32, false>(half, vec);
+    if (x_kind == ACT_BF16) return packed ? pick<ACT_BF16, true>(half, vec) : pick<ACT_BF16, false>(half, vec);
+    return packed ? pick<ACT_F16, true>(half, vec) : pick<ACT_F16, false>(half, vec);
 }
 
 }  // namespace qg

@@ -27,8 +27,38 @@ struct RopeArgs {
 };
 
 constexpr int ROPE_THREADS = 64;
-// vec: heads are handled in 8-element pieces (the rotated part splits into whole pieces); half: the pairing.
-const void* rope_kernel_ptr(int x_kind, bool half, bool vec);
+// vec: heads are handled in 8-element pieces (the rotated part splits into whole pieces); half: the pairing; packed: the cache's strides are
+// in bytes and its rows packed.
+const void* rope_kernel_ptr(int x_kind, bool half, bool vec, bool packed);
+
+struct CacheWriteArgs {
+    const void *k, *v;
+    long long k_token, k_head, v_token, v_head;
+    void *k_cache, *v_cache;
+    long long kc_page, kc_token, kc_head, vc_page, vc_token, vc_head;  // bytes
+    const long long* slots;
+    unsigned* err;
+    long long num_slots;
+    int tokens, heads, dim, page_size, page_shift;
+    int block_tokens;  // tokens of a block, at most CACHE_TOKENS
+};
+
+struct CacheReadArgs {
+    const uint8_t *k_cache, *v_cache;
+    long long kc_page, kc_token, kc_head, vc_page, vc_token, vc_head;  // bytes
+    void *k_out, *v_out;
+    long long k_token, k_head, v_token, v_head;
+    const int *pages, *out_start, *first;
+    long long pages_stride;
+    unsigned* err;
+    int out_kind, tokens, seqs, num_pages, heads, dim, page_size, page_shift;
+    long long reach;   // context tokens that may be read
+    int block_tokens;
+};
+
+constexpr int CACHE_THREADS = 256, CACHE_TOKENS = 32;
+const void* cache_write_kernel_ptr(int bits, int x_kind);
+const void* cache_read_kernel_ptr(int bits);
 
 struct AttnArgs {
     const void* q;

@@ -60,20 +60,32 @@ static bool same(const Region& a, const Region& b) {
     return a.p == b.p && a.s0 == b.s0 && a.s1 == b.s1 && a.size == b.size && a.n1 == b.n1;
 }
 
+// Packed caches: the bits of a code, 0 for the 16-bit kinds.
+static int packed_bits(int kind) { return kind == QGEMV_CACHE_Q4 ? 4 : kind == QGEMV_CACHE_Q8 ? 8 : 0; }
+static size_t row_bytes(int bits, int dim) { return (static_cast<size_t>(dim) * bits / 8 + dim / 32 * 4 + 15) / 16 * 16; }
+
 // A cache as two regions of pages: [num_pages, the span of a page].
 static size_t cache_bytes(const qgemv_cache& c, long long page, long long token, long long head) {
-    return static_cast<size_t>((c.num_pages - 1) * page + (c.page_size - 1) * token + (c.heads - 1) * head + c.dim) * 2;
+    const int bits = packed_bits(c.kind);
+    const size_t span = static_cast<size_t>((c.num_pages - 1) * page + (c.page_size - 1) * token + (c.heads - 1) * head);
+    return bits ? span + row_bytes(bits, c.dim) : (span + c.dim) * 2;
 }
 
 static int check_cache(const qgemv_cache* c) {
     if (!c->k || !c->v) return QGEMV_ERR_INVALID_ARG;
-    if (c->kind != QGEMV_ACT_BF16 && c->kind != QGEMV_ACT_F16) return QGEMV_ERR_INVALID_ARG;
-    if (c->num_pages < 1 || c->page_size < 1 || c->heads < 1 || c->dim < 8 || c->dim % 8) return QGEMV_ERR_INVALID_ARG;
+    const int bits = packed_bits(c->kind);
+    if (c->kind != QGEMV_ACT_BF16 && c->kind != QGEMV_ACT_F16 && !bits) return QGEMV_ERR_INVALID_ARG;
+    const int step = bits ? 32 : 8;
+    if (c->num_pages < 1 || c->page_size < 1 || c->heads < 1 || c->dim < step || c->dim % step) return QGEMV_ERR_INVALID_ARG;
     if (c->dim > 256) return QGEMV_ERR_UNSUPPORTED;
     const long long s[6] = {c->k_page, c->k_token, c->k_head, c->v_page, c->v_token, c->v_head};
-    for (long long v : s) {
-        if (v < 0 || v > (1ll << 40)) return QGEMV_ERR_INVALID_ARG;
-        if (v % 8) return QGEMV_ERR_MISALIGNED;
+    const long long sizes[3] = {c->num_pages, c->page_size, c->heads};
+    for (int i = 0; i < 6; ++i) {
+        if (s[i] < 0 || s[i] > (1ll << 40)) return QGEMV_ERR_INVALID_ARG;
+        if (s[i] % (bits ? 16 : 8)) return QGEMV_ERR_MISALIGNED;
+        if (!bits || sizes[i % 3] == 1) continue;
+        if (s[i] == 0) return QGEMV_ERR_INVALID_ARG;  // (rows that are one another)
+        if (s[i] > (i % 3 ? (1ll << 31) - 1 : 1ll << 39)) return QGEMV_ERR_UNSUPPORTED;
     }
     for (int i = 0; i < 6; i += 3)  // no offset of the kernels' arithmetic leaves 64 bits
         if (static_cast<double>(c->num_pages) * static_cast<double>(s[i]) + static_cast<double>(c->page_size) * static_cast<double>(s[i + 1]) +
@@ -81,6 +93,12 @@ static int check_cache(const qgemv_cache* c) {
             return QGEMV_ERR_UNSUPPORTED;
     if (!api_aligned(c->k, 16) || !api_aligned(c->v, 16)) return QGEMV_ERR_MISALIGNED;
     return QGEMV_OK;
+}
+
+static int log2_of(int v) {
+    int n = 0;
+    while (n < 30 && 1 << n < v) ++n;
+    return 1 << n == v ? n : -1;
 }
 
 // ---------------------------------------------------------------------------------------------- rotary positions
@@ -166,11 +184,120 @@ static int run_rope(const qgemv_rope_args* a, unsigned flags, void* stream) {
     long long y = (per_token + ROPE_THREADS - 1) / ROPE_THREADS;
     const long long enough = (32ll * sms + T - 1) / T;
     if (y > enough) y = enough;
+    const bool packed = has_c && packed_bits(a->cache->kind);
+    if (packed && a->k_out == a->k) y = 1;  // keys that are packed and turned in place: one block reads them before it writes them
     const bool pdl = (flags & QGEMV_FLAG_PDL) != 0;
-    cudaError_t e = launch_step(rope_kernel_ptr(a->x_kind, half, vec), dim3(static_cast<unsigned>(T), static_cast<unsigned>(y)),
+    cudaError_t e = launch_step(rope_kernel_ptr(a->x_kind, half, vec, packed), dim3(static_cast<unsigned>(T), static_cast<unsigned>(y)),
                                 ROPE_THREADS, 0, 1, pdl, static_cast<cudaStream_t>(stream), r);
     if (e != cudaSuccess) return api_cuda_fail(e);
     api_route(QGEMV_ROUTE_ROPE, pdl);
+    return QGEMV_OK;
+}
+
+// -------------------------------------------------------------------------------- writing and reading a packed cache
+
+// Tokens of a block: enough for a few passes of its threads over their pieces, fewer where the blocks would not fill the GPU.
+static int tokens_a_block(long long tokens, int sms, long long pieces) {
+    const long long few = (tokens + 4ll * sms - 1) / (4ll * sms), most = pieces < CACHE_THREADS ? CACHE_TOKENS : 16;
+    return static_cast<int>(few < 1 ? 1 : few > most ? most : few);
+}
+
+static int run_cache_write(const qgemv_cache_write_args* a, unsigned flags, void* stream) {
+    if (!a || (flags & ~QGEMV_FLAG_PDL) || !a->cache) return QGEMV_ERR_INVALID_ARG;
+    const int xs = elem_size(a->x_kind);
+    if (!xs || a->tokens < 0) return QGEMV_ERR_INVALID_ARG;
+    int st;
+    if ((st = check_cache(a->cache))) return st;
+    const qgemv_cache& c = *a->cache;
+    const int bits = packed_bits(c.kind);
+    if (!bits) return QGEMV_ERR_INVALID_ARG;
+    if (c.heads > 65536) return QGEMV_ERR_UNSUPPORTED;
+    if (a->tokens == 0) return QGEMV_OK;
+    if (!a->k || !a->v || !a->slots) return QGEMV_ERR_INVALID_ARG;
+    const Region k = {a->k, a->tokens, a->k_token, c.heads, a->k_head, c.dim, xs};
+    const Region v = {a->v, a->tokens, a->v_token, c.heads, a->v_head, c.dim, xs};
+    for (const Region* r : {&k, &v})
+        if ((st = r->check(8))) return st;
+    if (!api_aligned(a->slots, 8)) return QGEMV_ERR_MISALIGNED;
+    const size_t kb = cache_bytes(c, c.k_page, c.k_token, c.k_head), vb = cache_bytes(c, c.v_page, c.v_token, c.v_head);
+    for (const Region* r : {&k, &v})
+        if (api_overlaps(c.k, kb, r->p, r->bytes()) || api_overlaps(c.v, vb, r->p, r->bytes())) return QGEMV_ERR_OVERLAP;
+    const size_t ns = static_cast<size_t>(a->tokens) * 8;
+    if (api_overlaps(c.k, kb, a->slots, ns) || api_overlaps(c.v, vb, a->slots, ns)) return QGEMV_ERR_OVERLAP;
+    int sms;
+    unsigned* err;
+    if ((st = api_device(&sms, &err))) return st;
+    CacheWriteArgs w = {};
+    w.k = a->k, w.v = a->v;
+    w.k_token = a->k_token, w.k_head = a->k_head, w.v_token = a->v_token, w.v_head = a->v_head;
+    w.k_cache = c.k, w.v_cache = c.v;
+    w.kc_page = c.k_page, w.kc_token = c.k_token, w.kc_head = c.k_head;
+    w.vc_page = c.v_page, w.vc_token = c.v_token, w.vc_head = c.v_head;
+    w.slots = a->slots, w.err = err, w.num_slots = static_cast<long long>(c.num_pages) * c.page_size;
+    w.tokens = a->tokens, w.heads = c.heads, w.dim = c.dim, w.page_size = c.page_size, w.page_shift = log2_of(c.page_size);
+    w.block_tokens = tokens_a_block(a->tokens, sms, 2ll * c.heads * c.dim / 8);
+    const bool pdl = (flags & QGEMV_FLAG_PDL) != 0;
+    const unsigned blocks = static_cast<unsigned>((a->tokens + static_cast<long long>(w.block_tokens) - 1) / w.block_tokens);
+    cudaError_t e = launch_step(cache_write_kernel_ptr(bits, a->x_kind), dim3(blocks), CACHE_THREADS, 0, 1, pdl,
+                                static_cast<cudaStream_t>(stream), w);
+    if (e != cudaSuccess) return api_cuda_fail(e);
+    api_route(QGEMV_ROUTE_CACHE_WRITE, pdl);
+    return QGEMV_OK;
+}
+
+static int run_cache_read(const qgemv_cache_read_args* a, unsigned flags, void* stream) {
+    if (!a || (flags & ~QGEMV_FLAG_PDL) || !a->cache) return QGEMV_ERR_INVALID_ARG;
+    const int os = elem_size(a->out_kind);
+    if (!os || a->tokens < 0 || a->seqs < 0 || a->pages_stride < 0 || a->max_kv < 0) return QGEMV_ERR_INVALID_ARG;
+    int st;
+    if ((st = check_cache(a->cache))) return st;
+    const qgemv_cache& c = *a->cache;
+    const int bits = packed_bits(c.kind);
+    if (!bits) return QGEMV_ERR_INVALID_ARG;
+    if (c.heads > 65536) return QGEMV_ERR_UNSUPPORTED;
+    if (a->pages_stride > (1ll << 40) || static_cast<double>(a->seqs) * static_cast<double>(a->pages_stride) > SPAN_MAX)
+        return QGEMV_ERR_UNSUPPORTED;
+    if (a->tokens == 0 || a->seqs == 0) return QGEMV_OK;
+    if ((!a->k_out && !a->v_out) || !a->out_start || (!a->pages && a->pages_stride != 0)) return QGEMV_ERR_INVALID_ARG;
+    const Region k = {a->k_out, a->tokens, a->k_token, c.heads, a->k_head, c.dim, os};
+    const Region v = {a->v_out, a->tokens, a->v_token, c.heads, a->v_head, c.dim, os};
+    for (const Region* r : {&k, &v})
+        if (r->p && (st = r->check(8))) return st;
+    if (!api_aligned(a->pages, 4) || !api_aligned(a->out_start, 4) || (a->first && !api_aligned(a->first, 4))) return QGEMV_ERR_MISALIGNED;
+    struct Span { const void* p; size_t n; };
+    // (of a row of the page table no more is read than max_kv reaches)
+    const long long most = (static_cast<long long>(a->max_kv) + c.page_size - 1) / c.page_size;
+    const long long entries = a->pages_stride < most ? a->pages_stride : most;
+    const Span in[] = {{c.k, cache_bytes(c, c.k_page, c.k_token, c.k_head)},
+                       {c.v, cache_bytes(c, c.v_page, c.v_token, c.v_head)},
+                       {a->pages, static_cast<size_t>((a->seqs - 1) * a->pages_stride + entries) * 4},
+                       {a->out_start, (static_cast<size_t>(a->seqs) + 1) * 4},
+                       {a->first, a->first ? static_cast<size_t>(a->seqs) * 4 : 0}};
+    for (const Region* r : {&k, &v}) {
+        if (!r->p) continue;
+        for (const Span& s : in)
+            if (s.n && api_overlaps(r->p, r->bytes(), s.p, s.n)) return QGEMV_ERR_OVERLAP;
+    }
+    if (meet(k, v)) return QGEMV_ERR_OVERLAP;
+    int sms;
+    unsigned* err;
+    if ((st = api_device(&sms, &err))) return st;
+    CacheReadArgs r = {};
+    r.k_cache = static_cast<const uint8_t*>(c.k), r.v_cache = static_cast<const uint8_t*>(c.v);
+    r.kc_page = c.k_page, r.kc_token = c.k_token, r.kc_head = c.k_head;
+    r.vc_page = c.v_page, r.vc_token = c.v_token, r.vc_head = c.v_head;
+    r.k_out = a->k_out, r.v_out = a->v_out;
+    r.k_token = a->k_token, r.k_head = a->k_head, r.v_token = a->v_token, r.v_head = a->v_head;
+    r.pages = a->pages, r.out_start = a->out_start, r.first = a->first, r.pages_stride = a->pages_stride, r.err = err;
+    r.out_kind = a->out_kind, r.tokens = a->tokens, r.seqs = a->seqs, r.num_pages = c.num_pages;
+    r.heads = c.heads, r.dim = c.dim, r.page_size = c.page_size, r.page_shift = log2_of(c.page_size);
+    r.reach = a->pages_stride < most ? a->pages_stride * c.page_size : a->max_kv;
+    r.block_tokens = tokens_a_block(a->tokens, sms, ((a->k_out ? 1 : 0) + (a->v_out ? 1 : 0)) * static_cast<long long>(c.heads) * c.dim / 8);
+    const bool pdl = (flags & QGEMV_FLAG_PDL) != 0;
+    const unsigned blocks = static_cast<unsigned>((a->tokens + static_cast<long long>(r.block_tokens) - 1) / r.block_tokens);
+    cudaError_t e = launch_step(cache_read_kernel_ptr(bits), dim3(blocks), CACHE_THREADS, 0, 1, pdl, static_cast<cudaStream_t>(stream), r);
+    if (e != cudaSuccess) return api_cuda_fail(e);
+    api_route(QGEMV_ROUTE_CACHE_READ, pdl);
     return QGEMV_OK;
 }
 
@@ -404,11 +531,6 @@ static int run_attn(const qgemv_attn_args* a, unsigned flags, void* stream) {
     k.err = err, k.num_pages = c.num_pages, k.page_size = c.page_size, k.kv_heads = c.heads, k.dim = c.dim;
     k.tokens = a->tokens, k.heads = a->heads, k.group = a->heads / c.heads, k.seqs = a->seqs;
     k.max_q = a->max_q, k.max_kv = reach;
-    auto log2_of = [](int v) {
-        int n = 0;
-        while (1 << n < v) ++n;
-        return 1 << n == v ? n : -1;
-    };
     k.group_shift = log2_of(k.group), k.page_shift = log2_of(c.page_size);
     k.scale_log2 = a->scale * 1.44269504088896341f;
     k.window = a->window, k.causal = a->causal || a->window > 0;
@@ -556,6 +678,23 @@ int qgemv_rope(const qgemv_rope_args* args, unsigned flags, void* stream) {
     int st;
     if (api_injected(&st)) return st;
     return run_rope(args, flags, stream);
+}
+
+size_t qgemv_cache_row_bytes(int kind, int dim) {
+    const int bits = packed_bits(kind);
+    return !bits || dim < 32 || dim > 256 || dim % 32 ? 0 : row_bytes(bits, dim);
+}
+
+int qgemv_cache_write(const qgemv_cache_write_args* args, unsigned flags, void* stream) {
+    int st;
+    if (api_injected(&st)) return st;
+    return run_cache_write(args, flags, stream);
+}
+
+int qgemv_cache_read(const qgemv_cache_read_args* args, unsigned flags, void* stream) {
+    int st;
+    if (api_injected(&st)) return st;
+    return run_cache_read(args, flags, stream);
 }
 
 void qgemv_tune_attn(int kernel) { g_attn_kernel.store(kernel == 1 || kernel == 2 ? kernel : 0); }
