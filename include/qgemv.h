@@ -617,6 +617,9 @@ QGEMV_API int qgemv_attn(const qgemv_attn_args* args, unsigned flags, void* stre
  * sizes).  It never falls as a size grows.  No device needed. */
 #define QGEMV_ATTN_SCRATCH_HEAD 65536
 QGEMV_API size_t qgemv_attn_scratch_bytes(int seqs, int tokens, int heads, int kv_heads, int dim, int max_q, int max_kv);
+/* The same for a cache of the given kind.  Over a packed one, calls that are served better by the 128-row kernel (many new tokens) read a 16-bit
+ * copy of their contexts, which is made in the scratch: seqs * (max_kv + 128) rows of it, where a call's sizes allow such. */
+QGEMV_API size_t qgemv_attn_scratch_bytes_ex(int cache_kind, int seqs, int tokens, int heads, int kv_heads, int dim, int max_q, int max_kv);
 
 /*
  * Sampling: one token per row of logits [m, N] (kind QGEMV_ACT_F32 / BF16 / F16, rows `row_stride` elements apart), from

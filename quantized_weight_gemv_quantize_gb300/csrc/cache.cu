@@ -2,6 +2,7 @@
 //
 // Both move a token's pieces of 8 elements, keys' heads first, then values': a piece's place within the token is worked out once a thread and
 // kept over the tokens of a block; the tokens' places in the cache are looked up once a block, into shared memory.
+#include "attn.cuh"
 #include "cache_rows.cuh"
 
 namespace qg {
@@ -125,6 +126,63 @@ __global__ void __launch_bounds__(CACHE_THREADS) cache_read_kernel(const CacheRe
     }
 }
 
+// The keys and values that a batch's new tokens may see, in 16 bits and the order [page, head, token, dim] with pages of `page_size` tokens (a
+// divisor of the cache's), page n of sequence b at b * per_seq + n, and their page table (-1: a page outside the cache).  A block takes
+// CACHE_TOKENS tokens (blockIdx.x) of a sequence (blockIdx.y).  For attention by the 128-row kernel: every row tile of a sequence reads the copy.
+template <int BITS>
+__global__ void __launch_bounds__(CACHE_THREADS) cache_unpack_kernel(const CacheUnpackArgs u) {
+    __shared__ long long ks[CACHE_TOKENS], vs[CACHE_TOKENS];
+    const AttnArgs& a = u.a;
+    pdl_launch_dependents();
+    pdl_wait();
+    const int b = blockIdx.y;
+    const Seq s = find_seq(a, b);
+    const int t0 = static_cast<int>(blockIdx.x) * CACHE_TOKENS;
+    const int from = max(t0, first_key(a, s.first_pos)), to = min(t0 + CACHE_TOKENS, s.usable);
+    if (s.n <= 0 || from >= to) return;
+    if (threadIdx.x < CACHE_TOKENS) {
+        const int t = t0 + static_cast<int>(threadIdx.x);
+        long long k = -1, v = -1;
+        if (t >= from && t < to) {
+            const int nth = div_by(t, a.page_size, a.page_shift), token = t - nth * a.page_size;
+            const int page = a.pages[b * a.pages_stride + nth];
+            const bool there = page >= 0 && page < a.num_pages;
+            if (there) k = page * a.k_page + token * a.k_token, v = page * a.v_page + token * a.v_token;
+            else atomicOr(a.err, ERR_BAD_INDEX);
+            const int n = t / u.page_size;
+            if (t % u.page_size == 0 || t == from) u.table[b * u.per_seq + n] = there ? static_cast<int>(b * u.per_seq + n) : -1;
+        }
+        ks[threadIdx.x] = k, vs[threadIdx.x] = v;
+    }
+    __syncthreads();
+    const int per_head = a.dim / 8, half = a.kv_heads * per_head;
+    const Lay lay(2 * half);
+    if (lay.row >= lay.deep) return;
+    for (int p = lay.at; p < 2 * half; p += lay.wide) {
+        const bool is_v = p >= half;
+        const int in = is_v ? p - half : p, h = in / per_head, e = (in - h * per_head) * 8;
+        void* y = is_v ? u.v_copy : u.k_copy;
+        const uint8_t* rows = (is_v ? u.v + h * a.v_head : u.k + h * a.k_head);
+        const long long* place = is_v ? vs : ks;
+        for (int i0 = from - t0 + lay.row; i0 < to - t0; i0 += lay.deep * AHEAD) {
+            float x[AHEAD][8];
+#pragma unroll
+            for (int j = 0; j < AHEAD; ++j) {
+                const int i = i0 + j * lay.deep;
+                if (i < to - t0 && place[i] >= 0) get8<BITS>(rows + place[i], a.dim, e, x[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < AHEAD; ++j) {
+                const int i = i0 + j * lay.deep;
+                if (i >= to - t0 || place[i] < 0) continue;
+                const int n = (t0 + i) / u.page_size;
+                const long long row = ((b * u.per_seq + n) * a.kv_heads + h) * u.page_size + (t0 + i - n * u.page_size);
+                store8(u.kind, y, row * a.dim + e, x[j]);
+            }
+        }
+    }
+}
+
 template <int BITS>
 static const void* pick_write(int x_kind) {
     if (x_kind == ACT_F32) return (const void*)cache_write_kernel<BITS, ACT_F32>;
@@ -132,6 +190,7 @@ static const void* pick_write(int x_kind) {
 }
 
 const void* cache_write_kernel_ptr(int bits, int x_kind) { return bits == 4 ? pick_write<4>(x_kind) : pick_write<8>(x_kind); }
+const void* cache_unpack_kernel_ptr(int bits) { return bits == 4 ? (const void*)cache_unpack_kernel<4> : (const void*)cache_unpack_kernel<8>; }
 const void* cache_read_kernel_ptr(int bits) { return bits == 4 ? (const void*)cache_read_kernel<4> : (const void*)cache_read_kernel<8>; }
 
 }  // namespace qg

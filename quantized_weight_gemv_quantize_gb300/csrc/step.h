@@ -97,11 +97,41 @@ struct AttnTileArgs {
     AttnArgs a;
 };
 
+// The packed cache's kernel: the cache's two tensor maps, [head, page, token, row] with boxes of `box` rows.
+struct AttnPackedArgs {
+    alignas(64) unsigned long long k_map[16], v_map[16];
+    AttnArgs a;            // k and v are not used; the cache's strides are in bytes
+    const uint8_t *k, *v;
+    int pitch, box, bf16;  // bytes of a row; rows of a copy, 0: no tensor map, every row is copied by itself; type of q and out
+};
+
+// The copy in 16 bits that the 128-row kernel reads in place of a packed cache.
+struct CacheUnpackArgs {
+    AttnArgs a;              // the batch over the packed cache
+    const uint8_t *k, *v;
+    void *k_copy, *v_copy;
+    int* table;
+    long long per_seq;       // pages of a sequence in the copy
+    int page_size, kind;     // of the copy
+};
+const void* cache_unpack_kernel_ptr(int bits);
+
+struct PackedLaunch {
+    unsigned smem, threads, blocks;  // blocks an SM
+    int rows, keys;                  // rows of a row tile, keys of a warp's piece
+};
+// rows: the most rows (new tokens by query heads of a key/value head) of a sequence
+const void* attn_packed4_kernel_ptr(int dim, int rows, PackedLaunch* launch);
+const void* attn_packed8_kernel_ptr(int dim, int rows, PackedLaunch* launch);
+
 struct AttnPlan {
-    bool tiles;  // the 128-row tensor-memory kernel (else the 16-row one)
+    bool tiles;  // the 128-row tensor-memory kernel (else that of few rows)
+    PackedLaunch packed;  // a packed cache's kernel of few rows, where it is taken
+    const void* packed_fn;
     int chunk, parts, row_tiles, rows_part, whole, unit_shift;
     long long grid;
     size_t records, scratch;  // rows of parts' records, bytes of scratch
+    size_t copy;              // where in the scratch the copy of a packed cache begins
     size_t scratch_most;      // scratch that serves every call of these sizes or smaller ones
 };
 

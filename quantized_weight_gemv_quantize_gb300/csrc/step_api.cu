@@ -308,6 +308,8 @@ static std::atomic<int> g_attn_kernel{0};
 static size_t round32(size_t n) { return (n + 31) / 32 * 32; }
 
 constexpr int SMS = 152;
+constexpr int PACKED_BLOCKS = 3;  // blocks an SM of the packed cache's kernel, at most
+constexpr int PACKED_ROWS = 32;   // up to so many rows it is always taken
 
 // Parts that row tiles may be cut into, all together: as many waves of blocks as half the square root of the context's key tiles, at most
 // 16.  A wave costs its start and end, some 3 key tiles, so that more of them win nothing by the estimate below (the limit moves
@@ -322,8 +324,15 @@ static int rows_grid(int dim) { return dim <= 128 ? 2 * SMS : SMS; }
 static size_t scratch_of(size_t records, int dim) {
     return QGEMV_ATTN_SCRATCH_HEAD + round32(records * sizeof(float2)) + records * dim * sizeof(float);
 }
+// The copy in 16 bits of a packed cache's part that a batch sees, and its page table, for any page size (pages of the copy hold up to 128
+// tokens).  0: out of range.
+static size_t copy_bytes(int seqs, int kv_heads, int dim, int max_kv) {
+    const double tokens = static_cast<double>(seqs) * (static_cast<double>(max_kv) + 128);
+    if (seqs > 65535 || tokens > INT_MAX || tokens * kv_heads * dim * 4 > SPAN_MAX) return 0;
+    return (static_cast<size_t>(tokens) * (static_cast<size_t>(kv_heads) * dim * 4 + 4) + 511) / 256 * 256;
+}
 
-static int attn_plan(int seqs, int tokens, int heads, int kv_heads, int dim, int max_q, int max_kv, int window,
+static int attn_plan(int bits, int seqs, int tokens, int heads, int kv_heads, int dim, int max_q, int max_kv, int window,
                      AttnPlan* p) {
     if (seqs < 0 || tokens < 0 || heads < 1 || kv_heads < 1 || heads % kv_heads || dim < 8 || dim % 8 || max_q < 0 ||
         max_kv < 0)
@@ -376,12 +385,21 @@ static int attn_plan(int seqs, int tokens, int heads, int kv_heads, int dim, int
     const double rows_us = 8 + keys16 / 19000 * (seqs > 1 ? 0.75 : 1.0);
     const int forced = g_attn_kernel.load(std::memory_order_relaxed);
     p->tiles = dim <= 128 && (forced ? forced == 2 : rows > 32 && tiles_us < rows_us);
+    int tile_rows = 16;
+    size_t copy = 0;
+    if (bits) {
+        if (rows > INT_MAX / 2) return QGEMV_ERR_UNSUPPORTED;
+        p->packed_fn = (bits == 4 ? attn_packed4_kernel_ptr : attn_packed8_kernel_ptr)(dim, static_cast<int>(rows), &p->packed);
+        tile_rows = p->packed.rows;
+        copy = dim <= 128 && (forced ? forced == 2 : rows > PACKED_ROWS) ? copy_bytes(seqs, kv_heads, dim, max_kv) : 0;
+        p->tiles = copy > 0 && (forced == 2 || tiles_us + 10 < rows_us);
+    }
     size_t records = 0;
     if (!p->tiles) {
-        p->grid = rows_grid(dim);
+        p->grid = bits ? static_cast<long long>(p->packed.blocks) * SMS : rows_grid(dim);
         records = static_cast<size_t>(p->grid) * 2 * 16;
         // Units of 64 keys, longer ones where the bounds alone would let the whole (twice over, for its rounding) pass 32 bits.
-        const double row_tiles = static_cast<double>((rows + 15) / 16) * kv_heads * seqs;
+        const double row_tiles = static_cast<double>((rows + tile_rows - 1) / tile_rows) * kv_heads * seqs;
         p->unit_shift = 6;
         while (p->unit_shift < 30 && row_tiles * (static_cast<double>(max_kv >> p->unit_shift) + 1) > 1e9) ++p->unit_shift;
         if (row_tiles > 1e9) return QGEMV_ERR_UNSUPPORTED;
@@ -399,8 +417,10 @@ static int attn_plan(int seqs, int tokens, int heads, int kv_heads, int dim, int
     }
     p->records = records;
     p->scratch = scratch_of(records, dim);
+    if (p->tiles && copy) p->copy = (p->scratch + 255) / 256 * 256, p->scratch = p->copy + copy;
     // What every call of these sizes or smaller ones is content with: the choices above do not grow with the sizes, these bounds do.
-    size_t most = dim <= 128 && forced == 2 ? 0 : static_cast<size_t>(rows_grid(dim)) * 2 * 16;
+    const int grid = bits ? PACKED_BLOCKS * SMS : rows_grid(dim);
+    size_t most = dim <= 128 && forced == 2 ? 0 : static_cast<size_t>(grid) * 2 * 16;
     if (dim <= 128 && (forced ? forced == 2 : rows > 32) && blocks >= 16) {
         const long long n = blocks / 8 < 32 ? blocks / 8 : 32, limit = parts_max(blocks);
         const long long parts = tiles < limit && tiles * n < limit ? tiles * n : limit;
@@ -408,13 +428,14 @@ static int attn_plan(int seqs, int tokens, int heads, int kv_heads, int dim, int
         if (cut > most) most = cut;
     }
     p->scratch_most = scratch_of(most, dim);
+    if (copy) p->scratch_most = (p->scratch_most + 255) / 256 * 256 + copy;
     return QGEMV_OK;
 }
 
 // Dynamic shared memory of a kernel, set once per device.
 static int allow_smem(const void* fn, unsigned smem) {
     static std::mutex mu;
-    static const void* done[64][16];
+    static const void* done[64][48];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return api_cuda_fail(e);
@@ -431,7 +452,8 @@ static int allow_smem(const void* fn, unsigned smem) {
     return QGEMV_ERR_UNSUPPORTED;
 }
 
-// Tensor map of 16-bit elements with 64 of them to a row of a box, in the 128-byte swizzle; strides in elements.  False where the
+// Tensor map of 16-bit elements with 64 of them to a row of a box, in the 128-byte swizzle, strides in elements; or of a packed cache's
+// rows as 32-bit words, strides in bytes, as they lie.  False where the
 // tensor cannot be described by one (then the kernel copies row by row).  Host arithmetic of the driver, about a microsecond.
 static bool tensor_map(unsigned long long (&map)[16], const void* base, int kind, const long long (&size)[4], const long long (&stride)[3],
                        const int (&box)[4]) {
@@ -450,19 +472,21 @@ static bool tensor_map(unsigned long long (&map)[16], const void* base, int kind
     }();
     if (!encode) return false;
     static_assert(sizeof(CUtensorMap) == sizeof(map), "");
+    const bool packed = packed_bits(kind) != 0;
     cuuint64_t dims[4], strides[3];
     cuuint32_t boxes[4];
     for (int i = 0; i < 4; ++i) dims[i] = static_cast<cuuint64_t>(size[i]), boxes[i] = static_cast<cuuint32_t>(box[i]);
     for (int i = 0; i < 3; ++i) {
         // (a dimension of one element is never stepped over: any valid stride will do)
-        const long long s = size[i + 1] > 1 ? stride[i] : size[0];
-        if (s <= 0 || s >= 1ll << 38 || s % 8) return false;
-        strides[i] = static_cast<cuuint64_t>(s) * 2;
+        const long long s = (size[i + 1] > 1 ? stride[i] : packed ? size[0] * 4 : size[0]) * (packed ? 1 : 2);
+        if (s <= 0 || s >= 1ll << 39 || s % 16) return false;
+        strides[i] = static_cast<cuuint64_t>(s);
     }
     const cuuint32_t ones[4] = {1, 1, 1, 1};
     return encode(reinterpret_cast<CUtensorMap*>(map),
-                  kind == QGEMV_ACT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
-                  const_cast<void*>(base), dims, strides, boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  packed ? CU_TENSOR_MAP_DATA_TYPE_UINT32 : kind == QGEMV_ACT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+                  const_cast<void*>(base), dims, strides, boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  packed ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -477,10 +501,11 @@ static int run_attn(const qgemv_attn_args* a, unsigned flags, void* stream) {
     int st;
     if ((st = check_cache(a->cache))) return st;
     const qgemv_cache& c = *a->cache;
-    if (c.kind != a->kind || a->tokens < 0 || a->seqs < 0 || a->pages_stride < 0 || a->window < 0) return QGEMV_ERR_INVALID_ARG;
+    const int bits = packed_bits(c.kind);
+    if ((!bits && c.kind != a->kind) || a->tokens < 0 || a->seqs < 0 || a->pages_stride < 0 || a->window < 0) return QGEMV_ERR_INVALID_ARG;
     if (!(a->scale > 0.f && a->scale <= 1e30f)) return QGEMV_ERR_INVALID_ARG;  // NaN too
     AttnPlan p;
-    if ((st = attn_plan(a->seqs, a->tokens, a->heads, c.heads, c.dim, a->max_q, a->max_kv, a->window, &p))) return st;
+    if ((st = attn_plan(bits, a->seqs, a->tokens, a->heads, c.heads, c.dim, a->max_q, a->max_kv, a->window, &p))) return st;
     if (a->pages_stride > (1ll << 40) || static_cast<double>(a->seqs) * static_cast<double>(a->pages_stride) > SPAN_MAX)
         return QGEMV_ERR_UNSUPPORTED;
     // The keys that a row of the page table reaches, and the entries of a row that may be read.
@@ -537,15 +562,50 @@ static int run_attn(const qgemv_attn_args* a, unsigned flags, void* stream) {
     k.chunk = p.chunk, k.parts = p.parts, k.row_tiles = p.row_tiles, k.rows_part = p.rows_part, k.whole = p.whole;
     k.unit_shift = p.unit_shift;
     const bool pdl = (flags & QGEMV_FLAG_PDL) != 0;
+    qgemv_cache copy = c;
     unsigned smem, threads;
-    const void* fn = (p.tiles ? attn_tiles_kernel_ptr : attn_rows_kernel_ptr)(a->kind == QGEMV_ACT_BF16, c.dim, &smem, &threads);
+    const void* fn;
+    if (bits && !p.tiles) fn = p.packed_fn, smem = p.packed.smem, threads = p.packed.threads;
+    else fn = (p.tiles ? attn_tiles_kernel_ptr : attn_rows_kernel_ptr)(a->kind == QGEMV_ACT_BF16, c.dim, &smem, &threads);
     if ((st = allow_smem(fn, smem))) return st;
-    cudaError_t e;
+    // The largest power of two, up to `most`, that divides the page.
+    auto part_of_page = [&](int most) {
+        while (c.page_size % most) most /= 2;
+        return most;
+    };
+    cudaError_t e = cudaSuccess;
+    bool chained = pdl;  // the kernel that computes starts with the tail of the one before it, and waits there
+    if (bits && p.tiles) {
+        CacheUnpackArgs u = {};
+        u.a = k, u.k = static_cast<const uint8_t*>(c.k), u.v = static_cast<const uint8_t*>(c.v);
+        u.page_size = part_of_page(128), u.kind = a->kind;
+        u.per_seq = (static_cast<long long>(reach) + u.page_size - 1) / u.page_size;
+        const size_t rows = static_cast<size_t>(u.per_seq) * a->seqs * u.page_size, bytes = rows * c.heads * c.dim * 2;
+        u.k_copy = static_cast<uint8_t*>(a->scratch) + p.copy;
+        u.v_copy = static_cast<uint8_t*>(u.k_copy) + bytes;
+        u.table = reinterpret_cast<int*>(static_cast<uint8_t*>(u.v_copy) + bytes);
+        if (reach > 0) {
+            e = launch_step(cache_unpack_kernel_ptr(bits), dim3(static_cast<unsigned>((reach + CACHE_TOKENS - 1) / CACHE_TOKENS), static_cast<unsigned>(a->seqs)),
+                            CACHE_THREADS, 0, 1, pdl, static_cast<cudaStream_t>(stream), u);
+            if (e != cudaSuccess) return api_cuda_fail(e);
+            chained = true;
+        }
+        // from here on the copy is the cache
+        copy.kind = a->kind, copy.k = u.k_copy, copy.v = u.v_copy, copy.num_pages = static_cast<int>(u.per_seq * a->seqs), copy.page_size = u.page_size;
+        if (copy.num_pages < 1) copy.num_pages = 1;
+        copy.k_token = copy.v_token = c.dim, copy.k_head = copy.v_head = static_cast<long long>(u.page_size) * c.dim;
+        copy.k_page = copy.v_page = copy.k_head * c.heads;
+        k.k = static_cast<const uint16_t*>(copy.k), k.v = static_cast<const uint16_t*>(copy.v);
+        k.k_page = copy.k_page, k.k_token = copy.k_token, k.k_head = copy.k_head;
+        k.v_page = copy.v_page, k.v_token = copy.v_token, k.v_head = copy.v_head;
+        k.pages = u.table, k.pages_stride = u.per_seq;
+        k.num_pages = copy.num_pages, k.page_size = copy.page_size, k.page_shift = log2_of(copy.page_size);
+    }
     if (p.tiles) {
         AttnTileArgs ta = {};
+        const qgemv_cache& c = copy;
         // The tokens of one copy: the largest power of two that divides the page and a key tile; 8 is the swizzle's period.
-        int box = 128;
-        while (c.page_size % box) box /= 2;
+        const int box = part_of_page(128);
         const long long cache[4] = {c.dim, c.page_size, c.num_pages, c.heads};
         if (box >= 8 && tensor_map(ta.k_map, c.k, c.kind, cache, {c.k_token, c.k_page, c.k_head}, {64, box, 1, 1}) &&
             tensor_map(ta.v_map, c.v, c.kind, cache, {c.v_token, c.v_page, c.v_head}, {64, box, 1, 1}))
@@ -554,7 +614,7 @@ static int run_attn(const qgemv_attn_args* a, unsigned flags, void* stream) {
                                                    {a->q_head, a->q_token, c.dim}, {64, k.group, 128 / k.group, 1});
         k.wide = api_aligned(a->out, 32) && api_aligned(k.part_sum, 32) && a->out_token % 16 == 0 && a->out_head % 16 == 0 && c.dim % 16 == 0;
         ta.a = k;
-        e = launch_step(fn, dim3(static_cast<unsigned>(p.grid < sms ? p.grid : sms)), threads, smem, 1, pdl, static_cast<cudaStream_t>(stream), ta);
+        e = launch_step(fn, dim3(static_cast<unsigned>(p.grid < sms ? p.grid : sms)), threads, smem, 1, chained, static_cast<cudaStream_t>(stream), ta);
         if (e == cudaSuccess && p.parts > 1) {
             // starts with the tail of the kernel before it, and waits there
             const long long rows = (static_cast<long long>(p.row_tiles) * k.kv_heads * k.seqs - p.whole) * p.rows_part;
@@ -562,11 +622,21 @@ static int run_attn(const qgemv_attn_args* a, unsigned flags, void* stream) {
                             dim3(static_cast<unsigned>((rows + JOIN_WARPS - 1) / JOIN_WARPS)), JOIN_WARPS * 32, 0, 1, true,
                             static_cast<cudaStream_t>(stream), k);
         }
+    } else if (bits) {
+        AttnPackedArgs pk = {};
+        pk.a = k, pk.k = static_cast<const uint8_t*>(c.k), pk.v = static_cast<const uint8_t*>(c.v);
+        pk.pitch = static_cast<int>(row_bytes(bits, c.dim)), pk.bf16 = a->kind == QGEMV_ACT_BF16;
+        const int box = part_of_page(p.packed.keys);  // 8 rows begin at multiples of 128 bytes, as a tensor-map copy has to
+        const long long cache[4] = {pk.pitch / 4, c.page_size, c.num_pages, c.heads};
+        if (box >= 8 && tensor_map(pk.k_map, c.k, c.kind, cache, {c.k_token, c.k_page, c.k_head}, {pk.pitch / 4, box, 1, 1}) &&
+            tensor_map(pk.v_map, c.v, c.kind, cache, {c.v_token, c.v_page, c.v_head}, {pk.pitch / 4, box, 1, 1}))
+            pk.box = box;
+        e = launch_step(fn, dim3(static_cast<unsigned>(p.grid)), threads, smem, 1, pdl, static_cast<cudaStream_t>(stream), pk);
     } else {
         e = launch_step(fn, dim3(static_cast<unsigned>(p.grid)), threads, smem, 1, pdl, static_cast<cudaStream_t>(stream), k);
     }
     if (e != cudaSuccess) return api_cuda_fail(e);
-    api_route(p.tiles ? QGEMV_ROUTE_ATTN_TILES : QGEMV_ROUTE_ATTN_ROWS, pdl);
+    api_route(p.tiles ? QGEMV_ROUTE_ATTN_TILES : bits ? QGEMV_ROUTE_ATTN_PACKED : QGEMV_ROUTE_ATTN_ROWS, pdl);
     return QGEMV_OK;
 }
 
@@ -701,7 +771,15 @@ void qgemv_tune_attn(int kernel) { g_attn_kernel.store(kernel == 1 || kernel == 
 
 size_t qgemv_attn_scratch_bytes(int seqs, int tokens, int heads, int kv_heads, int dim, int max_q, int max_kv) {
     AttnPlan p;
-    return attn_plan(seqs, tokens, heads, kv_heads, dim, max_q, max_kv, 0, &p) ? 0 : (p.scratch_most + 255) / 256 * 256;
+    return attn_plan(0, seqs, tokens, heads, kv_heads, dim, max_q, max_kv, 0, &p) ? 0 : (p.scratch_most + 255) / 256 * 256;
+}
+
+size_t qgemv_attn_scratch_bytes_ex(int cache_kind, int seqs, int tokens, int heads, int kv_heads, int dim, int max_q, int max_kv) {
+    AttnPlan p;
+    const int bits = packed_bits(cache_kind);
+    if (!bits && cache_kind != QGEMV_ACT_BF16 && cache_kind != QGEMV_ACT_F16) return 0;
+    if (bits && dim % 32) return 0;
+    return attn_plan(bits, seqs, tokens, heads, kv_heads, dim, max_q, max_kv, 0, &p) ? 0 : (p.scratch_most + 255) / 256 * 256;
 }
 
 int qgemv_attn(const qgemv_attn_args* args, unsigned flags, void* stream) {

@@ -21,7 +21,8 @@ def toward(x, up):
 def pack(x, bits):
     """(codes uint8 [..., dim], steps fp16, bases fp16 [..., dim/32]) of x [..., dim] fp32."""
     top = F32((1 << bits) - 1)
-    x = x.astype(F32).reshape(*x.shape[:-1], -1, 32)
+    shape = x.shape
+    x = x.astype(F32).reshape(*shape[:-1], shape[-1] // 32, 32)
     nan = np.isnan(x).any(-1)
     x = np.clip(np.where(np.isnan(x), F32(0), x), F32(-65504), F32(65504))
     m = toward(x.min(-1), False)
@@ -30,7 +31,7 @@ def pack(x, bits):
     with np.errstate(divide="ignore"):
         r = np.where(d == 0, F32(0), F32(1) / d.astype(F32)).astype(F32)
     c = np.minimum(np.rint((x - m.astype(F32)[..., None]) * r[..., None]), top).astype(np.uint8)
-    return c.reshape(*c.shape[:-2], -1), d, np.where(nan, F16(np.nan), m)
+    return c.reshape(shape), d, np.where(nan, F16(np.nan), m)
 
 
 def to_bytes(codes, d, m, bits):
@@ -46,7 +47,7 @@ def parts(rows, bits, dim):
     """(codes, steps, bases) that rows of bytes hold, the codes as whole numbers."""
     n, g = dim * bits // 8, dim // 32
     b = rows[..., :n]
-    codes = b if bits == 8 else np.stack([b & 15, b >> 4], -1).reshape(*b.shape[:-1], dim)
+    codes = b if bits == 8 else np.stack([b & 15, b >> 4], -1).reshape(*rows.shape[:-1], dim)
     scale = np.ascontiguousarray(rows[..., n:n + 4 * g]).view(F16)
     return codes, scale[..., :g], scale[..., g:]
 
