@@ -20,11 +20,6 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool l
     const int n = live ? 16 : 0;  // 0 source bytes: the 16 bytes are filled with zeros and src is not read
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 template <int DP>
 struct RowsShape {
     static constexpr int WARPS = 4;
@@ -263,7 +258,7 @@ __global__ void __launch_bounds__(RowsShape<DP>::WARPS * 32) attn_rows_kernel(co
     pdl_launch_dependents();
     pdl_wait();
     divide_rows<16, 16>(
-        a, &last, [&](const Tile& t, long long record) { attend<DP, BF>(a, t, record, smem); },
+        a, a.kv_heads, 1, 128, &last, [&](const Tile& t, long long record) { attend<DP, BF>(a, t, record * 16, smem); },
         [&](const Tile& t) {
             constexpr int THREADS = RowsShape<DP>::WARPS * 32;
             if (t.rows <= THREADS / (DP / 4)) join_rows<DP, THREADS, BF, 1>(a, t);

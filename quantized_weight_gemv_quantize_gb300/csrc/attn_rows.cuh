@@ -4,6 +4,11 @@
 
 namespace qg {
 
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t at) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
@@ -58,10 +63,11 @@ __device__ __forceinline__ void join_rows(const AttnArgs& a, const Tile& t) {
         if (r0 + k * ROWS < t.rows) put_row4<BF>(a, t, r0 + k * ROWS, d, x[k], m[k], l[k]);
 }
 
-// A block's parts of the batch's row tiles of ROWS rows, one after another: attend(t, record) computes one, into the result or into its record,
-// join(t) joins the parts of one; both are called by the whole block.  Ranges of keys begin at multiples of STEP.  `last` is in shared memory.
+// A block's parts of the batch's row tiles, one after another: attend(t, record) computes one, into the result or into its record, join(t) joins the
+// parts of one; both are called by the whole block.  A row tile is ROWS rows of each of `heads` key/value heads, `groups` times those make all of
+// them.  Ranges of keys begin at multiples of STEP; less than `few` keys are not worth a block.  `last` is in shared memory.
 template <int ROWS, int STEP, class Attend, class Join>
-__device__ __forceinline__ void divide_rows(const AttnArgs& a, unsigned* last, Attend&& attend, Join&& join) {
+__device__ __forceinline__ void divide_rows(const AttnArgs& a, int groups, int heads, unsigned few, unsigned* last, Attend&& attend, Join&& join) {
     const unsigned lane = threadIdx.x % 32, me = blockIdx.x, blocks = gridDim.x, seqs = a.seqs, unit = a.unit_shift;
     // A sequence in the division of the work: its row tiles, each as many units of keys (64, or more where 32 bits would not
     // hold the whole) as any of its rows may see, at least one (a row that sees nothing has its zeros written).
@@ -73,7 +79,7 @@ __device__ __forceinline__ void divide_rows(const AttnArgs& a, unsigned* last, A
         sq = find_seq(a, static_cast<int>(b));
         int lo, hi;
         find_keys(a, sq, 0, sq.n * a.group, STEP, &lo, &hi);
-        sq_tiles = (sq.n * a.group + ROWS - 1) / ROWS * a.kv_heads;
+        sq_tiles = (sq.n * a.group + ROWS - 1) / ROWS * groups;
         sq_units = max(1u, (static_cast<unsigned>(hi - lo) + (1u << unit) - 1) >> unit);
     };
     // Sum over all sequences, 32 at a time (a lane each), every warp for itself.
@@ -86,7 +92,7 @@ __device__ __forceinline__ void divide_rows(const AttnArgs& a, unsigned* last, A
         return __reduce_add_sync(0xffffffffu, v);
     };
     if (seqs <= 32) read_seq(lane);
-    const unsigned least = max(1u, 128u >> unit);  // less than 128 keys are not worth a block
+    const unsigned least = max(1u, few >> unit);
     const unsigned units = sum_of([&] { return sq_tiles * sq_units; }), row_tiles = sum_of([&] { return sq_tiles; });
     // A block's share.  Where there are no more row tiles than blocks, it is made as long as it takes for every block to have a part
     // of one row tile only: a second part costs a block's start and end again, some 400 keys' time.  The row tiles' keys are then
@@ -142,10 +148,10 @@ __device__ __forceinline__ void divide_rows(const AttnArgs& a, unsigned* last, A
         t.seq = static_cast<int>(b);
         t.q0 = sq.q0, t.first_pos = sq.first_pos;
         if (sq.n * a.group <= ROWS) {
-            t.kv_head = static_cast<int>(nth), t.row0 = 0;
+            t.kv_head = static_cast<int>(nth) * heads, t.row0 = 0;
         } else {
-            const unsigned in_head = sq_tiles / a.kv_heads;
-            t.kv_head = static_cast<int>(nth / in_head), t.row0 = static_cast<int>(nth % in_head * ROWS);
+            const unsigned in_head = sq_tiles / groups;
+            t.kv_head = static_cast<int>(nth / in_head) * heads, t.row0 = static_cast<int>(nth % in_head * ROWS);
         }
         t.rows = min(ROWS, sq.n * a.group - t.row0);
         int lo, hi;
@@ -159,7 +165,7 @@ __device__ __forceinline__ void divide_rows(const AttnArgs& a, unsigned* last, A
         t.index = first;
         // A block has at most two parts of split row tiles: one that another block began (record 2 b) and one that it begins
         // itself (record 2 b + 1).
-        attend(t, (2 * me + (t.part == 0 ? 1 : 0)) * 16);
+        attend(t, 2 * me + (t.part == 0 ? 1 : 0));
         if (t.parts > 1) {
             // The block that arrives last joins the parts (in their order, so the result does not depend on which one that
             // is) and puts the counter back to zero.

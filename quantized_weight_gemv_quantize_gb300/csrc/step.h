@@ -97,12 +97,15 @@ struct AttnTileArgs {
     AttnArgs a;
 };
 
-// The packed cache's kernel: the cache's two tensor maps, [head, page, token, row] with boxes of `box` rows.
+// The packed cache's kernel: the cache's two tensor maps, [head, page, token, row] with boxes of 16 rows of a block's heads.
 struct AttnPackedArgs {
     alignas(64) unsigned long long k_map[16], v_map[16];
     AttnArgs a;            // k and v are not used; the cache's strides are in bytes
     const uint8_t *k, *v;
-    int pitch, box, bf16;  // bytes of a row; rows of a copy, 0: no tensor map, every row is copied by itself; type of q and out
+    int pitch, bf16;       // bytes of a row; type of q and out
+    int line;              // 16 keys from a multiple of 16 on lie on one page, and the tensor maps serve
+    int hb_shift;          // log2 of the key/value heads that a block takes side by side
+    unsigned few;          // keys that are not worth a block
 };
 
 // The copy in 16 bits that the 128-row kernel reads in place of a packed cache.
@@ -118,15 +121,18 @@ const void* cache_unpack_kernel_ptr(int bits);
 
 struct PackedLaunch {
     unsigned smem, threads, blocks;  // blocks an SM
-    int rows, keys;                  // rows of a row tile, keys of a warp's piece
+    int rows, warps;                 // rows of a row tile and head, warps of a block
 };
 // rows: the most rows (new tokens by query heads of a key/value head) of a sequence
 const void* attn_packed4_kernel_ptr(int dim, int rows, PackedLaunch* launch);
 const void* attn_packed8_kernel_ptr(int dim, int rows, PackedLaunch* launch);
+const void* attn_packed4f_kernel_ptr(int dim, int rows, PackedLaunch* launch);  // f16
+const void* attn_packed8f_kernel_ptr(int dim, int rows, PackedLaunch* launch);
 
 struct AttnPlan {
     bool tiles;  // the 128-row tensor-memory kernel (else that of few rows)
     PackedLaunch packed;  // a packed cache's kernel of few rows, where it is taken
+    int hb_shift;         // of it
     const void* packed_fn;
     int chunk, parts, row_tiles, rows_part, whole, unit_shift;
     long long grid;

@@ -6,6 +6,7 @@
 #include <math.h>
 #include <mutex>
 #include <stddef.h>
+#include <stdlib.h>
 
 #include "../../include/qgemv.h"
 #include "internal.h"
@@ -332,7 +333,7 @@ static size_t copy_bytes(int seqs, int kv_heads, int dim, int max_kv) {
     return (static_cast<size_t>(tokens) * (static_cast<size_t>(kv_heads) * dim * 4 + 4) + 511) / 256 * 256;
 }
 
-static int attn_plan(int bits, int seqs, int tokens, int heads, int kv_heads, int dim, int max_q, int max_kv, int window,
+static int attn_plan(int bits, bool f16, int seqs, int tokens, int heads, int kv_heads, int dim, int max_q, int max_kv, int window,
                      AttnPlan* p) {
     if (seqs < 0 || tokens < 0 || heads < 1 || kv_heads < 1 || heads % kv_heads || dim < 8 || dim % 8 || max_q < 0 ||
         max_kv < 0)
@@ -389,18 +390,26 @@ static int attn_plan(int bits, int seqs, int tokens, int heads, int kv_heads, in
     size_t copy = 0;
     if (bits) {
         if (rows > INT_MAX / 2) return QGEMV_ERR_UNSUPPORTED;
-        p->packed_fn = (bits == 4 ? attn_packed4_kernel_ptr : attn_packed8_kernel_ptr)(dim, static_cast<int>(rows), &p->packed);
+        p->packed_fn = (bits == 4 ? f16 ? attn_packed4f_kernel_ptr : attn_packed4_kernel_ptr : f16 ? attn_packed8f_kernel_ptr : attn_packed8_kernel_ptr)(
+            dim, static_cast<int>(rows), &p->packed);
         tile_rows = p->packed.rows;
+        // heads side by side
+        const long long one = (rows + tile_rows - 1) / tile_rows * kv_heads * seqs;
+        const char* env = getenv("HB");
+        int most_hb = env ? atoi(env) : 3;
+        while (p->hb_shift < most_hb && (2 << p->hb_shift) <= p->packed.warps && kv_heads % (2 << p->hb_shift) == 0 &&
+               (env || (one >> (p->hb_shift + 1)) * 8 >= static_cast<long long>(p->packed.blocks) * SMS))
+            ++p->hb_shift;
         copy = dim <= 128 && (forced ? forced == 2 : rows > PACKED_ROWS) ? copy_bytes(seqs, kv_heads, dim, max_kv) : 0;
         p->tiles = copy > 0 && (forced == 2 || tiles_us + 10 < rows_us);
     }
     size_t records = 0;
     if (!p->tiles) {
         p->grid = bits ? static_cast<long long>(p->packed.blocks) * SMS : rows_grid(dim);
-        records = static_cast<size_t>(p->grid) * 2 * 16;
+        records = static_cast<size_t>(p->grid) * 2 * (bits ? p->packed.warps * p->packed.rows : 16);
         // Units of 64 keys, longer ones where the bounds alone would let the whole (twice over, for its rounding) pass 32 bits.
         const double row_tiles = static_cast<double>((rows + tile_rows - 1) / tile_rows) * kv_heads * seqs;
-        p->unit_shift = 6;
+        p->unit_shift = bits ? 5 : 6;
         while (p->unit_shift < 30 && row_tiles * (static_cast<double>(max_kv >> p->unit_shift) + 1) > 1e9) ++p->unit_shift;
         if (row_tiles > 1e9) return QGEMV_ERR_UNSUPPORTED;
     } else {
@@ -419,8 +428,8 @@ static int attn_plan(int bits, int seqs, int tokens, int heads, int kv_heads, in
     p->scratch = scratch_of(records, dim);
     if (p->tiles && copy) p->copy = (p->scratch + 255) / 256 * 256, p->scratch = p->copy + copy;
     // What every call of these sizes or smaller ones is content with: the choices above do not grow with the sizes, these bounds do.
-    const int grid = bits ? PACKED_BLOCKS * SMS : rows_grid(dim);
-    size_t most = dim <= 128 && forced == 2 ? 0 : static_cast<size_t>(grid) * 2 * 16;
+    // (a packed cache's kernels have 2 blocks an SM with records of 64 rows, 3 with 64, or 3 with 32 for heads beyond 128)
+    size_t most = dim <= 128 && forced == 2 ? 0 : static_cast<size_t>(bits ? PACKED_BLOCKS * SMS * (dim > 128 ? 32 : 64) : rows_grid(dim) * 16) * 2;
     if (dim <= 128 && (forced ? forced == 2 : rows > 32) && blocks >= 16) {
         const long long n = blocks / 8 < 32 ? blocks / 8 : 32, limit = parts_max(blocks);
         const long long parts = tiles < limit && tiles * n < limit ? tiles * n : limit;
@@ -453,7 +462,7 @@ static int allow_smem(const void* fn, unsigned smem) {
 }
 
 // Tensor map of 16-bit elements with 64 of them to a row of a box, in the 128-byte swizzle, strides in elements; or of a packed cache's
-// rows as 32-bit words, strides in bytes, as they lie.  False where the
+// rows as 32-bit words, as they lie, strides in bytes.  False where the
 // tensor cannot be described by one (then the kernel copies row by row).  Host arithmetic of the driver, about a microsecond.
 static bool tensor_map(unsigned long long (&map)[16], const void* base, int kind, const long long (&size)[4], const long long (&stride)[3],
                        const int (&box)[4]) {
@@ -478,7 +487,7 @@ static bool tensor_map(unsigned long long (&map)[16], const void* base, int kind
     for (int i = 0; i < 4; ++i) dims[i] = static_cast<cuuint64_t>(size[i]), boxes[i] = static_cast<cuuint32_t>(box[i]);
     for (int i = 0; i < 3; ++i) {
         // (a dimension of one element is never stepped over: any valid stride will do)
-        const long long s = (size[i + 1] > 1 ? stride[i] : packed ? size[0] * 4 : size[0]) * (packed ? 1 : 2);
+        const long long s = size[i + 1] > 1 ? stride[i] * (packed ? 1 : 2) : size[0] * (packed ? 4 : 2);
         if (s <= 0 || s >= 1ll << 39 || s % 16) return false;
         strides[i] = static_cast<cuuint64_t>(s);
     }
@@ -505,7 +514,7 @@ static int run_attn(const qgemv_attn_args* a, unsigned flags, void* stream) {
     if ((!bits && c.kind != a->kind) || a->tokens < 0 || a->seqs < 0 || a->pages_stride < 0 || a->window < 0) return QGEMV_ERR_INVALID_ARG;
     if (!(a->scale > 0.f && a->scale <= 1e30f)) return QGEMV_ERR_INVALID_ARG;  // NaN too
     AttnPlan p;
-    if ((st = attn_plan(bits, a->seqs, a->tokens, a->heads, c.heads, c.dim, a->max_q, a->max_kv, a->window, &p))) return st;
+    if ((st = attn_plan(bits, a->kind == QGEMV_ACT_F16, a->seqs, a->tokens, a->heads, c.heads, c.dim, a->max_q, a->max_kv, a->window, &p))) return st;
     if (a->pages_stride > (1ll << 40) || static_cast<double>(a->seqs) * static_cast<double>(a->pages_stride) > SPAN_MAX)
         return QGEMV_ERR_UNSUPPORTED;
     // The keys that a row of the page table reaches, and the entries of a row that may be read.
@@ -626,11 +635,11 @@ static int run_attn(const qgemv_attn_args* a, unsigned flags, void* stream) {
         AttnPackedArgs pk = {};
         pk.a = k, pk.k = static_cast<const uint8_t*>(c.k), pk.v = static_cast<const uint8_t*>(c.v);
         pk.pitch = static_cast<int>(row_bytes(bits, c.dim)), pk.bf16 = a->kind == QGEMV_ACT_BF16;
-        const int box = part_of_page(p.packed.keys);  // 8 rows begin at multiples of 128 bytes, as a tensor-map copy has to
-        const long long cache[4] = {pk.pitch / 4, c.page_size, c.num_pages, c.heads};
-        if (box >= 8 && tensor_map(pk.k_map, c.k, c.kind, cache, {c.k_token, c.k_page, c.k_head}, {pk.pitch / 4, box, 1, 1}) &&
-            tensor_map(pk.v_map, c.v, c.kind, cache, {c.v_token, c.v_page, c.v_head}, {pk.pitch / 4, box, 1, 1}))
-            pk.box = box;
+        const int words = pk.pitch / 4, side = 1 << p.hb_shift;
+        const long long cache[4] = {words, c.page_size, c.num_pages, c.heads};
+        pk.line = c.page_size % 16 == 0 && tensor_map(pk.k_map, c.k, c.kind, cache, {c.k_token, c.k_page, c.k_head}, {words, 16, 1, side}) &&
+                  tensor_map(pk.v_map, c.v, c.kind, cache, {c.v_token, c.v_page, c.v_head}, {words, 16, 1, side});
+        pk.hb_shift = p.hb_shift, pk.few = p.hb_shift ? 32 : 128;
         e = launch_step(fn, dim3(static_cast<unsigned>(p.grid)), threads, smem, 1, pdl, static_cast<cudaStream_t>(stream), pk);
     } else {
         e = launch_step(fn, dim3(static_cast<unsigned>(p.grid)), threads, smem, 1, pdl, static_cast<cudaStream_t>(stream), k);
@@ -771,7 +780,7 @@ void qgemv_tune_attn(int kernel) { g_attn_kernel.store(kernel == 1 || kernel == 
 
 size_t qgemv_attn_scratch_bytes(int seqs, int tokens, int heads, int kv_heads, int dim, int max_q, int max_kv) {
     AttnPlan p;
-    return attn_plan(0, seqs, tokens, heads, kv_heads, dim, max_q, max_kv, 0, &p) ? 0 : (p.scratch_most + 255) / 256 * 256;
+    return attn_plan(0, false, seqs, tokens, heads, kv_heads, dim, max_q, max_kv, 0, &p) ? 0 : (p.scratch_most + 255) / 256 * 256;
 }
 
 size_t qgemv_attn_scratch_bytes_ex(int cache_kind, int seqs, int tokens, int heads, int kv_heads, int dim, int max_q, int max_kv) {
@@ -779,7 +788,7 @@ size_t qgemv_attn_scratch_bytes_ex(int cache_kind, int seqs, int tokens, int hea
     const int bits = packed_bits(cache_kind);
     if (!bits && cache_kind != QGEMV_ACT_BF16 && cache_kind != QGEMV_ACT_F16) return 0;
     if (bits && dim % 32) return 0;
-    return attn_plan(bits, seqs, tokens, heads, kv_heads, dim, max_q, max_kv, 0, &p) ? 0 : (p.scratch_most + 255) / 256 * 256;
+    return attn_plan(bits, false, seqs, tokens, heads, kv_heads, dim, max_q, max_kv, 0, &p) ? 0 : (p.scratch_most + 255) / 256 * 256;
 }
 
 int qgemv_attn(const qgemv_attn_args* args, unsigned flags, void* stream) {
