@@ -34,7 +34,7 @@ struct PackedShape {
                                                                    // eight rows' pieces then lie in different banks)
     static constexpr bool HEAVY = NT == 2 || DP == 256;  // sums that leave room for fewer warps
     static constexpr int WARPS = HEAVY ? 4 : 8, BLOCKS = HEAVY ? 3 : 2;
-    static constexpr int SIDE = WARPS * 16 * PITCH;      // 16 keys, or values, of every warp
+    static constexpr int SIDE = WARPS * 16 * PITCH + 256;  // 16 keys, or values, of every warp, and room to keep rows of several heads apart
     static constexpr int ROOM = (HEAVY ? 74 : 111) * 1024;
     static constexpr int KT = 4 * SIDE <= ROOM / 2 ? 2 : 1;  // a round is KT times 16 keys of every warp
     static constexpr int STAGE = KT * 2 * SIDE;
@@ -50,11 +50,11 @@ struct PackedShape {
 __device__ __forceinline__ void mbar_arrive(uint32_t bar, uint32_t one) {
     asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t@q mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(bar), "r"(one) : "memory");
 }
-// Rows of 16 tokens of one page and of some heads, by heads.
-__device__ __forceinline__ void tma_rows(uint32_t dst, const unsigned long long* map, int token, int page, int head, uint32_t bar) {
+// 16 tokens of one page and of some heads.
+__device__ __forceinline__ void tma_box(uint32_t dst, const unsigned long long* map, int x, int y, int page, int head, uint32_t bar) {
     asm volatile(
         "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-        "l"(map), "r"(0), "r"(token), "r"(page), "r"(head), "r"(bar)
+        "l"(map), "r"(x), "r"(y), "r"(page), "r"(head), "r"(bar)
         : "memory");
 }
 __device__ __forceinline__ void copy_row(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
@@ -150,17 +150,20 @@ __device__ __forceinline__ void attend_packed(const AttnPackedArgs& pa, const Ti
         }
         return w;
     };
-    const int box_bytes = heads * 16 * pitch;
+    // rows are `rp` bytes apart in a box and heads `hp`
+    const bool by_rows = pa.copies == COPY_ROWS;
+    const int rp = by_rows ? heads * pitch + 16 : pitch, hp = by_rows ? pitch : 16 * pitch;
+    const int box_bytes = by_rows ? 16 * rp : heads * 16 * pitch;
     auto box_key = [&](int r, int n) { return t.k0 + r * per_round + n * 16; };
     auto box_at = [&](int n) { return n % KT * 2 * S::SIDE + n / KT * box_bytes; };
     auto put_live = [&](int to, int n, int key, unsigned live) {
         ring.lives[to * 16 + n] = live | (live == 0xffffu && key >= low && key + 15 <= high ? PLAIN : 0u);
     };
     Where ahead = {-1, 0};
-    if (pa.line && warp < rounds && lane < warps * KT) ahead = look_up(box_key(warp, lane), 16);
+    if (pa.copies != COPY_EACH && warp < rounds && lane < warps * KT) ahead = look_up(box_key(warp, lane), 16);
     auto issue = [&](int r, int to) {
         const uint32_t bar = smem_addr(&ring.full[to]), dst = store + to * S::STAGE;
-        if (pa.line) {
+        if (pa.copies != COPY_EACH) {
             const int key = box_key(r, lane), left = t.k1 - key, before = t.first - key;
             const bool there = ahead.page >= 0;
             unsigned live = there ? 0xffffu : 0u;
@@ -173,8 +176,12 @@ __device__ __forceinline__ void attend_packed(const AttnPackedArgs& pa, const Ti
             if (lane == 0) mbar_arrive_expect_tx(bar, 2u * boxes * box_bytes);
             __syncwarp();
             if (there) {
-                tma_rows(dst + box_at(lane), pa.k_map, ahead.token, ahead.page, t.kv_head, bar);
-                tma_rows(dst + S::SIDE + box_at(lane), pa.v_map, ahead.token, ahead.page, t.kv_head, bar);
+                // (map coordinates: COPY_BOXES 0, token, page, head; COPY_ROWS the heads' place in a token's rows, token, page; COPY_HEADS the token's place in
+                // a head's rows, head, page)
+                const int x = by_rows ? t.kv_head * pitch / 8 : pa.copies == COPY_HEADS ? ahead.token * (pitch / 8) : 0;
+                const int y = pa.copies == COPY_HEADS ? t.kv_head : ahead.token, z = pa.copies == COPY_BOXES ? t.kv_head : 0;
+                tma_box(dst + box_at(lane), pa.k_map, x, y, ahead.page, z, bar);
+                tma_box(dst + S::SIDE + box_at(lane), pa.v_map, x, y, ahead.page, z, bar);
             }
             ahead.page = -1;
             if (r + S::WARPS < rounds && lane < warps * KT) ahead = look_up(box_key(r + S::WARPS, lane), 16);
@@ -321,15 +328,15 @@ __device__ __forceinline__ void attend_packed(const AttnPackedArgs& pa, const Ti
 
     // This lane's addresses within a slot, for the loads of eight rows' chunks: two chunks of keys (of values, SIDE on) 0 to 7 and 8 to 15 each;
     const int row8 = lane & 7, sel = lane >> 3;
-    const uint32_t mine = store + (nth_warp * heads + hh) * 16 * pitch;
-    const uint32_t row_at = mine + (row8 + (sel & 1) * 8) * pitch + (sel >> 1) * 16;
+    const uint32_t mine = store + nth_warp * box_bytes + hh * hp;
+    const uint32_t row_at = mine + (row8 + (sel & 1) * 8) * rp + (sel >> 1) * 16;
     // steps and bases as an operand, eight keys and eight halves a quarter: for keys, 0 to 7, 8 to 15, then their second eight halves or the first again;
-    const uint32_t ks_at = mine + (lane & 15) * pitch + codes + (G > 4 ? (lane >> 4) * 16 : 0);
+    const uint32_t ks_at = mine + (lane & 15) * rp + codes + (G > 4 ? (lane >> 4) * 16 : 0);
     // for values (turned), keys 8 to 15 are the third quarter, and the second eight halves, or zeros, the second and the fourth;
     const bool zeros = G <= 4 && (sel & 1);
-    const uint32_t vs_at = mine + S::SIDE + (row8 + (sel >> 1) * 8) * pitch + codes + (sel & 1) * 16;
-    // and the steps of key g8.
-    const uint32_t step_at = mine + g8 * pitch + codes;
+    const uint32_t vs_at = mine + S::SIDE + (row8 + (sel >> 1) * 8) * rp + codes + (sel & 1) * 16;
+    // and the steps of keys g8 and g8 + 8.
+    const uint32_t step_at = mine + g8 * rp + codes, step8 = 8 * rp;
     const uint32_t keep_k0 = 2 * t4 < 2 * gd ? 0xffffffffu : 0u;          // halves beyond a row's steps and bases are anything
     const uint32_t keep_k1 = 8 + 2 * t4 < 2 * gd ? 0xffffffffu : 0u;
     const uint32_t steps = g8 < gd ? 0x80008000u : 0u;                     // rows of the turned steps and bases that are steps
@@ -369,7 +376,7 @@ __device__ __forceinline__ void attend_packed(const AttnPackedArgs& pa, const Ti
 #pragma unroll
                 for (int kt = 0; kt < KT; ++kt)
                     if (lane < 16 && !(live[kt] >> lane & 1u)) {
-                        const uint32_t to = mine + at + kt * 2 * S::SIDE + S::SIDE + lane * pitch + codes;
+                        const uint32_t to = mine + at + kt * 2 * S::SIDE + S::SIDE + lane * rp + codes;
                         asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(to), "r"(0) : "memory");
                         if (G > 4 && pitch - codes > 16) asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(to + 16), "r"(0) : "memory");
                     }
@@ -391,7 +398,7 @@ __device__ __forceinline__ void attend_packed(const AttnPackedArgs& pa, const Ti
                 uint32_t w[4];  // steps and bases of key g8, g8 + 8; the second eight halves, or the same again
                 ldsm4(w, ks_at + from);
                 float d[2][G];
-                lds_halves(d[0], step_at + from), lds_halves(d[1], step_at + from + 8 * pitch);
+                lds_halves(d[0], step_at + from), lds_halves(d[1], step_at + step8 + from);
                 if (!WHOLE || G == 2) w[0] &= keep_k0, w[1] &= keep_k0;
                 if ((!WHOLE || G == 2) && G <= 4) w[2] &= keep_k0, w[3] &= keep_k0;
                 if constexpr (G > 4)
@@ -474,7 +481,7 @@ __device__ __forceinline__ void attend_packed(const AttnPackedArgs& pa, const Ti
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         float d[G], most = 2.f;
-                        lds_halves(d, step_at + at + kt * 2 * S::SIDE + S::SIDE + 8 * h * pitch);
+                        lds_halves(d, step_at + at + kt * 2 * S::SIDE + S::SIDE + h * step8);
 #pragma unroll
                         for (int j = 0; j < G; ++j)
                             if (WHOLE || j < gd) most = fmaxf(most, d[j]);

@@ -97,13 +97,17 @@ struct AttnTileArgs {
     AttnArgs a;
 };
 
-// The packed cache's kernel: the cache's two tensor maps, [head, page, token, row] with boxes of 16 rows of a block's heads.
+// How a block of the packed cache's kernel copies 16 keys of its heads: every row by itself; by a tensor map of [token][all heads' rows], where they lie
+// together; of [head][all tokens' rows], where those do; or of [head][token][row].
+enum PackedCopies { COPY_EACH, COPY_ROWS, COPY_HEADS, COPY_BOXES };
+
+// The packed cache's kernel: the cache's two tensor maps, in units of 8 bytes.
 struct AttnPackedArgs {
     alignas(64) unsigned long long k_map[16], v_map[16];
     AttnArgs a;            // k and v are not used; the cache's strides are in bytes
     const uint8_t *k, *v;
     int pitch, bf16;       // bytes of a row; type of q and out
-    int line;              // 16 keys from a multiple of 16 on lie on one page, and the tensor maps serve
+    int copies;            // PackedCopies
     int hb_shift;          // log2 of the key/value heads that a block takes side by side
     unsigned few;          // keys that are not worth a block
 };

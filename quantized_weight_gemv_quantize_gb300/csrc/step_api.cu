@@ -462,7 +462,7 @@ static int allow_smem(const void* fn, unsigned smem) {
 }
 
 // Tensor map of 16-bit elements with 64 of them to a row of a box, in the 128-byte swizzle, strides in elements; or of a packed cache's
-// rows as 32-bit words, as they lie, strides in bytes.  False where the
+// rows in units of 8 bytes, as they lie, strides in bytes.  False where the
 // tensor cannot be described by one (then the kernel copies row by row).  Host arithmetic of the driver, about a microsecond.
 static bool tensor_map(unsigned long long (&map)[16], const void* base, int kind, const long long (&size)[4], const long long (&stride)[3],
                        const int (&box)[4]) {
@@ -487,13 +487,13 @@ static bool tensor_map(unsigned long long (&map)[16], const void* base, int kind
     for (int i = 0; i < 4; ++i) dims[i] = static_cast<cuuint64_t>(size[i]), boxes[i] = static_cast<cuuint32_t>(box[i]);
     for (int i = 0; i < 3; ++i) {
         // (a dimension of one element is never stepped over: any valid stride will do)
-        const long long s = size[i + 1] > 1 ? stride[i] * (packed ? 1 : 2) : size[0] * (packed ? 4 : 2);
+        const long long s = size[i + 1] > 1 ? stride[i] * (packed ? 1 : 2) : size[0] * (packed ? 8 : 2);
         if (s <= 0 || s >= 1ll << 39 || s % 16) return false;
         strides[i] = static_cast<cuuint64_t>(s);
     }
     const cuuint32_t ones[4] = {1, 1, 1, 1};
     return encode(reinterpret_cast<CUtensorMap*>(map),
-                  packed ? CU_TENSOR_MAP_DATA_TYPE_UINT32 : kind == QGEMV_ACT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+                  packed ? CU_TENSOR_MAP_DATA_TYPE_INT64 : kind == QGEMV_ACT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
                   const_cast<void*>(base), dims, strides, boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
                   packed ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -635,10 +635,22 @@ static int run_attn(const qgemv_attn_args* a, unsigned flags, void* stream) {
         AttnPackedArgs pk = {};
         pk.a = k, pk.k = static_cast<const uint8_t*>(c.k), pk.v = static_cast<const uint8_t*>(c.v);
         pk.pitch = static_cast<int>(row_bytes(bits, c.dim)), pk.bf16 = a->kind == QGEMV_ACT_BF16;
-        const int words = pk.pitch / 4, side = 1 << p.hb_shift;
-        const long long cache[4] = {words, c.page_size, c.num_pages, c.heads};
-        pk.line = c.page_size % 16 == 0 && tensor_map(pk.k_map, c.k, c.kind, cache, {c.k_token, c.k_page, c.k_head}, {words, 16, 1, side}) &&
-                  tensor_map(pk.v_map, c.v, c.kind, cache, {c.v_token, c.v_page, c.v_head}, {words, 16, 1, side});
+        // 16 tokens of a page at a time; lines of 656 or 1280 bytes come faster than the 80 of a row
+        const int units = pk.pitch / 8, side = 1 << p.hb_shift;
+        auto maps = [&](const long long (&size)[4], const long long (&ks)[3], const long long (&vs)[3], const int (&box)[4]) {
+            return tensor_map(pk.k_map, c.k, c.kind, size, ks, box) && tensor_map(pk.v_map, c.v, c.kind, size, vs, box);
+        };
+        const int want = getenv("CP") ? atoi(getenv("CP")) : 0;
+        if (c.page_size % 16 == 0) {
+            if ((!want || want == 2) && c.k_token == pk.pitch && c.v_token == pk.pitch && 16 * units <= 256 &&
+                maps({static_cast<long long>(c.page_size) * units, c.heads, c.num_pages, 1}, {c.k_head, c.k_page, 16}, {c.v_head, c.v_page, 16}, {16 * units, side, 1, 1}))
+                pk.copies = COPY_HEADS;
+            else if ((!want || want == 1) && side == p.packed.warps && c.k_head == pk.pitch && c.v_head == pk.pitch && side * units + 2 <= 256 &&
+                     maps({static_cast<long long>(c.heads) * units, c.page_size, c.num_pages, 1}, {c.k_token, c.k_page, 16}, {c.v_token, c.v_page, 16}, {side * units + 2, 16, 1, 1}))
+                pk.copies = COPY_ROWS;
+            else if (maps({units, c.page_size, c.num_pages, c.heads}, {c.k_token, c.k_page, c.k_head}, {c.v_token, c.v_page, c.v_head}, {units, 16, 1, side}))
+                pk.copies = COPY_BOXES;
+        }
         pk.hb_shift = p.hb_shift, pk.few = p.hb_shift ? 32 : 128;
         e = launch_step(fn, dim3(static_cast<unsigned>(p.grid)), threads, smem, 1, pdl, static_cast<cudaStream_t>(stream), pk);
     } else {
