@@ -32,10 +32,9 @@ struct PackedShape {
     static constexpr int CODES = DP * BITS / 8;                    // bytes of a row's codes
     static constexpr int PITCH = (CODES + DP / 8 + 15) / 16 * 16;  // bytes of a row (16 bytes times an odd number for heads of 64 and 128:
                                                                    // eight rows' pieces then lie in different banks)
-    static constexpr bool HEAVY = NT == 2 || DP == 256;  // sums that leave room for fewer warps
-    static constexpr int WARPS = HEAVY ? 4 : 8, BLOCKS = HEAVY ? 3 : 2;
+    static constexpr int WARPS = 4, BLOCKS = NT == 2 || DP == 256 ? 2 : 3;  // 255 or 168 registers a thread
     static constexpr int SIDE = WARPS * 16 * PITCH + 256;  // 16 keys, or values, of every warp, and room to keep rows of several heads apart
-    static constexpr int ROOM = (HEAVY ? 74 : 111) * 1024;
+    static constexpr int ROOM = (BLOCKS == 2 ? 111 : 74) * 1024;
     static constexpr int KT = 4 * SIDE <= ROOM / 2 ? 2 : 1;  // a round is KT times 16 keys of every warp
     static constexpr int STAGE = KT * 2 * SIDE;
     static constexpr int FIT = ROOM / STAGE, STAGES = FIT > 6 ? 6 : FIT;
@@ -707,7 +706,7 @@ __global__ void __launch_bounds__(PackedShape<DP, BITS, NT>::WARPS * 32, PackedS
     int slot = 0;
     unsigned parity = 0;
     divide_rows<S::ROWS, 16>(
-        pa.a, pa.a.kv_heads >> pa.hb_shift, 1 << pa.hb_shift, pa.few, &last,
+        pa.a, pa.a.kv_heads >> pa.hb_shift, 1 << pa.hb_shift, pa.few, &last, smem,
         [&](const Tile& t, long long record) { attend_packed<DP, BITS, NT, WHOLE, FINE>(pa, t, record, smem, smem_addr(plain), ring, slot, parity); },
         [&](const Tile& t) { join_packed<DP, BITS, NT>(pa, t); });
 }

@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(RowsShape<DP>::WARPS * 32) attn_rows_kernel(co
     pdl_launch_dependents();
     pdl_wait();
     divide_rows<16, 16>(
-        a, a.kv_heads, 1, 128, &last, [&](const Tile& t, long long record) { attend<DP, BF>(a, t, record * 16, smem); },
+        a, a.kv_heads, 1, 128, &last, smem, [&](const Tile& t, long long record) { attend<DP, BF>(a, t, record * 16, smem); },
         [&](const Tile& t) {
             constexpr int THREADS = RowsShape<DP>::WARPS * 32;
             if (t.rows <= THREADS / (DP / 4)) join_rows<DP, THREADS, BF, 1>(a, t);

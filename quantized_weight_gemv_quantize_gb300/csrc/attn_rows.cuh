@@ -65,9 +65,11 @@ __device__ __forceinline__ void join_rows(const AttnArgs& a, const Tile& t) {
 
 // A block's parts of the batch's row tiles, one after another: attend(t, record) computes one, into the result or into its record, join(t) joins the
 // parts of one; both are called by the whole block.  A row tile is ROWS rows of each of `heads` key/value heads, `groups` times those make all of
-// them.  Ranges of keys begin at multiples of STEP; less than `few` keys are not worth a block.  `last` is in shared memory.
+// them.  Ranges of keys begin at multiples of STEP; less than `few` keys are not worth a block.  `last` and `room`
+// (KEPT pairs of words, free until attend is called) are in shared memory.
+constexpr unsigned KEPT = 1024;
 template <int ROWS, int STEP, class Attend, class Join>
-__device__ __forceinline__ void divide_rows(const AttnArgs& a, int groups, int heads, unsigned few, unsigned* last, Attend&& attend, Join&& join) {
+__device__ __forceinline__ void divide_rows(const AttnArgs& a, int groups, int heads, unsigned few, unsigned* last, void* room, Attend&& attend, Join&& join) {
     const unsigned lane = threadIdx.x % 32, me = blockIdx.x, blocks = gridDim.x, seqs = a.seqs, unit = a.unit_shift;
     // A sequence in the division of the work: its row tiles, each as many units of keys (64, or more where 32 bits would not
     // hold the whole) as any of its rows may see, at least one (a row that sees nothing has its zeros written).
@@ -82,16 +84,28 @@ __device__ __forceinline__ void divide_rows(const AttnArgs& a, int groups, int h
         sq_tiles = (sq.n * a.group + ROWS - 1) / ROWS * groups;
         sq_units = max(1u, (static_cast<unsigned>(hi - lo) + (1u << unit) - 1) >> unit);
     };
+    // The division goes over the sequences some ten times: up to 32 stay in registers, a lane each, up to KEPT in shared memory.
+    uint2* const kept = static_cast<uint2*>(room);
+    const bool keep = seqs > 32 && seqs <= KEPT;
+    if (seqs <= 32) read_seq(lane);
+    if (keep) {
+        for (unsigned b = threadIdx.x; b < seqs; b += blockDim.x) read_seq(b), kept[b] = make_uint2(sq_units, sq_tiles);
+        __syncthreads();
+    }
+    auto count_seq = [&](unsigned b) {
+        if (!keep) return read_seq(b);
+        const uint2 u = b < seqs ? kept[b] : make_uint2(1u, 0u);
+        sq_units = u.x, sq_tiles = u.y;
+    };
     // Sum over all sequences, 32 at a time (a lane each), every warp for itself.
     auto sum_of = [&](auto&& f) {
         unsigned v = 0;
         for (unsigned b0 = 0; b0 < seqs; b0 += 32) {
-            if (seqs > 32) read_seq(b0 + lane);
+            if (seqs > 32) count_seq(b0 + lane);
             v += f();
         }
         return __reduce_add_sync(0xffffffffu, v);
     };
-    if (seqs <= 32) read_seq(lane);
     const unsigned least = max(1u, few >> unit);
     const unsigned units = sum_of([&] { return sq_tiles * sq_units; }), row_tiles = sum_of([&] { return sq_tiles; });
     // A block's share.  Where there are no more row tiles than blocks, it is made as long as it takes for every block to have a part
@@ -111,7 +125,7 @@ __device__ __forceinline__ void divide_rows(const AttnArgs& a, int groups, int h
     const unsigned start = me * share;
     unsigned at = 0, b = seqs, per = 1;
     for (unsigned b0 = 0; b0 < seqs; b0 += 32) {
-        if (seqs > 32) read_seq(b0 + lane);
+        if (seqs > 32) count_seq(b0 + lane);
         per = counted();
         const unsigned own = sq_tiles * per;
         unsigned sum = own;
@@ -125,12 +139,21 @@ __device__ __forceinline__ void divide_rows(const AttnArgs& a, int groups, int h
             const int l = __ffs(holds) - 1;
             b = b0 + l;
             at += __shfl_sync(0xffffffffu, sum - own, l);
+            per = __shfl_sync(0xffffffffu, per, l);
+            if (keep) {
+                read_seq(b);
+                break;
+            }
             sq.q0 = __shfl_sync(0xffffffffu, sq.q0, l), sq.n = __shfl_sync(0xffffffffu, sq.n, l);
             sq.first_pos = __shfl_sync(0xffffffffu, sq.first_pos, l), sq.usable = __shfl_sync(0xffffffffu, sq.usable, l);
-            per = __shfl_sync(0xffffffffu, per, l), sq_tiles = __shfl_sync(0xffffffffu, sq_tiles, l);
+            sq_tiles = __shfl_sync(0xffffffffu, sq_tiles, l);
             break;
         }
         at += __shfl_sync(0xffffffffu, sum, 31);
+    }
+    if (keep) {
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // (copies may write there next)
+        __syncthreads();
     }
     if (b == seqs) return;  // past the end of the work
     unsigned nth = (start - at) / per;

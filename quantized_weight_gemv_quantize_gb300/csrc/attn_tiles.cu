@@ -208,7 +208,8 @@ __device__ __forceinline__ long long part_at(const AttnArgs& a, const Tile& t, i
 // A block takes parts of row tiles one after the other, the next one's number from a counter (the first from its own), until there
 // are no more; each role goes on to the next as soon as its own work on this one is done, so that the next one's keys and queries are on
 // their way while the last rows are written.  What a part computes does not depend on who takes it.
-template <int DP, bool BF>
+// UNITS: f16 queries that stand for others times a power of two a row, with the scale of each row's scores (base 2) in a.units; results in bf16.
+template <int DP, bool BF, bool UNITS>
 __global__ void __launch_bounds__(TILE_THREADS, 1) attn_tiles_kernel(const __grid_constant__ AttnTileArgs ta) {
     using S = TilesShape<DP>;
     const AttnArgs& a = ta.a;
@@ -523,6 +524,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) attn_tiles_kernel(const __gri
                 g += blocks;
                 continue;
             }
+            const float scale = !UNITS ? a.scale_log2 : r < t.rows ? a.units[out_at(a, t, r, a.heads, 1)] : 1.f;
             const int pos = row_pos(a, t, r);
             const int hi = a.causal ? min(t.k1 - 1, pos) : t.k1 - 1, lo = first_key(a, pos);
             float m = NEG_INF, l = 0.f;  // m: the maximum in use (less the lift), in units of the scaled scores (base 2)
@@ -553,7 +555,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) attn_tiles_kernel(const __gri
                         for (int e = 0; e < 32; e += 2) {
                             tops[e / 2 & 1] = max3(tops[e / 2 & 1], c[e], c[e + 1]);
                             float x, y;
-                            fma2(x, y, c[e], c[e + 1], a.scale_log2, -base);
+                            fma2(x, y, c[e], c[e + 1], scale, -base);
                             x = exp2_approx(x), y = exp2_approx(y);
                             add2(sums[e & 2], sums[(e & 2) + 1], x, y);
                             p[q * 16 + e / 2] = pack16<BF>(x, y);
@@ -567,7 +569,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) attn_tiles_kernel(const __gri
                 weigh(m == NEG_INF ? 0.f : m);
                 sh.top[i][half][tr] = top;
                 pair_sync();
-                top = fmaxf(top, sh.top[i][half ^ 1][tr]) * a.scale_log2;
+                top = fmaxf(top, sh.top[i][half ^ 1][tr]) * scale;
                 const bool move = top > m + (Lift<BF>::TILES + Lift<BF>::LAG);
                 if (__any_sync(0xffffffffu, move)) {
                     const float to = top - Lift<BF>::TILES, f = move ? exp2_approx(m - to) : 1.f;  // 0 for the first keys that the row sees
@@ -626,7 +628,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) attn_tiles_kernel(const __gri
                 if (row && whole) {
                     uint32_t w[16];
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) w[e] = pack16<BF>(o[2 * e] * inv, o[2 * e + 1] * inv);
+                    for (int e = 0; e < 16; ++e) w[e] = pack16<BF || UNITS>(o[2 * e] * inv, o[2 * e + 1] * inv);
                     uint16_t* out = static_cast<uint16_t*>(a.out) + to + d;
                     if (a.wide) {
 #pragma unroll
@@ -680,18 +682,19 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) attn_join_kernel(const AttnAr
 }
 
 template <int DP>
-static const void* pick(bool bf16, unsigned* smem, unsigned* threads) {
+static const void* pick(bool bf16, bool units, unsigned* smem, unsigned* threads) {
     *smem = TilesShape<DP>::SMEM;
     *threads = TILE_THREADS;
-    return bf16 ? (const void*)attn_tiles_kernel<DP, true> : (const void*)attn_tiles_kernel<DP, false>;
+    if (units) return (const void*)attn_tiles_kernel<DP, false, true>;
+    return bf16 ? (const void*)attn_tiles_kernel<DP, true, false> : (const void*)attn_tiles_kernel<DP, false, false>;
 }
 
 const void* attn_join_kernel_ptr(bool bf16) {
     return bf16 ? (const void*)attn_join_kernel<true> : (const void*)attn_join_kernel<false>;
 }
 
-const void* attn_tiles_kernel_ptr(bool bf16, int dim, unsigned* smem, unsigned* threads) {
-    return dim <= 64 ? pick<64>(bf16, smem, threads) : pick<128>(bf16, smem, threads);
+const void* attn_tiles_kernel_ptr(bool bf16, bool units, int dim, unsigned* smem, unsigned* threads) {
+    return dim <= 64 ? pick<64>(bf16, units, smem, threads) : pick<128>(bf16, units, smem, threads);
 }
 
 }  // namespace qg

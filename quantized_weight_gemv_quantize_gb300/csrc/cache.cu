@@ -126,9 +126,13 @@ __global__ void __launch_bounds__(CACHE_THREADS) cache_read_kernel(const CacheRe
     }
 }
 
-// The keys and values that a batch's new tokens may see, in 16 bits and the order [page, head, token, dim] with pages of `page_size` tokens (a
+// The keys and values that a batch's new tokens may see, in f16 and the order [page, head, token, dim] with pages of `page_size` tokens (a
 // divisor of the cache's), page n of sequence b at b * per_seq + n, and their page table (-1: a page outside the cache).  A block takes
 // CACHE_TOKENS tokens (blockIdx.x) of a sequence (blockIdx.y).  For attention by the 128-row kernel: every row tile of a sequence reads the copy.
+//
+// The copy is f16 whatever the queries' type: 11 bits of a value, where bf16's 8 would cost a context of 24000 keys as much again as the rounding of
+// the result (0.0076 of it against 0.0017).  bf16 queries are taken along: in f16, times the power of two that brings the row's largest element to
+// [2^9, 2^10), so that elements down to 2^-23 of it keep their 8 bits.
 template <int BITS>
 __global__ void __launch_bounds__(CACHE_THREADS) cache_unpack_kernel(const CacheUnpackArgs u) {
     __shared__ long long ks[CACHE_TOKENS], vs[CACHE_TOKENS];
@@ -137,6 +141,27 @@ __global__ void __launch_bounds__(CACHE_THREADS) cache_unpack_kernel(const Cache
     pdl_wait();
     const int b = blockIdx.y;
     const Seq s = find_seq(a, b);
+    if (static_cast<int>(blockIdx.x) >= u.key_blocks) {  // a warp a row of dim elements, up to 128
+        const int j0 = (static_cast<int>(blockIdx.x) - u.key_blocks) * UNPACK_QUERIES, rows = min(UNPACK_QUERIES, s.n - j0) * a.heads;
+        const int lane = threadIdx.x % 32, e = 4 * lane;
+        for (int i = threadIdx.x / 32; i < rows; i += CACHE_THREADS / 32) {
+            const long long tok = s.q0 + j0 + i / a.heads;
+            const int h = i % a.heads;
+            uint2 w = make_uint2(0u, 0u);
+            if (e < a.dim) w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.q) + tok * a.q_token + h * a.q_head + e);
+            float x[4] = {__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xFFFF0000u)};
+            float top = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
+#pragma unroll
+            for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const int up = top > 0.f ? min(126, 136 - static_cast<int>(__float_as_uint(top) >> 23)) : 0;
+            const float by = __uint_as_float(static_cast<uint32_t>(127 + up) << 23), back = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+            if (e < a.dim)
+                *reinterpret_cast<uint2*>(u.q_copy + (tok * a.heads + h) * a.dim + e) =
+                    make_uint2(pack16<false>(x[0] * by, x[1] * by), pack16<false>(x[2] * by, x[3] * by));
+            if (lane == 0) u.units[tok * a.heads + h] = fminf(fmaxf(back * a.scale_log2, 1e-37f), 3e38f);
+        }
+        return;
+    }
     const int t0 = static_cast<int>(blockIdx.x) * CACHE_TOKENS;
     const int from = max(t0, first_key(a, s.first_pos)), to = min(t0 + CACHE_TOKENS, s.usable);
     if (s.n <= 0 || from >= to) return;
@@ -177,7 +202,9 @@ __global__ void __launch_bounds__(CACHE_THREADS) cache_unpack_kernel(const Cache
                 if (i >= to - t0 || place[i] < 0) continue;
                 const int n = (t0 + i) / u.page_size;
                 const long long row = ((b * u.per_seq + n) * a.kv_heads + h) * u.page_size + (t0 + i - n * u.page_size);
-                store8(u.kind, y, row * a.dim + e, x[j]);
+#pragma unroll
+                for (float& v : x[j]) v = fminf(fmaxf(v, -65504.f), 65504.f);  // (d c + m may end a step's rounding beyond the largest f16)
+                store8(ACT_F16, y, row * a.dim + e, x[j]);
             }
         }
     }

@@ -31,6 +31,8 @@ constexpr int ROPE_THREADS = 64;
 // in bytes and its rows packed.
 const void* rope_kernel_ptr(int x_kind, bool half, bool vec, bool packed);
 
+constexpr int UNPACK_QUERIES = 4;  // tokens of a block that takes queries
+
 struct CacheWriteArgs {
     const void *k, *v;
     long long k_token, k_head, v_token, v_head;
@@ -79,6 +81,7 @@ struct AttnArgs {
     int max_kv;  // bound of the keys that may be read: the caller's, or what a row of the page table reaches
     int group_shift, page_shift;  // log2 of group and page_size, -1 where they are no powers of two
     float scale_log2;   // scale * log2(e): the softmax runs in base 2
+    const float* units; // or that of each row (token-major), for queries that are scaled row by row
     int causal, window;
     int unit_shift;  // 16-row kernel: the work is divided in units of 2^unit_shift keys
     // 128-row kernel: keys of a part, parts of a row tile and row tiles of a sequence and key/value head in the grid, rows of a
@@ -119,7 +122,10 @@ struct CacheUnpackArgs {
     void *k_copy, *v_copy;
     int* table;
     long long per_seq;       // pages of a sequence in the copy
-    int page_size, kind;     // of the copy
+    int page_size;           // of the copy
+    int key_blocks;          // blocks of a sequence that copy keys; those beyond them take its queries
+    uint16_t* q_copy;        // bf16 queries in f16, times a power of two a row, and what the rows' scores are scaled by; null: they stay
+    float* units;
 };
 const void* cache_unpack_kernel_ptr(int bits);
 
@@ -146,7 +152,7 @@ struct AttnPlan {
 };
 
 const void* attn_rows_kernel_ptr(bool bf16, int dim, unsigned* smem, unsigned* threads);
-const void* attn_tiles_kernel_ptr(bool bf16, int dim, unsigned* smem, unsigned* threads);
+const void* attn_tiles_kernel_ptr(bool bf16, bool units, int dim, unsigned* smem, unsigned* threads);
 const void* attn_join_kernel_ptr(bool bf16);
 constexpr int JOIN_WARPS = 8;  // rows of a block of the joining kernel
 

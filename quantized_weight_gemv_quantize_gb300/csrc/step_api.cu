@@ -6,7 +6,6 @@
 #include <math.h>
 #include <mutex>
 #include <stddef.h>
-#include <stdlib.h>
 
 #include "../../include/qgemv.h"
 #include "internal.h"
@@ -309,7 +308,6 @@ static std::atomic<int> g_attn_kernel{0};
 static size_t round32(size_t n) { return (n + 31) / 32 * 32; }
 
 constexpr int SMS = 152;
-constexpr int PACKED_BLOCKS = 3;  // blocks an SM of the packed cache's kernel, at most
 constexpr int PACKED_ROWS = 32;   // up to so many rows it is always taken
 
 // Parts that row tiles may be cut into, all together: as many waves of blocks as half the square root of the context's key tiles, at most
@@ -326,11 +324,12 @@ static size_t scratch_of(size_t records, int dim) {
     return QGEMV_ATTN_SCRATCH_HEAD + round32(records * sizeof(float2)) + records * dim * sizeof(float);
 }
 // The copy in 16 bits of a packed cache's part that a batch sees, and its page table, for any page size (pages of the copy hold up to 128
-// tokens).  0: out of range.
-static size_t copy_bytes(int seqs, int kv_heads, int dim, int max_kv) {
-    const double tokens = static_cast<double>(seqs) * (static_cast<double>(max_kv) + 128);
-    if (seqs > 65535 || tokens > INT_MAX || tokens * kv_heads * dim * 4 > SPAN_MAX) return 0;
-    return (static_cast<size_t>(tokens) * (static_cast<size_t>(kv_heads) * dim * 4 + 4) + 511) / 256 * 256;
+// tokens), and of its queries.  0: out of range.
+static size_t copy_bytes(int seqs, int tokens, int heads, int kv_heads, int dim, int max_kv) {
+    const double keys = static_cast<double>(seqs) * (static_cast<double>(max_kv) + 128), rows = static_cast<double>(tokens) * heads;
+    if (seqs > 65535 || keys > INT_MAX || keys * kv_heads * dim * 4 > SPAN_MAX || rows * dim * 2 > SPAN_MAX) return 0;
+    const size_t cache = static_cast<size_t>(keys) * (static_cast<size_t>(kv_heads) * dim * 4 + 4);
+    return (cache + static_cast<size_t>(rows) * (dim * 2 + 4) + 1023) / 256 * 256;
 }
 
 static int attn_plan(int bits, bool f16, int seqs, int tokens, int heads, int kv_heads, int dim, int max_q, int max_kv, int window,
@@ -393,14 +392,17 @@ static int attn_plan(int bits, bool f16, int seqs, int tokens, int heads, int kv
         p->packed_fn = (bits == 4 ? f16 ? attn_packed4f_kernel_ptr : attn_packed4_kernel_ptr : f16 ? attn_packed8f_kernel_ptr : attn_packed8_kernel_ptr)(
             dim, static_cast<int>(rows), &p->packed);
         tile_rows = p->packed.rows;
-        // heads side by side
+        // Heads side by side: as many as leave 64 row tiles (fewer have to be cut into more parts, whose joining one block does), where the blocks have
+        // 18 pieces of 32 keys of a head each to do (40 for four heads).  1, 2 and 4 heads, 32 and 8 heads of 128, us: 4 bits, 48 sequences of up to
+        // 16384 190 / 119 / 106 (one head's rows alone are fetched with their neighbours'), 16 such 45.9 / 41.9 / 49.7, 8 such 32.6 / 31.5 / 43.3,
+        // 16 of up to 2000 16.4 / 19.2 / 25.6, one of 100003 42 / 51 / 94; 8 bits, 33 of up to 16384 121 / 105 / 104, with a window of 1024
+        // 29.4 / 25.1 / 31.9.
         const long long one = (rows + tile_rows - 1) / tile_rows * kv_heads * seqs;
-        const char* env = getenv("HB");
-        int most_hb = env ? atoi(env) : 3;
-        while (p->hb_shift < most_hb && (2 << p->hb_shift) <= p->packed.warps && kv_heads % (2 << p->hb_shift) == 0 &&
-               (env || (one >> (p->hb_shift + 1)) * 8 >= static_cast<long long>(p->packed.blocks) * SMS))
+        const double pieces = static_cast<double>(one) * keys_of(tile_rows, 16) / 32 / (p->packed.blocks * SMS);
+        while ((2 << p->hb_shift) <= p->packed.warps && kv_heads % (2 << p->hb_shift) == 0 && one >> (p->hb_shift + 1) >= 64 &&
+               pieces >= (p->hb_shift ? 40 : 18))
             ++p->hb_shift;
-        copy = dim <= 128 && (forced ? forced == 2 : rows > PACKED_ROWS) ? copy_bytes(seqs, kv_heads, dim, max_kv) : 0;
+        copy = dim <= 128 && (forced ? forced == 2 : rows > PACKED_ROWS) ? copy_bytes(seqs, tokens, heads, kv_heads, dim, max_kv) : 0;
         p->tiles = copy > 0 && (forced == 2 || tiles_us + 10 < rows_us);
     }
     size_t records = 0;
@@ -428,8 +430,9 @@ static int attn_plan(int bits, bool f16, int seqs, int tokens, int heads, int kv
     p->scratch = scratch_of(records, dim);
     if (p->tiles && copy) p->copy = (p->scratch + 255) / 256 * 256, p->scratch = p->copy + copy;
     // What every call of these sizes or smaller ones is content with: the choices above do not grow with the sizes, these bounds do.
-    // (a packed cache's kernels have 2 blocks an SM with records of 64 rows, 3 with 64, or 3 with 32 for heads beyond 128)
-    size_t most = dim <= 128 && forced == 2 ? 0 : static_cast<size_t>(bits ? PACKED_BLOCKS * SMS * (dim > 128 ? 32 : 64) : rows_grid(dim) * 16) * 2;
+    // (a packed cache's kernels have 3 blocks an SM with records of 32 rows, 2 with 64 for more than 8 rows, or 2 with 32 for heads beyond 128)
+    const int packed_most = dim > 128 ? 2 * 32 : rows > 8 ? 2 * 64 : 3 * 32;
+    size_t most = dim <= 128 && forced == 2 ? 0 : static_cast<size_t>(bits ? SMS * packed_most : rows_grid(dim) * 16) * 2;
     if (dim <= 128 && (forced ? forced == 2 : rows > 32) && blocks >= 16) {
         const long long n = blocks / 8 < 32 ? blocks / 8 : 32, limit = parts_max(blocks);
         const long long parts = tiles < limit && tiles * n < limit ? tiles * n : limit;
@@ -575,7 +578,8 @@ static int run_attn(const qgemv_attn_args* a, unsigned flags, void* stream) {
     unsigned smem, threads;
     const void* fn;
     if (bits && !p.tiles) fn = p.packed_fn, smem = p.packed.smem, threads = p.packed.threads;
-    else fn = (p.tiles ? attn_tiles_kernel_ptr : attn_rows_kernel_ptr)(a->kind == QGEMV_ACT_BF16, c.dim, &smem, &threads);
+    else if (!p.tiles) fn = attn_rows_kernel_ptr(a->kind == QGEMV_ACT_BF16, c.dim, &smem, &threads);
+    else fn = attn_tiles_kernel_ptr(a->kind == QGEMV_ACT_BF16, bits && a->kind == QGEMV_ACT_BF16, c.dim, &smem, &threads);
     if ((st = allow_smem(fn, smem))) return st;
     // The largest power of two, up to `most`, that divides the page.
     auto part_of_page = [&](int most) {
@@ -587,20 +591,30 @@ static int run_attn(const qgemv_attn_args* a, unsigned flags, void* stream) {
     if (bits && p.tiles) {
         CacheUnpackArgs u = {};
         u.a = k, u.k = static_cast<const uint8_t*>(c.k), u.v = static_cast<const uint8_t*>(c.v);
-        u.page_size = part_of_page(128), u.kind = a->kind;
+        u.page_size = part_of_page(128);
         u.per_seq = (static_cast<long long>(reach) + u.page_size - 1) / u.page_size;
         const size_t rows = static_cast<size_t>(u.per_seq) * a->seqs * u.page_size, bytes = rows * c.heads * c.dim * 2;
+        auto after = [](void* p, size_t n) { return static_cast<void*>(static_cast<uint8_t*>(p) + (n + 255) / 256 * 256); };
         u.k_copy = static_cast<uint8_t*>(a->scratch) + p.copy;
-        u.v_copy = static_cast<uint8_t*>(u.k_copy) + bytes;
-        u.table = reinterpret_cast<int*>(static_cast<uint8_t*>(u.v_copy) + bytes);
-        if (reach > 0) {
-            e = launch_step(cache_unpack_kernel_ptr(bits), dim3(static_cast<unsigned>((reach + CACHE_TOKENS - 1) / CACHE_TOKENS), static_cast<unsigned>(a->seqs)),
-                            CACHE_THREADS, 0, 1, pdl, static_cast<cudaStream_t>(stream), u);
+        u.v_copy = after(u.k_copy, bytes);
+        u.table = static_cast<int*>(after(u.v_copy, bytes));
+        u.key_blocks = static_cast<int>((reach + CACHE_TOKENS - 1ll) / CACHE_TOKENS);
+        int blocks = u.key_blocks;
+        if (a->kind == QGEMV_ACT_BF16) {
+            const int max_q = a->max_q < a->tokens ? a->max_q : a->tokens;
+            u.q_copy = static_cast<uint16_t*>(after(u.table, static_cast<size_t>(u.per_seq) * a->seqs * 4));
+            u.units = static_cast<float*>(after(u.q_copy, static_cast<size_t>(a->tokens) * a->heads * c.dim * 2));
+            blocks += (max_q + UNPACK_QUERIES - 1) / UNPACK_QUERIES;
+            k.q = u.q_copy, k.q_token = static_cast<long long>(a->heads) * c.dim, k.q_head = c.dim, k.units = u.units;
+        }
+        if (blocks > 0) {
+            e = launch_step(cache_unpack_kernel_ptr(bits), dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(a->seqs)), CACHE_THREADS, 0, 1, pdl,
+                            static_cast<cudaStream_t>(stream), u);
             if (e != cudaSuccess) return api_cuda_fail(e);
             chained = true;
         }
         // from here on the copy is the cache
-        copy.kind = a->kind, copy.k = u.k_copy, copy.v = u.v_copy, copy.num_pages = static_cast<int>(u.per_seq * a->seqs), copy.page_size = u.page_size;
+        copy.kind = QGEMV_ACT_F16, copy.k = u.k_copy, copy.v = u.v_copy, copy.num_pages = static_cast<int>(u.per_seq * a->seqs), copy.page_size = u.page_size;
         if (copy.num_pages < 1) copy.num_pages = 1;
         copy.k_token = copy.v_token = c.dim, copy.k_head = copy.v_head = static_cast<long long>(u.page_size) * c.dim;
         copy.k_page = copy.v_page = copy.k_head * c.heads;
@@ -619,8 +633,8 @@ static int run_attn(const qgemv_attn_args* a, unsigned flags, void* stream) {
         if (box >= 8 && tensor_map(ta.k_map, c.k, c.kind, cache, {c.k_token, c.k_page, c.k_head}, {64, box, 1, 1}) &&
             tensor_map(ta.v_map, c.v, c.kind, cache, {c.v_token, c.v_page, c.v_head}, {64, box, 1, 1}))
             k.box = box;
-        k.q_map = 128 % k.group == 0 && tensor_map(ta.q_map, a->q, c.kind, {c.dim, a->heads, a->tokens, 1},
-                                                   {a->q_head, a->q_token, c.dim}, {64, k.group, 128 / k.group, 1});
+        k.q_map = 128 % k.group == 0 && tensor_map(ta.q_map, k.q, c.kind, {c.dim, a->heads, a->tokens, 1},
+                                                   {k.q_head, k.q_token, c.dim}, {64, k.group, 128 / k.group, 1});
         k.wide = api_aligned(a->out, 32) && api_aligned(k.part_sum, 32) && a->out_token % 16 == 0 && a->out_head % 16 == 0 && c.dim % 16 == 0;
         ta.a = k;
         e = launch_step(fn, dim3(static_cast<unsigned>(p.grid < sms ? p.grid : sms)), threads, smem, 1, chained, static_cast<cudaStream_t>(stream), ta);
@@ -640,12 +654,11 @@ static int run_attn(const qgemv_attn_args* a, unsigned flags, void* stream) {
         auto maps = [&](const long long (&size)[4], const long long (&ks)[3], const long long (&vs)[3], const int (&box)[4]) {
             return tensor_map(pk.k_map, c.k, c.kind, size, ks, box) && tensor_map(pk.v_map, c.v, c.kind, size, vs, box);
         };
-        const int want = getenv("CP") ? atoi(getenv("CP")) : 0;
         if (c.page_size % 16 == 0) {
-            if ((!want || want == 2) && c.k_token == pk.pitch && c.v_token == pk.pitch && 16 * units <= 256 &&
+            if (c.k_token == pk.pitch && c.v_token == pk.pitch && 16 * units <= 256 &&
                 maps({static_cast<long long>(c.page_size) * units, c.heads, c.num_pages, 1}, {c.k_head, c.k_page, 16}, {c.v_head, c.v_page, 16}, {16 * units, side, 1, 1}))
                 pk.copies = COPY_HEADS;
-            else if ((!want || want == 1) && side == p.packed.warps && c.k_head == pk.pitch && c.v_head == pk.pitch && side * units + 2 <= 256 &&
+            else if (side == p.packed.warps && c.k_head == pk.pitch && c.v_head == pk.pitch && side * units + 2 <= 256 &&
                      maps({static_cast<long long>(c.heads) * units, c.page_size, c.num_pages, 1}, {c.k_token, c.k_page, 16}, {c.v_token, c.v_page, 16}, {side * units + 2, 16, 1, 1}))
                 pk.copies = COPY_ROWS;
             else if (maps({units, c.page_size, c.num_pages, c.heads}, {c.k_token, c.k_page, c.k_head}, {c.v_token, c.v_page, c.v_head}, {units, 16, 1, side}))

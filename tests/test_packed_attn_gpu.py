@@ -8,7 +8,9 @@ Tolerances, from the arithmetic (p the probabilities, k = d c + m in blocks of 3
    of the largest p, times the largest code or |m|, a key, and more where a step is above 2, by that half step;
  - so with A = sum p (d c + |m|): out is off by u |ref| + (2^-10 + 4 off + 2^-18) A + 2^-34 sum_t (L + |m|) max(1, d/2), lse by
    off + 2^-20 max(1, |lse|).
-The 128-row kernel reads a 16-bit copy: its results are those of the same call on such a copy made by qgemv_cache_read, bit for bit.
+The 128-row kernel reads an f16 copy: with f16 queries its results are those of the same call on such a copy made by qgemv_cache_read, bit for bit.
+With bf16 ones the formula holds with keys and values rounded to f16 (2^-11 of each: off grows by 2^-11 scale sum |q||k|, the output by 2^-11 of sum
+p |v|), p to f16 once (those below 2^-21 of the largest lose bits: 2^-32 |v| a key).
 """
 import math
 
@@ -100,7 +102,7 @@ class Packed:
         return qg.attn_args(q, cache, self.table, self.starts, self.lens, self.out, self.scratch, max_q, max_kv, self.scale, causal, window,
                             self.lse)
 
-    def check(self, causal=True, window=0):
+    def check(self, causal=True, window=0, copy=False):
         out, lse, first, u = f64(self.out), None if self.lse is None else f64(self.lse), 0, U[self.dtype]
         top_code = (1 << self.bits) - 1
         for b, (n, c) in enumerate(zip(self.new, self.ctx)):
@@ -131,6 +133,9 @@ class Packed:
                 want, A = p @ v[:, kv], p @ vmag[:, kv]
                 off = 2.0 ** -19 * self.scale * (np.abs(qh) @ kmag[:, kv].T).max(1, initial=0.0)[:, None]
                 floor = 2.0 ** -34 * ((top_code + vm[:, kv].max(-1)) * np.maximum(1, vd[:, kv].max(-1) / 2)).sum() if c else 0.0
+                if copy:
+                    off = off + 2.0 ** -11 * self.scale * (np.abs(qh) @ np.abs(k[:, kv]).T).max(1, initial=0.0)[:, None]
+                    A, floor = p @ np.abs(v[:, kv]), 2.0 ** -32 * np.abs(v[:, kv]).max(-1).sum()
                 tol = u * np.abs(want) + (2.0 ** -10 + 4 * off + 2.0 ** -18) * A + floor + TINY[self.dtype]
                 err = np.abs(out[first:first + n, h] - want)
                 assert np.all(err <= tol), (b, h, float((err - tol).max()), np.unravel_index((err - tol).argmax(), err.shape))
@@ -206,35 +211,56 @@ def test_attention_many_sequences(case, kind, rows_kernel):
         assert int(s.scratch[:qg.QGEMV_ATTN_SCRATCH_HEAD].sum()) == 0
 
 
-@pytest.mark.parametrize("kind", ["Q4", "Q8"])
-@pytest.mark.parametrize("new,page,dtype,mask", [([300], 64, B16, {}), ([150, 20], 16, H16, dict(window=70)), ([129, 0, 64], 5, B16, {}),
-                                                 ([40], 48, H16, dict(causal=False)), ([260], 128, B16, {})])
-def test_many_rows_equal_the_same_call_on_a_copy(new, page, dtype, mask, kind):
-    ctx = [900, 260, 333][:len(new)]
-    s = Packed(5, kind, new, ctx, 8, 2, 128, page, dtype)
+MANY = [([300], 64, {}), ([150, 20], 16, dict(window=70)), ([129, 0, 64], 5, {}), ([40], 48, dict(causal=False)), ([260], 128, {}), ([7, 3], 16, {})]
+
+
+@pytest.fixture
+def copying():
     qg.qgemv_tune_attn(2)
-    try:
+    yield
+    qg.qgemv_tune_attn(0)
+
+
+@pytest.mark.parametrize("kind", ["Q4", "Q8"])
+@pytest.mark.parametrize("new,page,mask", MANY)
+def test_many_rows_equal_the_same_call_on_a_copy(new, page, mask, kind, copying):
+    ctx = [900, 260, 333][:len(new)]
+    s = Packed(5, kind, new, ctx, 8, 2, 128, page, H16)
+    a = s.args(**mask)
+    qg.qgemv_route_reset()
+    qg.qgemv_attn(a)
+    assert qg.qgemv_route_counts()[qg.ROUTE_ATTN_TILES] == 1
+    packed = s.out.clone(), s.lse.clone()
+    # the contexts one after another in a 16-bit cache of the same pages
+    starts = np.concatenate([[0], np.cumsum(ctx)]).astype(np.int32)
+    k, v = (torch.zeros(sum(ctx), 2, 128, dtype=H16, device="cuda") for _ in range(2))
+    qg.qgemv_cache_read(qg.cache_read_args(qg.packed_cache(kind, s.kc, s.vc, 128), s.table, torch.from_numpy(starts).cuda(), k, v))
+    kc, vc = (torch.zeros(*s.kc.shape[:3], 128, dtype=H16, device="cuda") for _ in range(2))
+    for b, c in enumerate(ctx):
+        t = torch.arange(c, device="cuda")
+        where = s.table[b, t // page].long(), t % page
+        kc[where], vc[where] = k[starts[b]:starts[b + 1]], v[starts[b]:starts[b + 1]]
+    out, lse = torch.full_like(s.out, 7.0), torch.full_like(s.lse, 7.0)
+    qg.qgemv_attn(qg.attn_args(s.q, qg.kv_cache(kc, vc), s.table, s.starts, s.lens, out, s.scratch, max(new), max(ctx), s.scale, lse=lse, **mask))
+    assert torch.equal(out, packed[0]) and torch.equal(lse, packed[1])
+    assert int(s.scratch[:qg.QGEMV_ATTN_SCRATCH_HEAD].sum()) == 0
+
+
+@pytest.mark.parametrize("kind", ["Q4", "Q8"])
+@pytest.mark.parametrize("D", [64, 96, 128])
+@pytest.mark.parametrize("new,page,mask", MANY)
+def test_many_rows(new, page, mask, D, kind, copying):
+    ctx = [900, 260, 333][:len(new)]
+    for qscale in (1.0, 1e-6, 3e4):  # (bf16 queries of any size: rows scaled by powers of two)
+        s = Packed(6, kind, new, ctx, 6, 2, D, page, B16, scale=D ** -0.5 / qscale)
+        s.q.mul_(qscale)
         a = s.args(**mask)
-        qg.qgemv_route_reset()
         qg.qgemv_attn(a)
-        assert qg.qgemv_route_counts()[qg.ROUTE_ATTN_TILES] == 1
-        packed = s.out.clone(), s.lse.clone()
-        # the contexts one after another in a 16-bit cache of the same pages
-        starts = np.concatenate([[0], np.cumsum(ctx)]).astype(np.int32)
-        k, v = (torch.zeros(sum(ctx), 2, 128, dtype=dtype, device="cuda") for _ in range(2))
-        qg.qgemv_cache_read(qg.cache_read_args(qg.packed_cache(kind, s.kc, s.vc, 128), s.table, torch.from_numpy(starts).cuda(), k, v))
-        kc, vc = (torch.zeros(*s.kc.shape[:3], 128, dtype=dtype, device="cuda") for _ in range(2))
-        for b, c in enumerate(ctx):
-            t = torch.arange(c, device="cuda")
-            where = s.table[b, t // page].long(), t % page
-            kc[where], vc[where] = k[starts[b]:starts[b + 1]], v[starts[b]:starts[b + 1]]
-        out, lse = torch.full_like(s.out, 7.0), torch.full_like(s.lse, 7.0)
-        qg.qgemv_attn(qg.attn_args(s.q, qg.kv_cache(kc, vc), s.table, s.starts, s.lens, out, s.scratch, max(new), max(ctx), s.scale, lse=lse,
-                                   **mask))
-        assert torch.equal(out, packed[0]) and torch.equal(lse, packed[1])
+        s.check(copy=True, **mask)
         assert int(s.scratch[:qg.QGEMV_ATTN_SCRATCH_HEAD].sum()) == 0
-    finally:
-        qg.qgemv_tune_attn(0)
+        first = s.out.clone()
+        qg.qgemv_attn(a, qg.QGEMV_FLAG_PDL)
+        assert torch.equal(first, s.out)
 
 
 @pytest.mark.parametrize("kind", ["Q4", "Q8"])
