@@ -51,16 +51,19 @@ __global__ void __launch_bounds__(CACHE_THREADS) cache_write_kernel(const CacheW
         uint8_t* rows = static_cast<uint8_t*>(is_v ? a.v_cache : a.k_cache) + (is_v ? a.vc_head : a.kc_head) * h;
         const long long* place = is_v ? vs : ks;
         for (int t0 = lay.row; t0 < n; t0 += lay.deep * AHEAD) {
-            float v[AHEAD][8];
+            Raw8<XK> v[AHEAD];
 #pragma unroll
             for (int j = 0; j < AHEAD; ++j) {
                 const int t = t0 + j * lay.deep;
-                if (t < n && place[t] >= 0) load8<XK>(x, (first + t) * token_step + src, v[j]);
+                if (t < n && place[t] >= 0) v[j].load(x, (first + t) * token_step + src);
             }
 #pragma unroll
             for (int j = 0; j < AHEAD; ++j) {
                 const int t = t0 + j * lay.deep;
-                if (t < n && place[t] >= 0) put8<BITS>(rows + place[t], a.dim, e, v[j]);
+                if (t >= n || place[t] < 0) continue;
+                float w[8];
+                v[j].values(w);
+                put8<BITS>(rows + place[t], a.dim, e, w);
             }
         }
     }
@@ -109,18 +112,18 @@ __global__ void __launch_bounds__(CACHE_THREADS) cache_read_kernel(const CacheRe
         const uint8_t* rows = (is_v ? a.v_cache : a.k_cache) + (is_v ? a.vc_head : a.kc_head) * h;
         const long long* place = is_v ? vs : ks;
         for (int t0 = lay.row; t0 < n; t0 += lay.deep * AHEAD) {
-            float v[AHEAD][8];
+            Packed8<BITS> v[AHEAD] = {};
 #pragma unroll
             for (int j = 0; j < AHEAD; ++j) {
                 const int t = t0 + j * lay.deep;
-#pragma unroll
-                for (float& w : v[j]) w = 0.f;
-                if (t < n && place[t] >= 0) get8<BITS>(rows + place[t], a.dim, e, v[j]);
+                if (t < n && place[t] >= 0) v[j].load(rows + place[t], a.dim, e);
             }
 #pragma unroll
             for (int j = 0; j < AHEAD; ++j) {
                 const int t = t0 + j * lay.deep;
-                if (t < n && place[t] >= -1) store8(a.out_kind, y, (first + t) * token_step + dst, v[j]);
+                float x[8];
+                v[j].values(x);  // (nothing: zeros)
+                if (t < n && place[t] >= -1) store8(a.out_kind, y, (first + t) * token_step + dst, x);
             }
         }
     }
@@ -190,11 +193,11 @@ __global__ void __launch_bounds__(CACHE_THREADS) cache_unpack_kernel(const Cache
         const uint8_t* rows = (is_v ? u.v + h * a.v_head : u.k + h * a.k_head);
         const long long* place = is_v ? vs : ks;
         for (int i0 = from - t0 + lay.row; i0 < to - t0; i0 += lay.deep * AHEAD) {
-            float x[AHEAD][8];
+            Packed8<BITS> w[AHEAD] = {};
 #pragma unroll
             for (int j = 0; j < AHEAD; ++j) {
                 const int i = i0 + j * lay.deep;
-                if (i < to - t0 && place[i] >= 0) get8<BITS>(rows + place[i], a.dim, e, x[j]);
+                if (i < to - t0 && place[i] >= 0) w[j].load(rows + place[i], a.dim, e);
             }
 #pragma unroll
             for (int j = 0; j < AHEAD; ++j) {
@@ -202,9 +205,11 @@ __global__ void __launch_bounds__(CACHE_THREADS) cache_unpack_kernel(const Cache
                 if (i >= to - t0 || place[i] < 0) continue;
                 const int n = (t0 + i) / u.page_size;
                 const long long row = ((b * u.per_seq + n) * a.kv_heads + h) * u.page_size + (t0 + i - n * u.page_size);
+                float x[8];
+                w[j].values(x);
 #pragma unroll
-                for (float& v : x[j]) v = fminf(fmaxf(v, -65504.f), 65504.f);  // (d c + m may end a step's rounding beyond the largest f16)
-                store8(ACT_F16, y, row * a.dim + e, x[j]);
+                for (float& v : x) v = fminf(fmaxf(v, -65504.f), 65504.f);  // (d c + m may end a step's rounding beyond the largest f16)
+                store8(ACT_F16, y, row * a.dim + e, x);
             }
         }
     }

@@ -14,22 +14,34 @@ __device__ __forceinline__ float load1(const void* x, long long i) {
     return h2f(w);
 }
 
-// Eight consecutive values, 16-byte aligned, widened exactly.
+// Eight consecutive values, 16-byte aligned, as they lie there; widened exactly.
 template <int XK>
-__device__ __forceinline__ void load8(const void* x, long long i, float (&v)[8]) {
-    if constexpr (XK == ACT_F32) {
-        const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(x) + i);
-        const float4 a = p[0], b = p[1];
-        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-    } else {
-        const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + i);
-        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+struct Raw8 {
+    uint4 u[XK == ACT_F32 ? 2 : 1];
+    __device__ __forceinline__ void load(const void* x, long long i) {
+        const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(x) + i * (XK == ACT_F32 ? 4 : 2));
+        u[0] = p[0];
+        if constexpr (XK == ACT_F32) u[1] = p[1];
+    }
+    __device__ __forceinline__ void values(float (&v)[8]) const {
+        if constexpr (XK == ACT_F32) {
+            v[0] = __uint_as_float(u[0].x), v[1] = __uint_as_float(u[0].y), v[2] = __uint_as_float(u[0].z), v[3] = __uint_as_float(u[0].w);
+            v[4] = __uint_as_float(u[1].x), v[5] = __uint_as_float(u[1].y), v[6] = __uint_as_float(u[1].z), v[7] = __uint_as_float(u[1].w);
+        } else {
+            const uint32_t w[4] = {u[0].x, u[0].y, u[0].z, u[0].w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            v[2 * j] = XK == ACT_BF16 ? __uint_as_float(w[j] << 16) : h2f(w[j]);
-            v[2 * j + 1] = XK == ACT_BF16 ? __uint_as_float(w[j] & 0xFFFF0000u) : h2f(w[j] >> 16);
+            for (int j = 0; j < 4; ++j) {
+                v[2 * j] = XK == ACT_BF16 ? __uint_as_float(w[j] << 16) : h2f(w[j]);
+                v[2 * j + 1] = XK == ACT_BF16 ? __uint_as_float(w[j] & 0xFFFF0000u) : h2f(w[j] >> 16);
+            }
         }
     }
+};
+template <int XK>
+__device__ __forceinline__ void load8(const void* x, long long i, float (&v)[8]) {
+    Raw8<XK> r;
+    r.load(x, i);
+    r.values(v);
 }
 
 __device__ __forceinline__ uint32_t pack2(int kind, float a, float b) {
@@ -55,48 +67,57 @@ __device__ __forceinline__ void store8(int kind, void* y, long long i, const flo
     }
 }
 
+__device__ __forceinline__ float max_or_nan(float a, float b) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+
 // Elements e .. e + 7 (e a multiple of 8) of a row of `dim`.  Four consecutive lanes, the first at a multiple of 4, hold a block: they
 // find its least and largest value together, and each writes its own codes.  All four call this, with the same `row`.
 //
 // The base is rounded down and the step up, so that every value lies within the codes: none is cut off by more than the rounding of
 // the fp32 arithmetic.  The product with 1 / d stands for the quotient (one instruction an element instead of eight); it moves a code by
-// one only where the value lies within 2^-14 steps of the middle of two.
+// one only where the value lies within 2^-14 steps of the middle of two.  Values beyond +-65504 need no clamp of their own: the block's ends are
+// clamped, and the codes to 0 .. L.  A code comes out of the low bits of t + 1.5 2^23, which rounds t to a whole number, ties to even; the
+// sum of those words times powers of two packs the codes, with the words' upper bits taken off at once.
 template <int BITS>
-__device__ __forceinline__ void put8(uint8_t* row, int dim, int e, float (&x)[8]) {
+__device__ __forceinline__ void put8(uint8_t* row, int dim, int e, const float (&x)[8]) {
     constexpr float TOP = (1 << BITS) - 1;
     const unsigned team = 0xFu << (threadIdx.x & 28);
     float lo = x[0], hi = x[0];
-    bool nan = false;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        nan |= x[j] != x[j];
-        x[j] = fminf(fmaxf(x[j], -65504.f), 65504.f);
-    }
-    lo = x[0], hi = x[0];
-#pragma unroll
-    for (int j = 1; j < 8; ++j) lo = fminf(lo, x[j]), hi = fmaxf(hi, x[j]);
+    for (int j = 1; j < 8; ++j) lo = fminf(lo, x[j]), hi = max_or_nan(hi, x[j]);
 #pragma unroll
     for (int o = 1; o < 4; o *= 2) {
         lo = fminf(lo, __shfl_xor_sync(team, lo, o));
-        hi = fmaxf(hi, __shfl_xor_sync(team, hi, o));
+        hi = max_or_nan(hi, __shfl_xor_sync(team, hi, o));
     }
-    nan = __any_sync(team, nan);
-    __half m = __float2half_rd(lo);
+    const bool nan = hi != hi;
+    lo = fminf(fmaxf(lo, -65504.f), 65504.f), hi = fminf(fmaxf(hi, -65504.f), 65504.f);
+    const __half m = __float2half_rd(lo);
     const float mf = __half2float(m);
     __half d = __float2half_ru(__fdiv_rn(__fsub_rn(hi, mf), TOP));
     if (nan) d = __ushort_as_half(0);
     const float df = __half2float(d), rate = df == 0.f ? 0.f : __frcp_rn(df);
     uint32_t c[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) c[j] = __float2uint_rn(fminf(__fmul_rn(__fsub_rn(x[j], mf), rate), TOP));
+    for (int j = 0; j < 8; ++j) {
+        const float t = fminf(fmaxf(__fmul_rn(__fsub_rn(x[j], mf), rate), 0.f), TOP);
+        c[j] = __float_as_uint(__fadd_rn(t, 12582912.f));  // 0x4B400000 + code
+    }
+    constexpr uint32_t BIAS = 0x4B400000u;
     if constexpr (BITS == 4) {
-        uint32_t w = 0;
+        uint32_t w = 0u - BIAS * 0x11111111u;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) w |= c[j] << (4 * j);
+        for (int j = 0; j < 8; ++j) w += c[j] * (1u << (4 * j));
         *reinterpret_cast<uint32_t*>(row + e / 2) = w;
     } else {
-        *reinterpret_cast<uint2*>(row + e) =
-            make_uint2(c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24, c[4] | c[5] << 8 | c[6] << 16 | c[7] << 24);
+        uint32_t w[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            w[j] = c[4 * j] + c[4 * j + 1] * (1u << 8) + c[4 * j + 2] * (1u << 16) + c[4 * j + 3] * (1u << 24) - BIAS * 0x01010101u;
+        *reinterpret_cast<uint2*>(row + e) = make_uint2(w[0], w[1]);
     }
     if (e % 32 == 0) {
         __half* scale = reinterpret_cast<__half*>(row + dim * BITS / 8);
@@ -105,24 +126,30 @@ __device__ __forceinline__ void put8(uint8_t* row, int dim, int e, float (&x)[8]
     }
 }
 
-// The values of elements e .. e + 7 of a row.
+// Elements e .. e + 7 of a row as they lie there, and their values.
 template <int BITS>
-__device__ __forceinline__ void get8(const uint8_t* row, int dim, int e, float (&x)[8]) {
-    const __half* scale = reinterpret_cast<const __half*>(row + dim * BITS / 8);
+struct Packed8 {
     uint32_t w[BITS / 4];
-    if constexpr (BITS == 4) {
-        w[0] = *reinterpret_cast<const uint32_t*>(row + e / 2);
-    } else {
-        const uint2 u = *reinterpret_cast<const uint2*>(row + e);
-        w[0] = u.x, w[1] = u.y;
+    uint16_t d, m;
+    __device__ __forceinline__ void load(const uint8_t* row, int dim, int e) {
+        if constexpr (BITS == 4) {
+            w[0] = __ldg(reinterpret_cast<const uint32_t*>(row + e / 2));
+        } else {
+            const uint2 u = __ldg(reinterpret_cast<const uint2*>(row + e));
+            w[0] = u.x, w[1] = u.y;
+        }
+        const uint16_t* scale = reinterpret_cast<const uint16_t*>(row + dim * BITS / 8) + e / 32;
+        d = __ldg(scale), m = __ldg(scale + dim / 32);
     }
-    const float d = __half2float(scale[e / 32]), m = __half2float(scale[dim / 32 + e / 32]);
+    __device__ __forceinline__ void values(float (&x)[8]) const {
+        const float df = h2f(d), mf = h2f(m);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const uint32_t c = w[j * BITS / 32] >> (j * BITS % 32) & ((1u << BITS) - 1u);
-        // (d c is exact in fp32, so that this rounds once)
-        x[j] = __fmaf_rn(d, i2f_small(static_cast<int>(c)), m);
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t c = w[j * BITS / 32] >> (j * BITS % 32) & ((1u << BITS) - 1u);
+            // (d c is exact in fp32, so that this rounds once)
+            x[j] = __fmaf_rn(df, i2f_small(static_cast<int>(c)), mf);
+        }
     }
-}
+};
 
 }  // namespace qg
