@@ -217,6 +217,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) attn_tiles_kernel(const __gri
     __shared__ TilesShared sh;
     pdl_launch_dependents();
     pdl_wait();
+    fence_copies();
     // A value that all lanes have, in a form that is uniform for the compiler too: control flow, addresses and descriptors that hang on it
     // then are, and take no registers of the threads.
     auto uniform = [](int v) { return __reduce_max_sync(0xffffffffu, v); };

@@ -133,13 +133,13 @@ struct Packed8 {
     uint16_t d, m;
     __device__ __forceinline__ void load(const uint8_t* row, int dim, int e) {
         if constexpr (BITS == 4) {
-            w[0] = __ldg(reinterpret_cast<const uint32_t*>(row + e / 2));
+            w[0] = *reinterpret_cast<const uint32_t*>(row + e / 2);
         } else {
-            const uint2 u = __ldg(reinterpret_cast<const uint2*>(row + e));
+            const uint2 u = *reinterpret_cast<const uint2*>(row + e);
             w[0] = u.x, w[1] = u.y;
         }
         const uint16_t* scale = reinterpret_cast<const uint16_t*>(row + dim * BITS / 8) + e / 32;
-        d = __ldg(scale), m = __ldg(scale + dim / 32);
+        d = scale[0], m = scale[dim / 32];
     }
     __device__ __forceinline__ void values(float (&x)[8]) const {
         const float df = h2f(d), mf = h2f(m);

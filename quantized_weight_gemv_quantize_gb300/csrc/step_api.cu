@@ -403,7 +403,16 @@ static int attn_plan(int bits, bool f16, int seqs, int tokens, int heads, int kv
                pieces >= (p->hb_shift ? 40 : 18))
             ++p->hb_shift;
         copy = dim <= 128 && (forced ? forced == 2 : rows > PACKED_ROWS) ? copy_bytes(seqs, tokens, heads, kv_heads, dim, max_kv) : 0;
-        p->tiles = copy > 0 && (forced == 2 || tiles_us + 10 < rows_us);
+        // More than 32 rows: by what both would take, in us.  The packed cache's kernel goes over the keys once for 16 rows, 18 row tiles and keys a ns
+        // in 4 bits and 15 in 8; the other needs its copy first (160 or 288 bytes read and 512 written a key and head of 128, at 4.5 TB/s).  Of
+        // several sequences with one bound the mean is taken to be 0.45 of it.  Measured, 8 key/value heads, 4 bits, packed / copy: 64 rows over
+        // 4000 23.2 / 37.3, 256 rows 47.6 / 43.6; over 24000 64 rows 51.5 / 72.3, 128 rows 88.7 / 73.0; over 100000 64 rows 153 / 221, 128 rows
+        // 314 / 222; 32 sequences of up to 4000 64 rows 99 / 194, 128 rows 167 / 190, 256 rows 278 / 218; 8 bits, 24000, 64 rows 59.9 / 74.5,
+        // 128 rows 111 / 76.
+        const double part = seqs > 1 ? 0.45 : 1.0;
+        const double packed_us = 15 + part * static_cast<double>((rows + 15) / 16) * kv_heads * seqs * keys_of(16, 16) / (bits == 4 ? 18000 : 15000);
+        const double copy_us = 5 + part * static_cast<double>(seqs) * keys * kv_heads * static_cast<double>(dim) * (4 + bits / 4.0 + 0.25) / 4.5e6;
+        p->tiles = copy > 0 && (forced == 2 || tiles_us + copy_us < packed_us);
     }
     size_t records = 0;
     if (!p->tiles) {
@@ -447,7 +456,7 @@ static int attn_plan(int bits, bool f16, int seqs, int tokens, int heads, int kv
 // Dynamic shared memory of a kernel, set once per device.
 static int allow_smem(const void* fn, unsigned smem) {
     static std::mutex mu;
-    static const void* done[64][48];
+    static const void* done[64][96];  // (there are some 60 such kernels)
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return api_cuda_fail(e);
