@@ -657,7 +657,7 @@ __device__ __forceinline__ void attend_packed(const AttnPackedArgs& pa, const Ti
 }
 
 // Joins the parts of a row tile that begins in block t.index: four elements of a row a thread, one pass over the parts with the maximum and the
-// sum running along, sixteen parts' loads on their way at once.
+// sum running along, eight parts' loads on their way at once.
 template <int DP, int BITS, int NT>
 __device__ __forceinline__ void join_packed(const AttnPackedArgs& pa, const Tile& t) {
     using S = PackedShape<DP, BITS, NT>;
@@ -669,7 +669,7 @@ __device__ __forceinline__ void join_packed(const AttnPackedArgs& pa, const Tile
         float m = NEG_INF, l = 0.f;
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
         const int rec = static_cast<int>(2 * t.index * S::WARPS + hh) * S::ROWS + r;
-#pragma unroll 16
+#pragma unroll 8
         for (int p = 0; p < t.parts; ++p) {
             const int at = rec + (2 * p + (p == 0 ? 1 : 0)) * S::WARPS * S::ROWS;
             const float2 s = __ldcg(a.part_stat + at);
