@@ -134,6 +134,31 @@ __device__ __forceinline__ void attend_packed(const AttnPackedArgs& pa, const Ti
     // keys that every row sees: low .. high
     const int high = a.causal ? min(t.k1 - 1, row_pos(a, t, 0)) : t.k1 - 1, low = first_key(a, row_pos(a, t, t.rows - 1));
 
+    // ---- queries: column g8 (+ 8) of the products.  A lane holds, of every block, the elements whose codes it meets: 4 bits, elements 8 t4 ..
+    // 8 t4 + 7 of the block; 8 bits, 4 t4 .. 4 t4 + 3 of either half.  They are asked for before the copies, which would keep them waiting.
+    Tile own = t;
+    own.kv_head = head;
+    uint32_t qw[NT][G][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const int r = g8 + 8 * nt;
+        const uint16_t* src = static_cast<const uint16_t*>(a.q) + out_at(a, own, min(r, t.rows - 1), a.q_token, a.q_head);
+#pragma unroll
+        for (int s = 0; s < G; ++s) {
+            uint32_t (&w)[4] = qw[nt][s];
+            w[0] = w[1] = w[2] = w[3] = 0u;
+            if (r < t.rows && (WHOLE || s < gd)) {
+                if constexpr (BITS == 4) {
+                    const uint4 u = *reinterpret_cast<const uint4*>(src + 32 * s + 8 * t4);
+                    w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+                } else {
+                    const uint2 u = *reinterpret_cast<const uint2*>(src + 32 * s + 4 * t4), v = *reinterpret_cast<const uint2*>(src + 32 * s + 16 + 4 * t4);
+                    w[0] = u.x, w[1] = u.y, w[2] = v.x, w[3] = v.y;
+                }
+            }
+        }
+    }
+
     // ---- copies.  A slot holds KT times: 16 keys of each warp, then their values, by boxes of 16 keys of all the heads.  Round r is asked for by
     // warp r % WARPS: lane n for box n, the keys 16 n of the round on, which are the (n % KT)th of the heads' (n / KT)th warps.  Its pages are looked
     // up a turn ahead.
@@ -224,33 +249,18 @@ __device__ __forceinline__ void attend_packed(const AttnPackedArgs& pa, const Ti
         }
     }
 
-    // ---- queries: column g8 (+ 8) of the products.  A lane holds, of every block, the elements whose codes it meets: 4 bits, elements 8 t4 ..
-    // 8 t4 + 7 of the block; 8 bits, 4 t4 .. 4 t4 + 3 of either half.
-    Tile own = t;
-    own.kv_head = head;
+    // ---- the queries as operands
     uint32_t qb[NT][G][4], mb[NT][G > 4 ? 2 : 1][2];
     float unit[NT][2];  // of the columns 2 t4, 2 t4 + 1 that this lane's sums belong to: 2^24 scale log2(e) over the row's power of two
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-        const int r = g8 + 8 * nt;
-        const uint16_t* src = static_cast<const uint16_t*>(a.q) + out_at(a, own, min(r, t.rows - 1), a.q_token, a.q_head);
         float q[G][8];
         float top = 0.f;
 #pragma unroll
         for (int s = 0; s < G; ++s) {
-            uint32_t w[4] = {};
-            if (r < t.rows && (WHOLE || s < gd)) {
-                if constexpr (BITS == 4) {
-                    const uint4 u = *reinterpret_cast<const uint4*>(src + 32 * s + 8 * t4);
-                    w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
-                } else {
-                    const uint2 u = *reinterpret_cast<const uint2*>(src + 32 * s + 4 * t4), v = *reinterpret_cast<const uint2*>(src + 32 * s + 16 + 4 * t4);
-                    w[0] = u.x, w[1] = u.y, w[2] = v.x, w[3] = v.y;
-                }
-            }
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const uint32_t h = w[j / 2] >> (16 * (j % 2)) & 0xFFFFu;
+                const uint32_t h = qw[nt][s][j / 2] >> (16 * (j % 2)) & 0xFFFFu;
                 q[s][j] = pa.bf16 ? __uint_as_float(h << 16) : h2f(h);
                 top = fmaxf(top, fabsf(q[s][j]));
             }
@@ -656,33 +666,51 @@ __device__ __forceinline__ void attend_packed(const AttnPackedArgs& pa, const Ti
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
-// Joins the parts of a row tile that begins in block t.index: four elements of a row a thread, one pass over the parts with the maximum and the
-// sum running along, eight parts' loads on their way at once.
-template <int DP, int BITS, int NT>
+// Joins the parts of a row tile that begins in block t.index: four elements of up to four rows a thread, one pass over the parts with the maxima and
+// the sums running along, sixteen loads on their way at once.
+template <int DP, int BITS, int NT, int ITEMS>
 __device__ __forceinline__ void join_packed(const AttnPackedArgs& pa, const Tile& t) {
     using S = PackedShape<DP, BITS, NT>;
+    constexpr int AT_ONCE = S::WARPS * 32 / (DP / 4);
     const AttnArgs& a = pa.a;
+    const int d = threadIdx.x % (DP / 4) * 4, rows = t.rows << pa.hb_shift;
+    if (d >= a.dim) return;
     Tile own = t;
-    for (int i = threadIdx.x; i < (t.rows << pa.hb_shift) * (DP / 4); i += S::WARPS * 32) {
-        const int hr = i / (DP / 4), d = i % (DP / 4) * 4, hh = hr / t.rows, r = hr - hh * t.rows;
-        if (d >= a.dim) continue;
-        float m = NEG_INF, l = 0.f;
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        const int rec = static_cast<int>(2 * t.index * S::WARPS + hh) * S::ROWS + r;
-#pragma unroll 8
-        for (int p = 0; p < t.parts; ++p) {
-            const int at = rec + (2 * p + (p == 0 ? 1 : 0)) * S::WARPS * S::ROWS;
-            const float2 s = __ldcg(a.part_stat + at);
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part_sum + static_cast<long long>(at) * a.dim + d));
-            const float top = fmaxf(m, s.x), base = top == NEG_INF ? 0.f : top;
-            const float keep = exp2_approx(m - base), w = exp2_approx(s.x - base);
-            m = top;
-            l = l * keep + w * s.y;
-            x.x = x.x * keep + w * v.x, x.y = x.y * keep + w * v.y, x.z = x.z * keep + w * v.z, x.w = x.w * keep + w * v.w;
+#pragma unroll 1
+    for (int first = threadIdx.x / (DP / 4); first < rows; first += AT_ONCE * ITEMS) {
+        float m[ITEMS], l[ITEMS];
+        float4 x[ITEMS];
+        int rec[ITEMS];
+#pragma unroll
+        for (int k = 0; k < ITEMS; ++k) {
+            m[k] = NEG_INF, l[k] = 0.f, x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            const int hr = min(first + k * AT_ONCE, rows - 1), hh = hr / t.rows;  // (rows past the last one read its record)
+            rec[k] = static_cast<int>(2 * t.index * S::WARPS + hh) * S::ROWS + hr - hh * t.rows;
         }
-        own.kv_head = t.kv_head + hh;
-        if (pa.bf16) put_row4<true>(a, own, r, d, x, m, l);
-        else put_row4<false>(a, own, r, d, x, m, l);
+#pragma unroll(16 / ITEMS)
+        for (int p = 0; p < t.parts; ++p) {
+            const int part = (2 * p + (p == 0 ? 1 : 0)) * S::WARPS * S::ROWS;
+#pragma unroll
+            for (int k = 0; k < ITEMS; ++k) {
+                const int at = rec[k] + part;
+                const float2 s = __ldcg(a.part_stat + at);
+                const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part_sum + static_cast<long long>(at) * a.dim + d));
+                const float top = fmaxf(m[k], s.x), base = top == NEG_INF ? 0.f : top;
+                const float keep = exp2_approx(m[k] - base), w = exp2_approx(s.x - base);
+                m[k] = top;
+                l[k] = l[k] * keep + w * s.y;
+                x[k].x = x[k].x * keep + w * v.x, x[k].y = x[k].y * keep + w * v.y;
+                x[k].z = x[k].z * keep + w * v.z, x[k].w = x[k].w * keep + w * v.w;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < ITEMS; ++k) {
+            const int hr = first + k * AT_ONCE, hh = hr / t.rows, r = hr - hh * t.rows;
+            if (hr >= rows) break;
+            own.kv_head = t.kv_head + hh;
+            if (pa.bf16) put_row4<true>(a, own, r, d, x[k], m[k], l[k]);
+            else put_row4<false>(a, own, r, d, x[k], m[k], l[k]);
+        }
     }
 }
 
@@ -709,7 +737,10 @@ __global__ void __launch_bounds__(PackedShape<DP, BITS, NT>::WARPS * 32, PackedS
     divide_rows<S::ROWS, 16>(
         pa.a, pa.a.kv_heads >> pa.hb_shift, 1 << pa.hb_shift, pa.few, &last, smem,
         [&](const Tile& t, long long record) { attend_packed<DP, BITS, NT, WHOLE, FINE>(pa, t, record, smem, smem_addr(plain), ring, slot, parity); },
-        [&](const Tile& t) { join_packed<DP, BITS, NT>(pa, t); });
+        [&](const Tile& t) {
+            if ((t.rows << pa.hb_shift) <= S::WARPS * 32 / (DP / 4)) join_packed<DP, BITS, NT, 1>(pa, t);
+            else join_packed<DP, BITS, NT, 4>(pa, t);
+        });
 }
 
 template <int BITS, bool FINE, int DP, int NT, bool WHOLE>
