@@ -107,23 +107,26 @@ __global__ void __launch_bounds__(CACHE_THREADS) cache_read_kernel(const CacheRe
     for (int p = lay.at; p < pieces; p += lay.wide) {
         const bool is_v = !a.k_out || p >= half;
         const int in = p >= half ? p - half : p, h = in / per_head, e = (in - h * per_head) * 8;
-        const long long dst = (is_v ? a.v_head : a.k_head) * h + e, token_step = is_v ? a.v_token : a.k_token;
-        void* y = is_v ? a.v_out : a.k_out;
+        const int size = a.out_kind == ACT_F32 ? 4 : 2;
+        const long long token_step = (is_v ? a.v_token : a.k_token) * size;
+        char* y = static_cast<char*>(is_v ? a.v_out : a.k_out) + ((is_v ? a.v_head : a.k_head) * h + e) * size + (first + lay.row) * token_step;
         const uint8_t* rows = (is_v ? a.v_cache : a.k_cache) + (is_v ? a.vc_head : a.kc_head) * h;
+        const uint8_t *codes = rows + e * BITS / 8, *step = rows + a.dim * BITS / 8 + e / 32 * 2;
         const long long* place = is_v ? vs : ks;
         for (int t0 = lay.row; t0 < n; t0 += lay.deep * AHEAD) {
             Packed8<BITS> v[AHEAD] = {};
 #pragma unroll
             for (int j = 0; j < AHEAD; ++j) {
                 const int t = t0 + j * lay.deep;
-                if (t < n && place[t] >= 0) v[j].load(rows + place[t], a.dim, e);
+                if (t < n && place[t] >= 0) v[j].load(codes, step, a.dim / 16, place[t]);
             }
 #pragma unroll
             for (int j = 0; j < AHEAD; ++j) {
                 const int t = t0 + j * lay.deep;
                 float x[8];
                 v[j].values(x);  // (nothing: zeros)
-                if (t < n && place[t] >= -1) store8(a.out_kind, y, (first + t) * token_step + dst, x);
+                if (t < n && place[t] >= -1) store8(a.out_kind, y, 0, x);
+                y += lay.deep * token_step;
             }
         }
     }
@@ -177,8 +180,8 @@ __global__ void __launch_bounds__(CACHE_THREADS) cache_unpack_kernel(const Cache
             const bool there = page >= 0 && page < a.num_pages;
             if (there) k = page * a.k_page + token * a.k_token, v = page * a.v_page + token * a.v_token;
             else atomicOr(a.err, ERR_BAD_INDEX);
-            const int n = t / u.page_size;
-            if (t % u.page_size == 0 || t == from) u.table[b * u.per_seq + n] = there ? static_cast<int>(b * u.per_seq + n) : -1;
+            const int n = t >> u.page_shift;
+            if ((t & (u.page_size - 1)) == 0 || t == from) u.table[b * u.per_seq + n] = there ? static_cast<int>(b * u.per_seq + n) : -1;
         }
         ks[threadIdx.x] = k, vs[threadIdx.x] = v;
     }
@@ -191,20 +194,21 @@ __global__ void __launch_bounds__(CACHE_THREADS) cache_unpack_kernel(const Cache
         const int in = is_v ? p - half : p, h = in / per_head, e = (in - h * per_head) * 8;
         void* y = is_v ? u.v_copy : u.k_copy;
         const uint8_t* rows = (is_v ? u.v + h * a.v_head : u.k + h * a.k_head);
+        const uint8_t *codes = rows + e * BITS / 8, *step = rows + a.dim * BITS / 8 + e / 32 * 2;
         const long long* place = is_v ? vs : ks;
         for (int i0 = from - t0 + lay.row; i0 < to - t0; i0 += lay.deep * AHEAD) {
             Packed8<BITS> w[AHEAD] = {};
 #pragma unroll
             for (int j = 0; j < AHEAD; ++j) {
                 const int i = i0 + j * lay.deep;
-                if (i < to - t0 && place[i] >= 0) w[j].load(rows + place[i], a.dim, e);
+                if (i < to - t0 && place[i] >= 0) w[j].load(codes, step, a.dim / 16, place[i]);
             }
 #pragma unroll
             for (int j = 0; j < AHEAD; ++j) {
                 const int i = i0 + j * lay.deep;
                 if (i >= to - t0 || place[i] < 0) continue;
-                const int n = (t0 + i) / u.page_size;
-                const long long row = ((b * u.per_seq + n) * a.kv_heads + h) * u.page_size + (t0 + i - n * u.page_size);
+                const int n = (t0 + i) >> u.page_shift;  // (a power of two)
+                const long long row = ((b * u.per_seq + n) * a.kv_heads + h) * u.page_size + (t0 + i - (n << u.page_shift));
                 float x[8];
                 w[j].values(x);
 #pragma unroll

@@ -126,28 +126,35 @@ __device__ __forceinline__ void put8(uint8_t* row, int dim, int e, const float (
     }
 }
 
-// Elements e .. e + 7 of a row as they lie there, and their values.
+// Elements e .. e + 7 of a row as they lie there, and their values.  The places of the codes, the step and the base within a row are a thread's own.
 template <int BITS>
 struct Packed8 {
     uint32_t w[BITS / 4];
     uint16_t d, m;
-    __device__ __forceinline__ void load(const uint8_t* row, int dim, int e) {
+    // codes, step: those of the first row, `place` bytes before this one; the base lies `base` bytes after the step
+    __device__ __forceinline__ void load(const uint8_t* codes, const uint8_t* step, int base, long long place) {
         if constexpr (BITS == 4) {
-            w[0] = *reinterpret_cast<const uint32_t*>(row + e / 2);
+            w[0] = *reinterpret_cast<const uint32_t*>(codes + place);
         } else {
-            const uint2 u = *reinterpret_cast<const uint2*>(row + e);
+            const uint2 u = *reinterpret_cast<const uint2*>(codes + place);
             w[0] = u.x, w[1] = u.y;
         }
-        const uint16_t* scale = reinterpret_cast<const uint16_t*>(row + dim * BITS / 8) + e / 32;
-        d = scale[0], m = scale[dim / 32];
+        const uint8_t* const s = step + place;
+        d = *reinterpret_cast<const uint16_t*>(s), m = *reinterpret_cast<const uint16_t*>(s + base);
     }
+    // A code becomes a float where it stands: its bits, anywhere below bit 20, in the mantissa of 2^23, which is taken off again (exactly); the power of
+    // 16 by which it stands too high is taken off the step.  (d c is exact in fp32, so that the last step alone rounds.)
     __device__ __forceinline__ void values(float (&x)[8]) const {
         const float df = h2f(d), mf = h2f(m);
+        constexpr uint32_t TWO23 = 0x4B000000u;
+        if constexpr (BITS == 4) {
+            const float ds[4] = {df, df * 0.0625f, df * 0.00390625f, df * 0.000244140625f};
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint32_t c = w[j * BITS / 32] >> (j * BITS % 32) & ((1u << BITS) - 1u);
-            // (d c is exact in fp32, so that this rounds once)
-            x[j] = __fmaf_rn(df, i2f_small(static_cast<int>(c)), mf);
+            for (int j = 0; j < 8; ++j)
+                x[j] = __fmaf_rn(ds[j & 3], __uint_as_float(((j < 4 ? w[0] : w[0] >> 16) & 0xFu << (4 * (j & 3))) | TWO23) - 8388608.f, mf);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = __fmaf_rn(df, __uint_as_float(__byte_perm(w[j / 4], TWO23, 0x7650 | (j & 3))) - 8388608.f, mf);
         }
     }
 };

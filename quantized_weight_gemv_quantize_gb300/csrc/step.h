@@ -122,7 +122,7 @@ struct CacheUnpackArgs {
     void *k_copy, *v_copy;
     int* table;
     long long per_seq;       // pages of a sequence in the copy
-    int page_size;           // of the copy
+    int page_size, page_shift;  // of the copy: a power of two
     int key_blocks;          // blocks of a sequence that copy keys; those beyond them take its queries
     uint16_t* q_copy;        // bf16 queries in f16, times a power of two a row, and what the rows' scores are scaled by; null: they stay
     float* units;

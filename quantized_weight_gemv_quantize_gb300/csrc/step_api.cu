@@ -600,7 +600,7 @@ static int run_attn(const qgemv_attn_args* a, unsigned flags, void* stream) {
     if (bits && p.tiles) {
         CacheUnpackArgs u = {};
         u.a = k, u.k = static_cast<const uint8_t*>(c.k), u.v = static_cast<const uint8_t*>(c.v);
-        u.page_size = part_of_page(128);
+        u.page_size = part_of_page(128), u.page_shift = log2_of(u.page_size);
         u.per_seq = (static_cast<long long>(reach) + u.page_size - 1) / u.page_size;
         const size_t rows = static_cast<size_t>(u.per_seq) * a->seqs * u.page_size, bytes = rows * c.heads * c.dim * 2;
         auto after = [](void* p, size_t n) { return static_cast<void*>(static_cast<uint8_t*>(p) + (n + 255) / 256 * 256); };
