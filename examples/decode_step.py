@@ -4,7 +4,7 @@ cache, o GEMV, lm_head GEMV, sampling; captured as one CUDA graph and replayed.
 The "model" is one attention sublayer of the 0.6b-class shapes (16 query and 8 key/value heads of 128) between an embedding and
 an lm_head, with random weights: it shows the calls, their order and their buffers, not a language.
 
-    python examples/decode_step.py [--seqs 4] [--prompt 100] [--steps 32]
+    python examples/decode_step.py [--seqs 4] [--prompt 100] [--steps 32] [--cache bf16|Q8|Q4]
 """
 import argparse
 import os
@@ -24,7 +24,7 @@ HIDDEN, HEADS, KV_HEADS, DIM, VOCAB, PAGE = 1024, 16, 8, 128, 151936, 32
 class Decoder:
     """Weights, cache and buffers of `seqs` sequences of at most `longest` tokens.  seqs * new <= 16: the GEMVs' rows."""
 
-    def __init__(self, seqs, longest, seed=0):
+    def __init__(self, seqs, longest, seed=0, kind="bf16"):
         def weight(fmt, n, k, tag):
             return torch.from_numpy(gen.weights(fmt, n, k, gen.derive(seed, tag))).cuda()
 
@@ -35,14 +35,16 @@ class Decoder:
         g.manual_seed(seed)
         self.embedding = torch.randn(VOCAB, HIDDEN, generator=g, device="cuda")
         pages = -(-longest // PAGE)
-        self.k_cache = torch.zeros(seqs * pages, PAGE, KV_HEADS, DIM, dtype=torch.bfloat16, device="cuda")
+        packed = kind != "bf16"
+        row = (qg.qgemv_cache_row_bytes(kind, DIM), torch.uint8) if packed else (DIM, torch.bfloat16)
+        self.k_cache = torch.zeros(seqs * pages, PAGE, KV_HEADS, row[0], dtype=row[1], device="cuda")
         self.v_cache = torch.zeros_like(self.k_cache)
-        self.cache = qg.kv_cache(self.k_cache, self.v_cache)
+        self.cache = qg.packed_cache(kind, self.k_cache, self.v_cache, DIM) if packed else qg.kv_cache(self.k_cache, self.v_cache)
         self.table = torch.randperm(seqs * pages, generator=g, device="cuda").to(torch.int32).view(seqs, pages)
         freqs, self.mscale = qg.qgemv_rope_freqs(DIM, 1e6)
         self.freqs = freqs.cuda()
         self.kv_len = torch.zeros(seqs, dtype=torch.int32, device="cuda")
-        need = qg.qgemv_attn_scratch_bytes(seqs, 16, HEADS, KV_HEADS, DIM, 16 // seqs, longest)  # of every smaller call too
+        need = qg.qgemv_attn_scratch_bytes(seqs, 16, HEADS, KV_HEADS, DIM, 16 // seqs, longest, self.cache)  # of every smaller call too
         self.scratch = torch.zeros(need, dtype=torch.uint8, device="cuda")
         self.buffers = {}
 
@@ -111,9 +113,9 @@ class Decoder:
         qg.qgemv_sample(self.logits, *self.settings, self.u, self.token, self.prob, flags)
 
 
-def generate(seqs, prompt, steps, seed=0, graph=True):
+def generate(seqs, prompt, steps, seed=0, graph=True, kind="bf16"):
     """The sampled tokens [steps, seqs], their probabilities, and the time of a step in microseconds."""
-    d = Decoder(seqs, prompt + steps, seed)
+    d = Decoder(seqs, prompt + steps, seed, kind)
     d.sampler()
     g = torch.Generator(device="cuda")
     g.manual_seed(seed + 1)
@@ -146,11 +148,12 @@ if __name__ == "__main__":
     p.add_argument("--seqs", type=int, default=4)
     p.add_argument("--prompt", type=int, default=100)
     p.add_argument("--steps", type=int, default=32)
+    p.add_argument("--cache", choices=("bf16", "Q8", "Q4"), default="bf16")
     a = p.parse_args()
     if not 1 <= a.seqs <= 16 or a.prompt < 1 or a.steps < 1:
         p.error("1 to 16 sequences, at least one token and one step")
     qg.build()
     for graph in (False, True):
-        out, prob, us = generate(a.seqs, a.prompt, a.steps, graph=graph)
+        out, prob, us = generate(a.seqs, a.prompt, a.steps, graph=graph, kind=a.cache)
         print(f"{'one graph a step' if graph else 'call by call'}: {us:.1f} us a step; sequence 0: {out[:8, 0].tolist()} ...")
     sys.exit(1 if qg.qgemv_device_error() else 0)

@@ -368,8 +368,9 @@ QGEMV_API int qgemv_plan_info_chunk(int fmt, int m, int N, int Kc, int num_sms, 
  * 1 = whenever they fit, 2 = never.  Rows are bit-identical either way. */
 QGEMV_API void qgemv_tune_pairs(int mode);
 
-/* Tuning hook: qgemv_attn's kernel, 0 = planner decides, 1 = the 16-row kernel, 2 = the 128-row kernel (heads of up to 128).  It
- * also decides what qgemv_attn_scratch_bytes says. */
+/* Tuning hook: qgemv_attn's kernel, 0 = planner decides, 1 = the 16-row kernel (over a packed cache its own kernel), 2 = the 128-row
+ * kernel (heads of up to 128; over a packed cache with the copy before it).  It also decides what qgemv_attn_scratch_bytes and
+ * qgemv_attn_scratch_bytes_ex say. */
 QGEMV_API void qgemv_tune_attn(int kernel);
 
 QGEMV_API void qgemv_tune_override(int ctas_per_sm, int lanes_log2, int rows_per_tile, int stages,
@@ -445,7 +446,8 @@ typedef struct {
  * A block of values x, each clamped to +-65504 first, is written as follows, with L = 15 or 255, every operation rounded to fp32:
  *     m = the largest fp16 <= min x;   d = the smallest fp16 >= (max x - m) / L;   r = 1 / d;
  *     c = min(L, rint((x - m) * r))   (ties to even; 0 where d = 0)
- * so a value is off by at most d/2 (1 + 2^-12).  A block with a NaN is written as m = NaN, d = 0.
+ * so a value is off by at most d/2 (1 + 2^-12).  A block with a NaN is written as m = NaN, d = 0.  (A block that reaches up to 65504 may
+ * stand for more than that by 2^-10 of its range, which may be +inf where it is read back to fp16.)
  */
 #define QGEMV_CACHE_Q4 4
 #define QGEMV_CACHE_Q8 8
@@ -492,7 +494,8 @@ QGEMV_API int qgemv_rope_freqs(int rot_dim, double theta, int scaling, double fa
  * q [tokens, heads, dim], k and v [tokens, kv_heads, dim], of kind x_kind (QGEMV_ACT_F32: a GEMV's output, e.g. three
  * slices of one qkv row; QGEMV_ACT_BF16; QGEMV_ACT_F16), the last dimension contiguous, token and head strides in elements.
  * q_out [tokens, heads, dim] and k_out [tokens, kv_heads, dim]: QGEMV_ACT_BF16 / QGEMV_ACT_F16 / QGEMV_ACT_F32 by
- * out_kind.  cache (may be NULL): rotated keys and the values go to slot slots[t] of it (of the cache's kind); a
+ * out_kind.  cache (may be NULL): rotated keys and the values go to slot slots[t] of it (rounded once to the cache's kind, or packed
+ * as above from the fp32 results); a
  * negative slot writes nothing (a padding token).  A slot beyond the cache writes nothing and sets
  * QGEMV_DEVERR_BAD_INDEX in the device error word.  Slots that are >= 0 must differ: two tokens with one slot leave
  * unspecified values there.
@@ -578,7 +581,12 @@ QGEMV_API int qgemv_cache_read(const qgemv_cache_read_args* args, unsigned flags
  * once, unnormalised, their sum taken before the rounding; with f16, those below 2^-29 of the row's largest, or 2^-21 in the 128-row
  * kernel, have fewer bits, and none below 2^-40 or 2^-32); out is rounded once.
  *
- * kind (QGEMV_ACT_BF16 / QGEMV_ACT_F16): type of q and out, and the cache's.  q, out [tokens, heads, cache->dim], last
+ * Over a packed cache (QGEMV_CACHE_Q4 / QGEMV_CACHE_Q8) k_t and v_t are the values d * c + m, and q and out are of either type.  Few rows a
+ * sequence read the codes themselves.  q then counts in f16 times a power of two of its own row: 11 bits (bf16: all 8) for elements down to 2^-19 of
+ * the row's largest, an error of 2^-30 of that below.  The probabilities keep 11 bits for bf16 results and about 20 for f16 ones, those below
+ * 2^-24 of the row's largest fewer.  Many rows read a copy of the contexts in f16 (11 bits, held to +-65504), which the call makes in
+ * the scratch, and the probabilities are rounded as f16's above.
+ * kind (QGEMV_ACT_BF16 / QGEMV_ACT_F16): type of q and out, and the cache's unless that is packed.  q, out [tokens, heads, cache->dim], last
  * dimension contiguous, 16-byte aligned, strides multiples of 8 elements.  lse: fp32 [tokens, heads] or NULL.
  * max_q, max_kv (at most 2^30): bounds of n_b and kv_len[b] over the batch, for the choice of kernel and its launch; the
  * values on the device must keep to them: tokens beyond max_q are left unwritten, context beyond max_kv or beyond the
@@ -586,8 +594,8 @@ QGEMV_API int qgemv_cache_read(const qgemv_cache_read_args* args, unsigned flags
  * were masked and sets QGEMV_DEVERR_BAD_INDEX in the device error word.
  * What lies in the cache beyond kv_len, or before the window of a sequence's first new token, is never used, whatever its bits, and the
  * pages that lie there wholly are not looked up (their entries may be anything).  Keys and values that some token of the call sees must
- * be finite.
- * scratch: at least qgemv_attn_scratch_bytes(...) bytes, 16-byte aligned, whose first QGEMV_ATTN_SCRATCH_HEAD bytes must be
+ * be finite, as must the steps and bases of a packed cache there.
+ * scratch: at least qgemv_attn_scratch_bytes(...) bytes (qgemv_attn_scratch_bytes_ex where the cache is packed), 16-byte aligned, whose first QGEMV_ATTN_SCRATCH_HEAD bytes must be
  * zero before the first call (e.g. cudaMemset once); each call leaves them zero again, so calls of any sizes may share one
  * scratch that is large enough for each: that of the largest sizes is (see below).  Calls that share a scratch must be ordered.
  * The result does not depend on timing: parts of a long context are joined in a fixed order.
@@ -617,8 +625,8 @@ QGEMV_API int qgemv_attn(const qgemv_attn_args* args, unsigned flags, void* stre
  * sizes).  It never falls as a size grows.  No device needed. */
 #define QGEMV_ATTN_SCRATCH_HEAD 65536
 QGEMV_API size_t qgemv_attn_scratch_bytes(int seqs, int tokens, int heads, int kv_heads, int dim, int max_q, int max_kv);
-/* The same for a cache of the given kind.  Over a packed one, calls that are served better by the 128-row kernel (many new tokens) read a 16-bit
- * copy of their contexts, which is made in the scratch: seqs * (max_kv + 128) rows of it, where a call's sizes allow such. */
+/* The same for a cache of the given kind.  Over a packed one, calls that are served better by the 128-row kernel (many new tokens) read a copy of
+ * their contexts in f16, which is made in the scratch: up to seqs * (max_kv + 128) tokens of it, where a call's sizes allow such. */
 QGEMV_API size_t qgemv_attn_scratch_bytes_ex(int cache_kind, int seqs, int tokens, int heads, int kv_heads, int dim, int max_q, int max_kv);
 
 /*
