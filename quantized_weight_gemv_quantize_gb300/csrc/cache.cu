@@ -4,10 +4,12 @@
 // kept over the tokens of a block; the tokens' places in the cache are looked up once a block, into shared memory.
 //
 // Both are bound by memory for long runs, with the arithmetic of a value close behind (issue slots 70% taken), and by their launch for short ones.  8
-// heads of 128 (us; bytes at a copy's rate in brackets): 16000 tokens written in 4 bits from bf16 27 (12.6), from fp32 37 (22), in 8 bits 29 (15); read back
-// to bf16 18.7 (12.6); 100003 tokens read to bf16 97 (79), in 8 bits 109 (89); one token either way 7, of which 5 are the caller's.  Steps on the way: with the
-// values converted as they came and one token a thread in flight 55.7 and 31; values packed until they are stored, four tokens in flight and the codes'
-// arithmetic as in put8 27 and 20.6; codes made floats where they stand (Packed8) 18.7.
+// heads of 128 (us; bytes at a copy's rate in brackets): 16000 tokens written in 4 bits from bf16 24.8 (12.6), from fp32 29 (22), in 8 bits 25 (15); read back
+// to bf16 18.8 (12.6); 100003 tokens read to bf16 97 (79), in 8 bits 109 (89); one token either way 7, of which 5 are the caller's.  Steps on the way, writing
+// and reading 16000: values converted as they came, one token a thread in flight 55.7 and 31; values packed until they are stored, four tokens
+// in flight, the codes' arithmetic as in codes8 27 and 20.6; codes made floats where they stand (Packed8) 18.8; a block's step and base found once, not
+// by each of its four lanes, 24.8.  Blocks of 128 threads write as fast or faster than ones of 256 (fp32 29 for 33) and read 16000 tokens slower (20.7), long
+// runs a little faster (8 bits 105).
 #include "attn.cuh"
 #include "cache_rows.cuh"
 
@@ -17,18 +19,18 @@ namespace qg {
 // token are a multiple of 8, so that a block of 32 elements stays with four neighbouring lanes.)
 struct Lay {
     int wide, at, deep, row;  // this thread: pieces at, at + wide, ... of the block's tokens row, row + deep, ...
-    __device__ __forceinline__ Lay(int pieces) {
-        wide = min(pieces, CACHE_THREADS);
-        deep = CACHE_THREADS / wide;
+    __device__ __forceinline__ Lay(int pieces, int threads) {
+        wide = min(pieces, threads);
+        deep = threads / wide;
         at = threadIdx.x % wide, row = threadIdx.x / wide;
     }
 };
 
-// Four tokens' loads of a thread are on their way at once.
+// Four tokens' loads of a thread are on their way at once, as many as lanes share a block of 32 elements.
 constexpr int AHEAD = 4;
 
 template <int BITS, int XK>
-__global__ void __launch_bounds__(CACHE_THREADS) cache_write_kernel(const CacheWriteArgs a) {
+__global__ void __launch_bounds__(WRITE_THREADS) cache_write_kernel(const CacheWriteArgs a) {
     __shared__ long long ks[CACHE_TOKENS], vs[CACHE_TOKENS];
     pdl_launch_dependents();
     pdl_wait();
@@ -47,8 +49,9 @@ __global__ void __launch_bounds__(CACHE_THREADS) cache_write_kernel(const CacheW
     }
     __syncthreads();
     const int per_head = a.dim / 8, half = a.heads * per_head;
-    const Lay lay(2 * half);
+    const Lay lay(2 * half, WRITE_THREADS);
     if (lay.row >= lay.deep) return;  // (threads beyond the last whole token)
+    const unsigned team = 0xFu << (threadIdx.x & 28);
     for (int p = lay.at; p < 2 * half; p += lay.wide) {
         const bool is_v = p >= half;
         const int h = (is_v ? p - half : p) / per_head, e = (p - (is_v ? half : 0) - h * per_head) * 8;
@@ -57,26 +60,47 @@ __global__ void __launch_bounds__(CACHE_THREADS) cache_write_kernel(const CacheW
         uint8_t* rows = static_cast<uint8_t*>(is_v ? a.v_cache : a.k_cache) + (is_v ? a.vc_head : a.kc_head) * h;
         const long long* place = is_v ? vs : ks;
         for (int t0 = lay.row; t0 < n; t0 += lay.deep * AHEAD) {
-            Raw8<XK> v[AHEAD];
+            Raw8<XK> v[AHEAD] = {};
+            long long to[AHEAD];
 #pragma unroll
             for (int j = 0; j < AHEAD; ++j) {
                 const int t = t0 + j * lay.deep;
-                if (t < n && place[t] >= 0) v[j].load(x, (first + t) * token_step + src);
+                to[j] = t < n ? place[t] : -1;
+                if (to[j] >= 0) v[j].load(x, (first + t) * token_step + src);
             }
+            float lo[AHEAD], hi[AHEAD], w[8];
 #pragma unroll
             for (int j = 0; j < AHEAD; ++j) {
-                const int t = t0 + j * lay.deep;
-                if (t >= n || place[t] < 0) continue;
-                float w[8];
                 v[j].values(w);
-                put8<BITS>(rows + place[t], a.dim, e, w);
+                ends8(w, lo[j], hi[j]);
+            }
+            // The four lanes of a block of 32 have a token each: its ends from the others, its step and base for them.
+#pragma unroll
+            for (int half = 2; half; half /= 2) {
+#pragma unroll
+                for (int i = 0; i < half; ++i) {
+                    const bool upper = threadIdx.x & half;
+                    const float lo_in = __shfl_xor_sync(team, upper ? lo[i] : lo[i + half], half), lo_own = upper ? lo[i + half] : lo[i];
+                    const float hi_in = __shfl_xor_sync(team, upper ? hi[i] : hi[i + half], half), hi_own = upper ? hi[i + half] : hi[i];
+                    lo[i] = fminf(lo_own, lo_in), hi[i] = max_or_nan(hi_own, hi_in);
+                }
+            }
+            const BlockScale<BITS> s(lo[0], hi[0]);
+            const long long own = threadIdx.x & 2 ? (threadIdx.x & 1 ? to[3] : to[2]) : (threadIdx.x & 1 ? to[1] : to[0]);
+            if (own >= 0) s.put(rows + own, a.dim, e);
+#pragma unroll
+            for (int j = 0; j < AHEAD; ++j) {
+                const float m = __shfl_sync(team, s.m, j, 4), rate = __shfl_sync(team, s.rate, j, 4);
+                if (to[j] < 0) continue;
+                v[j].values(w);
+                codes8<BITS>(rows + to[j], e, w, m, rate);
             }
         }
     }
 }
 
 template <int BITS>
-__global__ void __launch_bounds__(CACHE_THREADS) cache_read_kernel(const CacheReadArgs a) {
+__global__ void __launch_bounds__(READ_THREADS) cache_read_kernel(const CacheReadArgs a) {
     __shared__ long long ks[CACHE_TOKENS], vs[CACHE_TOKENS];  // place of a row in the cache, -1: zeros, -2: not a row of any sequence
     pdl_launch_dependents();
     pdl_wait();
@@ -108,7 +132,7 @@ __global__ void __launch_bounds__(CACHE_THREADS) cache_read_kernel(const CacheRe
     __syncthreads();
     const int per_head = a.dim / 8, half = a.heads * per_head;
     const int pieces = half * ((a.k_out ? 1 : 0) + (a.v_out ? 1 : 0));
-    const Lay lay(pieces);
+    const Lay lay(pieces, READ_THREADS);
     if (lay.row >= lay.deep) return;
     for (int p = lay.at; p < pieces; p += lay.wide) {
         const bool is_v = !a.k_out || p >= half;
@@ -146,7 +170,7 @@ __global__ void __launch_bounds__(CACHE_THREADS) cache_read_kernel(const CacheRe
 // the result (0.0076 of it against 0.0017).  bf16 queries are taken along: in f16, times the power of two that brings the row's largest element to
 // [2^9, 2^10), so that elements down to 2^-23 of it keep their 8 bits.
 template <int BITS>
-__global__ void __launch_bounds__(CACHE_THREADS) cache_unpack_kernel(const CacheUnpackArgs u) {
+__global__ void __launch_bounds__(READ_THREADS) cache_unpack_kernel(const CacheUnpackArgs u) {
     __shared__ long long ks[CACHE_TOKENS], vs[CACHE_TOKENS];
     const AttnArgs& a = u.a;
     pdl_launch_dependents();
@@ -156,7 +180,7 @@ __global__ void __launch_bounds__(CACHE_THREADS) cache_unpack_kernel(const Cache
     if (static_cast<int>(blockIdx.x) >= u.key_blocks) {  // a warp a row of dim elements, up to 128
         const int j0 = (static_cast<int>(blockIdx.x) - u.key_blocks) * UNPACK_QUERIES, rows = min(UNPACK_QUERIES, s.n - j0) * a.heads;
         const int lane = threadIdx.x % 32, e = 4 * lane;
-        for (int i = threadIdx.x / 32; i < rows; i += CACHE_THREADS / 32) {
+        for (int i = threadIdx.x / 32; i < rows; i += READ_THREADS / 32) {
             const long long tok = s.q0 + j0 + i / a.heads;
             const int h = i % a.heads;
             uint2 w = make_uint2(0u, 0u);
@@ -193,7 +217,7 @@ __global__ void __launch_bounds__(CACHE_THREADS) cache_unpack_kernel(const Cache
     }
     __syncthreads();
     const int per_head = a.dim / 8, half = a.kv_heads * per_head;
-    const Lay lay(2 * half);
+    const Lay lay(2 * half, READ_THREADS);
     if (lay.row >= lay.deep) return;
     for (int p = lay.at; p < 2 * half; p += lay.wide) {
         const bool is_v = p >= half;

@@ -73,37 +73,49 @@ __device__ __forceinline__ float max_or_nan(float a, float b) {
     return y;
 }
 
-// Elements e .. e + 7 (e a multiple of 8) of a row of `dim`.  Four consecutive lanes, the first at a multiple of 4, hold a block: they
-// find its least and largest value together, and each writes its own codes.  All four call this, with the same `row`.
+// The step and base of a block by its least and largest value (NaN where one is).
 //
 // The base is rounded down and the step up, so that every value lies within the codes: none is cut off by more than the rounding of
 // the fp32 arithmetic.  The product with 1 / d stands for the quotient (one instruction an element instead of eight); it moves a code by
-// one only where the value lies within 2^-14 steps of the middle of two.  Values beyond +-65504 need no clamp of their own: the block's ends are
-// clamped, and the codes to 0 .. L.  A code comes out of the low bits of t + 1.5 2^23, which rounds t to a whole number, ties to even; the
-// sum of those words times powers of two packs the codes, with the words' upper bits taken off at once.
+// one only where the value lies within 2^-14 steps of the middle of two.
 template <int BITS>
-__device__ __forceinline__ void put8(uint8_t* row, int dim, int e, const float (&x)[8]) {
-    constexpr float TOP = (1 << BITS) - 1;
-    const unsigned team = 0xFu << (threadIdx.x & 28);
-    float lo = x[0], hi = x[0];
+struct BlockScale {
+    static constexpr float TOP = (1 << BITS) - 1;
+    float m, rate;
+    uint16_t d16, m16;
+    __device__ __forceinline__ BlockScale(float lo, float hi) {
+        const bool nan = hi != hi;
+        lo = fminf(fmaxf(lo, -65504.f), 65504.f), hi = fminf(fmaxf(hi, -65504.f), 65504.f);
+        const __half mh = __float2half_rd(lo);
+        m = __half2float(mh);
+        __half d = __float2half_ru(__fdiv_rn(__fsub_rn(hi, m), TOP));
+        if (nan) d = __ushort_as_half(0);
+        const float df = __half2float(d);
+        rate = df == 0.f ? 0.f : __frcp_rn(df);
+        d16 = __half_as_ushort(d), m16 = nan ? 0x7E00 : __half_as_ushort(mh);
+    }
+    // at element e of a row
+    __device__ __forceinline__ void put(uint8_t* row, int dim, int e) const {
+        uint16_t* scale = reinterpret_cast<uint16_t*>(row + dim * BITS / 8);
+        scale[e / 32] = d16, scale[dim / 32 + e / 32] = m16;
+    }
+};
+
+__device__ __forceinline__ void ends8(const float (&x)[8], float& lo, float& hi) {
+    lo = hi = x[0];
 #pragma unroll
     for (int j = 1; j < 8; ++j) lo = fminf(lo, x[j]), hi = max_or_nan(hi, x[j]);
-#pragma unroll
-    for (int o = 1; o < 4; o *= 2) {
-        lo = fminf(lo, __shfl_xor_sync(team, lo, o));
-        hi = max_or_nan(hi, __shfl_xor_sync(team, hi, o));
-    }
-    const bool nan = hi != hi;
-    lo = fminf(fmaxf(lo, -65504.f), 65504.f), hi = fminf(fmaxf(hi, -65504.f), 65504.f);
-    const __half m = __float2half_rd(lo);
-    const float mf = __half2float(m);
-    __half d = __float2half_ru(__fdiv_rn(__fsub_rn(hi, mf), TOP));
-    if (nan) d = __ushort_as_half(0);
-    const float df = __half2float(d), rate = df == 0.f ? 0.f : __frcp_rn(df);
+}
+
+// The codes of 8 values, for element e.  Values beyond +-65504 need no clamp of their own: the block's ends are clamped, and the codes
+// to 0 .. L.  A code comes out of the low bits of t + 1.5 2^23, which rounds t to a whole number, ties to even; the
+// sum of those words times powers of two packs the codes, with the words' upper bits taken off at once.
+template <int BITS>
+__device__ __forceinline__ void codes8(uint8_t* row, int e, const float (&x)[8], float m, float rate) {
     uint32_t c[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const float t = fminf(fmaxf(__fmul_rn(__fsub_rn(x[j], mf), rate), 0.f), TOP);
+        const float t = fminf(fmaxf(__fmul_rn(__fsub_rn(x[j], m), rate), 0.f), BlockScale<BITS>::TOP);
         c[j] = __float_as_uint(__fadd_rn(t, 12582912.f));  // 0x4B400000 + code
     }
     constexpr uint32_t BIAS = 0x4B400000u;
@@ -119,11 +131,23 @@ __device__ __forceinline__ void put8(uint8_t* row, int dim, int e, const float (
             w[j] = c[4 * j] + c[4 * j + 1] * (1u << 8) + c[4 * j + 2] * (1u << 16) + c[4 * j + 3] * (1u << 24) - BIAS * 0x01010101u;
         *reinterpret_cast<uint2*>(row + e) = make_uint2(w[0], w[1]);
     }
-    if (e % 32 == 0) {
-        __half* scale = reinterpret_cast<__half*>(row + dim * BITS / 8);
-        scale[e / 32] = d;
-        scale[dim / 32 + e / 32] = nan ? __ushort_as_half(0x7E00) : m;
+}
+
+// Elements e .. e + 7 (e a multiple of 8) of a row of `dim`.  Four consecutive lanes, the first at a multiple of 4, hold a block: they
+// find its least and largest value together, and each writes its own codes.  All four call this, with the same `row`.
+template <int BITS>
+__device__ __forceinline__ void put8(uint8_t* row, int dim, int e, const float (&x)[8]) {
+    const unsigned team = 0xFu << (threadIdx.x & 28);
+    float lo, hi;
+    ends8(x, lo, hi);
+#pragma unroll
+    for (int o = 1; o < 4; o *= 2) {
+        lo = fminf(lo, __shfl_xor_sync(team, lo, o));
+        hi = max_or_nan(hi, __shfl_xor_sync(team, hi, o));
     }
+    const BlockScale<BITS> s(lo, hi);
+    codes8<BITS>(row, e, x, s.m, s.rate);
+    if (e % 32 == 0) s.put(row, dim, e);
 }
 
 // Elements e .. e + 7 of a row as they lie there, and their values.  The places of the codes, the step and the base within a row are a thread's own.

@@ -12,7 +12,9 @@ namespace qg {
 // took 89.4, streaming loads changed nothing (69.7).  24 blocks an SM (40 registers): with more registers 81.8 us, with 32 spilled ones 70.0; interleaved pairs need no more than 32.
 //
 // With a packed cache (PACKED) the block takes its keys and values in a pass of their own, by blocks of 32 elements: four lanes turn 8 elements each
-// (a key's partner elements are read again, from L1) and pack them together.
+// (a key's partner elements are read again, from L1) and pack them together.  16000 tokens as above, us, 8 bits and 4 bits with the bytes at a copy's rate in
+// brackets: bf16 74 (54) and 74 (51), interleaved 76 and 75, fp32 92 (83) and 90 (80), interleaved 88 and 86.  As many blocks an SM as without:
+// with 16 88, with 20 80 (half); 28 and more spill there (77).
 //
 // One block serves one token (blockIdx.x) and every gridDim.y-th group of its pieces.  A piece of a query or key head is
 // 8 pairs (half layout: 8 elements and their 8 partners), 4 pairs (interleaved: 8 elements) or 8 elements that are copied;
@@ -68,7 +70,7 @@ __device__ __forceinline__ void pack_token(const RopeArgs& a, const float2* cs, 
 }
 
 template <int XK, bool HALF, bool VEC, bool PACKED>
-__global__ void __launch_bounds__(ROPE_THREADS, HALF && VEC && !PACKED ? 24 : PACKED ? 16 : 32) rope_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(ROPE_THREADS, HALF && VEC || PACKED && !VEC ? 24 : 32) rope_kernel(const RopeArgs a) {
     __shared__ float2 cs[128];
     pdl_launch_dependents();
     pdl_wait();

@@ -58,7 +58,7 @@ struct CacheReadArgs {
     int block_tokens;
 };
 
-constexpr int CACHE_THREADS = 256, CACHE_TOKENS = 32;
+constexpr int WRITE_THREADS = 128, READ_THREADS = 256, CACHE_TOKENS = 32;
 const void* cache_write_kernel_ptr(int bits, int x_kind);
 const void* cache_read_kernel_ptr(int bits);
 

@@ -197,8 +197,8 @@ static int run_rope(const qgemv_rope_args* a, unsigned flags, void* stream) {
 // -------------------------------------------------------------------------------- writing and reading a packed cache
 
 // Tokens of a block: enough for a few passes of its threads over their pieces, fewer where the blocks would not fill the GPU.
-static int tokens_a_block(long long tokens, int sms, long long pieces) {
-    const long long few = (tokens + 4ll * sms - 1) / (4ll * sms), most = pieces < CACHE_THREADS ? CACHE_TOKENS : 16;
+static int tokens_a_block(long long tokens, int sms, long long pieces, int threads) {
+    const long long few = (tokens + 4ll * sms - 1) / (4ll * sms), most = pieces < threads ? CACHE_TOKENS : 16;
     return static_cast<int>(few < 1 ? 1 : few > most ? most : few);
 }
 
@@ -235,10 +235,10 @@ static int run_cache_write(const qgemv_cache_write_args* a, unsigned flags, void
     w.vc_page = c.v_page, w.vc_token = c.v_token, w.vc_head = c.v_head;
     w.slots = a->slots, w.err = err, w.num_slots = static_cast<long long>(c.num_pages) * c.page_size;
     w.tokens = a->tokens, w.heads = c.heads, w.dim = c.dim, w.page_size = c.page_size, w.page_shift = log2_of(c.page_size);
-    w.block_tokens = tokens_a_block(a->tokens, sms, 2ll * c.heads * c.dim / 8);
+    w.block_tokens = tokens_a_block(a->tokens, sms, 2ll * c.heads * c.dim / 8, WRITE_THREADS);
     const bool pdl = (flags & QGEMV_FLAG_PDL) != 0;
     const unsigned blocks = static_cast<unsigned>((a->tokens + static_cast<long long>(w.block_tokens) - 1) / w.block_tokens);
-    cudaError_t e = launch_step(cache_write_kernel_ptr(bits, a->x_kind), dim3(blocks), CACHE_THREADS, 0, 1, pdl,
+    cudaError_t e = launch_step(cache_write_kernel_ptr(bits, a->x_kind), dim3(blocks), WRITE_THREADS, 0, 1, pdl,
                                 static_cast<cudaStream_t>(stream), w);
     if (e != cudaSuccess) return api_cuda_fail(e);
     api_route(QGEMV_ROUTE_CACHE_WRITE, pdl);
@@ -292,10 +292,10 @@ static int run_cache_read(const qgemv_cache_read_args* a, unsigned flags, void* 
     r.out_kind = a->out_kind, r.tokens = a->tokens, r.seqs = a->seqs, r.num_pages = c.num_pages;
     r.heads = c.heads, r.dim = c.dim, r.page_size = c.page_size, r.page_shift = log2_of(c.page_size);
     r.reach = a->pages_stride < most ? a->pages_stride * c.page_size : a->max_kv;
-    r.block_tokens = tokens_a_block(a->tokens, sms, ((a->k_out ? 1 : 0) + (a->v_out ? 1 : 0)) * static_cast<long long>(c.heads) * c.dim / 8);
+    r.block_tokens = tokens_a_block(a->tokens, sms, ((a->k_out ? 1 : 0) + (a->v_out ? 1 : 0)) * static_cast<long long>(c.heads) * c.dim / 8, READ_THREADS);
     const bool pdl = (flags & QGEMV_FLAG_PDL) != 0;
     const unsigned blocks = static_cast<unsigned>((a->tokens + static_cast<long long>(r.block_tokens) - 1) / r.block_tokens);
-    cudaError_t e = launch_step(cache_read_kernel_ptr(bits), dim3(blocks), CACHE_THREADS, 0, 1, pdl, static_cast<cudaStream_t>(stream), r);
+    cudaError_t e = launch_step(cache_read_kernel_ptr(bits), dim3(blocks), READ_THREADS, 0, 1, pdl, static_cast<cudaStream_t>(stream), r);
     if (e != cudaSuccess) return api_cuda_fail(e);
     api_route(QGEMV_ROUTE_CACHE_READ, pdl);
     return QGEMV_OK;
@@ -617,7 +617,7 @@ static int run_attn(const qgemv_attn_args* a, unsigned flags, void* stream) {
             k.q = u.q_copy, k.q_token = static_cast<long long>(a->heads) * c.dim, k.q_head = c.dim, k.units = u.units;
         }
         if (blocks > 0) {
-            e = launch_step(cache_unpack_kernel_ptr(bits), dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(a->seqs)), CACHE_THREADS, 0, 1, pdl,
+            e = launch_step(cache_unpack_kernel_ptr(bits), dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(a->seqs)), READ_THREADS, 0, 1, pdl,
                             static_cast<cudaStream_t>(stream), u);
             if (e != cudaSuccess) return api_cuda_fail(e);
             chained = true;
