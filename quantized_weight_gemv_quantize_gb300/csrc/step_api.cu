@@ -323,13 +323,13 @@ static int rows_grid(int dim) { return dim <= 128 ? 2 * SMS : SMS; }
 static size_t scratch_of(size_t records, int dim) {
     return QGEMV_ATTN_SCRATCH_HEAD + round32(records * sizeof(float2)) + records * dim * sizeof(float);
 }
-// The copy in 16 bits of a packed cache's part that a batch sees, and its page table, for any page size (pages of the copy hold up to 128
-// tokens), and of its queries.  0: out of range.
+// The copy in f16 of a packed cache's part that a batch sees, and its page table, for any page size (pages of the copy hold up to 128
+// tokens), and of its queries, four pieces rounded up to 256 bytes each.  0: out of range.
 static size_t copy_bytes(int seqs, int tokens, int heads, int kv_heads, int dim, int max_kv) {
     const double keys = static_cast<double>(seqs) * (static_cast<double>(max_kv) + 128), rows = static_cast<double>(tokens) * heads;
     if (seqs > 65535 || keys > INT_MAX || keys * kv_heads * dim * 4 > SPAN_MAX || rows * dim * 2 > SPAN_MAX) return 0;
     const size_t cache = static_cast<size_t>(keys) * (static_cast<size_t>(kv_heads) * dim * 4 + 4);
-    return (cache + static_cast<size_t>(rows) * (dim * 2 + 4) + 1023) / 256 * 256;
+    return (cache + static_cast<size_t>(rows) * (dim * 2 + 4) + 4 * 256 + 255) / 256 * 256;
 }
 
 static int attn_plan(int bits, bool f16, int seqs, int tokens, int heads, int kv_heads, int dim, int max_q, int max_kv, int window,
