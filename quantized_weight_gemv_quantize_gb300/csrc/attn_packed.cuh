@@ -675,11 +675,13 @@ __device__ __forceinline__ void attend_packed(const AttnPackedArgs& pa, const Ti
 }
 
 // Joins the parts of a row tile that begins in block t.index: four elements of up to four rows a thread, one pass over the parts with the maxima and
-// the sums running along, sixteen loads on their way at once.
+// the sums running along.  Eight parts of one row, or four of four, are on their way at once, what is left by twos: more (16, or copies into the ring
+// as far ahead as it has room) took longer, since few blocks join and none has this code at hand (one of 100003: 8 42.0 us, 16 44.1; 25000
+// 19.5 and 21.1; all of 16 before any is used 51.7).
 template <int DP, int BITS, int NT, int ITEMS>
 __device__ __forceinline__ void join_packed(const AttnPackedArgs& pa, const Tile& t) {
     using S = PackedShape<DP, BITS, NT>;
-    constexpr int AT_ONCE = S::WARPS * 32 / (DP / 4);
+    constexpr int AT_ONCE = S::WARPS * 32 / (DP / 4), PARTS = ITEMS == 1 ? 8 : 16 / ITEMS;
     const AttnArgs& a = pa.a;
     const int d = threadIdx.x % (DP / 4) * 4, rows = t.rows << pa.hb_shift;
     if (d >= a.dim) return;
@@ -695,8 +697,7 @@ __device__ __forceinline__ void join_packed(const AttnPackedArgs& pa, const Tile
             const int hr = min(first + k * AT_ONCE, rows - 1), hh = hr / t.rows;  // (rows past the last one read its record)
             rec[k] = static_cast<int>(2 * t.index * S::WARPS + hh) * S::ROWS + hr - hh * t.rows;
         }
-#pragma unroll(16 / ITEMS)
-        for (int p = 0; p < t.parts; ++p) {
+        auto take = [&](int p) {
             const int part = (2 * p + (p == 0 ? 1 : 0)) * S::WARPS * S::ROWS;
 #pragma unroll
             for (int k = 0; k < ITEMS; ++k) {
@@ -710,7 +711,20 @@ __device__ __forceinline__ void join_packed(const AttnPackedArgs& pa, const Tile
                 x[k].x = x[k].x * keep + w * v.x, x[k].y = x[k].y * keep + w * v.y;
                 x[k].z = x[k].z * keep + w * v.z, x[k].w = x[k].w * keep + w * v.w;
             }
+        };
+        int p = 0;
+#pragma unroll 1
+        for (; p + PARTS <= t.parts; p += PARTS) {
+#pragma unroll
+            for (int j = 0; j < PARTS; ++j) take(p + j);
         }
+#pragma unroll 1
+        for (; ITEMS == 1 && p + 2 <= t.parts; p += 2) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) take(p + j);
+        }
+#pragma unroll 1
+        for (; p < t.parts; ++p) take(p);
 #pragma unroll
         for (int k = 0; k < ITEMS; ++k) {
             const int hr = first + k * AT_ONCE, hh = hr / t.rows, r = hr - hh * t.rows;

@@ -673,7 +673,9 @@ static int run_attn(const qgemv_attn_args* a, unsigned flags, void* stream) {
             else if (maps({units, c.page_size, c.num_pages, c.heads}, {c.k_token, c.k_page, c.k_head}, {c.v_token, c.v_page, c.v_head}, {units, 16, 1, side}))
                 pk.copies = COPY_BOXES;
         }
-        pk.hb_shift = p.hb_shift, pk.few = p.hb_shift ? 32 : 128;
+        // A block takes at least so many keys: a round of its warps' where heads lie side by side, else one or two.  More parts are done sooner and joined
+        // later, 0.1 us a part.  One sequence, 32 and 8 heads, 128 / 256 keys, us: 1500 11.3 / 13.3, 3000 12.9 / 12.8, 6000 16.7 / 13.3, 12000 17.3 / 17.1.
+        pk.hb_shift = p.hb_shift, pk.few = p.hb_shift ? 32 : reach > 2048 && a->window == 0 ? 256 : 128;
         e = launch_step(fn, dim3(static_cast<unsigned>(p.grid)), threads, smem, 1, pdl, static_cast<cudaStream_t>(stream), pk);
     } else {
         e = launch_step(fn, dim3(static_cast<unsigned>(p.grid)), threads, smem, 1, pdl, static_cast<cudaStream_t>(stream), k);
