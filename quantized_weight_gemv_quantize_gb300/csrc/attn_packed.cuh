@@ -719,7 +719,7 @@ __device__ __forceinline__ void join_packed(const AttnPackedArgs& pa, const Tile
             for (int j = 0; j < PARTS; ++j) take(p + j);
         }
 #pragma unroll 1
-        for (; ITEMS == 1 && p + 2 <= t.parts; p += 2) {
+        for (; p + 2 <= t.parts; p += 2) {
 #pragma unroll
             for (int j = 0; j < 2; ++j) take(p + j);
         }
