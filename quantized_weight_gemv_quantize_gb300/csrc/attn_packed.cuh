@@ -183,8 +183,8 @@ __device__ __forceinline__ void attend_packed(const AttnPackedArgs& pa, const Ti
         return w;
     };
     // rows are `rp` bytes apart in a box and heads `hp`
-    const bool by_rows = pa.copies == COPY_ROWS;
-    const int rp = by_rows ? heads * pitch + 16 : pitch, hp = by_rows ? pitch : 16 * pitch;
+    const bool by_rows = pa.copies == COPY_ROWS || pa.copies == COPY_TOKENS, by_map = pa.copies < COPY_TOKENS;
+    const int rp = by_rows ? heads * pitch + (heads == S::WARPS ? 16 : 0) : pitch, hp = by_rows ? pitch : 16 * pitch;
     const int box_bytes = by_rows ? 16 * rp : heads * 16 * pitch;
     auto box_key = [&](int r, int n) { return t.k0 + r * per_round + n * 16; };
     auto box_at = [&](int n) { return n % KT * 2 * S::SIDE + n / KT * box_bytes; };
@@ -192,10 +192,10 @@ __device__ __forceinline__ void attend_packed(const AttnPackedArgs& pa, const Ti
         ring.lives[to * 16 + n] = live | (live == 0xffffu && key >= low && key + 15 <= high ? PLAIN : 0u);
     };
     Where ahead = {-1, 0};
-    if (pa.copies != COPY_EACH && warp < rounds && lane < warps * KT) ahead = look_up(box_key(warp, lane), 16);
+    if (by_map && warp < rounds && lane < warps * KT) ahead = look_up(box_key(warp, lane), 16);
     auto issue = [&](int r, int to) {
         const uint32_t bar = smem_addr(&ring.full[to]), dst = store + to * S::STAGE;
-        if (pa.copies != COPY_EACH) {
+        if (by_map) {
             const int key = box_key(r, lane), left = t.k1 - key, before = t.first - key;
             const bool there = ahead.page >= 0;
             unsigned live = there ? 0xffffu : 0u;
@@ -218,7 +218,7 @@ __device__ __forceinline__ void attend_packed(const AttnPackedArgs& pa, const Ti
             ahead.page = -1;
             if (r + S::WARPS < rounds && lane < warps * KT) ahead = look_up(box_key(r + S::WARPS, lane), 16);
         } else {
-            // row by row, 32 keys at a time: first what there is, then the copies
+            // 32 keys at a time: first what there is, then the copies, of a token's rows, of a page's or of one
             unsigned rows = 0;
 #pragma unroll 1
             for (int k = lane; k - lane < per_round; k += 32) {
@@ -233,16 +233,22 @@ __device__ __forceinline__ void attend_packed(const AttnPackedArgs& pa, const Ti
             if (lane == 0) mbar_arrive_expect_tx(bar, 2u * rows * heads * pitch);
             __syncwarp();
 #pragma unroll 1
-            for (int k = lane; k < per_round; k += 32) {
-                const Where w = look_up(box_key(r, 0) + k, 1);
-                if (w.page < 0) continue;
+            for (int k = lane; k - lane < per_round; k += 32) {
+                Where w = {-1, 0};
+                if (k < per_round) w = look_up(box_key(r, 0) + k, 1);
+                const unsigned some = __ballot_sync(0xffffffffu, w.page >= 0);
+                const bool goes_on = pa.copies == COPY_RUNS && w.token != 0 && (lane & 15) && (some >> (lane - 1) & 1u);
+                const unsigned begin = __ballot_sync(0xffffffffu, w.page >= 0 && !goes_on), cut = lane < 31 ? (begin | ~some) >> (lane + 1) : 0u;
+                if (!(begin >> lane & 1u)) continue;
+                const int n = cut ? __ffs(cut) : 32 - lane;  // keys of the run that begins here
                 const uint8_t* kp = pa.k + w.page * a.k_page + w.token * a.k_token + t.kv_head * a.k_head;
                 const uint8_t* vp = pa.v + w.page * a.v_page + w.token * a.v_token + t.kv_head * a.v_head;
-                const uint32_t at = dst + box_at(k >> 4) + (k & 15) * pitch;
+                const uint32_t at = dst + box_at(k >> 4) + (k & 15) * rp;
+                const int bytes = by_rows ? heads * pitch : n * pitch;
 #pragma unroll 1
-                for (int h = 0; h < heads; ++h) {
-                    copy_row(at + h * 16 * pitch, kp + h * a.k_head, pitch, bar);
-                    copy_row(at + S::SIDE + h * 16 * pitch, vp + h * a.v_head, pitch, bar);
+                for (int h = 0; h < (by_rows ? 1 : heads); ++h) {
+                    copy_row(at + h * hp, kp + h * a.k_head, bytes, bar);
+                    copy_row(at + S::SIDE + h * hp, vp + h * a.v_head, bytes, bar);
                 }
             }
         }

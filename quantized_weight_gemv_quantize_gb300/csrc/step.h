@@ -100,9 +100,10 @@ struct AttnTileArgs {
     AttnArgs a;
 };
 
-// How a block of the packed cache's kernel copies 16 keys of its heads: every row by itself; by a tensor map of [token][all heads' rows], where they lie
-// together; of [head][all tokens' rows], where those do; or of [head][token][row].
-enum PackedCopies { COPY_EACH, COPY_ROWS, COPY_HEADS, COPY_BOXES };
+// How a block of the packed cache's kernel copies 16 keys of its heads.  On one page: by a tensor map of [token][all heads' rows], where they lie
+// together; of [head][all tokens' rows], where those do; or of [head][token][row].  Where pages are no multiple of 16: the heads' rows of a token, where they
+// lie together; a head's rows on a page, where those do; or every row by itself.
+enum PackedCopies { COPY_ROWS, COPY_HEADS, COPY_BOXES, COPY_TOKENS, COPY_RUNS, COPY_EACH };
 
 // The packed cache's kernel: the cache's two tensor maps, in units of 8 bytes.
 struct AttnPackedArgs {

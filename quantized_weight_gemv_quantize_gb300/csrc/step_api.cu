@@ -663,6 +663,8 @@ static int run_attn(const qgemv_attn_args* a, unsigned flags, void* stream) {
         auto maps = [&](const long long (&size)[4], const long long (&ks)[3], const long long (&vs)[3], const int (&box)[4]) {
             return tensor_map(pk.k_map, c.k, c.kind, size, ks, box) && tensor_map(pk.v_map, c.v, c.kind, size, vs, box);
         };
+        const bool rows_join = side > 1 && c.k_head == pk.pitch && c.v_head == pk.pitch, tokens_join = c.k_token == pk.pitch && c.v_token == pk.pitch;
+        pk.copies = rows_join ? COPY_TOKENS : tokens_join ? COPY_RUNS : COPY_EACH;
         if (c.page_size % 16 == 0) {
             if (c.k_token == pk.pitch && c.v_token == pk.pitch && 16 * units <= 256 &&
                 maps({static_cast<long long>(c.page_size) * units, c.heads, c.num_pages, 1}, {c.k_head, c.k_page, 16}, {c.v_head, c.v_page, 16}, {16 * units, side, 1, 1}))
