@@ -53,6 +53,9 @@ struct PackedShape {
     static_assert(STAGES >= 2 && WARPS * ROWS * (LINE + 2) * 4 <= SMEM, "");
 };
 
+__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
 // (by the threads with one != 0, without a branch)
 __device__ __forceinline__ void mbar_arrive(uint32_t bar, uint32_t one) {
     asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t@q mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(bar), "r"(one) : "memory");
@@ -129,6 +132,7 @@ __device__ __forceinline__ void attend_packed(const AttnPackedArgs& pa, const Ti
     constexpr int HS = BITS == 4 ? 0 : 8;  // 8-bit codes: the odd bytes are moved down
     constexpr int KT = S::KT;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g8 = lane / 4, t4 = lane % 4;
+    const uint32_t one = lane == 0;
     const int gd = WHOLE ? G : a.dim / 32;
     const int pitch = WHOLE ? S::PITCH : pa.pitch;
     const int codes = WHOLE ? S::CODES : a.dim * BITS / 8;
@@ -218,25 +222,18 @@ __device__ __forceinline__ void attend_packed(const AttnPackedArgs& pa, const Ti
             ahead.page = -1;
             if (r + S::WARPS < rounds && lane < warps * KT) ahead = look_up(box_key(r + S::WARPS, lane), 16);
         } else {
-            // 32 keys at a time: first what there is, then the copies, of a token's rows, of a page's or of one
-            unsigned rows = 0;
+            // 32 keys at a time, the next ones looked up before their copies: of a token's rows, of a page's or of one
+            auto key_at = [&](int k) { return k < per_round ? look_up(box_key(r, 0) + k, 1) : Where{-1, 0}; };
+            Where next = key_at(lane);
 #pragma unroll 1
             for (int k = lane; k - lane < per_round; k += 32) {
-                Where w = {-1, 0};
-                if (k < per_round) w = look_up(box_key(r, 0) + k, 1);
+                const Where w = next;
+                next = key_at(k + 32);
                 const unsigned some = __ballot_sync(0xffffffffu, w.page >= 0);
-                rows += __popc(some);
-                const int n = (k - lane) / 16 + lane;
-                if (lane < 2 && n < warps * KT) put_live(to, n, box_key(r, n), some >> (16 * lane) & 0xffffu);
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive_expect_tx(bar, 2u * rows * heads * pitch);
-            __syncwarp();
-#pragma unroll 1
-            for (int k = lane; k - lane < per_round; k += 32) {
-                Where w = {-1, 0};
-                if (k < per_round) w = look_up(box_key(r, 0) + k, 1);
-                const unsigned some = __ballot_sync(0xffffffffu, w.page >= 0);
+                const int box = (k - lane) / 16 + lane;
+                if (lane < 2 && box < warps * KT) put_live(to, box, box_key(r, box), some >> (16 * lane) & 0xffffu);
+                if (lane == 0) mbar_expect_tx(bar, 2u * __popc(some) * heads * pitch);
+                __syncwarp();
                 const bool goes_on = pa.copies == COPY_RUNS && w.token != 0 && (lane & 15) && (some >> (lane - 1) & 1u);
                 const unsigned begin = __ballot_sync(0xffffffffu, w.page >= 0 && !goes_on), cut = lane < 31 ? (begin | ~some) >> (lane + 1) : 0u;
                 if (!(begin >> lane & 1u)) continue;
@@ -251,6 +248,8 @@ __device__ __forceinline__ void attend_packed(const AttnPackedArgs& pa, const Ti
                     copy_row(at + S::SIDE + h * hp, vp + h * a.v_head, bytes, bar);
                 }
             }
+            __syncwarp();  // (what is there is written)
+            mbar_arrive(bar, one);
         }
     };
     // the first rounds: their slots were read in the row tile before, which ended with a barrier
@@ -363,7 +362,6 @@ __device__ __forceinline__ void attend_packed(const AttnPackedArgs& pa, const Ti
     const uint32_t keep_k0 = 2 * t4 < 2 * gd ? 0xffffffffu : 0u;          // halves beyond a row's steps and bases are anything
     const uint32_t keep_k1 = 8 + 2 * t4 < 2 * gd ? 0xffffffffu : 0u;
     const uint32_t steps = g8 < gd ? 0x80008000u : 0u;                     // rows of the turned steps and bases that are steps
-    const uint32_t one = lane == 0;
 
     auto wait = [&](const unsigned long long& bar, unsigned phase) {
         if (mbar_try_wait(smem_addr(&bar), phase)) return true;
