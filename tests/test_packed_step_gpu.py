@@ -186,6 +186,19 @@ def test_heads_side_by_side(heads, seqs, longest, kind, order, D, page):
     assert int(s.scratch[:qg.QGEMV_ATTN_SCRATCH_HEAD].sum()) == 0
 
 
+@pytest.mark.parametrize("heads,seqs,longest", [(2, 130, 1500), (4, 80, 2500)])
+@pytest.mark.parametrize("kind,order,D,page", [("Q4", "token-head", 128, 24), ("Q4", "token-head", 96, 8), ("Q4", "token-head", 128, 1),
+                                               ("Q4", "head-token", 128, 24), ("Q8", "head-token", 64, 8), ("Q8", "head-token", 128, 7)])
+def test_heads_side_by_side_over_short_pages(heads, seqs, longest, kind, order, D, page):
+    """Pages that are no multiple of 16 tokens: a token's rows at once, a page's runs, from any place of a page."""
+    rng = np.random.default_rng(page)
+    ctx = rng.integers(longest // 2, longest, seqs).tolist()
+    s = Packed(55, kind, [1] * seqs, ctx, heads, heads, D, page, H16, order=order)
+    qg.qgemv_attn(s.args())
+    s.check()
+    assert int(s.scratch[:qg.QGEMV_ATTN_SCRATCH_HEAD].sum()) == 0
+
+
 def test_more_sequences_than_are_kept():
     rng = np.random.default_rng(3)
     ctx = rng.integers(0, 90, 1100).tolist()
