@@ -595,7 +595,8 @@ QGEMV_API int qgemv_cache_read(const qgemv_cache_read_args* args, unsigned flags
  * What lies in the cache beyond kv_len, or before the window of a sequence's first new token, is never used, whatever its bits, and the
  * pages that lie there wholly are not looked up (their entries may be anything).  Keys and values that some token of the call sees must
  * be finite, as must the steps and bases of a packed cache there.
- * scratch: at least qgemv_attn_scratch_bytes(...) bytes (qgemv_attn_scratch_bytes_ex where the cache is packed), 16-byte aligned, whose first QGEMV_ATTN_SCRATCH_HEAD bytes must be
+ * scratch: at least qgemv_attn_scratch_bytes(...) bytes (over a packed cache qgemv_attn_scratch_least(...); with
+ * qgemv_attn_scratch_bytes_ex(...) many rows are faster, see there), 16-byte aligned, whose first QGEMV_ATTN_SCRATCH_HEAD bytes must be
  * zero before the first call (e.g. cudaMemset once); each call leaves them zero again, so calls of any sizes may share one
  * scratch that is large enough for each: that of the largest sizes is (see below).  Calls that share a scratch must be ordered.
  * The result does not depend on timing: parts of a long context are joined in a fixed order.
@@ -626,8 +627,13 @@ QGEMV_API int qgemv_attn(const qgemv_attn_args* args, unsigned flags, void* stre
 #define QGEMV_ATTN_SCRATCH_HEAD 65536
 QGEMV_API size_t qgemv_attn_scratch_bytes(int seqs, int tokens, int heads, int kv_heads, int dim, int max_q, int max_kv);
 /* The same for a cache of the given kind.  Over a packed one, calls that are served better by the 128-row kernel (many new tokens) read a copy of
- * their contexts in f16, which is made in the scratch: up to seqs * (max_kv + 128) tokens of it, where a call's sizes allow such. */
+ * their contexts in f16, which is made in the scratch: up to seqs * (max_kv + 128) tokens of it, where a call's sizes allow such.
+ * A call whose copy the given scratch has no room for is served by the packed cache's own kernel, which needs none: its results differ within
+ * their stated bits, and it is slower for many rows (32 and 8 heads of 128, 2000 new tokens over 24000: 3.2 ms for 0.6 to 0.7). */
 QGEMV_API size_t qgemv_attn_scratch_bytes_ex(int cache_kind, int seqs, int tokens, int heads, int kv_heads, int dim, int max_q, int max_kv);
+/* The scratch with which no call of these sizes or smaller ones is refused; less than that of qgemv_attn_scratch_bytes_ex over a packed cache,
+ * the same over a 16-bit one. */
+QGEMV_API size_t qgemv_attn_scratch_least(int cache_kind, int seqs, int tokens, int heads, int kv_heads, int dim, int max_q, int max_kv);
 
 /*
  * Sampling: one token per row of logits [m, N] (kind QGEMV_ACT_F32 / BF16 / F16, rows `row_stride` elements apart), from

@@ -168,8 +168,9 @@ def lib():
         L.qgemv_tune_attn.restype = None
         L.qgemv_attn_scratch_bytes.argtypes = [i32] * 7
         L.qgemv_attn_scratch_bytes.restype = sz
-        L.qgemv_attn_scratch_bytes_ex.argtypes = [i32] * 8
-        L.qgemv_attn_scratch_bytes_ex.restype = sz
+        for f in (L.qgemv_attn_scratch_bytes_ex, L.qgemv_attn_scratch_least):
+            f.argtypes = [i32] * 8
+            f.restype = sz
         L.qgemv_sample.argtypes = [i32, vp, ctypes.c_longlong, i32, i32, vp, vp, vp, vp, vp, vp, vp, ctypes.c_uint, vp]
         L.qgemv_sample.restype = i32
         ip = ctypes.POINTER(ctypes.c_int)
@@ -486,12 +487,15 @@ def qgemv_cache_read(args: QgemvCacheReadArgs, flags: int = 0, stream=None) -> N
     _check(lib().qgemv_cache_read(args, flags, _stream(stream)), "qgemv_cache_read")
 
 
-def qgemv_attn_scratch_bytes(seqs: int, tokens: int, heads: int, kv_heads: int, dim: int, max_q: int, max_kv: int, cache=None) -> int:
+def qgemv_attn_scratch_bytes(seqs: int, tokens: int, heads: int, kv_heads: int, dim: int, max_q: int, max_kv: int, cache=None,
+                             least: bool = False) -> int:
     """Scratch of every qgemv_attn call with these sizes or smaller seqs, tokens, max_q and max_kv, over a cache like `cache` (a record of kv_cache
-    or packed_cache; None: 16 bits); its first QGEMV_ATTN_SCRATCH_HEAD bytes must start as zeros."""
+    or packed_cache; None: 16 bits); its first QGEMV_ATTN_SCRATCH_HEAD bytes must start as zeros.  least: without room for a copy of a packed cache's contexts, with
+    which many rows are faster."""
     if cache is None:
         return int(lib().qgemv_attn_scratch_bytes(seqs, tokens, heads, kv_heads, dim, max_q, max_kv))
-    return int(lib().qgemv_attn_scratch_bytes_ex(cache.kind, seqs, tokens, heads, kv_heads, dim, max_q, max_kv))
+    size = lib().qgemv_attn_scratch_least if least else lib().qgemv_attn_scratch_bytes_ex
+    return int(size(cache.kind, seqs, tokens, heads, kv_heads, dim, max_q, max_kv))
 
 
 def attn_args(q, cache: QgemvCache, pages, q_start, kv_len, out, scratch, max_q: int, max_kv: int, scale: float,

@@ -142,6 +142,7 @@ const void* attn_packed8f_kernel_ptr(int dim, int rows, PackedLaunch* launch);
 
 struct AttnPlan {
     bool tiles;  // the 128-row tensor-memory kernel (else that of few rows)
+    bool forced; // by the tuning hook
     PackedLaunch packed;  // a packed cache's kernel of few rows, where it is taken
     int hb_shift;         // of it
     const void* packed_fn;
@@ -150,6 +151,7 @@ struct AttnPlan {
     size_t records, scratch;  // rows of parts' records, bytes of scratch
     size_t copy;              // where in the scratch the copy of a packed cache begins
     size_t scratch_most;      // scratch that serves every call of these sizes or smaller ones
+    size_t scratch_least;     // and that with which none of them is refused
 };
 
 const void* attn_rows_kernel_ptr(bool bf16, int dim, unsigned* smem, unsigned* threads);

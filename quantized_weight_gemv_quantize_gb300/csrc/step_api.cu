@@ -332,14 +332,15 @@ static size_t copy_bytes(int seqs, int tokens, int heads, int kv_heads, int dim,
     return (cache + static_cast<size_t>(rows) * (dim * 2 + 4) + 4 * 256 + 255) / 256 * 256;
 }
 
-static int attn_plan(int bits, bool f16, int seqs, int tokens, int heads, int kv_heads, int dim, int max_q, int max_kv, int window,
+// copies: whether a packed cache's contexts may be copied.
+static int attn_plan(int bits, bool f16, int seqs, int tokens, int heads, int kv_heads, int dim, int max_q, int max_kv, int window, bool copies,
                      AttnPlan* p) {
     if (seqs < 0 || tokens < 0 || heads < 1 || kv_heads < 1 || heads % kv_heads || dim < 8 || dim % 8 || max_q < 0 ||
         max_kv < 0)
         return QGEMV_ERR_INVALID_ARG;
     if (dim > 256 || heads > 65536) return QGEMV_ERR_UNSUPPORTED;
     *p = AttnPlan{};
-    p->scratch = p->scratch_most = QGEMV_ATTN_SCRATCH_HEAD;
+    p->scratch = p->scratch_most = p->scratch_least = QGEMV_ATTN_SCRATCH_HEAD;
     if (seqs == 0 || tokens == 0 || max_q == 0) return QGEMV_OK;
     if (max_q > tokens) max_q = tokens;
     const long long rows = static_cast<long long>(max_q) * (heads / kv_heads);
@@ -385,6 +386,7 @@ static int attn_plan(int bits, bool f16, int seqs, int tokens, int heads, int kv
     const double rows_us = 8 + keys16 / 19000 * (seqs > 1 ? 0.75 : 1.0);
     const int forced = g_attn_kernel.load(std::memory_order_relaxed);
     p->tiles = dim <= 128 && (forced ? forced == 2 : rows > 32 && tiles_us < rows_us);
+    p->forced = forced != 0;
     int tile_rows = 16;
     size_t copy = 0;
     if (bits) {
@@ -402,7 +404,7 @@ static int attn_plan(int bits, bool f16, int seqs, int tokens, int heads, int kv
         while ((2 << p->hb_shift) <= p->packed.warps && kv_heads % (2 << p->hb_shift) == 0 && one >> (p->hb_shift + 1) >= 64 &&
                pieces >= (p->hb_shift ? 40 : 18))
             ++p->hb_shift;
-        copy = dim <= 128 && (forced ? forced == 2 : rows > PACKED_ROWS) ? copy_bytes(seqs, tokens, heads, kv_heads, dim, max_kv) : 0;
+        copy = copies && dim <= 128 && (forced ? forced == 2 : rows > PACKED_ROWS) ? copy_bytes(seqs, tokens, heads, kv_heads, dim, max_kv) : 0;
         // More than 32 rows: by what both would take, in us.  The packed cache's kernel goes over the keys once for 16 rows, 18 row tiles and keys a ns
         // in 4 bits and 15 in 8; the other needs its copy first (160 or 288 bytes read and 512 written a key and head of 128, at 4.5 TB/s).  Of
         // several sequences with one bound the mean is taken to be 0.45 of it.  Measured, 8 key/value heads, 4 bits, packed / copy: 64 rows over
@@ -441,7 +443,8 @@ static int attn_plan(int bits, bool f16, int seqs, int tokens, int heads, int kv
     // What every call of these sizes or smaller ones is content with: the choices above do not grow with the sizes, these bounds do.
     // (a packed cache's kernels have 3 blocks an SM with records of 32 rows, 2 with 64 for more than 8 rows, or 2 with 32 for heads beyond 128)
     const int packed_most = dim > 128 ? 2 * 32 : rows > 8 ? 2 * 64 : 3 * 32;
-    size_t most = dim <= 128 && forced == 2 ? 0 : static_cast<size_t>(bits ? SMS * packed_most : rows_grid(dim) * 16) * 2;
+    const size_t few = static_cast<size_t>(bits ? SMS * packed_most : rows_grid(dim) * 16) * 2;
+    size_t most = dim <= 128 && forced == 2 ? 0 : few;
     if (dim <= 128 && (forced ? forced == 2 : rows > 32) && blocks >= 16) {
         const long long n = blocks / 8 < 32 ? blocks / 8 : 32, limit = parts_max(blocks);
         const long long parts = tiles < limit && tiles * n < limit ? tiles * n : limit;
@@ -450,7 +453,17 @@ static int attn_plan(int bits, bool f16, int seqs, int tokens, int heads, int kv
     }
     p->scratch_most = scratch_of(most, dim);
     if (copy) p->scratch_most = (p->scratch_most + 255) / 256 * 256 + copy;
+    p->scratch_least = bits && forced != 2 ? scratch_of(few, dim) : p->scratch_most;  // (without a copy, and the parts of the kernel that reads it)
     return QGEMV_OK;
+}
+
+static size_t scratch_size(int cache_kind, int seqs, int tokens, int heads, int kv_heads, int dim, int max_q, int max_kv, bool least) {
+    AttnPlan p;
+    const int bits = packed_bits(cache_kind);
+    if (!bits && cache_kind != QGEMV_ACT_BF16 && cache_kind != QGEMV_ACT_F16) return 0;
+    if (bits && dim % 32) return 0;
+    if (attn_plan(bits, false, seqs, tokens, heads, kv_heads, dim, max_q, max_kv, 0, true, &p)) return 0;
+    return ((least ? p.scratch_least : p.scratch_most) + 255) / 256 * 256;
 }
 
 // Dynamic shared memory of a kernel, set once per device.
@@ -526,7 +539,12 @@ static int run_attn(const qgemv_attn_args* a, unsigned flags, void* stream) {
     if ((!bits && c.kind != a->kind) || a->tokens < 0 || a->seqs < 0 || a->pages_stride < 0 || a->window < 0) return QGEMV_ERR_INVALID_ARG;
     if (!(a->scale > 0.f && a->scale <= 1e30f)) return QGEMV_ERR_INVALID_ARG;  // NaN too
     AttnPlan p;
-    if ((st = attn_plan(bits, a->kind == QGEMV_ACT_F16, a->seqs, a->tokens, a->heads, c.heads, c.dim, a->max_q, a->max_kv, a->window, &p))) return st;
+    auto plan = [&](bool copies) {
+        return attn_plan(bits, a->kind == QGEMV_ACT_F16, a->seqs, a->tokens, a->heads, c.heads, c.dim, a->max_q, a->max_kv, a->window, copies, &p);
+    };
+    if ((st = plan(true))) return st;
+    // a scratch without room for the copy: the packed cache's own kernel, which serves any number of rows
+    if (bits && p.tiles && !p.forced && a->scratch_bytes < p.scratch && (st = plan(false))) return st;
     if (a->pages_stride > (1ll << 40) || static_cast<double>(a->seqs) * static_cast<double>(a->pages_stride) > SPAN_MAX)
         return QGEMV_ERR_UNSUPPORTED;
     // The keys that a row of the page table reaches, and the entries of a row that may be read.
@@ -817,16 +835,15 @@ int qgemv_cache_read(const qgemv_cache_read_args* args, unsigned flags, void* st
 void qgemv_tune_attn(int kernel) { g_attn_kernel.store(kernel == 1 || kernel == 2 ? kernel : 0); }
 
 size_t qgemv_attn_scratch_bytes(int seqs, int tokens, int heads, int kv_heads, int dim, int max_q, int max_kv) {
-    AttnPlan p;
-    return attn_plan(0, false, seqs, tokens, heads, kv_heads, dim, max_q, max_kv, 0, &p) ? 0 : (p.scratch_most + 255) / 256 * 256;
+    return scratch_size(QGEMV_ACT_BF16, seqs, tokens, heads, kv_heads, dim, max_q, max_kv, false);
 }
 
 size_t qgemv_attn_scratch_bytes_ex(int cache_kind, int seqs, int tokens, int heads, int kv_heads, int dim, int max_q, int max_kv) {
-    AttnPlan p;
-    const int bits = packed_bits(cache_kind);
-    if (!bits && cache_kind != QGEMV_ACT_BF16 && cache_kind != QGEMV_ACT_F16) return 0;
-    if (bits && dim % 32) return 0;
-    return attn_plan(bits, false, seqs, tokens, heads, kv_heads, dim, max_q, max_kv, 0, &p) ? 0 : (p.scratch_most + 255) / 256 * 256;
+    return scratch_size(cache_kind, seqs, tokens, heads, kv_heads, dim, max_q, max_kv, false);
+}
+
+size_t qgemv_attn_scratch_least(int cache_kind, int seqs, int tokens, int heads, int kv_heads, int dim, int max_q, int max_kv) {
+    return scratch_size(cache_kind, seqs, tokens, heads, kv_heads, dim, max_q, max_kv, true);
 }
 
 int qgemv_attn(const qgemv_attn_args* args, unsigned flags, void* stream) {

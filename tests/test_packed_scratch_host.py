@@ -1,0 +1,58 @@
+"""The scratch of attention over a packed cache without a GPU: what its sizes serve, and what becomes of a call whose copy it has no room for."""
+import pytest
+
+import quantized_weight_gemv_quantize_gb300 as qg
+
+from .test_packed_host import BF16, F16, L, Q4, Q8, attn, cache, pytestmark, scratch  # noqa: F401
+
+SIZES = [(1, 1, 777), (48, 1, 16384), (48, 9, 131072), (16, 5, 4000), (1, 2000, 24000), (48, 2000, 16384), (2, 40, 300), (7, 130, 9000),
+         (256, 512, 131072)]
+
+
+def least(kind, *sizes):
+    return int(qg.lib().qgemv_attn_scratch_least(kind, *sizes))
+
+
+@pytest.fixture(params=[0, 1, 2], ids=["planned", "few rows", "many rows"])
+def hook(request):
+    qg.qgemv_tune_attn(request.param)
+    yield request.param
+    qg.qgemv_tune_attn(0)
+
+
+def rows_of(kind, dim=128):
+    row = qg.qgemv_cache_row_bytes(kind, dim)
+    return cache(kind=kind, dim=dim, k_page=16 * 8 * row, k_token=8 * row, k_head=row, v_page=16 * 8 * row, v_token=8 * row, v_head=row)
+
+
+def call(L, kind, dtype, seqs, new, ctx, n, window=0):  # noqa: F811
+    return L.qgemv_attn(attn(cache=rows_of(kind), kind=dtype, seqs=seqs, tokens=seqs * new, max_q=new, max_kv=ctx, window=window,
+                             pages_stride=-(-ctx // 16), scratch=1 << 46, scratch_bytes=n), 0, None)
+
+
+@pytest.mark.parametrize("kind", [Q4, Q8])
+@pytest.mark.parametrize("size", SIZES, ids=str)
+def test_a_scratch_without_room_for_the_copy_is_taken(L, kind, size, hook):  # noqa: F811
+    """Any number of rows is served without a copy, so that no call is refused for want of one."""
+    seqs, new, ctx = size
+    n = least(kind, seqs, seqs * new, 32, 8, 128, new, ctx)
+    assert qg.QGEMV_ATTN_SCRATCH_HEAD < n <= scratch(kind, seqs, seqs * new, 32, 8, 128, new, ctx)
+    if hook != 2:
+        assert n <= 64 << 20
+    for dtype in (BF16, F16):
+        for q, kv, window in ((new, ctx, 0), (new, ctx, 100), (max(1, new // 2), ctx, 0), (new, max(1, ctx // 3), 1000), (1, 1, 0)):
+            assert call(L, kind, dtype, seqs, q, kv, n, window) in (4, 5)
+            assert call(L, kind, dtype, seqs, q, kv, qg.QGEMV_ATTN_SCRATCH_HEAD, window) == 1
+    assert call(L, kind, BF16, 1, min(new, 2), min(ctx, 50), n) in (4, 5)
+
+
+def test_the_least_of_a_16_bit_cache_is_all_of_it(L, hook):  # noqa: F811
+    for seqs, new, ctx in SIZES:
+        assert least(BF16, seqs, seqs * new, 32, 8, 128, new, ctx) == qg.qgemv_attn_scratch_bytes(seqs, seqs * new, 32, 8, 128, new, ctx)
+    assert least(0, 1, 1, 32, 8, 128, 1, 1) == 0 and least(Q4, 1, 1, 32, 8, 40, 1, 1) == 0 and least(Q4, 1, 1, 30, 8, 128, 1, 1) == 0
+
+
+def test_the_binding_asks_for_the_least(L):  # noqa: F811
+    c = rows_of(Q8)
+    assert qg.qgemv_attn_scratch_bytes(1, 2000, 32, 8, 128, 2000, 24000, cache=c, least=True) == least(Q8, 1, 2000, 32, 8, 128, 2000, 24000)
+    assert qg.qgemv_attn_scratch_bytes(1, 2000, 32, 8, 128, 2000, 24000, cache=c) == scratch(Q8, 1, 2000, 32, 8, 128, 2000, 24000)
