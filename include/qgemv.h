@@ -627,9 +627,12 @@ QGEMV_API int qgemv_attn(const qgemv_attn_args* args, unsigned flags, void* stre
 #define QGEMV_ATTN_SCRATCH_HEAD 65536
 QGEMV_API size_t qgemv_attn_scratch_bytes(int seqs, int tokens, int heads, int kv_heads, int dim, int max_q, int max_kv);
 /* The same for a cache of the given kind.  Over a packed one, calls that are served better by the 128-row kernel (many new tokens) read a copy of
- * their contexts in f16, which is made in the scratch: up to seqs * (max_kv + 128) tokens of it, where a call's sizes allow such.
+ * their contexts in f16, which is made in the scratch: seqs * (max_kv + 128) tokens of kv_heads * dim * 4 + 4 bytes and tokens * heads rows of
+ * dim * 2 + 4 (the sequences' bounds, whatever their lengths, windows and shared pages).  Of that the size counts at most QGEMV_ATTN_COPY_MAX bytes; a
+ * scratch that is larger by what a copy takes beyond that is used for it too.  One scratch serves the calls of all layers, one after another.
  * A call whose copy the given scratch has no room for is served by the packed cache's own kernel, which needs none: its results differ within
  * their stated bits, and it is slower for many rows (32 and 8 heads of 128, 2000 new tokens over 24000: 3.2 ms for 0.6 to 0.7). */
+#define QGEMV_ATTN_COPY_MAX 4294967296ull
 QGEMV_API size_t qgemv_attn_scratch_bytes_ex(int cache_kind, int seqs, int tokens, int heads, int kv_heads, int dim, int max_q, int max_kv);
 /* The scratch with which no call of these sizes or smaller ones is refused; less than that of qgemv_attn_scratch_bytes_ex over a packed cache,
  * the same over a 16-bit one. */

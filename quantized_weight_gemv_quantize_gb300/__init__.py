@@ -27,6 +27,7 @@ ROPE_SCALING = {"none": 0, "linear": 1, "base": 2, "parts": 3, "bands": 4}
 QGEMV_CACHE_Q4, QGEMV_CACHE_Q8 = 4, 8
 PACKED = {"Q4": QGEMV_CACHE_Q4, "Q8": QGEMV_CACHE_Q8}
 QGEMV_ATTN_SCRATCH_HEAD = 65536
+QGEMV_ATTN_COPY_MAX = 1 << 32
 QGEMV_DEVERR_BAD_INDEX = 4
 ROUTE_FUSED, ROUTE_GROUPED, ROUTE_PDL, ROUTE_Q5_K_M1, ROUTE_W8A16_CHANNEL_M1, ROUTE_ARGMAX, ROUTE_M16 = (
     33, 34, 35, 36, 44, 52, 53)

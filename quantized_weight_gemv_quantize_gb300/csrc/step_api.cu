@@ -324,13 +324,13 @@ static size_t scratch_of(size_t records, int dim) {
     return QGEMV_ATTN_SCRATCH_HEAD + round32(records * sizeof(float2)) + records * dim * sizeof(float);
 }
 // The copy in f16 of a packed cache's part that a batch sees, and its page table, for any page size (pages of the copy hold up to 128
-// tokens), and of its queries, four pieces rounded up to 256 bytes each.  0: out of range.
-static size_t copy_bytes(int seqs, int tokens, int heads, int kv_heads, int dim, int max_kv) {
+// tokens), and of its queries, four pieces rounded up to 256 bytes each.  The bytes, and whether a call can make it.
+static double copy_bytes(int seqs, int tokens, int heads, int kv_heads, int dim, int max_kv, bool* can) {
     const double keys = static_cast<double>(seqs) * (static_cast<double>(max_kv) + 128), rows = static_cast<double>(tokens) * heads;
-    if (seqs > 65535 || keys > INT_MAX || keys * kv_heads * dim * 4 > SPAN_MAX || rows * dim * 2 > SPAN_MAX) return 0;
-    const size_t cache = static_cast<size_t>(keys) * (static_cast<size_t>(kv_heads) * dim * 4 + 4);
-    return (cache + static_cast<size_t>(rows) * (dim * 2 + 4) + 4 * 256 + 255) / 256 * 256;
+    *can = seqs <= 65535 && keys <= INT_MAX && keys * kv_heads * dim * 4 <= SPAN_MAX && rows * dim * 2 <= SPAN_MAX;
+    return keys * (static_cast<double>(kv_heads) * dim * 4 + 4) + rows * (dim * 2 + 4) + 4 * 256;
 }
+static size_t round256(double n) { return (static_cast<size_t>(n) + 255) / 256 * 256; }
 
 // copies: whether a packed cache's contexts may be copied.
 static int attn_plan(int bits, bool f16, int seqs, int tokens, int heads, int kv_heads, int dim, int max_q, int max_kv, int window, bool copies,
@@ -388,7 +388,7 @@ static int attn_plan(int bits, bool f16, int seqs, int tokens, int heads, int kv
     p->tiles = dim <= 128 && (forced ? forced == 2 : rows > 32 && tiles_us < rows_us);
     p->forced = forced != 0;
     int tile_rows = 16;
-    size_t copy = 0;
+    size_t copy = 0, counted = 0;  // of this call; what the sizes' scratch has for it
     if (bits) {
         if (rows > INT_MAX / 2) return QGEMV_ERR_UNSUPPORTED;
         p->packed_fn = (bits == 4 ? f16 ? attn_packed4f_kernel_ptr : attn_packed4_kernel_ptr : f16 ? attn_packed8f_kernel_ptr : attn_packed8_kernel_ptr)(
@@ -404,7 +404,14 @@ static int attn_plan(int bits, bool f16, int seqs, int tokens, int heads, int kv
         while ((2 << p->hb_shift) <= p->packed.warps && kv_heads % (2 << p->hb_shift) == 0 && one >> (p->hb_shift + 1) >= 64 &&
                pieces >= (p->hb_shift ? 40 : 18))
             ++p->hb_shift;
-        copy = copies && dim <= 128 && (forced ? forced == 2 : rows > PACKED_ROWS) ? copy_bytes(seqs, tokens, heads, kv_heads, dim, max_kv) : 0;
+        if (dim <= 128 && (forced ? forced == 2 : rows > PACKED_ROWS)) {
+            bool can;
+            const double bytes = copy_bytes(seqs, tokens, heads, kv_heads, dim, max_kv, &can);
+            if (can && copies) copy = round256(bytes);
+            // (the same from the bound on, whether or not the call itself could make one that large: smaller calls may have theirs)
+            const size_t bound = forced ? size_t{1} << 62 : QGEMV_ATTN_COPY_MAX;
+            counted = bytes < static_cast<double>(bound) ? round256(bytes) : bound;
+        }
         // More than 32 rows: by what both would take, in us.  The packed cache's kernel goes over the keys once for 16 rows, 18 row tiles and keys a ns
         // in 4 bits and 15 in 8; the other needs its copy first (160 or 288 bytes read and 512 written a key and head of 128, at 4.5 TB/s).  Of
         // several sequences with one bound the mean is taken to be 0.45 of it.  Measured, 8 key/value heads, 4 bits, packed / copy: 64 rows over
@@ -452,7 +459,7 @@ static int attn_plan(int bits, bool f16, int seqs, int tokens, int heads, int kv
         if (cut > most) most = cut;
     }
     p->scratch_most = scratch_of(most, dim);
-    if (copy) p->scratch_most = (p->scratch_most + 255) / 256 * 256 + copy;
+    if (counted) p->scratch_most = (p->scratch_most + 255) / 256 * 256 + counted;
     p->scratch_least = bits && forced != 2 ? scratch_of(few, dim) : p->scratch_most;  // (without a copy, and the parts of the kernel that reads it)
     return QGEMV_OK;
 }

@@ -26,8 +26,8 @@ def rows_of(kind, dim=128):
 
 
 def call(L, kind, dtype, seqs, new, ctx, n, window=0):  # noqa: F811
-    return L.qgemv_attn(attn(cache=rows_of(kind), kind=dtype, seqs=seqs, tokens=seqs * new, max_q=new, max_kv=ctx, window=window,
-                             pages_stride=-(-ctx // 16), scratch=1 << 46, scratch_bytes=n), 0, None)
+    return L.qgemv_attn(attn(cache=rows_of(kind), q=1 << 41, out=1 << 42, pages=1 << 43, q_start=1 << 44, kv_len=1 << 45, kind=dtype, seqs=seqs, tokens=seqs * new, max_q=new, max_kv=ctx, window=window,
+                             pages_stride=-(-ctx // 16), scratch=1 << 50, scratch_bytes=n), 0, None)
 
 
 @pytest.mark.parametrize("kind", [Q4, Q8])
@@ -56,3 +56,34 @@ def test_the_binding_asks_for_the_least(L):  # noqa: F811
     c = rows_of(Q8)
     assert qg.qgemv_attn_scratch_bytes(1, 2000, 32, 8, 128, 2000, 24000, cache=c, least=True) == least(Q8, 1, 2000, 32, 8, 128, 2000, 24000)
     assert qg.qgemv_attn_scratch_bytes(1, 2000, 32, 8, 128, 2000, 24000, cache=c) == scratch(Q8, 1, 2000, 32, 8, 128, 2000, 24000)
+
+
+@pytest.mark.parametrize("heads,kv_heads,dim", [(4, 1, 32), (32, 8, 128), (16, 8, 64)])
+@pytest.mark.parametrize("kind", [Q4, Q8])
+def test_the_scratch_never_falls_at_the_ends_of_the_copys_range(L, kind, heads, kv_heads, dim):  # noqa: F811
+    """Around 65535 sequences and 2^31 tokens, beyond which a call makes no copy, and around the bytes that are counted for one."""
+    for new in (9, 17, 40, 512):
+        for fixed, sizes in (("context", [(s, c) for c in (0, 256, 4096) for s in (1, 300, 40000, 65534, 65535, 65536, 65537, 100000)]),
+                             ("sequences", [(s, c) for s in (1, 63, 64, 4096) for c in (1, 1 << 16, (1 << 19) - 129, 1 << 19, (1 << 25) - 129, (1 << 25) - 128,
+                                                                                         (1 << 25) - 127, 1 << 25, 1 << 27, 1 << 30)])):
+            last, key = 0, None
+            for s, c in sizes:
+                n = scratch(kind, s, s * new, heads, kv_heads, dim, new, c)
+                if n == 0:  # (more row tiles than the kernel's arithmetic takes: the sizes are refused)
+                    assert s * kv_heads * -(-new * (heads // kv_heads) // 16) > 10 ** 8
+                    continue
+                here = c if fixed == "context" else s
+                assert n >= (last if here == key else 0), (new, s, c)
+                # beside the copy, parts: up to 16 waves of 152 row tiles of 256 rows, dim floats and two more a row
+                assert n <= qg.QGEMV_ATTN_COPY_MAX + 16 * 152 * 256 * (4 * dim + 8) + (1 << 20)
+                last, key = n, here
+
+
+@pytest.mark.parametrize("kind", [Q4, Q8])
+def test_the_scratch_of_the_largest_sizes_serves_calls_with_and_without_a_copy(L, kind):  # noqa: F811
+    for most in ((65536, 9, 256), (65535, 9, 256), (64, 512, 1 << 26), (256, 512, 131072)):
+        seqs, new, ctx = most
+        n = scratch(kind, seqs, seqs * new, 32, 8, 128, new, ctx)
+        for s, q, c in (most, (1, new, min(ctx, 24000)), (seqs - 1, new, ctx), (min(seqs, 100), new, ctx), (seqs, 1, ctx), (2, new // 2, ctx // 2)):
+            for dtype in (BF16, F16):
+                assert call(L, kind, dtype, s, q, c, n) in (4, 5)
