@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(READ_THREADS) cache_unpack_kernel(const CacheU
                 float x[8];
                 w[j].values(x);
 #pragma unroll
-                for (float& v : x) v = fminf(fmaxf(v, -65504.f), 65504.f);  // (d c + m may end a step's rounding beyond the largest f16)
+                for (float& v : x) v = min_or_nan(max_or_nan(v, -65504.f), 65504.f);  // (d c + m may end a step's rounding beyond the largest f16)
                 store8(ACT_F16, y, row * a.dim + e, x);
             }
         }

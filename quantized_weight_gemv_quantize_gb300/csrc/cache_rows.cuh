@@ -73,6 +73,12 @@ __device__ __forceinline__ float max_or_nan(float a, float b) {
     return y;
 }
 
+__device__ __forceinline__ float min_or_nan(float a, float b) {
+    float y;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+
 // The step and base of a block by its least and largest value (NaN where one is).
 //
 // The base is rounded down and the step up, so that every value lies within the codes: none is cut off by more than the rounding of
