@@ -638,6 +638,12 @@ QGEMV_API size_t qgemv_attn_scratch_bytes_ex(int cache_kind, int seqs, int token
  * the same over a 16-bit one. */
 QGEMV_API size_t qgemv_attn_scratch_least(int cache_kind, int seqs, int tokens, int heads, int kv_heads, int dim, int max_q, int max_kv);
 
+/* Launch-plan introspection (no device needed), as qgemv_plan_info: fills out[0..3] for a qgemv_attn call of these sizes, with kind the type of q, whose
+ * scratch has room for whatever it would use: {the kernel, as its QGEMV_ROUTE_ATTN_ number; key/value heads that a block takes side by
+ * side; rows of a row tile; bytes of scratch that this needs}. */
+QGEMV_API int qgemv_attn_plan_info(int cache_kind, int kind, int seqs, int tokens, int heads, int kv_heads, int dim, int max_q, int max_kv, int window,
+                                   long long* out);
+
 /*
  * Sampling: one token per row of logits [m, N] (kind QGEMV_ACT_F32 / BF16 / F16, rows `row_stride` elements apart), from
  * one given uniform number u[i] in [0, 1) per row.  With top = max_n x_n and T = temperature[i]:

@@ -172,6 +172,8 @@ def lib():
         for f in (L.qgemv_attn_scratch_bytes_ex, L.qgemv_attn_scratch_least):
             f.argtypes = [i32] * 8
             f.restype = sz
+        L.qgemv_attn_plan_info.argtypes = [i32] * 10 + [ctypes.POINTER(ctypes.c_longlong)]
+        L.qgemv_attn_plan_info.restype = i32
         L.qgemv_sample.argtypes = [i32, vp, ctypes.c_longlong, i32, i32, vp, vp, vp, vp, vp, vp, vp, ctypes.c_uint, vp]
         L.qgemv_sample.restype = i32
         ip = ctypes.POINTER(ctypes.c_int)
@@ -608,6 +610,15 @@ def qgemv_plan_info_chunk(fmt, m: int, N: int, Kc: int, num_sms: int = 152, ctas
     buf = (ctypes.c_longlong * 15)()
     _check(lib().qgemv_plan_info_chunk(f, m, N, Kc, num_sms, ctas_per_sm, buf), "qgemv_plan_info_chunk")
     return dict(zip(PLAN_FIELDS + ("slot_row_stride",), [int(v) for v in buf]))
+
+
+def qgemv_attn_plan_info(cache_kind: int, kind: int, seqs: int, tokens: int, heads: int, kv_heads: int, dim: int, max_q: int, max_kv: int,
+                         window: int = 0) -> dict:
+    """The plan of a qgemv_attn call of these sizes with queries of `kind` (QGEMV_ACT_BF16 or QGEMV_ACT_F16): its kernel (a ROUTE_ATTN_ number), the
+    key/value heads that a block takes side by side, the rows of a row tile, and its scratch."""
+    buf = (ctypes.c_longlong * 4)()
+    _check(lib().qgemv_attn_plan_info(cache_kind, kind, seqs, tokens, heads, kv_heads, dim, max_q, max_kv, window, buf), "qgemv_attn_plan_info")
+    return dict(zip(("route", "heads_side", "tile_rows", "scratch_bytes"), [int(v) for v in buf]))
 
 
 def qgemv_tune_pairs(mode: int = 0) -> None:

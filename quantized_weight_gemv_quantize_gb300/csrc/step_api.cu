@@ -853,6 +853,21 @@ size_t qgemv_attn_scratch_least(int cache_kind, int seqs, int tokens, int heads,
     return scratch_size(cache_kind, seqs, tokens, heads, kv_heads, dim, max_q, max_kv, true);
 }
 
+int qgemv_attn_plan_info(int cache_kind, int kind, int seqs, int tokens, int heads, int kv_heads, int dim, int max_q, int max_kv, int window,
+                         long long* out) {
+    const int bits = packed_bits(cache_kind);
+    if (!out || window < 0 || (kind != QGEMV_ACT_BF16 && kind != QGEMV_ACT_F16) || (!bits && cache_kind != kind)) return QGEMV_ERR_INVALID_ARG;
+    if (bits && (dim < 32 || dim % 32)) return QGEMV_ERR_INVALID_ARG;
+    AttnPlan p;
+    const int st = attn_plan(bits, kind == QGEMV_ACT_F16, seqs, tokens, heads, kv_heads, dim, max_q, max_kv, window, true, &p);
+    if (st) return st;
+    out[0] = p.tiles ? QGEMV_ROUTE_ATTN_TILES : bits ? QGEMV_ROUTE_ATTN_PACKED : QGEMV_ROUTE_ATTN_ROWS;
+    out[1] = bits && !p.tiles ? 1 << p.hb_shift : 1;
+    out[2] = p.tiles ? 256 : bits && p.packed.rows ? p.packed.rows : 16;
+    out[3] = static_cast<long long>(p.scratch);
+    return QGEMV_OK;
+}
+
 int qgemv_attn(const qgemv_attn_args* args, unsigned flags, void* stream) {
     int st;
     if (api_injected(&st)) return st;
