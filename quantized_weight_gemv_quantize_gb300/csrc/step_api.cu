@@ -308,7 +308,11 @@ static std::atomic<int> g_attn_kernel{0};
 static size_t round32(size_t n) { return (n + 31) / 32 * 32; }
 
 constexpr int SMS = 152;
-constexpr int PACKED_ROWS = 32;   // up to so many rows it is always taken
+// Up to so many rows of a sequence the packed cache's own kernel is always taken.  64 rows, packed / copy in us, 8 key/value heads of 128 and of 64: 4 bits, one
+// sequence of 24000 50 / 69 and 38 / 51, of 100000 150 / 202 and 108 / 140, 8 of 16000 197 / 267 and 134 / 186, 32 of 4000 183 / 280 and
+// 128 / 195; 8 bits, 100000 195 / 204 and 120 / 140, 8 of 16000 232 / 269 and 140 / 186.  (96 rows: 4 bits 64 / 70 and 48 / 52, 214 / 202 and
+// 154 / 141, 290 / 269 and 198 / 188, 260 / 279 and 175 / 193.)
+constexpr int PACKED_ROWS = 64;
 
 // Parts that row tiles may be cut into, all together: as many waves of blocks as half the square root of the context's key tiles, at most
 // 16.  A wave costs its start and end, some 3 key tiles, so that more of them win nothing by the estimate below (the limit moves
@@ -412,15 +416,19 @@ static int attn_plan(int bits, bool f16, int seqs, int tokens, int heads, int kv
             const size_t bound = forced ? size_t{1} << 62 : QGEMV_ATTN_COPY_MAX;
             counted = bytes < static_cast<double>(bound) ? round256(bytes) : bound;
         }
-        // More than 32 rows: by what both would take, in us.  The packed cache's kernel goes over the keys once for 16 rows, 18 row tiles and keys a ns
-        // in 4 bits and 15 in 8; the other needs its copy first (160 or 288 bytes read and 512 written a key and head of 128, at 4.5 TB/s).  Of
-        // several sequences with one bound the mean is taken to be 0.45 of it.  Measured, 8 key/value heads, 4 bits, packed / copy: 64 rows over
-        // 4000 23.2 / 37.3, 256 rows 47.6 / 43.6; over 24000 64 rows 51.5 / 72.3, 128 rows 88.7 / 73.0; over 100000 64 rows 153 / 221, 128 rows
-        // 314 / 222; 32 sequences of up to 4000 64 rows 99 / 194, 128 rows 167 / 190, 256 rows 278 / 218; 8 bits, 24000, 64 rows 59.9 / 74.5,
-        // 128 rows 111 / 76.
-        const double part = seqs > 1 ? 0.45 : 1.0;
-        const double packed_us = 15 + part * static_cast<double>((rows + 15) / 16) * kv_heads * seqs * keys_of(16, 16) / (bits == 4 ? 18000 : 15000);
-        const double copy_us = 5 + part * static_cast<double>(seqs) * keys * kv_heads * static_cast<double>(dim) * (4 + bits / 4.0 + 0.25) / 4.5e6;
+        // More rows: by what both would take, in us.  The packed cache's kernel goes over the keys once for 16 rows, 22 row tiles and keys a ns in 4 bits and
+        // 17 in 8, for heads of up to 64 31 and 29; the other needs its copy first (160 or 288 bytes read and 512 written a key and head of 128, at
+        // 4.5 TB/s).  Of several sequences the lengths are not known here: the packed kernel and the copy go by their sum, the 128-row kernel by the longest, and the
+        // mean is taken to be two thirds of the bound, between equal lengths and lengths spread from nothing to the bound.  Over 146 batches, of equal lengths and of
+        // means of 0.36 to 0.66, with heads of 64 and of 128, windows and groups of 8, the choice then costs at most 1.12 of the better kernel's time for equal lengths
+        // and 1.19 for uneven ones; with the mean at 0.45 1.49 and 1.19, at the bound 1.11 and 1.56.  Measured, 8 key/value heads of 128, packed / copy: 4 bits, 256
+        // rows over 4000 42 / 45; over 24000 128 rows 85 / 70; 32 sequences of 4000 96 rows 260 / 279, 128 rows 330 / 273, of up to 4000 (0.47 of it in the
+        // mean) 64 rows 180 / 199, 128 rows 306 / 193; 8 of 16000 96 rows 290 / 269, 128 rows 376 / 260, of up to 16000 (0.36) 96 rows 118 / 183, 128 rows
+        // 161 / 175; 8 bits, 24000, 96 rows 79 / 71.
+        const double rate = dim <= 64 ? (bits == 4 ? 31000 : 29000) : bits == 4 ? 22000 : 17000;
+        const double mean = seqs > 1 ? 2.0 / 3 : 1.0;
+        const double packed_us = 15 + mean * static_cast<double>((rows + 15) / 16) * kv_heads * seqs * keys_of(16, 16) / rate;
+        const double copy_us = 5 + mean * static_cast<double>(seqs) * keys * kv_heads * static_cast<double>(dim) * (4 + bits / 4.0 + 0.25) / 4.5e6;
         p->tiles = copy > 0 && (forced == 2 || tiles_us + copy_us < packed_us);
     }
     size_t records = 0;

@@ -43,3 +43,34 @@ def test_refusals():
         bad[i] = v
         assert L.qgemv_attn_plan_info(*bad, buf) == 1, (i, v)
     assert L.qgemv_attn_plan_info(Q4, B16, 1, 1, 32, 8, 288, 1, 777, 0, buf) == 2
+
+
+# packed cache's own kernel against the 128-row kernel over the copy, measured (us), where one is clearly faster.  8 key/value heads, 32 query heads:
+# (cache, sequences, new tokens, bound of the contexts, dim, us of the packed kernel, of the copy); lengths equal to the bound, or as said
+CHOICES = [
+    (Q4, 1, 9, 100000, 64, 84.5, 140.2), (Q4, 1, 16, 100000, 64, 108.3, 140.0), (Q8, 1, 12, 100000, 64, 90.6, 140.4),
+    (Q4, 1, 16, 24000, 64, 37.6, 51.1), (Q8, 1, 16, 24000, 64, 39.2, 52.7), (Q4, 1, 16, 100000, 128, 150.3, 201.9),
+    (Q8, 1, 12, 100000, 128, 148.2, 203.1), (Q4, 8, 12, 16000, 128, 157.9, 268.2), (Q4, 32, 16, 4000, 128, 182.8, 279.7),
+    (Q4, 48, 16, 16384, 128, 486.9, 797.8),  # 0.42 of the bound in the mean
+    (Q4, 1, 32, 24000, 128, 85.3, 70.0), (Q4, 1, 64, 100000, 64, 398.3, 153.9), (Q8, 1, 32, 24000, 64, 66.7, 53.6),
+    (Q4, 2, 32, 24000, 128, 152.1, 110.9), (Q4, 8, 32, 16000, 128, 375.7, 259.6), (Q4, 8, 32, 16000, 64, 260.4, 183.0),
+    (Q8, 32, 32, 4000, 128, 397.3, 274.8), (Q4, 32, 32, 4000, 128, 330.3, 272.7),
+    (Q4, 8, 24, 16000, 128, 117.7, 183.4),   # 0.36 of the bound
+    (Q4, 32, 32, 4000, 128, 305.5, 192.8),   # 0.47 of the bound
+    (Q4, 48, 32, 16384, 128, 1063.5, 776.1), # 0.42 of the bound
+]
+
+
+@pytest.mark.parametrize("case", CHOICES, ids=str)
+def test_many_rows_go_to_the_faster_kernel(case):
+    """Whatever the lengths' mean is of their bound: no batch is judged by that of another."""
+    cache, seqs, new, ctx, dim, packed, copy = case
+    for kind in (B16, H16):
+        assert plan(cache, kind, seqs, new, ctx, dim=dim)["route"] == (PACKED if packed < copy else TILES)
+
+
+@pytest.mark.parametrize("cache", [Q4, Q8])
+def test_drafts_ask_for_no_copy(cache):
+    """Up to 64 rows of a sequence the copy is never faster, so that none is counted in the scratch of such calls."""
+    for seqs, new, ctx in ((48, 9, 131072), (64, 16, 32768), (300, 12, 1 << 17)):
+        assert qg.lib().qgemv_attn_scratch_bytes_ex(cache, seqs, seqs * new, 32, 8, 128, new, ctx) <= 64 << 20
