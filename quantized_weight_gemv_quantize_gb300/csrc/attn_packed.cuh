@@ -4,15 +4,16 @@
 //     <q, k> = sum_g d_g <q_g, c_g> + sum_g m_g sum(q_g),    out_g = sum_t (p_t d_tg) c_t + sum_t p_t m_tg.
 // Keys are the rows of the products (16 a step), queries the columns (8, or twice 8): S^T = K Q^T and O^T = V^T P^T.  A code is taken as an f16
 // without a conversion: its bits in the low places of a half are the subnormal c 2^-24 (or c 2^-20, four places higher), which the tensor cores
-// take exactly, so that one AND makes two operands; 2^24 comes off the fp32 sums, and the 2^4 between the halves of a byte is taken into q (for
+// take exactly, so that one AND makes two operands (a step's sum is cut 2^-23 below the largest product's nominal exponent, which a subnormal has as 2^-14: with 17
+// addends at most 17 2^-13 of the step's largest p d, or q d, is lost, 1/16 of it four places higher); 2^24 comes off the fp32 sums, and the 2^4 between the halves of a byte is taken into q (for
 // keys) and off at the end (for values).  ldmatrix, and its transposing form for the values, puts a byte's neighbours where an operand wants
 // them; which element of a head stands in which place of the sum does not matter, and q is laid out alike.
 // The steps d of keys are applied to the fp32 sums of their block, those of values to p (a product in f16); the bases are one more product: with the
 // block sums of q, in two f16 pieces (22 bits), and with p.
 //
 // q is taken in f16, times a power of two of its row that brings its largest element to [2^9, 2^10): elements down to 2^-19 of that keep 11
-// bits (a bf16 q all its 8), smaller ones are off by 2^-30 of it.  p is taken as two f16, 2^LIFT p rounded and the rest, so that its product with a
-// step is rounded once.  What that rounding leaves is multiplied by codes about Z, the middle one, in place of codes from 0: sum (p d)(c - Z)
+// bits (a bf16 q all its 8), smaller ones are off by 2^-30 of it.  p is taken in f16, 2^LIFT p rounded; for f16 results its rest too, so that its
+// product with a step is rounded once, to 11 bits.  What that rounding leaves is multiplied by codes about Z, the middle one, in place of codes from 0: sum (p d)(c - Z)
 // + sum p (m + Z d), where (p d) stands for the rounded product in both of its sums (one product with ones a block) and the last sum is
 // small.  Bits are lost where p d is below 2^-24 of what stands for a p of 2^-LIFT.  The running maximum may lag by 2^LAG, so that it rarely
 // moves; a step above 2 counts in the maximum with its own size, so that no product leaves f16.
