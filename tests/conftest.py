@@ -10,7 +10,8 @@ if ROOT not in sys.path:
 
 # Modules whose tests call the library with addresses that are none: it refuses the calls or, where no GPU is, fails to launch.  On a machine with a GPU a
 # call that is accepted after all, by a check that was relaxed or an expectation that is wrong, would launch a kernel on them.
-FAKE_ADDRESSES = {"test_boundary.py", "test_step_host.py", "test_step_edges_host.py", "test_packed_host.py", "test_packed_scratch_host.py"}
+FAKE_ADDRESSES = {"test_boundary.py", "test_step_host.py", "test_step_edges_host.py", "test_packed_host.py", "test_packed_scratch_host.py",
+                  "test_zz_no_alloc.py"}
 
 
 def keep_off_gpus(items, gpu):
