@@ -762,7 +762,7 @@ __global__ void __launch_bounds__(PackedShape<DP, BITS, NT>::WARPS * 32, PackedS
     fence_copies();
     int slot = 0;
     unsigned parity = 0;
-    divide_rows<S::ROWS, 16>(
+    divide_rows<S::ROWS, 16, true>(
         pa.a, pa.a.kv_heads >> pa.hb_shift, 1 << pa.hb_shift, pa.few, &last, smem,
         [&](const Tile& t, long long record) { attend_packed<DP, BITS, NT, WHOLE, FINE>(pa, t, record, smem, smem_addr(plain), ring, slot, parity); },
         [&](const Tile& t) {

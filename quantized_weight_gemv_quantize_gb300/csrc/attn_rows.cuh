@@ -66,12 +66,12 @@ __device__ __forceinline__ void join_rows(const AttnArgs& a, const Tile& t) {
 // A block's parts of the batch's row tiles, one after another: attend(t, record) computes one, into the result or into its record, join(t) joins the
 // parts of one; both are called by the whole block.  A row tile is ROWS rows of each of `heads` key/value heads, `groups` times those make all of
 // them.  Ranges of keys begin at multiples of STEP; less than `few` keys are not worth a block.  `last` and `room`
-// (KEPT pairs of words, free until attend is called) are in shared memory.
+// (with KEEP KEPT pairs of words, free until attend is called) are in shared memory.
 constexpr unsigned KEPT = 1024;
-template <int ROWS, int STEP, class Attend, class Join>
+template <int ROWS, int STEP, bool KEEP, class Attend, class Join>
 __device__ __forceinline__ void divide_rows(const AttnArgs& a, int groups, int heads, unsigned few, unsigned* last, void* room, Attend&& attend, Join&& join) {
     const unsigned lane = threadIdx.x % 32, me = blockIdx.x, blocks = gridDim.x, seqs = a.seqs, unit = a.unit_shift;
-    // A sequence in the division of the work: its row tiles, each as many units of keys (64, or more where 32 bits would not
+    // A sequence in the division of the work: its row tiles, each as many units of keys (64, over a packed cache 32, or more where 32 bits would not
     // hold the whole) as any of its rows may see, at least one (a row that sees nothing has its zeros written).
     Seq sq = {};
     unsigned sq_units = 1, sq_tiles = 0;
@@ -84,9 +84,9 @@ __device__ __forceinline__ void divide_rows(const AttnArgs& a, int groups, int h
         sq_tiles = (sq.n * a.group + ROWS - 1) / ROWS * groups;
         sq_units = max(1u, (static_cast<unsigned>(hi - lo) + (1u << unit) - 1) >> unit);
     };
-    // The division goes over the sequences some ten times: up to 32 stay in registers, a lane each, up to KEPT in shared memory.
+    // The division goes over the sequences some ten times: up to 32 stay in registers, a lane each, with KEEP up to KEPT in shared memory.
     uint2* const kept = static_cast<uint2*>(room);
-    const bool keep = seqs > 32 && seqs <= KEPT;
+    const bool keep = KEEP && seqs > 32 && seqs <= KEPT;
     if (seqs <= 32) read_seq(lane);
     if (keep) {
         for (unsigned b = threadIdx.x; b < seqs; b += blockDim.x) read_seq(b), kept[b] = make_uint2(sq_units, sq_tiles);

@@ -154,7 +154,7 @@ struct AttnPlan {
     size_t scratch_least;     // and that with which none of them is refused
 };
 
-const void* attn_rows_kernel_ptr(bool bf16, int dim, unsigned* smem, unsigned* threads);
+const void* attn_rows_kernel_ptr(bool bf16, int dim, int seqs, unsigned* smem, unsigned* threads);
 const void* attn_tiles_kernel_ptr(bool bf16, bool units, int dim, unsigned* smem, unsigned* threads);
 const void* attn_join_kernel_ptr(bool bf16);
 constexpr int JOIN_WARPS = 8;  // rows of a block of the joining kernel

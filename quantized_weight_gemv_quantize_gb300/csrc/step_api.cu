@@ -620,7 +620,7 @@ static int run_attn(const qgemv_attn_args* a, unsigned flags, void* stream) {
     unsigned smem, threads;
     const void* fn;
     if (bits && !p.tiles) fn = p.packed_fn, smem = p.packed.smem, threads = p.packed.threads;
-    else if (!p.tiles) fn = attn_rows_kernel_ptr(a->kind == QGEMV_ACT_BF16, c.dim, &smem, &threads);
+    else if (!p.tiles) fn = attn_rows_kernel_ptr(a->kind == QGEMV_ACT_BF16, c.dim, a->seqs, &smem, &threads);
     else fn = attn_tiles_kernel_ptr(a->kind == QGEMV_ACT_BF16, bits && a->kind == QGEMV_ACT_BF16, c.dim, &smem, &threads);
     if ((st = allow_smem(fn, smem))) return st;
     // The largest power of two, up to `most`, that divides the page.
