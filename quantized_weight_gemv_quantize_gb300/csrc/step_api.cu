@@ -427,9 +427,16 @@ static int attn_plan(int bits, bool f16, int seqs, int tokens, int heads, int kv
         // 161 / 175; 8 bits, 24000, 96 rows 79 / 71.
         const double rate = dim <= 64 ? (bits == 4 ? 31000 : 29000) : bits == 4 ? 22000 : 17000;
         const double mean = seqs > 1 ? 2.0 / 3 : 1.0;
-        const double packed_us = 15 + mean * static_cast<double>((rows + 15) / 16) * kv_heads * seqs * keys_of(16, 16) / rate;
+        // Row tiles of n rows of a key/value head: no more than all tokens make, and one more a sequence.  (max_q alone would take every sequence of a
+        // mixed step for a chunk.  One of 40, 500 and 2000 new tokens with 47 single ones, packed / copy: up to 4000 68 / 238 and 198 / 275, up to 16384 2355 / 1288.)
+        auto tiles_of = [&](int n) {
+            const double most = static_cast<double>((rows + n - 1) / n) * seqs, all = static_cast<double>(tokens) * (heads / kv_heads) / n + seqs;
+            return most < all ? most : all;
+        };
+        const double packed_us = 15 + mean * tiles_of(16) * kv_heads * keys_of(16, 16) / rate;
         const double copy_us = 5 + mean * static_cast<double>(seqs) * keys * kv_heads * static_cast<double>(dim) * (4 + bits / 4.0 + 0.25) / 4.5e6;
-        p->tiles = copy > 0 && (forced == 2 || tiles_us + copy_us < packed_us);
+        const double few_us = 9 + (tiles_us - 9) * tiles_of(256) * kv_heads / static_cast<double>(tiles);
+        p->tiles = copy > 0 && (forced == 2 || few_us + copy_us < packed_us);
     }
     size_t records = 0;
     if (!p->tiles) {

@@ -74,3 +74,11 @@ def test_drafts_ask_for_no_copy(cache):
     """Up to 64 rows of a sequence the copy is never faster, so that none is counted in the scratch of such calls."""
     for seqs, new, ctx in ((48, 9, 131072), (64, 16, 32768), (300, 12, 1 << 17)):
         assert qg.lib().qgemv_attn_scratch_bytes_ex(cache, seqs, seqs * new, 32, 8, 128, new, ctx) <= 64 << 20
+
+
+@pytest.mark.parametrize("cache", [Q4, Q8])
+def test_a_mixed_step_is_judged_by_all_its_tokens(cache):
+    """One chunk among 47 single tokens (us of the packed kernel / of the copy, 4 bits): not as if every sequence had a chunk."""
+    for new, ctx, route in ((40, 4000, PACKED), (500, 4000, PACKED), (2000, 16384, TILES)):  # 68 / 238, 198 / 275, 2355 / 1288
+        assert qg.qgemv_attn_plan_info(cache, B16, 48, new + 47, 32, 8, 128, new, ctx)["route"] == route
+        assert qg.qgemv_attn_plan_info(cache, B16, 48, 48 * new, 32, 8, 128, new, ctx)["route"] == TILES
