@@ -585,7 +585,7 @@ QGEMV_API int qgemv_cache_read(const qgemv_cache_read_args* args, unsigned flags
  * sequence read the codes themselves.  q then counts in f16 times a power of two of its own row: 11 bits (bf16: all 8) for elements down to 2^-19 of
  * the row's largest, an error of 2^-30 of that below.  The probabilities p keep 11 bits, and so do their products p d with the values' steps;
  * with f16 results p d is rounded from about 20 bits of p, and codes count from the middle one, Z = 8 or 128, so that of v = (m + Z d) + d (c - Z) either part's
- * sum is off by 2^-11 of what it adds up.  The sums of codes lose at most 2^-9 of the largest p d a step of 16 keys beside that.  Probabilities below 2^-24 of the row's largest have fewer bits.  Many rows read a copy of the contexts in f16 (11 bits, held to +-65504), which the call makes in
+ * sum is off by 2^-11 of what it adds up.  The sums of codes lose at most 17 2^-13 of the largest p d of 16 keys beside that.  Probabilities below 2^-24 of the row's largest have fewer bits.  Many rows read a copy of the contexts in f16 (11 bits, held to +-65504), which the call makes in
  * the scratch, and the probabilities are rounded as f16's above.
  * kind (QGEMV_ACT_BF16 / QGEMV_ACT_F16): type of q and out, and the cache's unless that is packed.  q, out [tokens, heads, cache->dim], last
  * dimension contiguous, 16-byte aligned, strides multiples of 8 elements.  lse: fp32 [tokens, heads] or NULL.

@@ -22,14 +22,16 @@
 // and sum; the warps of a head, then a row tile's parts over the blocks, are joined in a fixed order.  The copies are the block's: a ring of rounds, each
 // one or two pieces of 16 keys of every warp, rows as they lie, steps and bases with them; by tensor map, or where pages are no multiple of 16 tokens by
 // plain copies of a token's rows or of a run of tokens (pages of 24: 195 and 143 us for the 48 sequences' 99 below).
-// The warps take turns to issue a round; a slot is filled again two rounds after it was read, so that nobody waits for the slowest warp.
+// The warps take turns to issue a round.  Where the ring has 5 or 6 slots (heads of 64 in 4 bits, and more than 8 rows but for heads of 128 in 8 bits) a slot is filled
+// again two rounds after it was read, and nobody waits for the slowest warp; where 2 or 3 (up to 8 rows of heads of 128 and 256, among others) the issuing
+// warp waits for the round just before.  Rounds of half the size, with twice the slots, were slower there too (113 us for 99 below).
 // The warps of a block take 1 to 4 key/value heads side by side, the same keys of each: a row is 80 bytes for heads of 128 in 4 bits, so that where
 // a token's heads lie together a head alone fetched 2.6 times its bytes from memory (1166 MB for 442).
 //
 // Bound by memory in the loop (5.8 TB/s of codes, of 6.8 that a copy reaches; 297 instructions a warp for 16 keys of a head, issue slots 42% taken),
-// and by what comes before and after it: lengths and division 2 to 4 us, the first keys 4, joining 3 to 7.  Measured with 32 heads of 128 over 8 (us; bytes at a
+// and by what comes before and after it: lengths and division 2 to 4 us, the first keys 4, joining 3 to 7.  Measured over several GPUs with 32 heads of 128 over 8 (us; bytes at a
 // copy's rate in brackets): 4 bits, one sequence of 777 10.3 to 12.2 (0.15), one of 100003 41 (19), 48 sequences of up to 16384 99 (67); 8 bits, f16, up
-// to 5 drafts of 16 sequences over 4000 (16 heads) 32 to 35 (9), a window of 1024 over 33 sequences 25 to 28 (12).  Steps on the way, the 48 sequences: a ring
+// to 5 drafts of 16 sequences over 4000 (16 heads) 31 to 35 (9), a window of 1024 over 33 sequences 25 to 29 (12).  Steps on the way, the 48 sequences: a ring
 // of asynchronous 16-byte copies a warp, one head a block 200; heads side by side 130; the block's ring of whole lines 104; queries asked for before the copies 99.  Slower
 // were a copy a row (151 to 170), a ring a warp (121 to 145), a warp that only copies (116), rounds of one piece (113), even shares (107).
 #pragma once

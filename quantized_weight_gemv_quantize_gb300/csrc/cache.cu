@@ -3,8 +3,8 @@
 // Both move a token's pieces of 8 elements, keys' heads first, then values': a piece's place within the token is worked out once a thread and
 // kept over the tokens of a block; the tokens' places in the cache are looked up once a block, into shared memory.
 //
-// Both are bound by memory for long runs, with the arithmetic of a value close behind (issue slots 70% taken), and by their launch for short ones.  8
-// heads of 128 (us; bytes at a copy's rate in brackets): 16000 tokens written in 4 bits from bf16 24.8 (12.6), from fp32 29 (22), in 8 bits 25 (15); read back
+// Both are bound by memory for long runs, with the arithmetic of a value close behind (issue slots 65% taken by the write, 71% by the read), and by their launch for short
+// ones.  8 heads of 128 (us; bytes at a copy's rate in brackets): 16000 tokens written in 4 bits from bf16 23 to 25 (12.6), from fp32 29 (22), in 8 bits 25 (15), 31 (25); read back
 // to bf16 18.8 (12.6); 100003 tokens read to bf16 97 (79), in 8 bits 109 (89); one token either way 7, of which 5 are the caller's.  Steps on the way, writing
 // and reading 16000: values converted as they came, one token a thread in flight 55.7 and 31; values packed until they are stored, four tokens
 // in flight, the codes' arithmetic as in codes8 27 and 20.6; codes made floats where they stand (Packed8) 18.8; a block's step and base found once, not
