@@ -87,3 +87,10 @@ def test_the_scratch_of_the_largest_sizes_serves_calls_with_and_without_a_copy(L
         for s, q, c in (most, (1, new, min(ctx, 24000)), (seqs - 1, new, ctx), (min(seqs, 100), new, ctx), (seqs, 1, ctx), (2, new // 2, ctx // 2)):
             for dtype in (BF16, F16):
                 assert call(L, kind, dtype, s, q, c, n) in (4, 5)
+
+
+def test_the_bindings_bound_is_the_headers():
+    import os
+    import re
+    text = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "qgemv.h")).read()
+    assert int(re.search(r"#define QGEMV_ATTN_COPY_MAX (\d+)ull", text).group(1)) == qg.QGEMV_ATTN_COPY_MAX
